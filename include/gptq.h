@@ -264,6 +264,125 @@ gptq_status gptq_repack_act_order(void *stream, const uint32_t *qweight,
                                   int32_t bits, int32_t group, uint32_t *qweight_out,
                                   int32_t *perm_out, void *workspace, size_t ws_bytes);
 
+/* ---- Mixtures of experts: rows in the order of their experts, and back -------
+ * A layer with E experts sends each of T tokens to k of them. The packed
+ * products below, and gptq_accumulate_hessian on a slice of rows, want the
+ * rows of one expert contiguous. A slot is a pair (t, j), its number
+ * i = t k + j; R = T k.
+ *
+ * gptq_route: expert_ids (T x k int32, row pitch ldi >= k) -> the stable
+ * order of the slots by expert. offsets (E + 1 int32): expert e holds the
+ * places offsets[e] .. offsets[e + 1] - 1. rows (R int32): the token of each
+ * place. inverse (R int32, slot order): each slot's place. Ids outside
+ * [0, E) (padding, dropped tokens) hold no place: their inverse is -1, and
+ * rows is -1 from offsets[E] on. 1 <= E <= GPTQ_MAX_EXPERTS, k >= 1,
+ * T k < 2^31; T == 0 writes zero offsets. The order does not depend on
+ * timing. Workspace: gptq_route_workspace_bytes (0 for up to 4096 slots). */
+#define GPTQ_MAX_EXPERTS 1024
+gptq_status gptq_route_workspace_bytes(int64_t T, int64_t k, int64_t E, size_t *bytes);
+gptq_status gptq_route(void *stream, const int32_t *expert_ids, int64_t ldi, int64_t T, int64_t k, int64_t E,
+                       int32_t *offsets, int32_t *rows, int32_t *inverse, void *workspace, size_t ws_bytes);
+
+/* gptq_dispatch: Xs[inverse[t k + j]] = X[t] (bits copied; X: T x n, Xs: R x
+ * n, dtype dt, row pitches ldx, lds >= n). R is the number of rows of Xs:
+ * slots whose place is outside [0, R) are skipped, and rows of Xs that no
+ * slot names keep what they held. Places must be distinct.
+ *
+ * gptq_combine: Y[t] = sum_j weights[t k + j] Ys[inverse[t k + j]], summed in
+ * the order of j in fp32 and rounded once (Y: T x n, ydt; Ys: R x n, ysdt;
+ * weights: R fp32, or NULL for weights of one, which makes it the gradient of
+ * gptq_dispatch). Slots whose place is outside [0, R) add nothing; a token
+ * with none gets zeros.
+ *
+ * gptq_combine_grad: the gradients of gptq_combine for dY (T x n, dydt):
+ * dYs[inverse[i]] = weights[i] dY[t] (R x n, odt; rows that no slot names
+ * keep what they held) and dweights[i] = <dY[t], Ys[inverse[i]]> (R fp32, 0
+ * for a slot without a place; fp32 sums in a fixed order).
+ *
+ * dtypes are GPTQ_BF16 or GPTQ_F32, each argument its own; any alignment and
+ * pitch (16-byte aligned rows move in 16-byte pieces). No output may overlap
+ * an input. All asynchronous, no workspace. */
+gptq_status gptq_dispatch(void *stream, const void *X, int32_t dt, int64_t T, int64_t n, int64_t ldx, int64_t k,
+                          const int32_t *inverse, int64_t R, void *Xs, int64_t lds);
+gptq_status gptq_combine(void *stream, const void *Ys, int32_t ysdt, int64_t R, int64_t lds, const int32_t *inverse,
+                         const float *weights, int64_t T, int64_t n, int64_t k, void *Y, int32_t ydt, int64_t ldy);
+gptq_status gptq_combine_grad(void *stream, const void *dY, int32_t dydt, int64_t ldy, const void *Ys, int32_t ysdt,
+                              int64_t R, int64_t lds, const int32_t *inverse, const float *weights, int64_t T,
+                              int64_t n, int64_t k, void *dYs, int32_t odt, int64_t ldo, float *dweights);
+
+/* ---- Products of experts' packed weights --------------------------------------
+ * E layers of the same shape in the packed layout of gptq_dequant_matmul, one
+ * after another: qweight E x d_out x n*bits/32 words (16-byte aligned base),
+ * scales and zeros E x d_out x n/group; group a positive multiple of 32 that
+ * divides n, groups contiguous (layers quantized without act-order). offsets
+ * (E + 1 int32 on the device, as gptq_route writes them) split the R rows
+ * into the experts' segments; NULL with E = 1 gives all rows to the one
+ * layer. Rows from offsets[E] on are not read, and their outputs keep what
+ * they held. The offsets are read on the device (nothing waits for the host),
+ * clamped to [0, R] there.
+ *
+ * gptq_expert_matmul: Y[p] = X[rows[p]] W_hat_e^T for the rows p of expert e
+ * (Y: R x d_out, ydt bf16 or fp32, row pitch ldy; X: T x n bf16, row pitch
+ * ldx). rows (R int32, as gptq_route writes them; clamped to [0, T)) spares
+ * the copy of gptq_dispatch; NULL: X holds the R sorted rows (T >= R).
+ * Products of activations and integers are exact in fp32, sums are fp32 in a
+ * fixed order, and every group's sum is scaled in fp32: the weights are never
+ * rounded. Results are bitwise reproducible. Few rows per expert (R <= 16 E)
+ * take a matrix-vector form, in which an infinite activation may give NaN
+ * where the sum is infinite.
+ *
+ * gptq_expert_matmul_grad: dX[p] = dY[p] W_hat_e (dX: R x n, dxdt; dY: R x
+ * d_out bf16, row pitch ldy). The scale changes along this sum: with a bf16
+ * result each weight s (q - z) is rounded to bf16 once (relative 2^-8 at
+ * most); with an fp32 result it is taken in three bf16 pieces, which hold
+ * its fp32 value, at three times the matrix work. Sums are fp32 in a fixed
+ * order.
+ *
+ * d_out >= 1, n >= 1; R == 0 enqueues nothing. Rows of X and dY may have any
+ * alignment (16-byte aligned rows are faster). Asynchronous, no workspace.
+ * ("El balance de errores de la inferencia de pocos bits", section 6: decode
+ * and prefill are separate regimes of one dequantising product.) */
+gptq_status gptq_expert_matmul(void *stream, const void *X, int32_t xdt, int64_t T, int64_t n, int64_t ldx,
+                               const int32_t *rows, int64_t R, const int32_t *offsets, int64_t E,
+                               const uint32_t *qweight, const float *scales, const uint8_t *zeros, int64_t d_out,
+                               int32_t bits, int32_t group, void *Y, int32_t ydt, int64_t ldy);
+gptq_status gptq_expert_matmul_grad(void *stream, const void *dY, int32_t dydt, int64_t R, int64_t ldy,
+                                    const int32_t *offsets, int64_t E, const uint32_t *qweight, const float *scales,
+                                    const uint8_t *zeros, int64_t d_out, int64_t n, int32_t bits, int32_t group,
+                                    void *dX, int32_t dxdt, int64_t ldx);
+
+/* ---- Activations kept in 8 bits for the backward pass -------------------------
+ * X (T x n, bf16 or fp32, row pitch ldx) is kept as codes (T x 32 ceil(n / 32)
+ * int8, 16-byte aligned base, the columns past n zero) and exps (T x
+ * ceil(n / 32) uint8), one byte per group of 32 columns of a row:
+ *   exps = max(exponent field of max|x| - 6, 1) (fp32 fields: 127 is 1.0),
+ *   step = 2^(exps - 127), code = clamp(rint(x / step), -127, 127),
+ *   x_hat = code step.
+ * With 2^p <= max|x| < 2^(p + 1) the step is 2^(p - 6): errors are at most
+ * half a step, up to a whole one within half a step of 2^(p + 1). x_hat is
+ * exact in bf16. A group with an infinity or NaN has exps = 255 and codes 0
+ * and comes back as NaN.
+ *
+ * gptq_checkpoint_weight_grad: G (E x m x n fp32, contiguous) with
+ * G[e] = sum over the rows p of segment e of P[p]^T x_hat[rows[p]] (P: R x m
+ * bf16, row pitch ldp): the weight gradient of a linear layer (P = dY), or of
+ * an adapter's input factor (P = dY B), from the kept input. offsets, rows
+ * and E as above (one kept row per token serves its k places); an empty
+ * segment's G is zero. Products are exact, sums fp32 in a fixed order.
+ * Workspace: gptq_checkpoint_weight_grad_workspace_bytes (fp32 partial sums
+ * when few tiles split the rows). All asynchronous.
+ * ("Resumen Técnico: GPTQ-intrinsic LoRA", "Declaración del Problema": the
+ * low-rank factors beside the quantized layer, which tuning moves.) */
+gptq_status gptq_checkpoint_save(void *stream, const void *X, int32_t dt, int64_t T, int64_t n, int64_t ldx,
+                                 int8_t *codes, uint8_t *exps);
+gptq_status gptq_checkpoint_restore(void *stream, const int8_t *codes, const uint8_t *exps, int64_t T, int64_t n,
+                                    void *X, int32_t dt, int64_t ldx);
+gptq_status gptq_checkpoint_weight_grad_workspace_bytes(int64_t R, int64_t E, int64_t m, int64_t n, size_t *bytes);
+gptq_status gptq_checkpoint_weight_grad(void *stream, const void *P, int32_t pdt, int64_t R, int64_t m, int64_t ldp,
+                                        const int8_t *codes, const uint8_t *exps, int64_t T, int64_t n,
+                                        const int32_t *rows, const int32_t *offsets, int64_t E, float *G,
+                                        void *workspace, size_t ws_bytes);
+
 /* ---- EoRA: rank-r compensation of the compression error ----------------------
  * B (d_out x rank fp32, row-major) and A (rank x n fp32, row-major) such that
  * W_hat + B A is the best rank-r correction of W_hat in the layer loss

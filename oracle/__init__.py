@@ -14,6 +14,7 @@ packing    the LSB-first code bitstream and its inverse
 dequant    the dequantising product Y = X W_hat^T of a packed layer
 eora       the EoRA low-rank adapter of the compression error
 intrinsic  OLrC / Bid-Up refinement of a low-precision plus low-rank layer
+experts    rows by expert and back, products over experts, 8-bit activations
 memory     storage accounting used by the pages' worked examples
 
 Every function names the passage of the pages it follows. The pages are:

@@ -246,6 +246,61 @@ hipError_t launch_dequant_mm(hipStream_t s, const DqPlan& p, const uint16_t* X, 
                              int64_t ldx, const uint32_t* qw, const float* scales, const uint8_t* zeros,
                              int64_t d_out, int bits, int group, float* Y, int64_t ldy, float* part);
 
+// ---- route.hip: tokens in the order of their experts, and back
+constexpr int kRouteMaxExperts = 1024;
+constexpr int64_t kRouteOneBlock = 4096;    // slots up to which one workgroup does it all
+constexpr int64_t kRouteBlockSlots = 1024;  // slots per workgroup beyond
+size_t route_workspace(int64_t R, int64_t E);
+hipError_t launch_route(hipStream_t s, const int32_t* ids, int64_t ldi, int64_t T, int k, int E, int32_t* offsets,
+                        int32_t* rows, int32_t* inverse, void* ws);
+hipError_t launch_dispatch(hipStream_t s, const void* X, int esize, int64_t T, int64_t n, int64_t ldx, int k,
+                           const int32_t* inverse, int64_t R, void* Xs, int64_t lds);
+struct CombineArgs {
+  const void* Ys; int ys_bf16; int64_t R, lds;
+  const int32_t* inverse; const float* w;     // w may be null: weights of one
+  int64_t T, n; int k;
+  void* Y; int y_bf16; int64_t ldy;
+};
+hipError_t launch_combine(hipStream_t s, const CombineArgs& a);
+struct CombineGradArgs {
+  const void* dY; int dy_bf16; int64_t ldy;
+  const void* Ys; int ys_bf16; int64_t R, lds;
+  const int32_t* inverse; const float* w;
+  int64_t T, n; int k;
+  void* dYs; int out_bf16; int64_t ldo;
+  float* dw;
+};
+hipError_t launch_combine_grad(hipStream_t s, const CombineGradArgs& a);
+
+// ---- keep.hip: activations kept in 8 bits
+hipError_t launch_keep_save(hipStream_t s, const void* X, int bf16, int64_t T, int64_t n, int64_t ldx,
+                            int8_t* codes, uint8_t* exps);
+hipError_t launch_keep_restore(hipStream_t s, const int8_t* codes, const uint8_t* exps, int64_t T, int64_t n,
+                               void* X, int bf16, int64_t ldx);
+
+// ---- experts.hip: products of experts' packed weights, and the weight
+// gradient from kept activations
+struct ExpertArgs {
+  const void* A; int64_t lda;                 // X (T x n) or dY (R x d_out), bf16
+  const int32_t* rows; int T;                 // source row of each sorted row, or null
+  const int32_t* offsets; int E, R;           // null: one segment of all R rows
+  const uint32_t* qw; const float* scales; const uint8_t* zeros;
+  int64_t d_out, n; int bits, group;
+  void* Y; int y_bf16; int64_t ldy;
+};
+int64_t expert_grid(const ExpertArgs& a, int grad);   // an upper bound on the workgroups of a launch
+hipError_t launch_expert_mm(hipStream_t s, const ExpertArgs& a);
+hipError_t launch_expert_mm_grad(hipStream_t s, const ExpertArgs& a);
+struct KeepGradPlan {
+  int bm;               // rows of a tile of G: 32, 64 or 128
+  int splits;           // parts a segment's rows are split into
+  size_t part_bytes;    // fp32 partials when splits > 1
+};
+KeepGradPlan keep_grad_plan(int64_t R, int E, int64_t m, int64_t n);
+hipError_t launch_keep_grad(hipStream_t s, const KeepGradPlan& pl, const uint16_t* P, int64_t ldp, int64_t R, int64_t m,
+                            const int8_t* codes, const uint8_t* exps, int64_t T, int64_t n, const int32_t* rows,
+                            const int32_t* offsets, int E, float* G, float* part);
+
 // ---- eora.hip: rank-r compensation of a layer's error
 hipError_t launch_eora_delta(hipStream_t s, const void* W, int wbf16, int64_t ldw, const float* Wh,
                              int64_t d_out, int64_t n, float* D, DevStatus* st);

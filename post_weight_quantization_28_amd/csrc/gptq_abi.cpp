@@ -1024,6 +1024,229 @@ gptq_status gptq_dequant_matmul_noalloc(void* stream, const void* X, int32_t xdt
 }
 
 
+// ---------------------------------------------------------------- experts
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;       // places are int32
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 512;  // of one launch
+
+gptq_status dt_check(int32_t dt) {
+  return dt == GPTQ_BF16 || dt == GPTQ_F32 ? GPTQ_OK : fail(GPTQ_EINVAL, "dtype must be GPTQ_BF16 or GPTQ_F32");
+}
+
+bool mis(const void* p, int32_t dt) { return ((uintptr_t)p & (dt == GPTQ_BF16 ? 1 : 3)) != 0; }
+
+// Sizes of a call over slots: T tokens, k slots each, n columns.
+gptq_status slots_check(int64_t T, int64_t n, int64_t k, int64_t R) {
+  if (T < 0 || n < 0 || R < 0) return fail(GPTQ_EINVAL, "negative size");
+  if (k < 1) return fail(GPTQ_EINVAL, "k must be at least 1");
+  if (T > kMaxRows / k || R > kMaxRows) return fail(GPTQ_EINVAL, "too many slots (T k must be below 2^31)");
+  if (n > 0 && T > kMaxThreads / n) return fail(GPTQ_EINVAL, "T n is too large for one launch");
+  if (T > kMaxThreads / 256) return fail(GPTQ_EINVAL, "T is too large for one launch");
+  return GPTQ_OK;
+}
+
+gptq_status experts_check(int64_t E, const int32_t* offsets) {
+  if (E < 1 || E > GPTQ_MAX_EXPERTS) return fail(GPTQ_EINVAL, "need 1 <= E <= GPTQ_MAX_EXPERTS");
+  if (!offsets && E != 1) return fail(GPTQ_EINVAL, "offsets is NULL with more than one expert");
+  return GPTQ_OK;
+}
+
+// The checks that both expert products share (R > 0).
+gptq_status expert_weights_check(const ExpertArgs& a, int grad) {
+  if (!a.A || !a.qw || !a.scales || !a.zeros || !a.Y) return fail(GPTQ_EINVAL, "NULL pointer");
+  if (mis(a.A, GPTQ_BF16) || mis(a.Y, a.y_bf16 ? GPTQ_BF16 : GPTQ_F32))
+    return fail(GPTQ_EINVAL, "a matrix is not aligned to its elements");
+  if (((uintptr_t)a.qw & 15) != 0) return fail(GPTQ_EINVAL, "qweight must be 16-byte aligned");
+  if (a.d_out > kMaxRows || a.n > kMaxRows) return fail(GPTQ_EINVAL, "d_out or n too large");
+  if (expert_grid(a, grad) > kMaxThreads / 256) return fail(GPTQ_EINVAL, "product too large for one launch");
+  return GPTQ_OK;
+}
+
+gptq_status keep_check(int64_t T, int64_t n, int32_t dt, int64_t ldx, const void* X, const void* codes,
+                       const void* exps) {
+  gptq_status st = dt_check(dt);
+  if (st != GPTQ_OK) return st;
+  if (T < 0 || n < 0) return fail(GPTQ_EINVAL, "negative size");
+  if (T == 0 || n == 0) return GPTQ_OK;
+  if (n > kMaxRows || T > kMaxThreads / (4 * ceil_div(n, 32))) return fail(GPTQ_EINVAL, "T n is too large for one launch");
+  if (ldx < n) return fail(GPTQ_EINVAL, "ldx < n");
+  if (!X || !codes || !exps) return fail(GPTQ_EINVAL, "NULL pointer");
+  if (mis(X, dt)) return fail(GPTQ_EINVAL, "X is not aligned to its elements");
+  if (((uintptr_t)codes & 15) != 0) return fail(GPTQ_EINVAL, "codes must be 16-byte aligned");
+  return GPTQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gptq_status gptq_route_workspace_bytes(int64_t T, int64_t k, int64_t E, size_t* bytes) {
+  if (!bytes) return fail(GPTQ_EINVAL, "bytes is NULL");
+  if (E < 1 || E > GPTQ_MAX_EXPERTS) return fail(GPTQ_EINVAL, "need 1 <= E <= GPTQ_MAX_EXPERTS");
+  const gptq_status st = slots_check(T, 0, k, 0);
+  if (st != GPTQ_OK) return st;
+  *bytes = (route_workspace(T * k, E) + 255) / 256 * 256;
+  return GPTQ_OK;
+}
+
+gptq_status gptq_route(void* stream, const int32_t* expert_ids, int64_t ldi, int64_t T, int64_t k, int64_t E,
+                       int32_t* offsets, int32_t* rows, int32_t* inverse, void* workspace, size_t ws_bytes) {
+  size_t need = 0;
+  gptq_status st = gptq_route_workspace_bytes(T, k, E, &need);
+  if (st != GPTQ_OK) return st;
+  if (!offsets) return fail(GPTQ_EINVAL, "NULL pointer");
+  if (T > 0) {
+    if (ldi < k) return fail(GPTQ_EINVAL, "ldi < k");
+    if (!expert_ids || !rows || !inverse) return fail(GPTQ_EINVAL, "NULL pointer");
+  }
+  if ((st = check_ws(workspace, ws_bytes, need)) != GPTQ_OK) return st;
+  HIP_TRY(launch_route((hipStream_t)stream, expert_ids, ldi, T, (int)k, (int)E, offsets, rows, inverse, workspace),
+          "route");
+  return GPTQ_OK;
+}
+
+gptq_status gptq_dispatch(void* stream, const void* X, int32_t dt, int64_t T, int64_t n, int64_t ldx, int64_t k,
+                          const int32_t* inverse, int64_t R, void* Xs, int64_t lds) {
+  gptq_status st = dt_check(dt);
+  if (st != GPTQ_OK || (st = slots_check(T, n, k, R)) != GPTQ_OK) return st;
+  if (T == 0 || n == 0 || R == 0) return GPTQ_OK;
+  if (ldx < n || lds < n) return fail(GPTQ_EINVAL, "row pitch below n");
+  if (!X || !inverse || !Xs) return fail(GPTQ_EINVAL, "NULL pointer");
+  if (mis(X, dt) || mis(Xs, dt)) return fail(GPTQ_EINVAL, "a matrix is not aligned to its elements");
+  HIP_TRY(launch_dispatch((hipStream_t)stream, X, dt == GPTQ_BF16 ? 2 : 4, T, n, ldx, (int)k, inverse, R, Xs, lds),
+          "dispatch");
+  return GPTQ_OK;
+}
+
+gptq_status gptq_combine(void* stream, const void* Ys, int32_t ysdt, int64_t R, int64_t lds, const int32_t* inverse,
+                         const float* weights, int64_t T, int64_t n, int64_t k, void* Y, int32_t ydt, int64_t ldy) {
+  gptq_status st = dt_check(ysdt);
+  if (st != GPTQ_OK || (st = dt_check(ydt)) != GPTQ_OK || (st = slots_check(T, n, k, R)) != GPTQ_OK) return st;
+  if (T == 0 || n == 0) return GPTQ_OK;
+  if (ldy < n || (R > 0 && lds < n)) return fail(GPTQ_EINVAL, "row pitch below n");
+  if ((R > 0 && !Ys) || !inverse || !Y) return fail(GPTQ_EINVAL, "NULL pointer");
+  if (mis(Ys, ysdt) || mis(Y, ydt)) return fail(GPTQ_EINVAL, "a matrix is not aligned to its elements");
+  const CombineArgs a = {Ys, ysdt == GPTQ_BF16, R, lds, inverse, weights, T, n, (int)k, Y, ydt == GPTQ_BF16, ldy};
+  HIP_TRY(launch_combine((hipStream_t)stream, a), "combine");
+  return GPTQ_OK;
+}
+
+gptq_status gptq_combine_grad(void* stream, const void* dY, int32_t dydt, int64_t ldy, const void* Ys, int32_t ysdt,
+                              int64_t R, int64_t lds, const int32_t* inverse, const float* weights, int64_t T,
+                              int64_t n, int64_t k, void* dYs, int32_t odt, int64_t ldo, float* dweights) {
+  gptq_status st = dt_check(dydt);
+  if (st != GPTQ_OK || (st = dt_check(ysdt)) != GPTQ_OK || (st = dt_check(odt)) != GPTQ_OK ||
+      (st = slots_check(T, n, k, R)) != GPTQ_OK)
+    return st;
+  if (T == 0) return GPTQ_OK;
+  if (!inverse || !weights || !dweights) return fail(GPTQ_EINVAL, "NULL pointer");
+  if (n > 0) {
+    if (ldy < n || (R > 0 && (lds < n || ldo < n))) return fail(GPTQ_EINVAL, "row pitch below n");
+    if (!dY || (R > 0 && (!Ys || !dYs))) return fail(GPTQ_EINVAL, "NULL pointer");
+    if (mis(dY, dydt) || mis(Ys, ysdt) || mis(dYs, odt))
+      return fail(GPTQ_EINVAL, "a matrix is not aligned to its elements");
+  }
+  const CombineGradArgs a = {dY, dydt == GPTQ_BF16, ldy, Ys, ysdt == GPTQ_BF16, R, lds, inverse, weights,
+                             T,  n, (int)k, dYs, odt == GPTQ_BF16, ldo, dweights};
+  HIP_TRY(launch_combine_grad((hipStream_t)stream, a), "combine_grad");
+  return GPTQ_OK;
+}
+
+gptq_status gptq_expert_matmul(void* stream, const void* X, int32_t xdt, int64_t T, int64_t n, int64_t ldx,
+                               const int32_t* rows, int64_t R, const int32_t* offsets, int64_t E,
+                               const uint32_t* qweight, const float* scales, const uint8_t* zeros, int64_t d_out,
+                               int32_t bits, int32_t group, void* Y, int32_t ydt, int64_t ldy) {
+  gptq_status st = dq_check(R, n, d_out, bits, group);
+  if (st != GPTQ_OK || (st = experts_check(E, offsets)) != GPTQ_OK || (st = dt_check(ydt)) != GPTQ_OK) return st;
+  if (xdt != GPTQ_BF16) return fail(GPTQ_EINVAL, "expert_matmul takes bf16 activations");
+  if (n < 1 || d_out < 1) return fail(GPTQ_EINVAL, "need n >= 1 and d_out >= 1");
+  if (T < 0 || T > kMaxRows || R > kMaxRows) return fail(GPTQ_EINVAL, "T and R must be in [0, 2^31)");
+  if (R == 0) return GPTQ_OK;
+  if (rows ? T < 1 : T < R) return fail(GPTQ_EINVAL, "X has too few rows");
+  if (ldx < n) return fail(GPTQ_EINVAL, "ldx < n");
+  if (ldy < d_out) return fail(GPTQ_EINVAL, "ldy < d_out");
+  const ExpertArgs a = {X, ldx, rows, (int)T, offsets, (int)E, (int)R, qweight, scales, zeros,
+                        d_out, n, bits, group, Y, ydt == GPTQ_BF16, ldy};
+  if ((st = expert_weights_check(a, 0)) != GPTQ_OK) return st;
+  HIP_TRY(launch_expert_mm((hipStream_t)stream, a), "expert_matmul");
+  return GPTQ_OK;
+}
+
+gptq_status gptq_expert_matmul_grad(void* stream, const void* dY, int32_t dydt, int64_t R, int64_t ldy,
+                                    const int32_t* offsets, int64_t E, const uint32_t* qweight, const float* scales,
+                                    const uint8_t* zeros, int64_t d_out, int64_t n, int32_t bits, int32_t group,
+                                    void* dX, int32_t dxdt, int64_t ldx) {
+  gptq_status st = dq_check(R, n, d_out, bits, group);
+  if (st != GPTQ_OK || (st = experts_check(E, offsets)) != GPTQ_OK || (st = dt_check(dxdt)) != GPTQ_OK) return st;
+  if (dydt != GPTQ_BF16) return fail(GPTQ_EINVAL, "expert_matmul_grad takes a bf16 gradient");
+  if (n < 1 || d_out < 1) return fail(GPTQ_EINVAL, "need n >= 1 and d_out >= 1");
+  if (R > kMaxRows) return fail(GPTQ_EINVAL, "R must be in [0, 2^31)");
+  if (R == 0) return GPTQ_OK;
+  if (ldy < d_out) return fail(GPTQ_EINVAL, "ldy < d_out");
+  if (ldx < n) return fail(GPTQ_EINVAL, "ldx < n");
+  const ExpertArgs a = {dY, ldy, nullptr, (int)R, offsets, (int)E, (int)R, qweight, scales, zeros,
+                        d_out, n, bits, group, dX, dxdt == GPTQ_BF16, ldx};
+  if ((st = expert_weights_check(a, 1)) != GPTQ_OK) return st;
+  HIP_TRY(launch_expert_mm_grad((hipStream_t)stream, a), "expert_matmul_grad");
+  return GPTQ_OK;
+}
+
+// ---------------------------------------------------------------- kept activations
+gptq_status gptq_checkpoint_save(void* stream, const void* X, int32_t dt, int64_t T, int64_t n, int64_t ldx,
+                                 int8_t* codes, uint8_t* exps) {
+  const gptq_status st = keep_check(T, n, dt, ldx, X, codes, exps);
+  if (st != GPTQ_OK) return st;
+  HIP_TRY(launch_keep_save((hipStream_t)stream, X, dt == GPTQ_BF16, T, n, ldx, codes, exps), "checkpoint_save");
+  return GPTQ_OK;
+}
+
+gptq_status gptq_checkpoint_restore(void* stream, const int8_t* codes, const uint8_t* exps, int64_t T, int64_t n,
+                                    void* X, int32_t dt, int64_t ldx) {
+  const gptq_status st = keep_check(T, n, dt, ldx, X, codes, exps);
+  if (st != GPTQ_OK) return st;
+  HIP_TRY(launch_keep_restore((hipStream_t)stream, codes, exps, T, n, X, dt == GPTQ_BF16, ldx), "checkpoint_restore");
+  return GPTQ_OK;
+}
+
+gptq_status gptq_checkpoint_weight_grad_workspace_bytes(int64_t R, int64_t E, int64_t m, int64_t n, size_t* bytes) {
+  if (!bytes) return fail(GPTQ_EINVAL, "bytes is NULL");
+  if (R < 0 || m < 0 || n < 0) return fail(GPTQ_EINVAL, "negative size");
+  if (E < 1 || E > GPTQ_MAX_EXPERTS) return fail(GPTQ_EINVAL, "need 1 <= E <= GPTQ_MAX_EXPERTS");
+  if (R > kMaxRows || m > kMaxRows || n > kMaxRows || (m > 0 && n > 0 && E * m > kMaxThreads / n))
+    return fail(GPTQ_EINVAL, "gradient too large for one launch");
+  *bytes = (keep_grad_plan(R, (int)E, m, n).part_bytes + 255) / 256 * 256;
+  return GPTQ_OK;
+}
+
+gptq_status gptq_checkpoint_weight_grad(void* stream, const void* P, int32_t pdt, int64_t R, int64_t m, int64_t ldp,
+                                        const int8_t* codes, const uint8_t* exps, int64_t T, int64_t n,
+                                        const int32_t* rows, const int32_t* offsets, int64_t E, float* G,
+                                        void* workspace, size_t ws_bytes) {
+  size_t need = 0;
+  gptq_status st = gptq_checkpoint_weight_grad_workspace_bytes(R, E, m, n, &need);
+  if (st != GPTQ_OK || (st = experts_check(E, offsets)) != GPTQ_OK) return st;
+  if (pdt != GPTQ_BF16) return fail(GPTQ_EINVAL, "checkpoint_weight_grad takes a bf16 P");
+  if (T < 0 || T > kMaxRows) return fail(GPTQ_EINVAL, "T must be in [0, 2^31)");
+  if (m == 0 || n == 0) return GPTQ_OK;
+  if (!G) return fail(GPTQ_EINVAL, "NULL pointer");
+  if (R > 0) {
+    if (rows ? T < 1 : T < R) return fail(GPTQ_EINVAL, "the kept activations have too few rows");
+    if (ldp < m) return fail(GPTQ_EINVAL, "ldp < m");
+    if (!P || !codes || !exps) return fail(GPTQ_EINVAL, "NULL pointer");
+    if (mis(P, GPTQ_BF16)) return fail(GPTQ_EINVAL, "P is not aligned to its elements");
+    if (((uintptr_t)codes & 15) != 0) return fail(GPTQ_EINVAL, "codes must be 16-byte aligned");
+  }
+  if ((st = check_ws(workspace, ws_bytes, need)) != GPTQ_OK) return st;
+  const KeepGradPlan pl = keep_grad_plan(R, (int)E, m, n);
+  HIP_TRY(launch_keep_grad((hipStream_t)stream, pl, static_cast<const uint16_t*>(P), ldp, R, m, codes, exps, T, n, rows,
+                           offsets, (int)E, G, static_cast<float*>(workspace)),
+          "checkpoint_weight_grad");
+  return GPTQ_OK;
+}
+
 // ---------------------------------------------------------------- EoRA
 gptq_status gptq_eora_workspace_bytes(int64_t d_out, int64_t n, int32_t rank, int32_t with_h, size_t* bytes) {
   if (!bytes) return fail(GPTQ_EINVAL, "bytes is NULL");

@@ -1,0 +1,493 @@
+// Tokens in the order of their experts, and back.
+//
+// A mixture of experts sends token t to the experts ids[t][0..k). The packed
+// layers of this library work on contiguous rows, so the T k slots
+// i = t k + j are put in the stable order of their expert:
+//   offsets[e] = #{kept slots with an expert below e},
+//   inverse[i] = offsets[ids[i]] + #{kept slots i' < i with the same expert},
+//   rows[inverse[i]] = t.
+// A slot whose id is outside [0, E) is dropped: inverse[i] = -1, and the
+// last T k - offsets[E] entries of rows are -1. The way there copies
+// Xs[inverse[i]] = X[t]; the way back is Y[t] = sum_j w[t][j] Ys[inverse[t k + j]],
+// whose gradients are dYs[inverse[i]] = w[i] dY[t] and
+// dw[i] = <dY[t], Ys[inverse[i]]>; the gradient of the way there is the way
+// back with weights of one.
+//
+// The order is a counting sort whose ranks come from ballots, never from
+// atomics that return a place, so it does not depend on timing. Everything
+// here is bound by memory (or, for a few tokens, by the launches): the
+// copies are organised by token, so each row of X and dY is read once and
+// its k copies leave from registers, and the way back adds the k rows in
+// the order of j in fp32 and rounds once.
+#include "common.h"
+#include "dma.h"
+
+#include <algorithm>
+
+namespace gq {
+
+typedef unsigned int rt_u32x4_t __attribute__((ext_vector_type(4)));
+typedef float rt_f32x4_t __attribute__((ext_vector_type(4)));
+
+// ---------------------------------------------------------------- the order
+constexpr int kRtSteps = 4;          // 64-slot steps per wave
+constexpr int kRtMaxBuckets = kRouteMaxExperts + 1;   // the last bucket: dropped slots
+
+__device__ __forceinline__ int rt_bucket(const int32_t* __restrict__ ids, int64_t ldi, int k, int64_t i, int E) {
+  const int64_t t = i / k;
+  const int id = ids[t * ldi + (i - t * k)];
+  return (unsigned)id < (unsigned)E ? id : E;
+}
+
+// Lanes of the wave that hold the same bucket (active lanes only).
+__device__ __forceinline__ uint64_t rt_peers(int b, bool active, int nbits) {
+  uint64_t m = __ballot(active);
+  for (int i = 0; i < nbits; ++i) {
+    const bool bit = (b >> i) & 1;
+    const uint64_t v = __ballot(active && bit);
+    m &= bit ? v : ~v;
+  }
+  return m;
+}
+
+// Ranks of this wave's slots inside their buckets: loc[s] counts the wave's
+// earlier slots of the same bucket, and hist (this wave's row, zeroed)
+// receives the wave's totals.
+__device__ __forceinline__ void rt_rank(const int32_t* __restrict__ ids, int64_t ldi, int k, int64_t first,
+                                        int64_t R, int E, int nbits, uint16_t* hist, int (&bk)[kRtSteps],
+                                        int (&loc)[kRtSteps]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int s = 0; s < kRtSteps; ++s) {
+    const int64_t i = first + 64 * s + lane;
+    bk[s] = i < R ? rt_bucket(ids, ldi, k, i, E) : -1;
+  }
+#pragma unroll
+  for (int s = 0; s < kRtSteps; ++s) {
+    const bool act = bk[s] >= 0;
+    const uint64_t peers = rt_peers(bk[s], act, nbits);
+    const uint64_t before = peers & ((1ull << lane) - 1ull);
+    int base = 0;
+    if (act) {
+      base = hist[bk[s]];
+      loc[s] = base + __popcll(before);
+    }
+    // one lane per bucket adds the step's count; the fences keep the order of
+    // the wave's LDS accesses, whose lanes see each other's values
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (act && before == 0) hist[bk[s]] = (uint16_t)(base + __popcll(peers));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
+// Exclusive sums of v[0..nb) in place (all threads of the block; tmp: one
+// int per wave). Thread t owns ceil(nb / threads) consecutive entries.
+template <int THREADS>
+__device__ void rt_scan(int* v, int nb, int* tmp) {
+  const int per = (nb + THREADS - 1) / THREADS;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int b0 = threadIdx.x * per, b1 = min(nb, b0 + per);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) sum += v[b];
+  int inc = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 63) tmp[wave] = inc;
+  __syncthreads();
+  int run = inc - sum;
+  for (int w = 0; w < wave; ++w) run += tmp[w];
+  for (int b = b0; b < b1; ++b) {
+    const int c = v[b];
+    v[b] = run;
+    run += c;
+  }
+  __syncthreads();
+}
+
+// One workgroup's slots in order. base (LDS): the first place of each
+// bucket; the wave offsets come from the waves' histograms.
+__device__ __forceinline__ void rt_place(const int (&bk)[kRtSteps], const int (&loc)[kRtSteps], int64_t first,
+                                         int64_t R, int k, int E, const int* base, const uint16_t* hist, int nb,
+                                         int wave, int32_t* __restrict__ rows, int32_t* __restrict__ inverse) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int s = 0; s < kRtSteps; ++s) {
+    const int64_t i = first + 64 * s + lane;
+    if (i >= R) continue;
+    int p = base[bk[s]] + loc[s];
+    for (int w = 0; w < wave; ++w) p += hist[w * nb + bk[s]];
+    const bool kept = bk[s] < E;
+    rows[p] = kept ? (int32_t)(i / k) : -1;
+    inverse[i] = kept ? p : -1;
+  }
+}
+
+// All slots in one workgroup of 16 waves (R <= kRouteOneBlock): one launch,
+// which is what a decoding step pays for.
+__global__ void __launch_bounds__(1024)
+k_route_one(const int32_t* __restrict__ ids, int64_t ldi, int64_t R, int k, int E, int nbits,
+            int32_t* __restrict__ offsets, int32_t* __restrict__ rows, int32_t* __restrict__ inverse) {
+  __shared__ uint16_t hist[16 * kRtMaxBuckets];
+  __shared__ int base[kRtMaxBuckets];
+  __shared__ int tmp[16];
+  const int nb = E + 1, wave = threadIdx.x >> 6;
+  for (int i = threadIdx.x; i < 16 * nb; i += 1024) hist[i] = 0;
+  __syncthreads();
+  // wave-major slots, as many steps per wave as the slots need
+  const int64_t steps = ceil_div(R, 16 * 64);
+  const int64_t first = (int64_t)wave * steps * 64;
+  const int64_t end = min(R, first + steps * 64);
+  int bk[kRtSteps], loc[kRtSteps];
+  rt_rank(ids, ldi, k, first, end, E, nbits, hist + wave * nb, bk, loc);
+  __syncthreads();
+  for (int b = threadIdx.x; b < nb; b += 1024) {
+    int c = 0;
+    for (int w = 0; w < 16; ++w) c += hist[w * nb + b];
+    base[b] = c;
+  }
+  __syncthreads();
+  rt_scan<1024>(base, nb, tmp);
+  for (int b = threadIdx.x; b < nb; b += 1024) offsets[b] = base[b];
+  rt_place(bk, loc, first, end, k, E, base, hist, nb, wave, rows, inverse);
+}
+
+// Larger batches, three launches: bucket counts of each block of
+// kRouteBlockSlots slots (count[b][block]), ...
+__global__ void __launch_bounds__(256)
+k_route_count(const int32_t* __restrict__ ids, int64_t ldi, int64_t R, int k, int E, int nblocks,
+              int32_t* __restrict__ count) {
+  __shared__ int h[kRtMaxBuckets];
+  for (int b = threadIdx.x; b <= E; b += 256) h[b] = 0;
+  __syncthreads();
+  const int64_t i0 = (int64_t)blockIdx.x * kRouteBlockSlots;
+#pragma unroll
+  for (int s = 0; s < kRtSteps; ++s) {
+    const int64_t i = i0 + 256 * s + threadIdx.x;
+    if (i < R) atomicAdd(&h[rt_bucket(ids, ldi, k, i, E)], 1);
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b <= E; b += 256) count[(int64_t)b * nblocks + blockIdx.x] = h[b];
+}
+
+// ... their exclusive sums along the blocks, one workgroup per bucket, and
+// the buckets' totals, ...
+__global__ void __launch_bounds__(256)
+k_route_scan(int32_t* __restrict__ count, int nblocks, int32_t* __restrict__ total) {
+  __shared__ int tmp[4];
+  int32_t* __restrict__ c = count + (int64_t)blockIdx.x * nblocks;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int carry = 0;
+  for (int b0 = 0; b0 < nblocks; b0 += 256) {
+    const int b = b0 + threadIdx.x;
+    const int v = b < nblocks ? c[b] : 0;
+    int inc = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(inc, d);
+      if (lane >= d) inc += o;
+    }
+    if (lane == 63) tmp[wave] = inc;
+    __syncthreads();
+    int run = carry + inc - v, all = 0;
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) run += tmp[w];
+      all += tmp[w];
+    }
+    if (b < nblocks) c[b] = run;
+    carry += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) total[blockIdx.x] = carry;
+}
+
+// ... and the places.
+__global__ void __launch_bounds__(256)
+k_route_place(const int32_t* __restrict__ ids, int64_t ldi, int64_t R, int k, int E, int nbits, int nblocks,
+              const int32_t* __restrict__ count, const int32_t* __restrict__ total,
+              int32_t* __restrict__ offsets, int32_t* __restrict__ rows, int32_t* __restrict__ inverse) {
+  __shared__ uint16_t hist[4 * kRtMaxBuckets];
+  __shared__ int base[kRtMaxBuckets];
+  __shared__ int tmp[4];
+  const int nb = E + 1, wave = threadIdx.x >> 6;
+  for (int i = threadIdx.x; i < 4 * nb; i += 256) hist[i] = 0;
+  for (int b = threadIdx.x; b < nb; b += 256) base[b] = total[b];
+  __syncthreads();
+  rt_scan<256>(base, nb, tmp);
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < nb; b += 256) offsets[b] = base[b];
+  const int64_t first = (int64_t)blockIdx.x * kRouteBlockSlots + (int64_t)wave * (64 * kRtSteps);
+  int bk[kRtSteps], loc[kRtSteps];
+  rt_rank(ids, ldi, k, first, R, E, nbits, hist + wave * nb, bk, loc);
+  __syncthreads();
+  for (int b = threadIdx.x; b < nb; b += 256) base[b] += count[(int64_t)b * nblocks + blockIdx.x];
+  __syncthreads();
+  rt_place(bk, loc, first, R, k, E, base, hist, nb, wave, rows, inverse);
+}
+
+size_t route_workspace(int64_t R, int64_t E) {
+  if (R <= kRouteOneBlock) return 0;
+  const int64_t nblocks = ceil_div(R, kRouteBlockSlots);
+  return (size_t)(E + 1) * (size_t)(nblocks + 1) * sizeof(int32_t);
+}
+
+hipError_t launch_route(hipStream_t s, const int32_t* ids, int64_t ldi, int64_t T, int k, int E, int32_t* offsets,
+                        int32_t* rows, int32_t* inverse, void* ws) {
+  const int64_t R = T * k;
+  int nbits = 0;
+  while ((E >> nbits) != 0) ++nbits;      // buckets 0..E
+  if (R <= kRouteOneBlock) {
+    hipLaunchKernelGGL(k_route_one, dim3(1), dim3(1024), 0, s, ids, ldi, R, k, E, nbits, offsets, rows, inverse);
+    return hipGetLastError();
+  }
+  const int nblocks = (int)ceil_div(R, kRouteBlockSlots);
+  int32_t* total = static_cast<int32_t*>(ws);
+  int32_t* count = total + (E + 1);
+  hipLaunchKernelGGL(k_route_count, dim3(nblocks), dim3(256), 0, s, ids, ldi, R, k, E, nblocks, count);
+  hipLaunchKernelGGL(k_route_scan, dim3(E + 1), dim3(256), 0, s, count, nblocks, total);
+  hipLaunchKernelGGL(k_route_place, dim3(nblocks), dim3(256), 0, s, ids, ldi, R, k, E, nbits, nblocks, count, total,
+                     offsets, rows, inverse);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- rows there and back
+// A unit is 8 columns: 16 bytes of bf16, 32 of fp32. VEC: every row of both
+// sides is 16-byte aligned and n % 8 == 0, so units move as whole 16-byte
+// pieces; otherwise columns past n are guarded one by one.
+template <bool BF, bool VEC>
+__device__ __forceinline__ void rt_load8(const void* base, int64_t off, int ncols, float (&v)[8]) {
+  if constexpr (VEC && BF) {
+    const rt_u32x4_t u = *reinterpret_cast<const rt_u32x4_t*>(static_cast<const uint16_t*>(base) + off);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  } else if constexpr (VEC) {
+    const float* p = static_cast<const float*>(base) + off;
+    const rt_f32x4_t a = *reinterpret_cast<const rt_f32x4_t*>(p);
+    const rt_f32x4_t b = *reinterpret_cast<const rt_f32x4_t*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = 0.f;
+      if (i < ncols)
+        v[i] = BF ? bf16_to_f32(static_cast<const uint16_t*>(base)[off + i]) : static_cast<const float*>(base)[off + i];
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t rt_pack2(float a, float b) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  const bf2 p = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, p);
+}
+
+template <bool BF, bool VEC>
+__device__ __forceinline__ void rt_store8(void* base, int64_t off, int ncols, const float (&v)[8]) {
+  if constexpr (VEC && BF) {
+    const rt_u32x4_t u = {rt_pack2(v[0], v[1]), rt_pack2(v[2], v[3]), rt_pack2(v[4], v[5]), rt_pack2(v[6], v[7])};
+    *reinterpret_cast<rt_u32x4_t*>(static_cast<uint16_t*>(base) + off) = u;
+  } else if constexpr (VEC) {
+    float* p = static_cast<float*>(base) + off;
+    *reinterpret_cast<rt_f32x4_t*>(p) = (rt_f32x4_t){v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<rt_f32x4_t*>(p + 4) = (rt_f32x4_t){v[4], v[5], v[6], v[7]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < ncols) {
+        if constexpr (BF) static_cast<uint16_t*>(base)[off + i] = (uint16_t)rt_pack2(v[i], 0.f);
+        else static_cast<float*>(base)[off + i] = v[i];
+      }
+  }
+}
+
+// Xs[inverse[t k + j]] = X[t]: rows of `width` elements of U (16 bytes, or
+// one element when the rows are not aligned), copied bit by bit. One thread
+// per element of X's rows.
+template <typename U>
+__global__ void __launch_bounds__(256)
+k_dispatch(const U* __restrict__ X, int64_t ldx, int64_t T, int64_t width, int k,
+           const int32_t* __restrict__ inverse, int64_t R, U* __restrict__ Xs, int64_t lds) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= T * width) return;
+  const int64_t t = i / width, c = i - t * width;
+  const U v = X[t * ldx + c];
+  for (int j = 0; j < k; ++j) {
+    const int p = inverse[t * k + j];
+    if (p >= 0 && p < R) Xs[(int64_t)p * lds + c] = v;
+  }
+}
+
+// Y[t] = sum_j w[t][j] Ys[inverse[t k + j]]; four rows are loaded before the
+// first is added, so a thread has 64 to 128 bytes in flight.
+template <bool YSBF, bool YBF, bool VEC>
+__global__ void __launch_bounds__(256)
+k_combine(const void* __restrict__ Ys, int64_t lds, int64_t R, const int32_t* __restrict__ inverse,
+          const float* __restrict__ w, int64_t T, int64_t n, int64_t units, int k, void* __restrict__ Y, int64_t ldy) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= T * units) return;
+  const int64_t t = i / units, c = 8 * (i - t * units);
+  const int nc = (int)min((int64_t)8, n - c);
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    float v[4][8], wj[4];
+    bool ok[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u;
+      const int p = j < k ? inverse[t * k + j] : -1;
+      ok[u] = p >= 0 && p < R;
+      wj[u] = ok[u] ? (w ? w[t * k + j] : 1.f) : 0.f;
+      if (ok[u]) rt_load8<YSBF, VEC>(Ys, (int64_t)p * lds + c, nc, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (ok[u]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = fmaf(wj[u], v[u][e], sum[e]);
+      }
+  }
+  rt_store8<YBF, VEC>(Y, t * ldy + c, nc, sum);
+}
+
+// dYs[inverse[t k + j]] = w[t][j] dY[t], dw[t][j] = <dY[t], Ys[inverse[t k + j]]>.
+// One workgroup per token; kCgSlots slots per pass over the columns, so dY
+// is read once for up to that many. The dot products are fp32: a thread's
+// columns in order, then the lanes and the waves in a fixed tree. A dropped
+// slot has dw = 0 and writes no row.
+constexpr int kCgSlots = 8;
+template <bool DYBF, bool YSBF, bool OBF, bool VEC>
+__global__ void __launch_bounds__(256)
+k_combine_grad(const void* __restrict__ dY, int64_t ldy, const void* __restrict__ Ys, int64_t lds, int64_t R,
+               const int32_t* __restrict__ inverse, const float* __restrict__ w, int64_t n, int64_t units, int k,
+               void* __restrict__ dYs, int64_t ldo, float* __restrict__ dw) {
+  __shared__ float red[4][kCgSlots];
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int j0 = 0; j0 < k; j0 += kCgSlots) {
+    float dot[kCgSlots], wj[kCgSlots];
+    int p[kCgSlots];
+#pragma unroll
+    for (int u = 0; u < kCgSlots; ++u) {
+      const int j = j0 + u;
+      const int q = j < k ? inverse[t * k + j] : -1;
+      p[u] = q < R ? q : -1;
+      wj[u] = p[u] >= 0 ? w[t * k + j] : 0.f;
+      dot[u] = 0.f;
+    }
+    for (int64_t i = threadIdx.x; i < units; i += 256) {
+      const int64_t c = 8 * i;
+      const int nc = (int)min((int64_t)8, n - c);
+      float g[8];
+      rt_load8<DYBF, VEC>(dY, t * ldy + c, nc, g);
+#pragma unroll
+      for (int u = 0; u < kCgSlots; ++u) {
+        if (p[u] < 0) continue;
+        float y[8], o[8];
+        rt_load8<YSBF, VEC>(Ys, (int64_t)p[u] * lds + c, nc, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dot[u] = fmaf(g[e], y[e], dot[u]);
+          o[e] = wj[u] * g[e];
+        }
+        rt_store8<OBF, VEC>(dYs, (int64_t)p[u] * ldo + c, nc, o);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kCgSlots; ++u) {
+      float v = dot[u];
+#pragma unroll
+      for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+      if (lane == 0) red[wave][u] = v;
+    }
+    __syncthreads();
+    const int u = threadIdx.x;
+    if (u < kCgSlots && j0 + u < k) dw[t * k + j0 + u] = (red[0][u] + red[1][u]) + (red[2][u] + red[3][u]);
+    __syncthreads();
+  }
+}
+
+static bool rows_aligned(const void* p, int64_t ld, int esize) {
+  return ((uintptr_t)p & 15) == 0 && (ld * esize) % 16 == 0;
+}
+
+hipError_t launch_dispatch(hipStream_t s, const void* X, int esize, int64_t T, int64_t n, int64_t ldx, int k,
+                           const int32_t* inverse, int64_t R, void* Xs, int64_t lds) {
+  if (T <= 0 || n <= 0 || k <= 0) return hipSuccess;
+  if (rows_aligned(X, ldx, esize) && rows_aligned(Xs, lds, esize) && (n * esize) % 16 == 0) {
+    const int per = 16 / esize;
+    const int64_t width = n / per;
+    hipLaunchKernelGGL((k_dispatch<rt_u32x4_t>), dim3((unsigned)ceil_div(T * width, 256)), dim3(256), 0, s,
+                       static_cast<const rt_u32x4_t*>(X), ldx / per, T, width, k, inverse, R,
+                       static_cast<rt_u32x4_t*>(Xs), lds / per);
+  } else if (esize == 2) {
+    hipLaunchKernelGGL((k_dispatch<uint16_t>), dim3((unsigned)ceil_div(T * n, 256)), dim3(256), 0, s,
+                       static_cast<const uint16_t*>(X), ldx, T, n, k, inverse, R, static_cast<uint16_t*>(Xs), lds);
+  } else {
+    hipLaunchKernelGGL((k_dispatch<uint32_t>), dim3((unsigned)ceil_div(T * n, 256)), dim3(256), 0, s,
+                       static_cast<const uint32_t*>(X), ldx, T, n, k, inverse, R, static_cast<uint32_t*>(Xs), lds);
+  }
+  return hipGetLastError();
+}
+
+template <bool YSBF, bool YBF, bool VEC>
+static void combine_go(hipStream_t s, const CombineArgs& a) {
+  const int64_t units = ceil_div(a.n, 8);
+  hipLaunchKernelGGL((k_combine<YSBF, YBF, VEC>), dim3((unsigned)ceil_div(a.T * units, 256)), dim3(256), 0, s, a.Ys,
+                     a.lds, a.R, a.inverse, a.w, a.T, a.n, units, a.k, a.Y, a.ldy);
+}
+
+hipError_t launch_combine(hipStream_t s, const CombineArgs& a) {
+  if (a.T <= 0 || a.n <= 0) return hipSuccess;
+  const bool vec = a.n % 8 == 0 && rows_aligned(a.Ys, a.lds, a.ys_bf16 ? 2 : 4) &&
+                   rows_aligned(a.Y, a.ldy, a.y_bf16 ? 2 : 4);
+  switch ((a.ys_bf16 ? 4 : 0) | (a.y_bf16 ? 2 : 0) | (vec ? 1 : 0)) {
+    case 0: combine_go<false, false, false>(s, a); break;
+    case 1: combine_go<false, false, true>(s, a); break;
+    case 2: combine_go<false, true, false>(s, a); break;
+    case 3: combine_go<false, true, true>(s, a); break;
+    case 4: combine_go<true, false, false>(s, a); break;
+    case 5: combine_go<true, false, true>(s, a); break;
+    case 6: combine_go<true, true, false>(s, a); break;
+    default: combine_go<true, true, true>(s, a); break;
+  }
+  return hipGetLastError();
+}
+
+template <bool DYBF, bool YSBF, bool OBF>
+static void combine_grad_go(hipStream_t s, const CombineGradArgs& a, bool vec) {
+  const int64_t units = ceil_div(a.n, 8);
+  if (vec)
+    hipLaunchKernelGGL((k_combine_grad<DYBF, YSBF, OBF, true>), dim3((unsigned)a.T), dim3(256), 0, s, a.dY, a.ldy,
+                       a.Ys, a.lds, a.R, a.inverse, a.w, a.n, units, a.k, a.dYs, a.ldo, a.dw);
+  else
+    hipLaunchKernelGGL((k_combine_grad<DYBF, YSBF, OBF, false>), dim3((unsigned)a.T), dim3(256), 0, s, a.dY, a.ldy,
+                       a.Ys, a.lds, a.R, a.inverse, a.w, a.n, units, a.k, a.dYs, a.ldo, a.dw);
+}
+
+hipError_t launch_combine_grad(hipStream_t s, const CombineGradArgs& a) {
+  if (a.T <= 0 || a.k <= 0) return hipSuccess;
+  const bool vec = a.n % 8 == 0 && rows_aligned(a.dY, a.ldy, a.dy_bf16 ? 2 : 4) &&
+                   rows_aligned(a.Ys, a.lds, a.ys_bf16 ? 2 : 4) && rows_aligned(a.dYs, a.ldo, a.out_bf16 ? 2 : 4);
+  switch ((a.dy_bf16 ? 4 : 0) | (a.ys_bf16 ? 2 : 0) | (a.out_bf16 ? 1 : 0)) {
+    case 0: combine_grad_go<false, false, false>(s, a, vec); break;
+    case 1: combine_grad_go<false, false, true>(s, a, vec); break;
+    case 2: combine_grad_go<false, true, false>(s, a, vec); break;
+    case 3: combine_grad_go<false, true, true>(s, a, vec); break;
+    case 4: combine_grad_go<true, false, false>(s, a, vec); break;
+    case 5: combine_grad_go<true, false, true>(s, a, vec); break;
+    case 6: combine_grad_go<true, true, false>(s, a, vec); break;
+    default: combine_grad_go<true, true, true>(s, a, vec); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace gq

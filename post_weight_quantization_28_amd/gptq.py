@@ -77,6 +77,22 @@ def load():
         "gptq_repack_act_order_workspace_bytes": [c_i64, c_i64, ctypes.POINTER(c_sz)],
         "gptq_repack_act_order": [c_vp, c_vp, c_vp, c_i64, c_i64, ctypes.c_int32, ctypes.c_int32, c_vp, c_vp,
                                   c_vp, c_sz],
+        "gptq_route_workspace_bytes": [c_i64, c_i64, c_i64, ctypes.POINTER(c_sz)],
+        "gptq_route": [c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_sz],
+        "gptq_dispatch": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64],
+        "gptq_combine": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp,
+                         ctypes.c_int32, c_i64],
+        "gptq_combine_grad": [c_vp, c_vp, ctypes.c_int32, c_i64, c_vp, ctypes.c_int32, c_i64, c_i64, c_vp, c_vp,
+                              c_i64, c_i64, c_i64, c_vp, ctypes.c_int32, c_i64, c_vp],
+        "gptq_expert_matmul": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp,
+                               c_vp, c_i64, ctypes.c_int32, ctypes.c_int32, c_vp, ctypes.c_int32, c_i64],
+        "gptq_expert_matmul_grad": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_i64,
+                                    c_i64, ctypes.c_int32, ctypes.c_int32, c_vp, ctypes.c_int32, c_i64],
+        "gptq_checkpoint_save": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_vp],
+        "gptq_checkpoint_restore": [c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, ctypes.c_int32, c_i64],
+        "gptq_checkpoint_weight_grad_workspace_bytes": [c_i64, c_i64, c_i64, c_i64, ctypes.POINTER(c_sz)],
+        "gptq_checkpoint_weight_grad": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_i64,
+                                        c_vp, c_vp, c_i64, c_vp, c_vp, c_sz],
         "gptq_eora_workspace_bytes": [c_i64, c_i64, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(c_sz)],
         "gptq_eora": [c_vp, c_vp, ctypes.c_int, c_vp, c_i64, c_i64, c_i64, c_vp, ctypes.c_int32, ctypes.c_int32,
                       c_vp, c_vp, c_vp, c_vp, c_sz],
@@ -316,6 +332,289 @@ def repack_act_order(qweight, g_idx, n, bits, group, workspace=None):
                                      int(bits), int(group), _dev(out, "qweight_out"), _dev(perm, "perm"),
                                      wsp, c.value))
     return out, perm
+
+
+# ---------------------------------------------------------------- experts
+@dataclass
+class Route:
+    """Rows in the order of their experts: expert e holds places offsets[e] ..
+    offsets[e + 1] - 1; rows[p] is the token of place p (-1 from offsets[E]
+    on); inverse[t, j] the place of slot (t, j) (-1: dropped)."""
+    offsets: torch.Tensor
+    rows: torch.Tensor
+    inverse: torch.Tensor
+
+
+@dataclass
+class Checkpoint:
+    """Activations kept in 8 bits: codes (T x 32 ceil(n / 32) int8), exps (T x
+    ceil(n / 32) uint8) and the number of columns n."""
+    codes: torch.Tensor
+    exps: torch.Tensor
+    n: int
+
+
+def _null():
+    return ctypes.c_void_p(0)
+
+
+def _rows2d(t, name, dtypes, device=None):
+    """Pointer and row pitch of a matrix whose rows may lie apart."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be " + " or ".join(str(d).replace("torch.", "") for d in dtypes))
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    pitch = t.stride(0) if rows > 1 else max(cols, 1)
+    if rows > 1 and pitch < cols:
+        raise ValueError(f"{name}'s rows overlap")
+    return ctypes.c_void_p(t.data_ptr()), pitch
+
+
+def _dense(t, name, dtype, device, shape):
+    """Pointer of a contiguous tensor of this type and shape."""
+    _dev(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _on(device):
+    """The call runs on the tensors' device, on its current stream."""
+    return torch.cuda.device(device)
+
+
+def route(expert_ids, n_experts, workspace=None):
+    """Stable order of the slots of expert_ids (T x k int32) by expert; ids
+    outside [0, n_experts) are dropped. Returns a Route."""
+    lib = load()
+    p, ldi = _rows2d(expert_ids, "expert_ids", (torch.int32,))
+    T, k = expert_ids.shape
+    dev = expert_ids.device
+    c = ctypes.c_size_t(0)
+    _check(lib.gptq_route_workspace_bytes(T, k, int(n_experts), ctypes.byref(c)))
+    with _on(dev):
+        r = Route(torch.empty((n_experts + 1,), dtype=torch.int32, device=dev),
+                  torch.empty((T * k,), dtype=torch.int32, device=dev),
+                  torch.empty((T, k), dtype=torch.int32, device=dev))
+        ws, wsp = _workspace(c.value, dev, workspace)
+        _check(lib.gptq_route(_stream(), p, ldi, T, k, int(n_experts), _dev(r.offsets, "offsets"),
+                              _dev(r.rows, "rows"), _dev(r.inverse, "inverse"), wsp, c.value))
+    return r
+
+
+def _slots(inverse, device, T):
+    if not isinstance(inverse, torch.Tensor) or inverse.dim() != 2:
+        raise ValueError("inverse must have two dimensions")
+    if inverse.shape[0] != T:
+        raise ValueError(f"inverse has {inverse.shape[0]} rows for {T} tokens")
+    return _dense(inverse, "inverse", torch.int32, device, inverse.shape), inverse.shape[1]
+
+
+def dispatch(X, inverse, out=None):
+    """Xs (T k x n, X's type) with Xs[inverse[t, j]] = X[t]. Rows that no slot
+    names are left as they are (in a new tensor: undefined)."""
+    lib = load()
+    xp, ldx = _rows2d(X, "X", _FLOATS)
+    T, n = X.shape
+    dev = X.device
+    ip, k = _slots(inverse, dev, T)
+    with _on(dev):
+        Xs = out if out is not None else torch.empty((T * k, n), dtype=X.dtype, device=dev)
+        sp, lds = _rows2d(Xs, "out", (X.dtype,), dev)
+        if Xs.shape[1] != n:
+            raise ValueError(f"out must have {n} columns")
+        _check(lib.gptq_dispatch(_stream(), xp, _dtype_code(X), T, n, ldx, k, ip, Xs.shape[0], sp, lds))
+    return Xs
+
+
+def combine(Ys, inverse, weights=None, out=None, out_dtype=None):
+    """Y[t] = sum_j weights[t, j] Ys[inverse[t, j]] (weights of one when
+    None: the gradient of dispatch). Ys bf16 or fp32, weights fp32, Y in
+    out_dtype (default: Ys's type)."""
+    lib = load()
+    sp, lds = _rows2d(Ys, "Ys", _FLOATS)
+    R, n = Ys.shape
+    dev = Ys.device
+    T = inverse.shape[0]
+    ip, k = _slots(inverse, dev, T)
+    wp = _null() if weights is None else _dense(weights, "weights", torch.float32, dev, (T, k))
+    with _on(dev):
+        Y = out if out is not None else torch.empty((T, n), dtype=out_dtype or Ys.dtype, device=dev)
+        yp, ldy = _rows2d(Y, "out", _FLOATS, dev)
+        if tuple(Y.shape) != (T, n):
+            raise ValueError(f"out must have the shape {(T, n)}")
+        _check(lib.gptq_combine(_stream(), sp, _dtype_code(Ys), R, lds, ip, wp, T, n, k, yp, _dtype_code(Y), ldy))
+    return Y
+
+
+def combine_grad(dY, Ys, inverse, weights, out=None, out_dtype=None):
+    """(dYs, dweights) of combine: dYs[inverse[t, j]] = weights[t, j] dY[t]
+    (in out_dtype, default dY's type; rows that no slot names are left as they
+    are), dweights[t, j] = <dY[t], Ys[inverse[t, j]]> (fp32)."""
+    lib = load()
+    gp, ldy = _rows2d(dY, "dY", _FLOATS)
+    T, n = dY.shape
+    dev = dY.device
+    sp, lds = _rows2d(Ys, "Ys", _FLOATS, dev)
+    R = Ys.shape[0]
+    if Ys.shape[1] != n:
+        raise ValueError(f"Ys must have {n} columns")
+    ip, k = _slots(inverse, dev, T)
+    wp = _dense(weights, "weights", torch.float32, dev, (T, k))
+    with _on(dev):
+        dYs = out if out is not None else torch.empty((R, n), dtype=out_dtype or dY.dtype, device=dev)
+        op, ldo = _rows2d(dYs, "out", _FLOATS, dev)
+        if tuple(dYs.shape) != (R, n):
+            raise ValueError(f"out must have the shape {(R, n)}")
+        dw = torch.empty((T, k), dtype=torch.float32, device=dev)
+        _check(lib.gptq_combine_grad(_stream(), gp, _dtype_code(dY), ldy, sp, _dtype_code(Ys), R, lds, ip, wp, T, n, k,
+                                     op, _dtype_code(dYs), ldo, _dev(dw, "dweights")))
+    return dYs, dw
+
+
+def _expert_layers(qweight, scales, zeros, bits, group, n, device):
+    """Checks E stacked packed layers (or one layer without the first
+    dimension); returns E, d_out and the three pointers."""
+    if not isinstance(qweight, torch.Tensor) or qweight.dim() not in (2, 3):
+        raise ValueError("qweight must be (E x) d_out x words")
+    lead = tuple(qweight.shape[:-1])
+    E, d_out = lead if len(lead) == 2 else (1, lead[0])
+    if bits not in (2, 3, 4) or group <= 0:
+        raise GPTQError(EINVAL, "bits must be 2, 3 or 4 and group positive")
+    words, ng = (n * bits + 31) // 32, n // group
+    if qweight.dtype not in (torch.int32, torch.uint32):
+        raise TypeError("qweight must be int32 or uint32")
+    qp = _dense(qweight, "qweight", qweight.dtype, device, lead + (words,))
+    return (E, d_out, qp, _dense(scales, "scales", torch.float32, device, lead + (ng,)),
+            _dense(zeros, "zeros", torch.uint8, device, lead + (ng,)))
+
+
+def _segments(offsets, rows, E, device, R):
+    op = _null() if offsets is None else _dense(offsets, "offsets", torch.int32, device, (E + 1,))
+    rp = _null() if rows is None else _dense(rows, "rows", torch.int32, device, (R,))
+    return op, rp
+
+
+def expert_matmul(X, offsets, qweight, scales, zeros, bits, group, rows=None, out=None, out_dtype=torch.float32):
+    """Y[p] = X[rows[p]] W_hat_e^T for the rows p of expert e (offsets, rows:
+    from route). X bf16 (T x n); qweight E x d_out x n*bits/32, scales and
+    zeros E x d_out x n/group: E layers as quantize_layer packs them, without
+    act-order. rows None: X holds the sorted rows. offsets None: one layer,
+    all rows. Rows from offsets[E] on are left as they are."""
+    lib = load()
+    xp, ldx = _rows2d(X, "X", (torch.bfloat16,))
+    T, n = X.shape
+    dev = X.device
+    E, d_out, qp, sp, zp = _expert_layers(qweight, scales, zeros, bits, group, n, dev)
+    R = T if rows is None else rows.numel()
+    op, rp = _segments(offsets, rows, E, dev, R)
+    with _on(dev):
+        Y = out if out is not None else torch.empty((R, d_out), dtype=out_dtype, device=dev)
+        yp, ldy = _rows2d(Y, "out", _FLOATS, dev)
+        if tuple(Y.shape) != (R, d_out):
+            raise ValueError(f"out must have the shape {(R, d_out)}")
+        _check(lib.gptq_expert_matmul(_stream(), xp, BF16, T, n, ldx, rp, R, op, E, qp, sp, zp, d_out, int(bits),
+                                      int(group), yp, _dtype_code(Y), ldy))
+    return Y
+
+
+def expert_matmul_grad(dY, offsets, qweight, scales, zeros, bits, group, n, out=None, out_dtype=torch.bfloat16):
+    """dX[p] = dY[p] W_hat_e, the gradient of expert_matmul for its sorted
+    rows (dY: R x d_out bf16). A bf16 result rounds each weight to bf16 once;
+    an fp32 result takes it in three pieces at three times the work."""
+    lib = load()
+    gp, ldy = _rows2d(dY, "dY", (torch.bfloat16,))
+    R, d_out = dY.shape
+    dev = dY.device
+    E, d, qp, sp, zp = _expert_layers(qweight, scales, zeros, bits, group, n, dev)
+    if d != d_out:
+        raise ValueError(f"dY must have {d} columns")
+    op, _ = _segments(offsets, None, E, dev, R)
+    with _on(dev):
+        dX = out if out is not None else torch.empty((R, n), dtype=out_dtype, device=dev)
+        xp, ldx = _rows2d(dX, "out", _FLOATS, dev)
+        if tuple(dX.shape) != (R, n):
+            raise ValueError(f"out must have the shape {(R, n)}")
+        _check(lib.gptq_expert_matmul_grad(_stream(), gp, BF16, R, ldy, op, E, qp, sp, zp, d_out, n, int(bits),
+                                           int(group), xp, _dtype_code(dX), ldx))
+    return dX
+
+
+# ---------------------------------------------------------------- kept activations
+def checkpoint_save(X, out=None):
+    """X (T x n, bf16 or fp32) in 8 bits with a power-of-two step per 32
+    columns: a Checkpoint. ``out`` may hold a Checkpoint to write into."""
+    lib = load()
+    xp, ldx = _rows2d(X, "X", _FLOATS)
+    T, n = X.shape
+    dev = X.device
+    groups = (n + 31) // 32
+    with _on(dev):
+        c = out if out is not None else Checkpoint(torch.empty((T, 32 * groups), dtype=torch.int8, device=dev),
+                                                   torch.empty((T, groups), dtype=torch.uint8, device=dev), n)
+        cp, ep = _kept(c, dev)
+        if c.codes.shape[0] != T or c.n != n:
+            raise ValueError(f"out must keep {T} x {n} values")
+        _check(lib.gptq_checkpoint_save(_stream(), xp, _dtype_code(X), T, n, ldx, cp, ep))
+    return c
+
+
+def _kept(c, device):
+    groups = (c.n + 31) // 32
+    T = c.codes.shape[0]
+    return (_dense(c.codes, "codes", torch.int8, device, (T, 32 * groups)),
+            _dense(c.exps, "exps", torch.uint8, device, (T, groups)))
+
+
+def checkpoint_restore(kept, dtype=torch.bfloat16, out=None):
+    """The kept values (T x n), exact in bf16 and in fp32."""
+    lib = load()
+    dev = kept.codes.device
+    cp, ep = _kept(kept, dev)
+    T = kept.codes.shape[0]
+    with _on(dev):
+        X = out if out is not None else torch.empty((T, kept.n), dtype=dtype, device=dev)
+        xp, ldx = _rows2d(X, "out", _FLOATS, dev)
+        if tuple(X.shape) != (T, kept.n):
+            raise ValueError(f"out must have the shape {(T, kept.n)}")
+        _check(lib.gptq_checkpoint_restore(_stream(), cp, ep, T, kept.n, xp, _dtype_code(X), ldx))
+    return X
+
+
+def checkpoint_weight_grad(P, kept, offsets=None, rows=None, out=None, workspace=None):
+    """G (E x m x n fp32): G[e] = sum over the rows p of expert e of
+    P[p]^T x_hat[rows[p]], P (R x m bf16); offsets None: one sum over all
+    rows (E = 1), rows None: the kept rows are in P's order."""
+    lib = load()
+    pp, ldp = _rows2d(P, "P", (torch.bfloat16,))
+    R, m = P.shape
+    dev = P.device
+    cp, ep = _kept(kept, dev)
+    E = 1 if offsets is None else offsets.numel() - 1
+    op, rp = _segments(offsets, rows, E, dev, R)
+    c = ctypes.c_size_t(0)
+    _check(lib.gptq_checkpoint_weight_grad_workspace_bytes(R, E, m, kept.n, ctypes.byref(c)))
+    with _on(dev):
+        G = out if out is not None else torch.empty((E, m, kept.n), dtype=torch.float32, device=dev)
+        gp = _dense(G, "out", torch.float32, dev, (E, m, kept.n))
+        ws, wsp = _workspace(c.value, dev, workspace)
+        _check(lib.gptq_checkpoint_weight_grad(_stream(), pp, BF16, R, m, ldp, cp, ep, kept.codes.shape[0], kept.n, rp,
+                                               op, E, gp, wsp, c.value))
+    return G
 
 
 # ---------------------------------------------------------------- EoRA
