@@ -246,6 +246,12 @@ hipError_t launch_dequant_mm(hipStream_t s, const DqPlan& p, const uint16_t* X, 
                              int64_t ldx, const uint32_t* qw, const float* scales, const uint8_t* zeros,
                              int64_t d_out, int bits, int group, float* Y, int64_t ldy, float* part);
 
+// Outputs above this many bytes are stored past the caches (non-temporal):
+// they do not fit beside the inputs in the 256 MB last-level cache, and the
+// next reader finds nothing of them there either way. Smaller ones stay
+// cached for it.
+constexpr int64_t kStreamBytes = (int64_t)128 << 20;
+
 // ---- route.hip: tokens in the order of their experts, and back
 constexpr int kRouteMaxExperts = 1024;
 constexpr int64_t kRouteOneBlock = 4096;    // slots up to which one workgroup does it all

@@ -18,6 +18,7 @@
 #include "dma.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace gq {
 
@@ -299,61 +300,120 @@ k_expert_mv(const uint16_t* __restrict__ X, int T, int64_t n, int64_t ldx, const
 
 // ==================================================================== many rows
 //
-// 256 threads, four waves, a BM x 128 tile with BM = 32 MI WM
-// (v_mfma_f32_32x32x16_bf16; wave (wm, wn) holds MI x NI blocks). K advances
-// in stages of 64 through two LDS buffers: a stage's operands come from
-// registers that were loaded one stage ahead, the packed one is expanded to
-// bf16 on its way into LDS, once per workgroup, and one barrier per stage
-// separates the buffers. Operand layouts in LDS:
+// A BM x 128 tile per workgroup (v_mfma_f32_32x32x16_bf16; wave (wm, wn) holds
+// MI x NI blocks of 32 x 32). K advances in stages of 64 through two LDS
+// buffers. The operands of stage st + 2 are on their way into registers and
+// those of stage st + 1 are written into the other buffer, the packed one
+// expanded to bf16 on its way, in between the products of stage st: one
+// barrier per stage, and the expansion (once per workgroup, about three
+// operations per code) runs beside the matrix cores. Operand layouts in LDS:
 //  * K along a row ([row][64], 128 bytes): 16-byte piece c of row r at
 //    c ^ (r & 7), so eight rows' reads of one piece hit all banks;
-//  * K down the rows ([64][128], 256 bytes): piece c of row t at
-//    c ^ dma_swz(t), read with the transposing LDS read.
+//  * K down the rows ([64][W]): piece c of row t at c ^ dma_swz(t) ^ (c / 8),
+//    read with the transposing LDS read; the last term keeps the writes of
+//    wide column runs off each other's banks.
 constexpr int kExBK = 64;
-constexpr int kExBN = 128;
 
-template <int MI_, int NI_, int WM_>
+template <int MI_, int NI_, int WM_, int WN_>
 struct ExTile {
-  static constexpr int MI = MI_, NI = NI_, WM = WM_, WN = 4 / WM_;
-  static constexpr int BM = 32 * MI * WM;
-  static_assert(32 * NI * WN == kExBN, "four waves cover 128 columns");
+  static constexpr int MI = MI_, NI = NI_, WM = WM_, WN = WN_;
+  static constexpr int BM = 32 * MI * WM, BN = 32 * NI * WN, THREADS = 64 * WM * WN;
+  static constexpr int PA = BM * 8 / THREADS;   // 16-byte pieces of A per thread and stage
+  static constexpr int NB = BN * 8 / THREADS;   // 8-code units of B per thread and stage
 };
-using ExTile128 = ExTile<2, 2, 2>;
-using ExTile64 = ExTile<2, 1, 1>;
-using ExTile32 = ExTile<1, 1, 1>;
+using ExTileX = ExTile<4, 2, 2, 4>;      // 256 x 256, 8 waves
+using ExTile128 = ExTile<2, 2, 2, 2>;    // 128 x 128
+using ExTile64 = ExTile<2, 1, 1, 4>;     // 64 x 128
+using ExTile32 = ExTile<1, 1, 1, 4>;     // 32 x 128
+
+typedef __attribute__((address_space(3))) ex_u32x4_t lds_piece_t;
+typedef __attribute__((address_space(3))) const ex_bf16x8_t lds_frag_t;
 
 __device__ __forceinline__ uint32_t row_piece(int r, int c) { return (uint32_t)r * 128u + 16u * (c ^ (r & 7)); }
-__device__ __forceinline__ uint32_t col_piece(int t, int c) { return (uint32_t)t * 256u + 16u * (c ^ dma_swz(t)); }
-
-__device__ __forceinline__ ex_bf16x8_t frag_row(const uint8_t* buf, int row, int kk, int h) {
-  return *reinterpret_cast<const ex_bf16x8_t*>(buf + row_piece(row, 2 * kk + h));
+// W: columns of the tile
+template <int W>
+__device__ __forceinline__ uint32_t col_piece(int t, int c) {
+  return (uint32_t)t * (2 * W) + 16u * (c ^ dma_swz(t) ^ (c >> 3));
 }
-
-// Columns c0 .. c0 + 31, K slice kk of 16, from a [64][128] tile: lane l
-// gets K 16 kk + 8 (l / 32) .. + 7 of column c0 + l % 32.
-__device__ __forceinline__ ex_bf16x8_t frag_col(uint32_t buf, int c0, int kk, int lane) {
-  const int t = 16 * kk + 8 * (lane >> 5) + ((lane & 15) >> 2);
-  const int col = c0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-  const uint32_t o0 = col_piece(t, col >> 3) + 2 * (col & 7);
-  const uint32_t o1 = col_piece(t + 4, col >> 3) + 2 * (col & 7);
-  struct { v4i16_t a, b; } f = {lds_tr16(buf + o0), lds_tr16(buf + o1)};
-  return __builtin_bit_cast(ex_bf16x8_t, f);
-}
-
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
+__device__ __forceinline__ void lds_write(uint32_t at, ex_u32x4_t v) { *reinterpret_cast<lds_piece_t*>(at) = v; }
+__device__ __forceinline__ ex_bf16x8_t lds_frag(uint32_t at) { return *reinterpret_cast<lds_frag_t*>(at); }
 
-// 8 elements of a bf16 row from column c (limit: the row's length); vec:
-// 16-byte aligned rows and limit % 8 == 0.
-__device__ __forceinline__ ex_u32x4_t load_piece(const uint16_t* __restrict__ row, int64_t c, int64_t limit, bool vec) {
-  if (c >= limit) return (ex_u32x4_t){0u, 0u, 0u, 0u};
-  if (vec) return *reinterpret_cast<const ex_u32x4_t*>(row + c);
-  uint32_t v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = c + i < limit ? row[c + i] : 0u;
-  return (ex_u32x4_t){v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
+// Address of this lane's fragment of columns c0 .. c0 + 31 in a [64][W] tile
+// (K slice kk at + 32 W kk): lane l gets K 8 (l / 32) .. + 7 of column
+// c0 + l % 32 by two transposing reads.
+template <int W>
+__device__ __forceinline__ uint32_t col_frag_at(int c0, int lane) {
+  const int t = 8 * (lane >> 5) + ((lane & 15) >> 2);
+  const int col = c0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  return col_piece<W>(t, col >> 3) + 2 * (col & 7);
 }
+template <int W>
+__device__ __forceinline__ ex_bf16x8_t lds_col_frag(uint32_t at) {
+  struct { v4i16_t a, b; } f = {lds_tr16(at), lds_tr16(at + 4 * 2 * W)};
+  return __builtin_bit_cast(ex_bf16x8_t, f);
+}
+
+// 8 elements of a bf16 row from column c (limit: the row's length). VEC:
+// 16-byte aligned rows and limit % 8 == 0.
+template <bool VEC>
+__device__ __forceinline__ ex_u32x4_t load_piece(const uint16_t* __restrict__ row, int64_t c, int64_t limit) {
+  if constexpr (VEC) {   // one load in any case, so that the loads of a stage can be counted
+    const void* src = c < limit ? static_cast<const void*>(row + c) : kZeroChunk;
+    return *reinterpret_cast<const ex_u32x4_t*>(src);
+  } else {
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < limit ? row[c + i] : 0u;
+    return (ex_u32x4_t){v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
+  }
+}
+
+// The words of NB units of 8 codes, unit u0 (a multiple of NB) of a packed
+// row, and unit e of them minus z as floats.
+template <int BITS, int NB>
+struct UnitWords {
+  static constexpr int N = (BITS * NB * 8 + 31) / 32;
+  uint32_t w[N];
+  int sh;
+  __device__ __forceinline__ void load(const uint32_t* __restrict__ row, int64_t u0) {
+    const int64_t bit = u0 * (8 * BITS);
+    const uint32_t* __restrict__ p = row + (bit >> 5);
+    sh = BITS == 3 && NB == 2 ? (int)(bit & 31) : 0;     // 48 bits from bit 0 or 16
+    if constexpr (BITS == 4 && NB == 4) {
+      const ex_u32x4_t v = *reinterpret_cast<const ex_u32x4_t*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = v[i];
+    } else if constexpr (BITS == 4 && NB == 2) {
+      const uint64_t v = *reinterpret_cast<const uint64_t*>(p);
+      w[0] = (uint32_t)v;
+      w[1] = (uint32_t)(v >> 32);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = p[i];
+    }
+  }
+  __device__ __forceinline__ void get(int e, float z, float (&f)[8]) const {
+    if constexpr (BITS == 4) {
+      // byte i of lo / hi holds code 2 i / 2 i + 1: one conversion per code
+      const uint32_t lo = w[e] & 0x0F0F0F0Fu, hi = (w[e] >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = (float)((lo >> (8 * i)) & 0xFFu) - z;
+        f[2 * i + 1] = (float)((hi >> (8 * i)) & 0xFFu) - z;
+      }
+    } else {
+      const int base = 8 * BITS * e, wi = base >> 5;
+      uint64_t v = w[wi];
+      if (BITS == 3 && wi + 1 < N) v |= (uint64_t)w[wi + 1] << 32;
+      v >>= (base & 31) + sh;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = (float)(uint32_t)((v >> (BITS * i)) & ((1u << BITS) - 1u)) - z;
+    }
+  }
+};
 
 // Tile of workgroup b among nr row tiles x nc column tiles: the dispatcher
 // deals consecutive workgroups to the 8 XCDs in turn, so each XCD takes a
@@ -372,7 +432,7 @@ __device__ __forceinline__ bool tile_of(int64_t b, int nr, int nc, int& rt, int&
 }
 
 struct ExArgs {
-  const uint16_t* A; int64_t lda; int avec;   // X or dY
+  const uint16_t* A; int64_t lda;             // X or dY
   const int32_t* rows; int T;
   const int32_t* offsets; int E, R;
   const uint32_t* qw; const float* scales; const uint8_t* zeros;
@@ -381,107 +441,162 @@ struct ExArgs {
   int nrt, nct;
 };
 
+template <int B>
+using ex_const = std::integral_constant<int, B>;
+
+template <class F>
+__device__ __forceinline__ void for_four(F&& f) {
+  f(ex_const<0>{});
+  f(ex_const<1>{});
+  f(ex_const<2>{});
+  f(ex_const<3>{});
+}
+
 // ---- forward: K = n. The codes minus the zero point are exact in bf16, the
 // group's sum is scaled once in fp32 (tot += s acc), as in the one-layer
-// product.
-template <int BITS, class TL>
-__global__ void __launch_bounds__(256, 2)
+// product. GS: stages per group when fixed (groups of 64 and 128: the first
+// product of a group starts from zero, no test inside a stage), 0: groups
+// of any number of 32-code chunks, tested after every chunk.
+template <int BITS, class TL, int GS, bool VEC>
+__global__ void __launch_bounds__(TL::THREADS, 512 / TL::THREADS)
 k_expert_mm(ExArgs p) {
-  constexpr int MI = TL::MI, NI = TL::NI, BM = TL::BM, PA = BM / 32;
-  __shared__ __align__(16) uint8_t As[2][BM * 128];
-  __shared__ __align__(16) uint8_t Bs[2][kExBN * 128];
+  constexpr int MI = TL::MI, NI = TL::NI, BM = TL::BM, PA = TL::PA, NB = TL::NB, THREADS = TL::THREADS;
+  constexpr uint32_t ASZ = BM * 128, BSZ = TL::BN * 128, BUF = ASZ + BSZ;
+  __shared__ __align__(16) uint8_t smem[2 * BUF];
   int rt, ct;
   if (!tile_of(blockIdx.x, p.nrt, p.nct, rt, ct)) return;
   const Seg sg = find_tile(p.offsets, p.E, p.R, BM, rt);
   if (sg.e < 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave % TL::WM, wn = wave / TL::WM, h = lane >> 5, li = lane & 31;
-  const int64_t o0 = (int64_t)ct * kExBN;
+  const int64_t o0 = (int64_t)ct * TL::BN;
   const int64_t ngroups = p.n / p.group;
   const int cpg = p.group / 32, nchunks = (int)(p.n / 32), nst = (nchunks + 1) / 2;
+  const uint32_t lds = lds_addr(smem);
 
-  // staging: piece tid & 7 of rows tid / 8 + 32 i of A, chunk tid & 1 of row tid / 2 of B
+  // staging: piece tid % 8 of rows tid / 8 + (THREADS / 8) i of A; units
+  // NB (tid % (8 / NB)) .. of row tid / (8 / NB) of B
+  constexpr int AR = THREADS / 8, BU = 8 / NB;
+  const int ac = tid & 7, ar = tid >> 3, bu = NB * (tid % BU), br = tid / BU;
   const uint16_t* arow[PA];
 #pragma unroll
   for (int i = 0; i < PA; ++i)
-    arow[i] = p.A + source_row(p.rows, min(sg.row0 + (tid >> 3) + 32 * i, sg.hi - 1), p.T) * p.lda;
-  const int br = tid >> 1, bc = tid & 1;
+    arow[i] = p.A + source_row(p.rows, min(sg.row0 + ar + AR * i, sg.hi - 1), p.T) * p.lda;
   const int64_t bo = (int64_t)sg.e * p.d_out + min(o0 + br, p.d_out - 1);
   const uint32_t* __restrict__ qrow = p.qw + bo * ((int64_t)nchunks * BITS);
   const uint8_t* __restrict__ zrow = p.zeros + bo * ngroups;
+  const uint32_t aw = lds + row_piece(ar, ac);            // AR is a multiple of 8: rows apart keep the swizzle
+  uint32_t bw[NB];
+#pragma unroll
+  for (int e = 0; e < NB; ++e) bw[e] = lds + ASZ + row_piece(br, bu + e);
 
   ex_u32x4_t ra[PA];
-  uint32_t rb[BITS];
-  float rz = 0.f;
-  auto gload = [&](int st) {
+  UnitWords<BITS, NB> rb[2];
+  uint32_t rz[2];
+  auto aload = [&](int st) {
 #pragma unroll
-    for (int i = 0; i < PA; ++i) ra[i] = load_piece(arow[i], (int64_t)st * kExBK + 8 * (tid & 7), p.n, p.avec);
-    const int c = min(2 * st + bc, nchunks - 1);      // a chunk past the end meets zeros of A
-    load_chunk<BITS>(qrow + (int64_t)c * BITS, rb);
-    rz = (float)zrow[c / cpg];
+    for (int i = 0; i < PA; ++i) ra[i] = load_piece<VEC>(arow[i], (int64_t)st * kExBK + 8 * ac, p.n);
   };
-  auto lwrite = [&](int b) {
+  auto bload = [&](auto B, int st) {
+    const int c = min(2 * st + bu / 4, nchunks - 1);      // a chunk past the end meets zeros of A
+    rb[B].load(qrow, 4 * c + bu % 4);
+    const int g = GS == 1 ? st : (GS == 2 ? st >> 1 : c / cpg);
+    rz[B] = zrow[g];
+  };
+  auto awrite = [&](auto B) {
 #pragma unroll
-    for (int i = 0; i < PA; ++i)
-      *reinterpret_cast<ex_u32x4_t*>(As[b] + row_piece((tid >> 3) + 32 * i, tid & 7)) = ra[i];
+    for (int i = 0; i < PA; ++i) lds_write(aw + B * BUF + i * (AR * 128), ra[i]);
+  };
+  // part kk of the four that a stage's products interleave with
+  auto bwrite = [&](auto B, auto KK) {
+    constexpr int kk = decltype(KK)::value;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float f[8];
-      codes8<BITS>(rb, e, rz, f);
-      *reinterpret_cast<ex_u32x4_t*>(Bs[b] + row_piece(br, 4 * bc + e)) =
-          (ex_u32x4_t){pack_exact(f[0], f[1]), pack_exact(f[2], f[3]), pack_exact(f[4], f[5]), pack_exact(f[6], f[7])};
-    }
+    for (int e = 0; e < NB; ++e)
+      if (e * 4 / NB == kk) {
+        float f[8];
+        rb[B].get(e, (float)rz[B], f);
+        lds_write(bw[e] + B * BUF, (ex_u32x4_t){pack_exact(f[0], f[1]), pack_exact(f[2], f[3]),
+                                                 pack_exact(f[4], f[5]), pack_exact(f[6], f[7])});
+      }
   };
   const float* srow[NI];
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni)
     srow[ni] = p.scales + ((int64_t)sg.e * p.d_out + min(o0 + 32 * (NI * wn + ni) + li, p.d_out - 1)) * ngroups;
+  // fragment addresses of K slice kk (both operands have the lane's row at li)
+  uint32_t af[4], bf[4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    af[kk] = lds + row_piece(32 * MI * wm + li, 2 * kk + h);
+    bf[kk] = lds + ASZ + row_piece(32 * NI * wn + li, 2 * kk + h);
+  }
 
   ex_f32x16_t acc[MI][NI] = {}, tot[MI][NI] = {};
+  const ex_f32x16_t zero = {};
   float sc[NI];
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) sc[ni] = srow[ni][0];
   int cin = 0;
   int64_t g = 0;
-  gload(0);
-  for (int st = 0; st < nst; ++st) {
-    const int b = st & 1;
-    lwrite(b);
+  auto flush = [&]() {
+    ++g;
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) {
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) tot[mi][ni][r] = fmaf(sc[ni], acc[mi][ni][r], tot[mi][ni][r]);
+      sc[ni] = srow[ni][min(g, ngroups - 1)];
+    }
+  };
+  auto stage = [&](auto B, int st) {
+    constexpr int b = decltype(B)::value;
     __syncthreads();
-    if (st + 1 < nst) gload(st + 1);
+    aload(min(st + 1, nst - 1));
+    bload(B, min(st + 2, nst - 1));
+    __builtin_amdgcn_sched_barrier(0);    // the loads leave before the stage's products
+    ex_bf16x8_t fa[2][MI], fb[2][NI];
+    auto frags = [&](auto KK) {
+      constexpr int kk = decltype(KK)::value;
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
+      for (int mi = 0; mi < MI; ++mi) fa[kk & 1][mi] = lds_frag(af[kk] + b * BUF + mi * 4096);
 #pragma unroll
-      for (int k2 = 0; k2 < 2; ++k2) {
-        const int kk = 2 * hf + k2;
-        ex_bf16x8_t fa[MI], fb[NI];
+      for (int ni = 0; ni < NI; ++ni) fb[kk & 1][ni] = lds_frag(bf[kk] + b * BUF + ni * 4096);
+    };
+    frags(ex_const<0>{});
+    for_four([&](auto KK) {
+      constexpr int kk = decltype(KK)::value;
+      if constexpr (kk < 3) frags(ex_const<kk + 1>{});
 #pragma unroll
-        for (int mi = 0; mi < MI; ++mi) fa[mi] = frag_row(As[b], 32 * (MI * wm + mi) + li, kk, h);
+      for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni) fb[ni] = frag_row(Bs[b], 32 * (NI * wn + ni) + li, kk, h);
+        for (int ni = 0; ni < NI; ++ni)
+          acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              fa[kk & 1][mi], fb[kk & 1][ni], (GS == 1 || (GS == 2 && b == 0)) && kk == 0 ? zero : acc[mi][ni], 0, 0, 0);
+      bwrite(ex_const<1 - b>{}, KK);
+      if (GS == 0 && (kk & 1) == 1 && ++cin == cpg && g < ngroups) {   // the group is complete
+        flush();
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-          for (int ni = 0; ni < NI; ++ni)
-            acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[mi], fb[ni], acc[mi][ni], 0, 0, 0);
-      }
-      if (++cin == cpg && g < ngroups) {          // the group is complete
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-          for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              tot[mi][ni][r] = fmaf(sc[ni], acc[mi][ni][r], tot[mi][ni][r]);
-              acc[mi][ni][r] = 0.f;
-            }
+          for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = zero;
         cin = 0;
-        ++g;
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni) sc[ni] = srow[ni][min(g, ngroups - 1)];
       }
-    }
+    });
+    awrite(ex_const<1 - b>{});
+    if (GS == 1 || (GS == 2 && b == 1)) flush();
+  };
+  aload(0);
+  bload(ex_const<0>{}, 0);
+  bload(ex_const<1>{}, min(1, nst - 1));
+  awrite(ex_const<0>{});
+  for_four([&](auto KK) { bwrite(ex_const<0>{}, KK); });
+  int st = 0;
+  for (; st + 1 < nst; st += 2) {
+    stage(ex_const<0>{}, st);
+    stage(ex_const<1>{}, st + 1);
   }
+  if (st < nst) stage(ex_const<0>{}, st);
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) {
     const int64_t o = o0 + 32 * (NI * wn + ni) + li;
@@ -502,94 +617,138 @@ k_expert_mm(ExArgs p) {
 // weight, which adds to the sum's error what the bf16 rounding of the result
 // adds again). For results kept in fp32 the weight goes as NP = 3 bf16 pieces
 // and three products: 24 bits, what its fp32 value holds.
-template <int BITS, int NP, class TL>
-__global__ void __launch_bounds__(256, NP > 1 ? 1 : 2)
+template <int BITS, int NP, class TL, bool VEC>
+__global__ void __launch_bounds__(TL::THREADS, NP > 1 ? 1 : 512 / TL::THREADS)
 k_expert_mm_grad(ExArgs p) {
-  constexpr int MI = TL::MI, NI = TL::NI, BM = TL::BM, PA = BM / 32;
-  __shared__ __align__(16) uint8_t As[2][BM * 128];
-  __shared__ __align__(16) uint8_t Bs[2][NP][kExBK * 256];
+  constexpr int MI = TL::MI, NI = TL::NI, BM = TL::BM, BN = TL::BN, PA = TL::PA, NB = TL::NB, THREADS = TL::THREADS;
+  constexpr uint32_t ASZ = BM * 128, BSZ = kExBK * 2 * BN, BUF = ASZ + NP * BSZ;
+  __shared__ __align__(16) uint8_t smem[2 * BUF];
   int rt, ct;
   if (!tile_of(blockIdx.x, p.nrt, p.nct, rt, ct)) return;
   const Seg sg = find_tile(p.offsets, p.E, p.R, BM, rt);
   if (sg.e < 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave % TL::WM, wn = wave / TL::WM, h = lane >> 5, li = lane & 31;
-  const int64_t c0 = (int64_t)ct * kExBN;
+  const int64_t c0 = (int64_t)ct * TL::BN;
   const int64_t ngroups = p.n / p.group;
   const int nchunks = (int)(p.n / 32);
   const int nst = (int)ceil_div(p.d_out, kExBK);
+  const uint32_t lds = lds_addr(smem);
 
+  // staging: A as in the forward product; units NB (tid % BU) .. of output
+  // row tid / BU of B
+  constexpr int AR = THREADS / 8, BU = BN / 8 / NB;
+  const int ac = tid & 7, ar = tid >> 3, bu = NB * (tid % BU), br = tid / BU;
   const uint16_t* arow[PA];
 #pragma unroll
   for (int i = 0; i < PA; ++i)
-    arow[i] = p.A + source_row(p.rows, min(sg.row0 + (tid >> 3) + 32 * i, sg.hi - 1), p.T) * p.lda;
-  // B staging: chunk tid & 3 (32 columns) of output row tid / 4
-  const int br = tid >> 2, bc = tid & 3;
-  const int chunk = (int)(c0 / 32) + bc;
-  const bool cok = chunk < nchunks;
-  const int cc = min(chunk, nchunks - 1);
+    arow[i] = p.A + source_row(p.rows, min(sg.row0 + ar + AR * i, sg.hi - 1), p.T) * p.lda;
+  const int64_t unit = c0 / 8 + bu;
+  const bool cok = unit < 4 * (int64_t)nchunks;
+  const int64_t uc = cok ? unit : bu % 4;                  // columns past n: weights of 0
   const int64_t ebase = (int64_t)sg.e * p.d_out;
-  const int64_t gi = (int64_t)cc * 32 / p.group;
+  const int64_t gi = uc * 8 / p.group;
+  const uint32_t aw = lds + row_piece(ar, ac);
+  uint32_t bw[NB];
+#pragma unroll
+  for (int e = 0; e < NB; ++e) bw[e] = lds + ASZ + col_piece<BN>(br, bu + e);
 
   ex_u32x4_t ra[PA];
-  uint32_t rb[BITS];
-  float rs = 0.f, rz = 0.f;
-  auto gload = [&](int st) {
+  UnitWords<BITS, NB> rb[2];
+  float rs[2];
+  uint32_t rz[2];
+  bool rv[2];
+  auto aload = [&](int st) {
 #pragma unroll
-    for (int i = 0; i < PA; ++i) ra[i] = load_piece(arow[i], (int64_t)st * kExBK + 8 * (tid & 7), p.d_out, p.avec);
+    for (int i = 0; i < PA; ++i) ra[i] = load_piece<VEC>(arow[i], (int64_t)st * kExBK + 8 * ac, p.d_out);
+  };
+  auto bload = [&](auto B, int st) {
     const int64_t o = (int64_t)st * kExBK + br;
     const int64_t oc = ebase + min(o, p.d_out - 1);
-    load_chunk<BITS>(p.qw + (oc * nchunks + cc) * BITS, rb);
-    rs = cok && o < p.d_out ? p.scales[oc * ngroups + gi] : 0.f;   // outputs past d_out: weights of 0
-    rz = (float)p.zeros[oc * ngroups + gi];
+    rb[B].load(p.qw + oc * nchunks * BITS, uc);
+    rs[B] = p.scales[oc * ngroups + gi];
+    rz[B] = p.zeros[oc * ngroups + gi];
+    rv[B] = cok && o < p.d_out;                              // outputs past d_out: weights of 0
   };
-  auto lwrite = [&](int b) {
+  auto awrite = [&](auto B) {
 #pragma unroll
-    for (int i = 0; i < PA; ++i)
-      *reinterpret_cast<ex_u32x4_t*>(As[b] + row_piece((tid >> 3) + 32 * i, tid & 7)) = ra[i];
+    for (int i = 0; i < PA; ++i) lds_write(aw + B * BUF + i * (AR * 128), ra[i]);
+  };
+  auto bwrite = [&](auto B, auto KK) {
+    constexpr int kk = decltype(KK)::value;
+    const float scale = rv[B] ? rs[B] : 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float f[8];
-      codes8<BITS>(rb, e, rz, f);
+    for (int e = 0; e < NB; ++e)
+      if (e * 4 / NB == kk) {
+        float f[8];
+        rb[B].get(e, (float)rz[B], f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= rs;
+        for (int i = 0; i < 8; ++i) f[i] *= scale;
 #pragma unroll
-      for (int q = 0; q < NP; ++q) {
-        ex_u32x4_t v;
+        for (int q = 0; q < NP; ++q) {
+          ex_u32x4_t v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = ex_pack2(f[2 * i], f[2 * i + 1]);
-          f[2 * i] -= __uint_as_float(v[i] << 16);                 // what this piece leaves (exact)
-          f[2 * i + 1] -= __uint_as_float(v[i] & 0xFFFF0000u);
+          for (int i = 0; i < 4; ++i) {
+            v[i] = ex_pack2(f[2 * i], f[2 * i + 1]);
+            if (q + 1 < NP) {                                          // what this piece leaves (exact)
+              f[2 * i] -= __uint_as_float(v[i] << 16);
+              f[2 * i + 1] -= __uint_as_float(v[i] & 0xFFFF0000u);
+            }
+          }
+          lds_write(bw[e] + B * BUF + q * BSZ, v);
         }
-        *reinterpret_cast<ex_u32x4_t*>(Bs[b][q] + col_piece(br, 4 * bc + e)) = v;
       }
-    }
   };
+  uint32_t af[4], bf[NI];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) af[kk] = lds + row_piece(32 * MI * wm + li, 2 * kk + h);
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) bf[ni] = lds + ASZ + col_frag_at<BN>(32 * (NI * wn + ni), lane);
 
   ex_f32x16_t acc[MI][NI] = {};
-  gload(0);
-  for (int st = 0; st < nst; ++st) {
-    const int b = st & 1;
-    lwrite(b);
+  auto stage = [&](auto B, int st) {
+    constexpr int b = decltype(B)::value;
     __syncthreads();
-    if (st + 1 < nst) gload(st + 1);
+    aload(min(st + 1, nst - 1));
+    bload(B, min(st + 2, nst - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    ex_bf16x8_t fa[2][MI], fb[2][NP][NI];
+    auto frags = [&](auto KK) {
+      constexpr int kk = decltype(KK)::value;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      ex_bf16x8_t fa[MI];
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi) fa[mi] = frag_row(As[b], 32 * (MI * wm + mi) + li, kk, h);
+      for (int mi = 0; mi < MI; ++mi) fa[kk & 1][mi] = lds_frag(af[kk] + b * BUF + mi * 4096);
 #pragma unroll
       for (int q = 0; q < NP; ++q)
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni) {
-          const ex_bf16x8_t fb = frag_col(lds_addr(Bs[b][q]), 32 * (NI * wn + ni), kk, lane);
+        for (int ni = 0; ni < NI; ++ni)
+          fb[kk & 1][q][ni] = lds_col_frag<BN>(bf[ni] + b * BUF + q * BSZ + kk * (32 * BN));
+    };
+    frags(ex_const<0>{});
+    for_four([&](auto KK) {
+      constexpr int kk = decltype(KK)::value;
+      if constexpr (kk < 3) frags(ex_const<kk + 1>{});
 #pragma unroll
-          for (int mi = 0; mi < MI; ++mi)
-            acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[mi], fb, acc[mi][ni], 0, 0, 0);
-        }
-    }
+      for (int q = 0; q < NP; ++q)
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+          for (int ni = 0; ni < NI; ++ni)
+            acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk & 1][mi], fb[kk & 1][q][ni], acc[mi][ni], 0, 0, 0);
+      bwrite(ex_const<1 - b>{}, KK);
+    });
+    awrite(ex_const<1 - b>{});
+  };
+  aload(0);
+  bload(ex_const<0>{}, 0);
+  bload(ex_const<1>{}, min(1, nst - 1));
+  awrite(ex_const<0>{});
+  for_four([&](auto KK) { bwrite(ex_const<0>{}, KK); });
+  int st = 0;
+  for (; st + 1 < nst; st += 2) {
+    stage(ex_const<0>{}, st);
+    stage(ex_const<1>{}, st + 1);
   }
+  if (st < nst) stage(ex_const<0>{}, st);
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) {
     const int64_t c = c0 + 32 * (NI * wn + ni) + li;
@@ -611,21 +770,20 @@ k_expert_mm_grad(ExArgs p) {
 // length) when there are few tiles; their partial sums are added in order by
 // a second kernel.
 struct KgArgs {
-  const uint16_t* P; int64_t ldp; int pvec; int64_t m;
+  const uint16_t* P; int64_t ldp; int64_t m;
   const int8_t* codes; const uint8_t* exps; int T; int64_t n, pitch;   // pitch: codes per row
   const int32_t* rows; const int32_t* offsets; int E, R;
   int nmt, nnt, splits;
   float* out; int64_t split_stride;   // out[split][e][m][n]
 };
 
-template <class TL>
-__global__ void __launch_bounds__(256, 2)
+template <class TL, bool VEC>
+__global__ void __launch_bounds__(TL::THREADS, 512 / TL::THREADS)
 k_keep_grad(KgArgs p) {
-  constexpr int MI = TL::MI, NI = TL::NI, BM = TL::BM;
-  constexpr int AP = BM / 8;              // 16-byte pieces per row of P's tile
-  constexpr int PA = BM / 32;             // pieces per thread
-  __shared__ __align__(16) uint8_t As[2][kExBK * 256];
-  __shared__ __align__(16) uint8_t Bs[2][kExBK * 256];
+  constexpr int MI = TL::MI, NI = TL::NI, BM = TL::BM, BN = TL::BN, PA = TL::PA, NB = TL::NB, THREADS = TL::THREADS;
+  constexpr int AW = BM < 128 ? 128 : BM;                 // columns of P's tile in LDS
+  constexpr uint32_t ASZ = kExBK * 2 * AW, BUF = ASZ + kExBK * 2 * BN;
+  __shared__ __align__(16) uint8_t smem[2 * BUF];
   int rt, ct;
   if (!tile_of(blockIdx.x, p.nmt, p.nnt, rt, ct)) return;
   const int e = blockIdx.y, sp = blockIdx.z;
@@ -638,78 +796,116 @@ k_keep_grad(KgArgs p) {
   const int k0 = (int)min((int64_t)hi, lo + (int64_t)sp * per), k1 = (int)min((int64_t)hi, k0 + (int64_t)per);
   const int nst = (int)ceil_div(k1 - k0, kExBK);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave % TL::WM, wn = wave / TL::WM, h = lane >> 5, li = lane & 31;
-  const int64_t m0 = (int64_t)rt * BM, c0 = (int64_t)ct * kExBN;
+  const int wm = wave % TL::WM, wn = wave / TL::WM;
+  const int64_t m0 = (int64_t)rt * BM, c0 = (int64_t)ct * TL::BN;
+  const uint32_t lds = lds_addr(smem);
 
-  // staging: A piece tid % AP of rows tid / AP + (256 / AP) i; B 32 columns
-  // tid & 3 of row tid / 4
-  const int ap = tid % AP, ar = tid / AP;
-  const int br = tid >> 2, bc = tid & 3;
-  const int64_t bcol = c0 + 32 * bc;
+  // staging: A piece tid % AP of rows tid / AP + AR i; B units NB (tid % BU)
+  // .. of row tid / BU
+  constexpr int AP = BM / 8, AR = THREADS / AP, BU = BN / 8 / NB;
+  const int ap = tid % AP, ar = tid / AP, bu = NB * (tid % BU), br = tid / BU;
+  const int64_t bcol = c0 + 8 * bu;
   const bool bok = bcol < p.pitch;
-  ex_u32x4_t ra[PA], rb[2];
-  float rs = 0.f;
-  auto gload = [&](int st) {
+  static_assert(AR % 4 == 0, "rows apart keep the swizzle");
+  const uint32_t aw = lds + col_piece<AW>(ar, ap);
+  uint32_t bw[NB];
+#pragma unroll
+  for (int u = 0; u < NB; ++u) bw[u] = lds + ASZ + col_piece<BN>(br, bu + u);
+  ex_u32x4_t ra[PA], rb[2][NB / 2];
+  uint32_t rx[2];
+  bool rv[2];
+  const int64_t bc = bok ? bcol : 0;
+  // the source row of a stage is looked up one stage before its loads
+  auto lookup = [&](int st) { return (int)source_row(p.rows, min(k0 + st * kExBK + br, k1 - 1), p.T); };
+  int src = 0;
+  auto aload = [&](int st) {
 #pragma unroll
     for (int i = 0; i < PA; ++i) {
-      const int r = k0 + st * kExBK + ar + (256 / AP) * i;
-      ra[i] = r < k1 ? load_piece(p.P + (int64_t)r * p.ldp, m0 + 8 * ap, p.m, p.pvec) : (ex_u32x4_t){0u, 0u, 0u, 0u};
-    }
-    const int r = k0 + st * kExBK + br;
-    if (r < k1 && bok) {
-      const int64_t src = source_row(p.rows, r, p.T);
-      const ex_u32x4_t* c = reinterpret_cast<const ex_u32x4_t*>(p.codes + src * p.pitch + bcol);
-      rb[0] = c[0];
-      rb[1] = c[1];
-      const uint32_t x = p.exps[src * (p.pitch / 32) + bcol / 32];
-      rs = __uint_as_float(x == 255u ? 0x7FC00000u : x << 23);
-    } else {                               // rows past the part: zeros on both sides
-      rb[0] = rb[1] = (ex_u32x4_t){0u, 0u, 0u, 0u};
-      rs = 0.f;
+      const int r = k0 + st * kExBK + ar + AR * i;        // rows past the part: zeros on both sides
+      ra[i] = load_piece<VEC>(p.P + (int64_t)min(r, k1 - 1) * p.ldp, m0 + 8 * ap, r < k1 ? p.m : 0);
     }
   };
-  auto lwrite = [&](int b) {
+  auto bload = [&](auto B, int st) {
+    const ex_u32x4_t* c = reinterpret_cast<const ex_u32x4_t*>(p.codes + src * p.pitch + bc);
 #pragma unroll
-    for (int i = 0; i < PA; ++i)
-      *reinterpret_cast<ex_u32x4_t*>(As[b] + col_piece(ar + (256 / AP) * i, ap)) = ra[i];
+    for (int i = 0; i < NB / 2; ++i) rb[B][i] = c[i];
+    rx[B] = p.exps[src * (p.pitch / 32) + bc / 32];
+    rv[B] = k0 + st * kExBK + br < k1 && bok;
+    src = lookup(min(st + 1, nst - 1));
+  };
+  auto awrite = [&](auto B) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      ex_u32x4_t o;
+    for (int i = 0; i < PA; ++i) lds_write(aw + B * BUF + i * (AR * 2 * AW), ra[i]);
+  };
+  auto bwrite = [&](auto B, auto KK) {
+    constexpr int kk = decltype(KK)::value;
+    const float step = rv[B] ? __uint_as_float(rx[B] == 255u ? 0x7FC00000u : rx[B] << 23) : 0.f;
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        // codes + 128 as unsigned bytes: one conversion per code
-        const uint32_t u = rb[q >> 1][2 * (q & 1) + w] ^ 0x80808080u;
-        float f[4];
+    for (int q = 0; q < NB; ++q)
+      if (q * 4 / NB == kk) {
+        ex_u32x4_t o;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = ((float)((u >> (8 * i)) & 0xFFu) - 128.f) * rs;
-        o[2 * w] = pack_exact(f[0], f[1]);
-        o[2 * w + 1] = pack_exact(f[2], f[3]);
+        for (int w = 0; w < 2; ++w) {
+          // codes + 128 as unsigned bytes: one conversion per code
+          const uint32_t u = rb[B][q >> 1][2 * (q & 1) + w] ^ 0x80808080u;
+          float f[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = ((float)((u >> (8 * i)) & 0xFFu) - 128.f) * step;
+          o[2 * w] = pack_exact(f[0], f[1]);
+          o[2 * w + 1] = pack_exact(f[2], f[3]);
+        }
+        lds_write(bw[q] + B * BUF, o);
       }
-      *reinterpret_cast<ex_u32x4_t*>(Bs[b] + col_piece(br, 4 * bc + q)) = o;
-    }
   };
+  uint32_t af[MI], bf[NI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) af[mi] = lds + col_frag_at<AW>(32 * (MI * wm + mi), lane);
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) bf[ni] = lds + ASZ + col_frag_at<BN>(32 * (NI * wn + ni), lane);
 
   ex_f32x16_t acc[MI][NI] = {};
-  if (nst > 0) gload(0);
-  for (int st = 0; st < nst; ++st) {
-    const int b = st & 1;
-    lwrite(b);
+  auto stage = [&](auto B, int st) {
+    constexpr int b = decltype(B)::value;
     __syncthreads();
-    if (st + 1 < nst) gload(st + 1);
+    aload(min(st + 1, nst - 1));
+    bload(B, min(st + 2, nst - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    ex_bf16x8_t fa[2][MI], fb[2][NI];
+    auto frags = [&](auto KK) {
+      constexpr int kk = decltype(KK)::value;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      ex_bf16x8_t fa[MI], fb[NI];
+      for (int mi = 0; mi < MI; ++mi) fa[kk & 1][mi] = lds_col_frag<AW>(af[mi] + b * BUF + kk * (32 * AW));
 #pragma unroll
-      for (int mi = 0; mi < MI; ++mi) fa[mi] = frag_col(lds_addr(As[b]), 32 * (MI * wm + mi), kk, lane);
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni) fb[ni] = frag_col(lds_addr(Bs[b]), 32 * (NI * wn + ni), kk, lane);
+      for (int ni = 0; ni < NI; ++ni) fb[kk & 1][ni] = lds_col_frag<BN>(bf[ni] + b * BUF + kk * (32 * BN));
+    };
+    frags(ex_const<0>{});
+    for_four([&](auto KK) {
+      constexpr int kk = decltype(KK)::value;
+      if constexpr (kk < 3) frags(ex_const<kk + 1>{});
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni)
-          acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[mi], fb[ni], acc[mi][ni], 0, 0, 0);
-    }
+          acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk & 1][mi], fb[kk & 1][ni], acc[mi][ni], 0, 0, 0);
+      bwrite(ex_const<1 - b>{}, KK);
+    });
+    awrite(ex_const<1 - b>{});
+  };
+  if (nst > 0) {
+    src = lookup(0);
+    aload(0);
+    bload(ex_const<0>{}, 0);
+    bload(ex_const<1>{}, min(1, nst - 1));
+    awrite(ex_const<0>{});
+    for_four([&](auto KK) { bwrite(ex_const<0>{}, KK); });
   }
+  int st = 0;
+  for (; st + 1 < nst; st += 2) {
+    stage(ex_const<0>{}, st);
+    stage(ex_const<1>{}, st + 1);
+  }
+  if (st < nst) stage(ex_const<0>{}, st);
+  const int h = lane >> 5, li = lane & 31;
   float* __restrict__ out = p.out + (int64_t)sp * p.split_stride + (int64_t)e * p.m * p.n;
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) {
@@ -744,14 +940,16 @@ static bool bf16_rows_vec(const void* p, int64_t ld, int64_t cols) {
 // Rows of a tile: 16 is the matrix-vector form.
 static int expert_bm(const ExpertArgs& a, int grad) {
   const int64_t avg = ceil_div(a.R, a.E);
-  if (!grad && avg <= 16 && ((uintptr_t)a.A & 15) == 0 && a.lda % 8 == 0) return 16;
-  return avg <= 64 ? 64 : 128;
+  if (!bf16_rows_vec(a.A, a.lda, grad ? a.d_out : a.n)) return 64;
+  if (!grad && avg <= 16) return 16;
+  if (!grad || !a.y_bf16) return avg <= 64 ? 64 : 128;
+  return avg <= 64 ? 64 : (avg <= 512 ? 128 : 256);
 }
 
 int64_t expert_grid(const ExpertArgs& a, int grad) {
   const int bm = expert_bm(a, grad);
   const int64_t cols = grad ? a.n : a.d_out;
-  return row_tiles(a.R, a.E, bm) * ceil_div(cols, bm == 16 ? 32 : kExBN) + 8;
+  return row_tiles(a.R, a.E, bm) * ceil_div(cols, bm == 16 ? 32 : 128) + 8;
 }
 
 template <int BITS>
@@ -767,11 +965,10 @@ static void mv_go(hipStream_t s, const ExpertArgs& a) {
                        a.offsets, a.E, a.R, a.qw, a.scales, a.zeros, a.d_out, a.group, a.Y, a.y_bf16, a.ldy);
 }
 
-static ExArgs ex_args(const ExpertArgs& a, int BM, int64_t kdim, int64_t cols) {
+static ExArgs ex_args(const ExpertArgs& a, int BM, int BN, int64_t cols) {
   ExArgs p;
   p.A = static_cast<const uint16_t*>(a.A);
   p.lda = a.lda;
-  p.avec = bf16_rows_vec(a.A, a.lda, kdim) ? 1 : 0;
   p.rows = a.rows;
   p.T = a.T;
   p.offsets = a.offsets;
@@ -787,41 +984,56 @@ static ExArgs ex_args(const ExpertArgs& a, int BM, int64_t kdim, int64_t cols) {
   p.ybf16 = a.y_bf16;
   p.ldy = a.ldy;
   p.nrt = (int)row_tiles(a.R, a.E, BM);
-  p.nct = (int)ceil_div(cols, kExBN);
+  p.nct = (int)ceil_div(cols, BN);
   return p;
 }
 
 static dim3 tile_grid(int nr, int nc) { return dim3((unsigned)(8 * ceil_div((int64_t)nr * nc, 8))); }
 
-template <int BITS, class TL>
+template <int BITS, class TL, int GS, bool VEC>
 static void mm_go(hipStream_t s, const ExpertArgs& a) {
-  const ExArgs p = ex_args(a, TL::BM, a.n, a.d_out);
-  hipLaunchKernelGGL((k_expert_mm<BITS, TL>), tile_grid(p.nrt, p.nct), dim3(256), 0, s, p);
+  const ExArgs p = ex_args(a, TL::BM, TL::BN, a.d_out);
+  hipLaunchKernelGGL((k_expert_mm<BITS, TL, GS, VEC>), tile_grid(p.nrt, p.nct), dim3(TL::THREADS), 0, s, p);
 }
 
-template <int BITS, int NP, class TL>
+// Fixed group lengths are worth their own code at 4 bits, the common width.
+template <int BITS, class TL>
+static void mm_group(hipStream_t s, const ExpertArgs& a) {
+  if constexpr (BITS == 4) {
+    if (a.group == 64) return mm_go<4, TL, 1, true>(s, a);
+    if (a.group == 128) return mm_go<4, TL, 2, true>(s, a);
+  }
+  mm_go<BITS, TL, 0, true>(s, a);
+}
+
+template <int BITS, int NP, class TL, bool VEC>
 static void grad_go(hipStream_t s, const ExpertArgs& a) {
-  const ExArgs p = ex_args(a, TL::BM, a.d_out, a.n);
-  hipLaunchKernelGGL((k_expert_mm_grad<BITS, NP, TL>), tile_grid(p.nrt, p.nct), dim3(256), 0, s, p);
+  const ExArgs p = ex_args(a, TL::BM, TL::BN, a.n);
+  hipLaunchKernelGGL((k_expert_mm_grad<BITS, NP, TL, VEC>), tile_grid(p.nrt, p.nct), dim3(TL::THREADS), 0, s, p);
 }
 
 template <int BITS>
 static void fwd_bits(hipStream_t s, const ExpertArgs& a) {
+  if (!bf16_rows_vec(a.A, a.lda, a.n)) return mm_go<BITS, ExTile64, 0, false>(s, a);
   const int bm = expert_bm(a, 0);
   if (bm == 16) mv_go<BITS>(s, a);
-  else if (bm == 64) mm_go<BITS, ExTile64>(s, a);
-  else mm_go<BITS, ExTile128>(s, a);
+  else if (bm == 64) mm_group<BITS, ExTile64>(s, a);
+  else mm_group<BITS, ExTile128>(s, a);
 }
 
 template <int BITS>
 static void grad_bits(hipStream_t s, const ExpertArgs& a) {
-  const bool small = expert_bm(a, 1) == 64;
-  if (a.y_bf16) {
-    if (small) grad_go<BITS, 1, ExTile64>(s, a);
-    else grad_go<BITS, 1, ExTile128>(s, a);
+  const int bm = expert_bm(a, 1);
+  if (!bf16_rows_vec(a.A, a.lda, a.d_out)) {
+    if (a.y_bf16) grad_go<BITS, 1, ExTile64, false>(s, a);
+    else grad_go<BITS, 3, ExTile64, false>(s, a);
+  } else if (a.y_bf16) {
+    if (bm == 64) grad_go<BITS, 1, ExTile64, true>(s, a);
+    else if (bm == 128) grad_go<BITS, 1, ExTile128, true>(s, a);
+    else grad_go<BITS, 1, ExTileX, true>(s, a);
   } else {
-    if (small) grad_go<BITS, 3, ExTile64>(s, a);
-    else grad_go<BITS, 3, ExTile128>(s, a);
+    if (bm == 64) grad_go<BITS, 3, ExTile64, true>(s, a);
+    else grad_go<BITS, 3, ExTile128, true>(s, a);
   }
 }
 
@@ -843,8 +1055,8 @@ hipError_t launch_expert_mm_grad(hipStream_t s, const ExpertArgs& a) {
 
 KeepGradPlan keep_grad_plan(int64_t R, int E, int64_t m, int64_t n) {
   KeepGradPlan p{};
-  p.bm = m <= 32 ? 32 : (m <= 64 ? 64 : 128);
-  const int64_t tiles = ceil_div(m, p.bm) * ceil_div(n, kExBN) * E;
+  p.bm = m <= 32 ? 32 : (m <= 64 ? 64 : (m <= 128 ? 128 : 256));
+  const int64_t tiles = ceil_div(m, p.bm) * ceil_div(n, p.bm == 256 ? 256 : 128) * E;
   const int64_t seg = ceil_div(R, E);                 // rows of an average segment
   int64_t s = tiles > 0 ? 512 / tiles : 1;            // two workgroups per CU
   s = std::min<int64_t>(s, seg / 256);                // at least four stages each
@@ -854,9 +1066,10 @@ KeepGradPlan keep_grad_plan(int64_t R, int E, int64_t m, int64_t n) {
 }
 
 template <class TL>
-static void kg_go(hipStream_t s, const KgArgs& p) {
+static void kg_go(hipStream_t s, const KgArgs& p, bool vec) {
   const dim3 grid((unsigned)(8 * ceil_div((int64_t)p.nmt * p.nnt, 8)), (unsigned)p.E, (unsigned)p.splits);
-  hipLaunchKernelGGL((k_keep_grad<TL>), grid, dim3(256), 0, s, p);
+  if (vec) hipLaunchKernelGGL((k_keep_grad<TL, true>), grid, dim3(TL::THREADS), 0, s, p);
+  else hipLaunchKernelGGL((k_keep_grad<TL, false>), grid, dim3(TL::THREADS), 0, s, p);
 }
 
 hipError_t launch_keep_grad(hipStream_t s, const KeepGradPlan& pl, const uint16_t* P, int64_t ldp, int64_t R, int64_t m,
@@ -866,7 +1079,6 @@ hipError_t launch_keep_grad(hipStream_t s, const KeepGradPlan& pl, const uint16_
   KgArgs p;
   p.P = P;
   p.ldp = ldp;
-  p.pvec = bf16_rows_vec(P, ldp, m) ? 1 : 0;
   p.m = m;
   p.codes = codes;
   p.exps = exps;
@@ -878,13 +1090,15 @@ hipError_t launch_keep_grad(hipStream_t s, const KeepGradPlan& pl, const uint16_
   p.E = E;
   p.R = (int)R;
   p.nmt = (int)ceil_div(m, pl.bm);
-  p.nnt = (int)ceil_div(n, kExBN);
+  p.nnt = (int)ceil_div(n, pl.bm == 256 ? 256 : 128);
   p.splits = pl.splits;
   p.out = pl.splits > 1 ? part : G;
   p.split_stride = (int64_t)E * m * n;
-  if (pl.bm == 32) kg_go<ExTile32>(s, p);
-  else if (pl.bm == 64) kg_go<ExTile64>(s, p);
-  else kg_go<ExTile128>(s, p);
+  const bool vec = bf16_rows_vec(P, ldp, m);
+  if (pl.bm == 32) kg_go<ExTile32>(s, p, vec);
+  else if (pl.bm == 64) kg_go<ExTile64>(s, p, vec);
+  else if (pl.bm == 128) kg_go<ExTile128>(s, p, vec);
+  else kg_go<ExTileX>(s, p, vec);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || pl.splits <= 1) return err;
   const int64_t count = (int64_t)E * m * n;

@@ -253,13 +253,16 @@ hipError_t launch_route(hipStream_t s, const int32_t* ids, int64_t ldi, int64_t 
 }
 
 // ---------------------------------------------------------------- rows there and back
+// The rows of Ys and dY are read once, so they are loaded past the caches
+// (268 MB of Ys: 80 against 94 us).
 // A unit is 8 columns: 16 bytes of bf16, 32 of fp32. VEC: every row of both
 // sides is 16-byte aligned and n % 8 == 0, so units move as whole 16-byte
 // pieces; otherwise columns past n are guarded one by one.
 template <bool BF, bool VEC>
 __device__ __forceinline__ void rt_load8(const void* base, int64_t off, int ncols, float (&v)[8]) {
   if constexpr (VEC && BF) {
-    const rt_u32x4_t u = *reinterpret_cast<const rt_u32x4_t*>(static_cast<const uint16_t*>(base) + off);
+    const rt_u32x4_t u =
+        __builtin_nontemporal_load(reinterpret_cast<const rt_u32x4_t*>(static_cast<const uint16_t*>(base) + off));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = __uint_as_float(u[i] << 16);
@@ -267,8 +270,8 @@ __device__ __forceinline__ void rt_load8(const void* base, int64_t off, int ncol
     }
   } else if constexpr (VEC) {
     const float* p = static_cast<const float*>(base) + off;
-    const rt_f32x4_t a = *reinterpret_cast<const rt_f32x4_t*>(p);
-    const rt_f32x4_t b = *reinterpret_cast<const rt_f32x4_t*>(p + 4);
+    const rt_f32x4_t a = __builtin_nontemporal_load(reinterpret_cast<const rt_f32x4_t*>(p));
+    const rt_f32x4_t b = __builtin_nontemporal_load(reinterpret_cast<const rt_f32x4_t*>(p + 4));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[i] = a[i];
@@ -311,51 +314,59 @@ __device__ __forceinline__ void rt_store8(void* base, int64_t off, int ncols, co
 
 // Xs[inverse[t k + j]] = X[t]: rows of `width` elements of U (16 bytes, or
 // one element when the rows are not aligned), copied bit by bit. One thread
-// per element of X's rows.
-template <typename U>
+// per element of X's rows. STREAM: non-temporal stores (268 MB of copies, 8
+// per row: 37 against 51 us).
+template <typename U, bool STREAM>
 __global__ void __launch_bounds__(256)
-k_dispatch(const U* __restrict__ X, int64_t ldx, int64_t T, int64_t width, int k,
-           const int32_t* __restrict__ inverse, int64_t R, U* __restrict__ Xs, int64_t lds) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= T * width) return;
-  const int64_t t = i / width, c = i - t * width;
-  const U v = X[t * ldx + c];
+k_dispatch(const U* __restrict__ X, int64_t ldx, uint32_t T, uint32_t width, int k,
+           const int32_t* __restrict__ inverse, int R, U* __restrict__ Xs, int64_t lds) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t t = i / width, c = i - t * width;
+  if (t >= T) return;
+  const U v = X[(int64_t)t * ldx + c];
+  const int32_t* __restrict__ inv = inverse + (int64_t)t * k;
   for (int j = 0; j < k; ++j) {
-    const int p = inverse[t * k + j];
-    if (p >= 0 && p < R) Xs[(int64_t)p * lds + c] = v;
+    const int p = inv[j];
+    if ((unsigned)p < (unsigned)R) {
+      if constexpr (STREAM) __builtin_nontemporal_store(v, Xs + (int64_t)p * lds + c);
+      else Xs[(int64_t)p * lds + c] = v;
+    }
   }
 }
 
-// Y[t] = sum_j w[t][j] Ys[inverse[t k + j]]; four rows are loaded before the
-// first is added, so a thread has 64 to 128 bytes in flight.
-template <bool YSBF, bool YBF, bool VEC>
+// Y[t] = sum_j w[t][j] Ys[inverse[t k + j]]. KB rows (1, 2, 4 or 8: the
+// smallest that covers k, at most 8) are loaded before the first is added,
+// so a thread has up to 128 bytes of bf16 in flight.
+template <bool YSBF, bool YBF, bool VEC, int KB>
 __global__ void __launch_bounds__(256)
-k_combine(const void* __restrict__ Ys, int64_t lds, int64_t R, const int32_t* __restrict__ inverse,
-          const float* __restrict__ w, int64_t T, int64_t n, int64_t units, int k, void* __restrict__ Y, int64_t ldy) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= T * units) return;
-  const int64_t t = i / units, c = 8 * (i - t * units);
-  const int nc = (int)min((int64_t)8, n - c);
+k_combine(const void* __restrict__ Ys, int64_t lds, int R, const int32_t* __restrict__ inverse,
+          const float* __restrict__ w, uint32_t T, uint32_t n, uint32_t units, int k, void* __restrict__ Y, int64_t ldy) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t t = i / units, c = 8u * (i - t * units);
+  if (t >= T) return;
+  const int nc = (int)min(8u, n - c);
+  const int64_t s0 = (int64_t)t * k;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int j0 = 0; j0 < k; j0 += 4) {
-    float v[4][8], wj[4];
-    bool ok[4];
+  for (int j0 = 0; j0 < k; j0 += KB) {
+    float v[KB][8], wj[KB];
+    int p[KB];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int j = j0 + u;
-      const int p = j < k ? inverse[t * k + j] : -1;
-      ok[u] = p >= 0 && p < R;
-      wj[u] = ok[u] ? (w ? w[t * k + j] : 1.f) : 0.f;
-      if (ok[u]) rt_load8<YSBF, VEC>(Ys, (int64_t)p * lds + c, nc, v[u]);
+    for (int u = 0; u < KB; ++u) {
+      const bool in = j0 + u < k;
+      p[u] = in ? inverse[s0 + j0 + u] : -1;
+      wj[u] = w && in ? w[s0 + j0 + u] : 1.f;
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (ok[u]) {
+    for (int u = 0; u < KB; ++u)
+      if ((unsigned)p[u] < (unsigned)R) rt_load8<YSBF, VEC>(Ys, (int64_t)p[u] * lds + c, nc, v[u]);
+#pragma unroll
+    for (int u = 0; u < KB; ++u)
+      if ((unsigned)p[u] < (unsigned)R) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] = fmaf(wj[u], v[u][e], sum[e]);
       }
   }
-  rt_store8<YBF, VEC>(Y, t * ldy + c, nc, sum);
+  rt_store8<YBF, VEC>(Y, (int64_t)t * ldy + c, nc, sum);
 }
 
 // dYs[inverse[t k + j]] = w[t][j] dY[t], dw[t][j] = <dY[t], Ys[inverse[t k + j]]>.
@@ -425,24 +436,35 @@ hipError_t launch_dispatch(hipStream_t s, const void* X, int esize, int64_t T, i
   if (rows_aligned(X, ldx, esize) && rows_aligned(Xs, lds, esize) && (n * esize) % 16 == 0) {
     const int per = 16 / esize;
     const int64_t width = n / per;
-    hipLaunchKernelGGL((k_dispatch<rt_u32x4_t>), dim3((unsigned)ceil_div(T * width, 256)), dim3(256), 0, s,
-                       static_cast<const rt_u32x4_t*>(X), ldx / per, T, width, k, inverse, R,
+    const auto kernel = T * k * n * esize > kStreamBytes ? k_dispatch<rt_u32x4_t, true> : k_dispatch<rt_u32x4_t, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)ceil_div(T * width, 256)), dim3(256), 0, s,
+                       static_cast<const rt_u32x4_t*>(X), ldx / per, (uint32_t)T, (uint32_t)width, k, inverse, (int)R,
                        static_cast<rt_u32x4_t*>(Xs), lds / per);
   } else if (esize == 2) {
-    hipLaunchKernelGGL((k_dispatch<uint16_t>), dim3((unsigned)ceil_div(T * n, 256)), dim3(256), 0, s,
-                       static_cast<const uint16_t*>(X), ldx, T, n, k, inverse, R, static_cast<uint16_t*>(Xs), lds);
+    hipLaunchKernelGGL((k_dispatch<uint16_t, false>), dim3((unsigned)ceil_div(T * n, 256)), dim3(256), 0, s,
+                       static_cast<const uint16_t*>(X), ldx, (uint32_t)T, (uint32_t)n, k, inverse, (int)R, static_cast<uint16_t*>(Xs), lds);
   } else {
-    hipLaunchKernelGGL((k_dispatch<uint32_t>), dim3((unsigned)ceil_div(T * n, 256)), dim3(256), 0, s,
-                       static_cast<const uint32_t*>(X), ldx, T, n, k, inverse, R, static_cast<uint32_t*>(Xs), lds);
+    hipLaunchKernelGGL((k_dispatch<uint32_t, false>), dim3((unsigned)ceil_div(T * n, 256)), dim3(256), 0, s,
+                       static_cast<const uint32_t*>(X), ldx, (uint32_t)T, (uint32_t)n, k, inverse, (int)R, static_cast<uint32_t*>(Xs), lds);
   }
   return hipGetLastError();
 }
 
+template <bool YSBF, bool YBF, bool VEC, int KB>
+static void combine_kb(hipStream_t s, const CombineArgs& a) {
+  const int64_t units = ceil_div(a.n, 8);
+  hipLaunchKernelGGL((k_combine<YSBF, YBF, VEC, KB>), dim3((unsigned)ceil_div(a.T * units, 256)), dim3(256), 0, s, a.Ys,
+                     a.lds, (int)a.R, a.inverse, a.w, (uint32_t)a.T, (uint32_t)a.n, (uint32_t)units, a.k, a.Y, a.ldy);
+}
+
 template <bool YSBF, bool YBF, bool VEC>
 static void combine_go(hipStream_t s, const CombineArgs& a) {
-  const int64_t units = ceil_div(a.n, 8);
-  hipLaunchKernelGGL((k_combine<YSBF, YBF, VEC>), dim3((unsigned)ceil_div(a.T * units, 256)), dim3(256), 0, s, a.Ys,
-                     a.lds, a.R, a.inverse, a.w, a.T, a.n, units, a.k, a.Y, a.ldy);
+  if constexpr (VEC) {
+    if (a.k == 1) return combine_kb<YSBF, YBF, true, 1>(s, a);
+    if (a.k == 2) return combine_kb<YSBF, YBF, true, 2>(s, a);
+    if (a.k > 4) return combine_kb<YSBF, YBF, true, 8>(s, a);
+  }
+  combine_kb<YSBF, YBF, VEC, 4>(s, a);
 }
 
 hipError_t launch_combine(hipStream_t s, const CombineArgs& a) {

@@ -6,6 +6,7 @@ library is not built, or a tensor is not on the GPU, the calls raise.
 The names mirror include/gptq.h.
 """
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -354,8 +355,16 @@ class Checkpoint:
     n: int
 
 
-def _null():
-    return ctypes.c_void_p(0)
+# These calls are short enough for the binding's own time to show (three of
+# them per layer and token), so the checks below are written to cost little:
+# pointers travel as plain integers, sizes of workspaces are remembered, and
+# the device is switched only when it is not the current one.
+_FLOATS = (torch.bfloat16, torch.float32)
+_DTYPE_CODES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _type_error(name, dtypes):
+    return TypeError(f"{name} must be " + " or ".join(str(d).replace("torch.", "") for d in dtypes))
 
 
 def _rows2d(t, name, dtypes, device=None):
@@ -363,38 +372,64 @@ def _rows2d(t, name, dtypes, device=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be " + " or ".join(str(d).replace("torch.", "") for d in dtypes))
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions")
+        raise _type_error(name, dtypes)
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    pitch, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    pitch = t.stride(0) if rows > 1 else max(cols, 1)
-    if rows > 1 and pitch < cols:
+    if rows <= 1:
+        pitch = max(cols, 1)
+    elif pitch < cols:
         raise ValueError(f"{name}'s rows overlap")
-    return ctypes.c_void_p(t.data_ptr()), pitch
+    return t.data_ptr(), pitch
 
 
 def _dense(t, name, dtype, device, shape):
     """Pointer of a contiguous tensor of this type and shape."""
-    _dev(t, name)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype != dtype:
-        raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}")
+        raise _type_error(name, (dtype,))
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    return ctypes.c_void_p(t.data_ptr())
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-_FLOATS = (torch.bfloat16, torch.float32)
+def _call(device, f, *args):
+    """One call on the tensors' device, on its current stream."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        st = f(torch.cuda.current_stream(i).cuda_stream, *args)
+    else:
+        with torch.cuda.device(i):
+            st = f(torch.cuda.current_stream(i).cuda_stream, *args)
+    if st != OK:
+        _check(st)
 
 
-def _on(device):
-    """The call runs on the tensors' device, on its current stream."""
-    return torch.cuda.device(device)
+@functools.lru_cache(maxsize=1024)
+def _bytes(name, *sizes):
+    """Workspace bytes of a call, which follow from its sizes alone."""
+    out = ctypes.c_size_t(0)
+    _check(getattr(load(), name)(*sizes, ctypes.byref(out)))
+    return out.value
+
+
+def _scratch(nbytes, device, workspace):
+    if nbytes == 0:
+        return None, None
+    ws, p = _workspace(nbytes, device, workspace)
+    if ws.device != device:
+        raise ValueError(f"workspace is on {ws.device}, not on {device}")
+    return ws, p
 
 
 def route(expert_ids, n_experts, workspace=None):
@@ -404,24 +439,22 @@ def route(expert_ids, n_experts, workspace=None):
     p, ldi = _rows2d(expert_ids, "expert_ids", (torch.int32,))
     T, k = expert_ids.shape
     dev = expert_ids.device
-    c = ctypes.c_size_t(0)
-    _check(lib.gptq_route_workspace_bytes(T, k, int(n_experts), ctypes.byref(c)))
-    with _on(dev):
-        r = Route(torch.empty((n_experts + 1,), dtype=torch.int32, device=dev),
-                  torch.empty((T * k,), dtype=torch.int32, device=dev),
-                  torch.empty((T, k), dtype=torch.int32, device=dev))
-        ws, wsp = _workspace(c.value, dev, workspace)
-        _check(lib.gptq_route(_stream(), p, ldi, T, k, int(n_experts), _dev(r.offsets, "offsets"),
-                              _dev(r.rows, "rows"), _dev(r.inverse, "inverse"), wsp, c.value))
+    E = int(n_experts)
+    need = _bytes("gptq_route_workspace_bytes", T, k, E)
+    r = Route(torch.empty((E + 1,), dtype=torch.int32, device=dev),
+              torch.empty((T * k,), dtype=torch.int32, device=dev),
+              torch.empty((T, k), dtype=torch.int32, device=dev))
+    ws, wsp = _scratch(need, dev, workspace)
+    _call(dev, lib.gptq_route, p, ldi, T, k, E, r.offsets.data_ptr(), r.rows.data_ptr(), r.inverse.data_ptr(), wsp,
+          need)
     return r
 
 
 def _slots(inverse, device, T):
     if not isinstance(inverse, torch.Tensor) or inverse.dim() != 2:
         raise ValueError("inverse must have two dimensions")
-    if inverse.shape[0] != T:
-        raise ValueError(f"inverse has {inverse.shape[0]} rows for {T} tokens")
-    return _dense(inverse, "inverse", torch.int32, device, inverse.shape), inverse.shape[1]
+    k = inverse.shape[1]
+    return _dense(inverse, "inverse", torch.int32, device, (T, k)), k
 
 
 def dispatch(X, inverse, out=None):
@@ -432,13 +465,14 @@ def dispatch(X, inverse, out=None):
     T, n = X.shape
     dev = X.device
     ip, k = _slots(inverse, dev, T)
-    with _on(dev):
-        Xs = out if out is not None else torch.empty((T * k, n), dtype=X.dtype, device=dev)
-        sp, lds = _rows2d(Xs, "out", (X.dtype,), dev)
-        if Xs.shape[1] != n:
-            raise ValueError(f"out must have {n} columns")
-        _check(lib.gptq_dispatch(_stream(), xp, _dtype_code(X), T, n, ldx, k, ip, Xs.shape[0], sp, lds))
-    return Xs
+    if out is None:
+        out = torch.empty((T * k, n), dtype=X.dtype, device=dev)
+    sp, lds = _rows2d(out, "out", (X.dtype,), dev)
+    R, cols = out.shape
+    if cols != n:
+        raise ValueError(f"out must have {n} columns")
+    _call(dev, lib.gptq_dispatch, xp, _DTYPE_CODES[X.dtype], T, n, ldx, k, ip, R, sp, lds)
+    return out
 
 
 def combine(Ys, inverse, weights=None, out=None, out_dtype=None):
@@ -451,14 +485,14 @@ def combine(Ys, inverse, weights=None, out=None, out_dtype=None):
     dev = Ys.device
     T = inverse.shape[0]
     ip, k = _slots(inverse, dev, T)
-    wp = _null() if weights is None else _dense(weights, "weights", torch.float32, dev, (T, k))
-    with _on(dev):
-        Y = out if out is not None else torch.empty((T, n), dtype=out_dtype or Ys.dtype, device=dev)
-        yp, ldy = _rows2d(Y, "out", _FLOATS, dev)
-        if tuple(Y.shape) != (T, n):
-            raise ValueError(f"out must have the shape {(T, n)}")
-        _check(lib.gptq_combine(_stream(), sp, _dtype_code(Ys), R, lds, ip, wp, T, n, k, yp, _dtype_code(Y), ldy))
-    return Y
+    wp = None if weights is None else _dense(weights, "weights", torch.float32, dev, (T, k))
+    if out is None:
+        out = torch.empty((T, n), dtype=out_dtype or Ys.dtype, device=dev)
+    yp, ldy = _rows2d(out, "out", _FLOATS, dev)
+    if out.shape != (T, n):
+        raise ValueError(f"out must have the shape {(T, n)}")
+    _call(dev, lib.gptq_combine, sp, _DTYPE_CODES[Ys.dtype], R, lds, ip, wp, T, n, k, yp, _DTYPE_CODES[out.dtype], ldy)
+    return out
 
 
 def combine_grad(dY, Ys, inverse, weights, out=None, out_dtype=None):
@@ -470,20 +504,20 @@ def combine_grad(dY, Ys, inverse, weights, out=None, out_dtype=None):
     T, n = dY.shape
     dev = dY.device
     sp, lds = _rows2d(Ys, "Ys", _FLOATS, dev)
-    R = Ys.shape[0]
-    if Ys.shape[1] != n:
+    R, cols = Ys.shape
+    if cols != n:
         raise ValueError(f"Ys must have {n} columns")
     ip, k = _slots(inverse, dev, T)
     wp = _dense(weights, "weights", torch.float32, dev, (T, k))
-    with _on(dev):
-        dYs = out if out is not None else torch.empty((R, n), dtype=out_dtype or dY.dtype, device=dev)
-        op, ldo = _rows2d(dYs, "out", _FLOATS, dev)
-        if tuple(dYs.shape) != (R, n):
-            raise ValueError(f"out must have the shape {(R, n)}")
-        dw = torch.empty((T, k), dtype=torch.float32, device=dev)
-        _check(lib.gptq_combine_grad(_stream(), gp, _dtype_code(dY), ldy, sp, _dtype_code(Ys), R, lds, ip, wp, T, n, k,
-                                     op, _dtype_code(dYs), ldo, _dev(dw, "dweights")))
-    return dYs, dw
+    if out is None:
+        out = torch.empty((R, n), dtype=out_dtype or dY.dtype, device=dev)
+    op, ldo = _rows2d(out, "out", _FLOATS, dev)
+    if out.shape != (R, n):
+        raise ValueError(f"out must have the shape {(R, n)}")
+    dw = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _call(dev, lib.gptq_combine_grad, gp, _DTYPE_CODES[dY.dtype], ldy, sp, _DTYPE_CODES[Ys.dtype], R, lds, ip, wp, T, n,
+          k, op, _DTYPE_CODES[out.dtype], ldo, dw.data_ptr())
+    return out, dw
 
 
 def _expert_layers(qweight, scales, zeros, bits, group, n, device):
@@ -491,22 +525,21 @@ def _expert_layers(qweight, scales, zeros, bits, group, n, device):
     dimension); returns E, d_out and the three pointers."""
     if not isinstance(qweight, torch.Tensor) or qweight.dim() not in (2, 3):
         raise ValueError("qweight must be (E x) d_out x words")
-    lead = tuple(qweight.shape[:-1])
-    E, d_out = lead if len(lead) == 2 else (1, lead[0])
     if bits not in (2, 3, 4) or group <= 0:
         raise GPTQError(EINVAL, "bits must be 2, 3 or 4 and group positive")
-    words, ng = (n * bits + 31) // 32, n // group
     if qweight.dtype not in (torch.int32, torch.uint32):
         raise TypeError("qweight must be int32 or uint32")
-    qp = _dense(qweight, "qweight", qweight.dtype, device, lead + (words,))
-    return (E, d_out, qp, _dense(scales, "scales", torch.float32, device, lead + (ng,)),
-            _dense(zeros, "zeros", torch.uint8, device, lead + (ng,)))
+    lead = qweight.shape[:-1]
+    E, d_out = lead if len(lead) == 2 else (1, lead[0])
+    per_group = lead + (n // group,)
+    return (E, d_out, _dense(qweight, "qweight", qweight.dtype, device, lead + ((n * bits + 31) // 32,)),
+            _dense(scales, "scales", torch.float32, device, per_group),
+            _dense(zeros, "zeros", torch.uint8, device, per_group))
 
 
 def _segments(offsets, rows, E, device, R):
-    op = _null() if offsets is None else _dense(offsets, "offsets", torch.int32, device, (E + 1,))
-    rp = _null() if rows is None else _dense(rows, "rows", torch.int32, device, (R,))
-    return op, rp
+    return (None if offsets is None else _dense(offsets, "offsets", torch.int32, device, (E + 1,)),
+            None if rows is None else _dense(rows, "rows", torch.int32, device, (R,)))
 
 
 def expert_matmul(X, offsets, qweight, scales, zeros, bits, group, rows=None, out=None, out_dtype=torch.float32):
@@ -522,14 +555,14 @@ def expert_matmul(X, offsets, qweight, scales, zeros, bits, group, rows=None, ou
     E, d_out, qp, sp, zp = _expert_layers(qweight, scales, zeros, bits, group, n, dev)
     R = T if rows is None else rows.numel()
     op, rp = _segments(offsets, rows, E, dev, R)
-    with _on(dev):
-        Y = out if out is not None else torch.empty((R, d_out), dtype=out_dtype, device=dev)
-        yp, ldy = _rows2d(Y, "out", _FLOATS, dev)
-        if tuple(Y.shape) != (R, d_out):
-            raise ValueError(f"out must have the shape {(R, d_out)}")
-        _check(lib.gptq_expert_matmul(_stream(), xp, BF16, T, n, ldx, rp, R, op, E, qp, sp, zp, d_out, int(bits),
-                                      int(group), yp, _dtype_code(Y), ldy))
-    return Y
+    if out is None:
+        out = torch.empty((R, d_out), dtype=out_dtype, device=dev)
+    yp, ldy = _rows2d(out, "out", _FLOATS, dev)
+    if out.shape != (R, d_out):
+        raise ValueError(f"out must have the shape {(R, d_out)}")
+    _call(dev, lib.gptq_expert_matmul, xp, BF16, T, n, ldx, rp, R, op, E, qp, sp, zp, d_out, bits, group, yp,
+          _DTYPE_CODES[out.dtype], ldy)
+    return out
 
 
 def expert_matmul_grad(dY, offsets, qweight, scales, zeros, bits, group, n, out=None, out_dtype=torch.bfloat16):
@@ -544,14 +577,14 @@ def expert_matmul_grad(dY, offsets, qweight, scales, zeros, bits, group, n, out=
     if d != d_out:
         raise ValueError(f"dY must have {d} columns")
     op, _ = _segments(offsets, None, E, dev, R)
-    with _on(dev):
-        dX = out if out is not None else torch.empty((R, n), dtype=out_dtype, device=dev)
-        xp, ldx = _rows2d(dX, "out", _FLOATS, dev)
-        if tuple(dX.shape) != (R, n):
-            raise ValueError(f"out must have the shape {(R, n)}")
-        _check(lib.gptq_expert_matmul_grad(_stream(), gp, BF16, R, ldy, op, E, qp, sp, zp, d_out, n, int(bits),
-                                           int(group), xp, _dtype_code(dX), ldx))
-    return dX
+    if out is None:
+        out = torch.empty((R, n), dtype=out_dtype, device=dev)
+    xp, ldx = _rows2d(out, "out", _FLOATS, dev)
+    if out.shape != (R, n):
+        raise ValueError(f"out must have the shape {(R, n)}")
+    _call(dev, lib.gptq_expert_matmul_grad, gp, BF16, R, ldy, op, E, qp, sp, zp, d_out, n, bits, group, xp,
+          _DTYPE_CODES[out.dtype], ldx)
+    return out
 
 
 # ---------------------------------------------------------------- kept activations
@@ -563,14 +596,16 @@ def checkpoint_save(X, out=None):
     T, n = X.shape
     dev = X.device
     groups = (n + 31) // 32
-    with _on(dev):
-        c = out if out is not None else Checkpoint(torch.empty((T, 32 * groups), dtype=torch.int8, device=dev),
-                                                   torch.empty((T, groups), dtype=torch.uint8, device=dev), n)
-        cp, ep = _kept(c, dev)
-        if c.codes.shape[0] != T or c.n != n:
+    if out is None:
+        out = Checkpoint(torch.empty((T, 32 * groups), dtype=torch.int8, device=dev),
+                         torch.empty((T, groups), dtype=torch.uint8, device=dev), n)
+        cp, ep = out.codes.data_ptr(), out.exps.data_ptr()
+    else:
+        cp, ep = _kept(out, dev)
+        if out.codes.shape[0] != T or out.n != n:
             raise ValueError(f"out must keep {T} x {n} values")
-        _check(lib.gptq_checkpoint_save(_stream(), xp, _dtype_code(X), T, n, ldx, cp, ep))
-    return c
+    _call(dev, lib.gptq_checkpoint_save, xp, _DTYPE_CODES[X.dtype], T, n, ldx, cp, ep)
+    return out
 
 
 def _kept(c, device):
@@ -585,14 +620,14 @@ def checkpoint_restore(kept, dtype=torch.bfloat16, out=None):
     lib = load()
     dev = kept.codes.device
     cp, ep = _kept(kept, dev)
-    T = kept.codes.shape[0]
-    with _on(dev):
-        X = out if out is not None else torch.empty((T, kept.n), dtype=dtype, device=dev)
-        xp, ldx = _rows2d(X, "out", _FLOATS, dev)
-        if tuple(X.shape) != (T, kept.n):
-            raise ValueError(f"out must have the shape {(T, kept.n)}")
-        _check(lib.gptq_checkpoint_restore(_stream(), cp, ep, T, kept.n, xp, _dtype_code(X), ldx))
-    return X
+    T, n = kept.codes.shape[0], kept.n
+    if out is None:
+        out = torch.empty((T, n), dtype=dtype, device=dev)
+    xp, ldx = _rows2d(out, "out", _FLOATS, dev)
+    if out.shape != (T, n):
+        raise ValueError(f"out must have the shape {(T, n)}")
+    _call(dev, lib.gptq_checkpoint_restore, cp, ep, T, n, xp, _DTYPE_CODES[out.dtype], ldx)
+    return out
 
 
 def checkpoint_weight_grad(P, kept, offsets=None, rows=None, out=None, workspace=None):
@@ -604,17 +639,16 @@ def checkpoint_weight_grad(P, kept, offsets=None, rows=None, out=None, workspace
     R, m = P.shape
     dev = P.device
     cp, ep = _kept(kept, dev)
+    T, n = kept.codes.shape[0], kept.n
     E = 1 if offsets is None else offsets.numel() - 1
     op, rp = _segments(offsets, rows, E, dev, R)
-    c = ctypes.c_size_t(0)
-    _check(lib.gptq_checkpoint_weight_grad_workspace_bytes(R, E, m, kept.n, ctypes.byref(c)))
-    with _on(dev):
-        G = out if out is not None else torch.empty((E, m, kept.n), dtype=torch.float32, device=dev)
-        gp = _dense(G, "out", torch.float32, dev, (E, m, kept.n))
-        ws, wsp = _workspace(c.value, dev, workspace)
-        _check(lib.gptq_checkpoint_weight_grad(_stream(), pp, BF16, R, m, ldp, cp, ep, kept.codes.shape[0], kept.n, rp,
-                                               op, E, gp, wsp, c.value))
-    return G
+    need = _bytes("gptq_checkpoint_weight_grad_workspace_bytes", R, E, m, n)
+    if out is None:
+        out = torch.empty((E, m, n), dtype=torch.float32, device=dev)
+    gp = _dense(out, "out", torch.float32, dev, (E, m, n))
+    ws, wsp = _scratch(need, dev, workspace)
+    _call(dev, lib.gptq_checkpoint_weight_grad, pp, BF16, R, m, ldp, cp, ep, T, n, rp, op, E, gp, wsp, need)
+    return out
 
 
 # ---------------------------------------------------------------- EoRA
