@@ -34,6 +34,18 @@ struct Seg {
   int row0;     // the tile's first row
 };
 
+// Inclusive sum over the wave by lane shifts inside and across its rows of 16
+// (no LDS traffic: this stands in front of every product).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr 1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);   // row_shr 2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);   // row_shr 4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);   // row_shr 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast 15 into rows 1, 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast 31 into rows 2, 3
+  return v;
+}
+
 // Row tile rt of BM rows (every wave of the workgroup finds it for itself).
 __device__ __forceinline__ Seg find_tile(const int32_t* __restrict__ offsets, int E, int R, int BM, int rt) {
   const int lane = threadIdx.x & 63;
@@ -50,21 +62,15 @@ __device__ __forceinline__ Seg find_tile(const int32_t* __restrict__ offsets, in
       hi = min(max(offsets[e + 1], lo), R);
     }
     const int nt = (hi - lo + BM - 1) / BM;
-    int inc = nt;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(inc, d);
-      if (lane >= d) inc += o;
-    }
+    const int inc = wave_scan(nt);
     const uint64_t past = __ballot(before + inc > rt);
     if (past) {
       const int l = __ffsll((long long)past) - 1;
-      const int slo = __shfl(lo, l), shi = __shfl(hi, l);
-      const int first = before + __shfl(inc - nt, l);
-      return Seg{__builtin_amdgcn_readfirstlane(e0 + l), __builtin_amdgcn_readfirstlane(slo),
-                 __builtin_amdgcn_readfirstlane(shi), __builtin_amdgcn_readfirstlane(slo + (rt - first) * BM)};
+      const int slo = __builtin_amdgcn_readlane(lo, l), shi = __builtin_amdgcn_readlane(hi, l);
+      const int first = before + __builtin_amdgcn_readlane(inc - nt, l);
+      return Seg{e0 + l, slo, shi, slo + (rt - first) * BM};
     }
-    before += __shfl(inc, 63);
+    before += __builtin_amdgcn_readlane(inc, 63);
   }
   return Seg{-1, 0, 0, 0};
 }
@@ -148,6 +154,15 @@ __device__ __forceinline__ uint32_t pack_exact(float a, float b) {
 //    formed by one more product with ones, shared by the OB blocks. All of
 //    it in fp32: the offset costs up to a factor of about 6 of fp32's
 //    rounding. A row with an infinity gives NaN.
+//
+// Measured (median kernel times; two experts of 11008 x 4096 for one token /
+// 64 experts of 1408 x 2048 for 256 rows, 4 bits, groups of 128; 48.6 and 99
+// MB, 10 and 20 us at the rate of a large copy): 19.9 / 31.8 us. Of it about 2
+// are the launch and the look-up, 6 / 10 the unpacking and the products,
+// the rest the weights' way from memory. One load per scale and piece instead
+// of one per S pieces: 22.9 / 42.5; 8 waves per workgroup 22.0 / 67;
+// 16 outputs per wave 19.8 / 40; 64 outputs 23.5 / 32.6; the weights loaded
+// past the caches 20.9 / 32.9.
 template <int BITS>
 __device__ __forceinline__ ex_bf16x8_t mv_window(const uint32_t* __restrict__ chunk, int j, float z) {
   const int base = 8 * BITS * j, wi = base >> 5;
@@ -184,7 +199,7 @@ __device__ __forceinline__ ex_bf16x8_t mv_order(ex_u32x4_t x) {
   return __builtin_bit_cast(ex_bf16x8_t, u);
 }
 
-template <int BITS, bool WIDE, int WAVES, int OB>
+template <int BITS, bool WIDE, int WAVES, int OB, int S>
 __global__ void __launch_bounds__(64 * WAVES)
 k_expert_mv(const uint16_t* __restrict__ X, int T, int64_t n, int64_t ldx, const int32_t* __restrict__ rows,
             const int32_t* __restrict__ offsets, int E, int R, const uint32_t* __restrict__ qw,
@@ -208,8 +223,11 @@ k_expert_mv(const uint16_t* __restrict__ X, int T, int64_t n, int64_t ldx, const
     srow[b] = scales + o * ngroups;
     zrow[b] = zeros + o * ngroups;
   }
-  // rows past the segment read its last row; their results are not stored
-  const uint16_t* __restrict__ xrow = X + source_row(rows, min(sg.row0 + li, sg.hi - 1), T) * ldx;
+  // lanes of rows past the segment load nothing: rows of the product do not
+  // mix, and their results are not stored
+  const bool xok = sg.row0 + li < sg.hi;
+  const int prow = min(sg.row0 + li, sg.hi - 1);
+  int srcrow = rows ? rows[prow] : prow;
 
   ex_f32x4_t tot[OB];
 #pragma unroll
@@ -218,50 +236,72 @@ k_expert_mv(const uint16_t* __restrict__ X, int T, int64_t n, int64_t ldx, const
   const ex_bf16x8_t ones = __builtin_bit_cast(ex_bf16x8_t, ones_bits);
 
   if constexpr (WIDE) {
-    // U pieces' loads are issued before the first product
-    constexpr int U = 2;
-    for (int p0 = wave; p0 < npieces; p0 += U * WAVES) {
-      uint32_t w[U][OB][BITS];
-      ex_u32x4_t x[U][4];
-      float s[U][OB], z[U][OB];
+    // a wave owns consecutive pieces, four at a time: a row's 64 bytes per
+    // piece then share cache lines, and one load brings the scales (zero
+    // points) of the four, lane j's for piece j
+    const int per = (npieces + WAVES - 1) / WAVES;
+    const int pbeg = wave * per, pend = min(npieces, pbeg + per);
+    for (int p0 = pbeg; p0 < pend; p0 += S) {
+      uint32_t w[S][OB][BITS];
+      ex_u32x4_t x[S][4];
+      float s[OB];
+      uint32_t z[OB];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int p = min(p0 + u * WAVES, npieces - 1);
-        const int64_t g = (int64_t)p * 128 / group;
+      for (int u = 0; u < S; ++u)
 #pragma unroll
-        for (int b = 0; b < OB; ++b) {
-          load_chunk<BITS>(qrow[b] + ((int64_t)p * 4 + j) * BITS, w[u][b]);
-          s[u][b] = srow[b][g];
-          z[u][b] = (float)zrow[b][g];
-        }
+        for (int b = 0; b < OB; ++b)
+          load_chunk<BITS>(qrow[b] + ((int64_t)min(p0 + u, pend - 1) * 4 + j) * BITS, w[u][b]);
+      const int64_t g = (int64_t)min(p0 + (j & (S - 1)), pend - 1) * 128 / group;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[u][i] = *reinterpret_cast<const ex_u32x4_t*>(xrow + (int64_t)p * 128 + 32 * j + 8 * i);
+      for (int b = 0; b < OB; ++b) {
+        s[b] = srow[b][g];
+        z[b] = zrow[b][g];
+      }
+      // the weights leave before the row's index is waited for
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" : "+v"(srcrow));
+      const uint16_t* __restrict__ xrow = X + (int64_t)min(max(srcrow, 0), T - 1) * ldx;
+#pragma unroll
+      for (int u = 0; u < S; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("" : "=v"(x[u][i]));   // any value
+      if (xok) {
+#pragma unroll
+        for (int u = 0; u < S; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[u][i] = *reinterpret_cast<const ex_u32x4_t*>(xrow + (int64_t)min(p0 + u, pend - 1) * 128 + 32 * j + 8 * i);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (p0 + u * WAVES >= npieces) break;
+      for (int u = 0; u < S; ++u) {
+        if (p0 + u >= pend) break;
         ex_f32x4_t acc[OB], xs = {0.f, 0.f, 0.f, 0.f};
+        float su[OB], zu[OB];
 #pragma unroll
-        for (int b = 0; b < OB; ++b) acc[b] = (ex_f32x4_t){0.f, 0.f, 0.f, 0.f};
+        for (int b = 0; b < OB; ++b) {
+          acc[b] = (ex_f32x4_t){0.f, 0.f, 0.f, 0.f};
+          su[b] = __shfl(s[b], 16 * u + li);
+          zu[b] = (float)__shfl((int)z[b], 16 * u + li);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const ex_bf16x8_t a = BITS == 4 ? mv_order(x[u][i]) : __builtin_bit_cast(ex_bf16x8_t, x[u][i]);
 #pragma unroll
           for (int b = 0; b < OB; ++b)
-            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, mv_codes<BITS>(w[u][b], i, z[u][b]), acc[b], 0, 0, 0);
+            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, mv_codes<BITS>(w[u][b], i, zu[b]), acc[b], 0, 0, 0);
           if constexpr (BITS == 4) xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, ones, xs, 0, 0, 0);
         }
 #pragma unroll
         for (int b = 0; b < OB; ++b)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float v = BITS == 4 ? fmaf(-(16.f + z[u][b]), xs[r], acc[b][r]) : acc[b][r];
-            tot[b][r] = fmaf(s[u][b], v, tot[b][r]);
+            const float v = BITS == 4 ? fmaf(-(16.f + zu[b]), xs[r], acc[b][r]) : acc[b][r];
+            tot[b][r] = fmaf(su[b], v, tot[b][r]);
           }
       }
     }
   } else {
+    const uint16_t* __restrict__ xrow = X + (int64_t)min(max(srcrow, 0), T - 1) * ldx;
     for (int p = wave; p < npieces; p += WAVES) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -954,14 +994,14 @@ int64_t expert_grid(const ExpertArgs& a, int grad) {
 
 template <int BITS>
 static void mv_go(hipStream_t s, const ExpertArgs& a) {
-  constexpr int WAVES = 4, OB = 2;
+  constexpr int WAVES = 4, OB = 2, S = 2;
   const dim3 grid((unsigned)ceil_div(a.d_out, 16 * OB), (unsigned)row_tiles(a.R, a.E, 16));
   const uint16_t* X = static_cast<const uint16_t*>(a.A);
   if (a.group % 128 == 0)
-    hipLaunchKernelGGL((k_expert_mv<BITS, true, WAVES, OB>), grid, dim3(64 * WAVES), 0, s, X, a.T, a.n, a.lda, a.rows,
+    hipLaunchKernelGGL((k_expert_mv<BITS, true, WAVES, OB, S>), grid, dim3(64 * WAVES), 0, s, X, a.T, a.n, a.lda, a.rows,
                        a.offsets, a.E, a.R, a.qw, a.scales, a.zeros, a.d_out, a.group, a.Y, a.y_bf16, a.ldy);
   else
-    hipLaunchKernelGGL((k_expert_mv<BITS, false, WAVES, OB>), grid, dim3(64 * WAVES), 0, s, X, a.T, a.n, a.lda, a.rows,
+    hipLaunchKernelGGL((k_expert_mv<BITS, false, WAVES, OB, S>), grid, dim3(64 * WAVES), 0, s, X, a.T, a.n, a.lda, a.rows,
                        a.offsets, a.E, a.R, a.qw, a.scales, a.zeros, a.d_out, a.group, a.Y, a.y_bf16, a.ldy);
 }
 
