@@ -346,12 +346,14 @@ k_expert_mv(const uint16_t* __restrict__ X, int T, int64_t n, int64_t ldx, const
 // those of stage st + 1 are written into the other buffer, the packed one
 // expanded to bf16 on its way, in between the products of stage st: one
 // barrier per stage, and the expansion (once per workgroup, about three
-// operations per code) runs beside the matrix cores. Operand layouts in LDS:
+// operations per code) runs beside the matrix cores. Operand layouts in LDS
+// (64 banks: 16 lanes of 16 bytes meet in a
+// clock):
 //  * K along a row ([row][64], 128 bytes): 16-byte piece c of row r at
-//    c ^ (r & 7), so eight rows' reads of one piece hit all banks;
-//  * K down the rows ([64][W]): piece c of row t at c ^ dma_swz(t) ^ (c / 8),
-//    read with the transposing LDS read; the last term keeps the writes of
-//    wide column runs off each other's banks.
+//    c ^ ((r / 2) & 7), so sixteen rows' reads of one piece hit all banks;
+//  * K down the rows ([64][W]): piece c of row t at c ^ dma_swz(t) ^ x, read
+//    with the transposing LDS read; x (a bit of the row or of the column)
+//    keeps the writes of wide column runs off each other's banks.
 constexpr int kExBK = 64;
 
 template <int MI_, int NI_, int WM_, int WN_>
@@ -369,11 +371,12 @@ using ExTile32 = ExTile<1, 1, 1, 4>;     // 32 x 128
 typedef __attribute__((address_space(3))) ex_u32x4_t lds_piece_t;
 typedef __attribute__((address_space(3))) const ex_bf16x8_t lds_frag_t;
 
-__device__ __forceinline__ uint32_t row_piece(int r, int c) { return (uint32_t)r * 128u + 16u * (c ^ (r & 7)); }
+__device__ __forceinline__ uint32_t row_piece(int r, int c) { return (uint32_t)r * 128u + 16u * (c ^ ((r >> 1) & 7)); }
 // W: columns of the tile
 template <int W>
 __device__ __forceinline__ uint32_t col_piece(int t, int c) {
-  return (uint32_t)t * (2 * W) + 16u * (c ^ dma_swz(t) ^ (c >> 3));
+  const int x = W == 128 ? (t >> 1) & 1 : (c >> 4) & 1;
+  return (uint32_t)t * (2 * W) + 16u * (c ^ dma_swz(t) ^ x);
 }
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
@@ -525,7 +528,7 @@ k_expert_mm(ExArgs p) {
   const int64_t bo = (int64_t)sg.e * p.d_out + min(o0 + br, p.d_out - 1);
   const uint32_t* __restrict__ qrow = p.qw + bo * ((int64_t)nchunks * BITS);
   const uint8_t* __restrict__ zrow = p.zeros + bo * ngroups;
-  const uint32_t aw = lds + row_piece(ar, ac);            // AR is a multiple of 8: rows apart keep the swizzle
+  const uint32_t aw = lds + row_piece(ar, ac);            // AR is a multiple of 16: rows apart keep the swizzle
   uint32_t bw[NB];
 #pragma unroll
   for (int e = 0; e < NB; ++e) bw[e] = lds + ASZ + row_piece(br, bu + e);
@@ -803,6 +806,401 @@ k_expert_mm_grad(ExArgs p) {
   }
 }
 
+// ---- many rows per expert, 4 bits: the DMA ring
+//
+// 256 x 256 x 32 stages, 8 waves of 128 x 64 (128 accumulators per lane). The
+// tiles above spend their time on the way of A through registers: without its
+// loads the forward product took 27% less, although they hit the L1. Here
+// everything comes by LDS-DMA and is counted by hand, so the compiler waits
+// for none of it:
+//  * A's slots are a ring of four, its DMA three stages ahead; packed codes,
+//    zero points and scales land in buffers of their own, the codes of st + 2
+//    before stage st;
+//  * every wave issues a number of DMA instructions per stage that is known at
+//    compile time, and the barrier that opens a stage leaves exactly the stage
+//    before's in flight, so everything older has landed;
+//  * during stage st the codes of st + 2 are expanded into B's ring, in between
+//    the products, and the first K slice of st + 1 is read before its barrier,
+//    so products never wait for LDS behind one.
+// A group's scale leaves the forward sum without a second set of
+// accumulators: the sum is kept in units of the current group's scale, and at
+// a group's end all of it is multiplied by s_g / s_(g+1). That is one rounded
+// multiplication per group and element, as the other tiles' one fused
+// addition is. Groups whose scale is outside 2^-40 .. 2^40 (zero among them)
+// use the unit 1 and have their weights s (q - z) rounded to bf16 instead.
+// DMA of 16 bytes, a dword or a byte (widened to a dword) per lane from
+// base + voff to lds + (16 or 4) lane.
+__device__ __forceinline__ void xdma16(uint32_t voff, const void* base, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(lds) : "memory");
+}
+__device__ __forceinline__ void xdma4(uint32_t voff, const void* base, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(lds) : "memory");
+}
+__device__ __forceinline__ void xdma1(uint32_t voff, const void* base, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %1" ::"v"(voff), "s"(base), "s"(lds) : "memory");
+}
+template <int VM>
+__device__ __forceinline__ void xbarrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+typedef __attribute__((address_space(3))) const uint32_t lds_word_t;
+typedef __attribute__((address_space(3))) const uint64_t lds_dword_t;
+__device__ __forceinline__ uint32_t lds_u32(uint32_t at) { return *reinterpret_cast<lds_word_t*>(at); }
+__device__ __forceinline__ uint64_t lds_u64(uint32_t at) { return *reinterpret_cast<lds_dword_t*>(at); }
+
+// Piece c of row r of a [row][32] tile (64 bytes a row).
+__device__ __forceinline__ uint32_t xrow_piece(int r, int c) { return (uint32_t)r * 64u + 16u * (c ^ ((r >> 2) & 3)); }
+
+// The 8 codes of w times f, minus z f, rounded once: codes - z + 128 as
+// bytes (one addition per four), then (t - 128) f in one fma.
+__device__ __forceinline__ ex_u32x4_t xexpand(uint32_t w, uint32_t bias, float f) {
+  const uint32_t lo = (w & 0x0F0F0F0Fu) + bias, hi = ((w >> 4) & 0x0F0F0F0Fu) + bias;
+  const float m = -128.f * f;
+  ex_u32x4_t o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = ex_pack2(fmaf((float)((lo >> (8 * i)) & 0xFFu), f, m), fmaf((float)((hi >> (8 * i)) & 0xFFu), f, m));
+  return o;
+}
+
+// One MFMA, then VALU operations and LDS reads of its share, N times.
+template <int N, int READS, int VALUS, int I = 0>
+__device__ __forceinline__ void xinterleave() {
+  if constexpr (I < N) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    constexpr int r = (I + 1) * READS / N - I * READS / N;
+    if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(0x100, r, 0);
+    if constexpr (VALUS > 0) __builtin_amdgcn_sched_group_barrier(0x002, VALUS, 0);
+    xinterleave<N, READS, VALUS, I + 1>();
+  }
+}
+
+// Forward, groups that are multiples of 128. A block is four stages (128
+// codes, 64 bytes of a row): its codes, zero points and scales come as whole
+// blocks, two buffers of each, so that a row's 64 bytes are fetched at once (a
+// stage's 16 bytes per row and fetch made 166 instead of 50 million requests to
+// the L2). B's slots are a ring of three, addressed at run time.
+constexpr uint32_t kFA = 0, kFB = 4 * 16384, kFRaw = kFB + 3 * 16384, kFScale = kFRaw + 2 * 16384,
+                   kFZero = kFScale + 2 * 1024, kFLds = kFZero + 2 * 1024;
+__global__ void __launch_bounds__(512, 2)
+k_expert_ring(ExArgs p) {
+  constexpr int MI = 4, NI = 2;
+  __shared__ __align__(16) uint8_t smem[kFLds];
+  int rt, ct;
+  if (!tile_of(blockIdx.x, p.nrt, p.nct, rt, ct)) return;
+  const Seg sg = find_tile(p.offsets, p.E, p.R, 256, rt);
+  if (sg.e < 0) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, li = lane & 31;
+  const int64_t o0 = (int64_t)ct * 256;
+  const int64_t ngroups = p.n / p.group;
+  const int nblk = (int)(p.n / 128), bpg = p.group / 128;     // blocks, blocks per group
+  const int nst = 4 * nblk;
+  const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+
+  // A: instruction 2 wave + i moves rows 16 (2 wave + i) + lane / 4 of a
+  // stage; codes: the same rows of B, 64 bytes of a block
+  uint32_t va[2], vq[2];
+  const int64_t ebase = (int64_t)sg.e * p.d_out;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 16 * (2 * wave + i) + (lane >> 2);
+    const uint32_t c = 16 * ((lane & 3) ^ ((r >> 2) & 3));
+    va[i] = (uint32_t)(source_row(p.rows, min(sg.row0 + r, sg.hi - 1), p.T) * p.lda * 2 + c);
+    vq[i] = (uint32_t)(min(o0 + r, p.d_out - 1) * (p.n / 2) + c);
+  }
+  // scales (waves 0..3) and zero points (4..7) of a block: one row per lane
+  const int w4 = wave & 3;
+  const uint32_t vs = (uint32_t)(min(o0 + 64 * w4 + lane, p.d_out - 1) * ngroups);
+  const char* abase = reinterpret_cast<const char*>(p.A);
+  const char* qbase = reinterpret_cast<const char*>(p.qw) + ebase * (p.n / 2);
+  const char* sbase = reinterpret_cast<const char*>(p.scales + ebase * ngroups);
+  const char* zbase = reinterpret_cast<const char*>(p.zeros + ebase * ngroups);
+  auto issue_a = [&](int st, int slot) {
+    const int c = min(st, nst - 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      xdma16(va[i], abase + (int64_t)c * 64,
+             __builtin_amdgcn_readfirstlane(lds + kFA + slot * 16384 + (2 * wave + i) * 1024));
+  };
+  auto issue_q = [&](int b, int i) {
+    xdma16(vq[i], qbase + (int64_t)min(b, nblk - 1) * 64,
+           __builtin_amdgcn_readfirstlane(lds + kFRaw + (b & 1) * 16384 + (2 * wave + i) * 1024));
+  };
+  auto issue_g = [&](int b) {
+    const int g = min(b, nblk - 1) / bpg;
+    if (wave < 4) xdma4(vs * 4u, sbase + (int64_t)g * 4, __builtin_amdgcn_readfirstlane(lds + kFScale + (b & 1) * 1024 + w4 * 256));
+    else xdma1(vs, zbase + g, __builtin_amdgcn_readfirstlane(lds + kFZero + (b & 1) * 1024 + w4 * 256));
+  };
+  // expansion of a stage's codes: half tid % 2 (16 codes) of output row tid / 2
+  const int xr = tid >> 1, xh = tid & 1;
+  const uint32_t xq = lds + kFRaw + xr * 64 + xh * 8;
+  const uint32_t xd0 = lds + kFB + xrow_piece(xr, 2 * xh), xd1 = lds + kFB + xrow_piece(xr, 2 * xh + 1);
+  const uint32_t xz = lds + kFZero + 4 * xr, xs = lds + kFScale + 4 * xr;
+  auto unit_ok = [](float s) { return fabsf(s) >= 0x1p-40f && fabsf(s) <= 0x1p40f; };
+  auto expand = [&](int b, int i, uint32_t slot) {
+    const uint64_t w = lds_u64(xq + (b & 1) * 16384 + 16 * (i ^ ((xr >> 2) & 3)));
+    const uint32_t bias = (0x80u - lds_u32(xz + (b & 1) * 1024)) * 0x01010101u;
+    const float s = __uint_as_float(lds_u32(xs + (b & 1) * 1024));
+    const float f = unit_ok(s) ? 1.f : s;
+    lds_write(xd0 + slot, xexpand((uint32_t)w, bias, f));
+    lds_write(xd1 + slot, xexpand((uint32_t)(w >> 32), bias, f));
+  };
+  uint32_t af[2], bf[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    af[k] = lds + kFA + xrow_piece(128 * wm + li, 2 * k + h);
+    bf[k] = lds + kFB + xrow_piece(64 * wn + li, 2 * k + h);
+  }
+  ex_bf16x8_t fa[2][MI], fb[2][NI];
+  auto read = [&](auto SL, auto KK, uint32_t bslot) {
+    constexpr int sl = decltype(SL)::value, kk = decltype(KK)::value;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) fa[kk][mi] = lds_frag(af[kk] + sl * 16384 + mi * 2048);
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) fb[kk][ni] = lds_frag(bf[kk] + bslot + ni * 2048);
+  };
+  ex_f32x16_t acc[MI][NI] = {};
+  auto multiply = [&](auto KK) {
+    constexpr int kk = decltype(KK)::value;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni)
+        acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk][mi], fb[kk][ni], acc[mi][ni], 0, 0, 0);
+  };
+
+  for (int st = 0; st < 3; ++st) issue_a(st, st);
+  issue_q(0, 0);
+  issue_q(0, 1);
+  issue_g(0);
+  issue_q(1, 0);
+  xbarrier<0>();
+  uint32_t b0 = 0, b1 = 16384, b2 = 2 * 16384;        // B's slots of stages st, st + 1, st + 2
+  expand(0, 0, b0);
+  expand(0, 1, b1);
+  const uint32_t su = lds + kFScale + 4 * (64 * wn + li);
+  float unit[NI];                                      // the current unit of each of the lane's columns
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) {
+    const float s = __uint_as_float(lds_u32(su + 128 * ni));
+    unit[ni] = unit_ok(s) ? s : 1.f;
+  }
+  xbarrier<0>();
+  read(ex_const<0>{}, ex_const<0>{}, b0);
+  // DMA instructions of a wave in stage i of a block: A 2; codes of the next
+  // block but one in stages 3 and 0, scales or zero points in stage 0
+  int left = bpg;                                      // blocks left of the group
+  auto stage = [&](auto I, int blk) {
+    constexpr int i = decltype(I)::value;
+    xbarrier<i == 0 ? 3 : (i == 1 ? 4 : 2)>();         // what stage i - 1 issued may still fly
+    issue_a(4 * blk + i + 3, (i + 3) & 3);
+    if constexpr (i == 0) {
+      issue_q(blk + 1, 1);
+      issue_g(blk + 1);
+    }
+    if constexpr (i == 3) issue_q(blk + 2, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    read(I, ex_const<1>{}, b0);
+    expand(i < 2 ? blk : blk + 1, (i + 2) & 3, b2);
+    multiply(ex_const<0>{});
+    xinterleave<8, 9, 6>();
+    __builtin_amdgcn_sched_barrier(0);
+    read(ex_const<(i + 1) & 3>{}, ex_const<0>{}, b1);
+    multiply(ex_const<1>{});
+    xinterleave<8, 6, 1>();
+    __builtin_amdgcn_sched_barrier(0);
+    const uint32_t t = b0;
+    b0 = b1;
+    b1 = b2;
+    b2 = t;
+  };
+  for (int blk = 0; blk < nblk; ++blk) {
+    for_four([&](auto I) { stage(I, blk); });
+    if (--left == 0 && blk + 1 < nblk) {               // the group is complete: into the next one's unit
+      left = bpg;
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        const float s = __uint_as_float(lds_u32(su + ((blk + 1) & 1) * 1024 + 128 * ni));
+        const float next = unit_ok(s) ? s : 1.f;
+        const float r = unit[ni] / next;
+        unit[ni] = next;
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) acc[mi][ni][q] *= r;
+      }
+    }
+  }
+  // no DMA may land in LDS that this workgroup no longer owns
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) {
+    const int64_t o = o0 + 64 * wn + 32 * ni + li;
+    if (o >= p.d_out) continue;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = sg.row0 + 128 * wm + 32 * mi + 8 * (r >> 2) + 4 * h + (r & 3);
+        if (row < sg.hi) store_out(p.Y, p.ybf16, (int64_t)row * p.ldy + o, unit[ni] * acc[mi][ni][r]);
+      }
+  }
+}
+
+// Gradient: the rows of a stage's 32 outputs hold 128 contiguous bytes of
+// codes each, so codes, scales and zero points (one of each per row and
+// 32-column chunk, whatever the group) come stage by stage, four ahead.
+constexpr int kGPer = 4;                               // DMA instructions per wave and stage
+constexpr uint32_t kGSlot = 32768, kGRaw = 4 * kGSlot, kGScale = kGRaw + 4 * 4096, kGZero = kGScale + 4 * 1024,
+                   kGDump = kGZero + 4 * 1024, kGLds = kGDump + 256;   // kGDump: never read
+__global__ void __launch_bounds__(512, 2)
+k_expert_ring_grad(ExArgs p) {
+  constexpr int MI = 4, NI = 2;
+  __shared__ __align__(16) uint8_t smem[kGLds];
+  int rt, ct;
+  if (!tile_of(blockIdx.x, p.nrt, p.nct, rt, ct)) return;
+  const Seg sg = find_tile(p.offsets, p.E, p.R, 256, rt);
+  if (sg.e < 0) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, li = lane & 31;
+  const int64_t c0 = (int64_t)ct * 256;
+  const int64_t ngroups = p.n / p.group;
+  const int nchunks = (int)(p.n / 32), cpg = p.group / 32;
+  const int nst = (int)(p.d_out / 32);
+  const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+
+  uint32_t va[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 16 * (2 * wave + i) + (lane >> 2);
+    const int64_t src = source_row(p.rows, min(sg.row0 + r, sg.hi - 1), p.T);
+    va[i] = (uint32_t)(src * p.lda * 2 + 16 * ((lane & 3) ^ ((r >> 2) & 3)));
+  }
+  // output row 32 st + 8 w + lane / 8, chunk lane % 8 of the tile's 256
+  // columns (chunks past n: the last one; their columns are not stored)
+  const int w4 = wave & 3;
+  const int row = 8 * w4 + (lane >> 3);
+  const int chunk = min((int)(c0 / 32) + (lane & 7), nchunks - 1);
+  const uint32_t vq = (uint32_t)(((int64_t)row * nchunks + chunk) * 16);
+  const uint32_t vs = (uint32_t)((int64_t)row * ngroups + chunk / cpg);
+  const int64_t ebase = (int64_t)sg.e * p.d_out;
+  const char* qbase = reinterpret_cast<const char*>(p.qw + ebase * nchunks * 4);
+  const char* sbase = reinterpret_cast<const char*>(p.scales + ebase * ngroups);
+  const char* zbase = reinterpret_cast<const char*>(p.zeros + ebase * ngroups);
+  const char* abase = reinterpret_cast<const char*>(p.A);
+  const int64_t qstep = (int64_t)32 * nchunks * 16, gstep = 32 * ngroups;
+
+  auto issue_a = [&](int st, int slot) {
+    const int c = min(st, nst - 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      xdma16(va[i], abase + (int64_t)c * 64, __builtin_amdgcn_readfirstlane(lds + slot * kGSlot + (2 * wave + i) * 1024));
+  };
+  // two instructions per wave: codes and scales, or zero points and a dummy
+  auto issue_b = [&](int st) {
+    const int64_t c = min(st, nst - 1);
+    if (wave < 4) {
+      xdma16(vq, qbase + c * qstep, __builtin_amdgcn_readfirstlane(lds + kGRaw + (st & 3) * 4096 + w4 * 1024));
+      xdma4(vs * 4u, sbase + c * gstep * 4, __builtin_amdgcn_readfirstlane(lds + kGScale + (st & 3) * 1024 + w4 * 256));
+    } else {
+      xdma1(vs, zbase + c * gstep, __builtin_amdgcn_readfirstlane(lds + kGZero + (st & 3) * 1024 + w4 * 256));
+      xdma4(0u, kZeroChunk, __builtin_amdgcn_readfirstlane(lds + kGDump));
+    }
+  };
+  // expansion: columns 16 (tid % 16) .. of output row tid / 16
+  const int xr = tid >> 4, xc = tid & 15;
+  const uint32_t xq = lds + kGRaw + xr * 128 + xc * 8;
+  const uint32_t xz = lds + kGZero + 4 * (xr * 8 + (xc >> 1)), xs = lds + kGScale + 4 * (xr * 8 + (xc >> 1));
+  const uint32_t xd0 = lds + 16384 + col_piece<256>(xr, 2 * xc), xd1 = lds + 16384 + col_piece<256>(xr, 2 * xc + 1);
+  auto expand = [&](int st, int slot) {
+    const uint64_t w = lds_u64(xq + (st & 3) * 4096);
+    const uint32_t bias = (0x80u - lds_u32(xz + (st & 3) * 1024)) * 0x01010101u;
+    const float s = __uint_as_float(lds_u32(xs + (st & 3) * 1024));
+    lds_write(xd0 + slot * kGSlot, xexpand((uint32_t)w, bias, s));
+    lds_write(xd1 + slot * kGSlot, xexpand((uint32_t)(w >> 32), bias, s));
+  };
+  // fragment addresses (slots 2 and 3 are past the offset field of 0)
+  uint32_t af[2][2], bf[2][2];                        // [slot / 2][kk], [slot / 2][ni]
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      af[q][k] = lds + q * 2 * kGSlot + xrow_piece(128 * wm + li, 2 * k + h);
+      bf[q][k] = lds + q * 2 * kGSlot + 16384 + col_frag_at<256>(64 * wn + 32 * k, lane);
+    }
+  ex_bf16x8_t fa[2][MI], fb[2][NI];
+  auto read = [&](auto SL, auto KK) {
+    constexpr int sl = decltype(SL)::value, kk = decltype(KK)::value;
+    constexpr uint32_t so = (sl & 1) * kGSlot;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) fa[kk][mi] = lds_frag(af[sl >> 1][kk] + so + mi * 2048);
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) fb[kk][ni] = lds_col_frag<256>(bf[sl >> 1][ni] + so + kk * 8192);
+  };
+  ex_f32x16_t acc[MI][NI] = {};
+  auto multiply = [&](auto KK) {
+    constexpr int kk = decltype(KK)::value;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni)
+        acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk][mi], fb[kk][ni], acc[mi][ni], 0, 0, 0);
+  };
+
+  for (int st = 0; st < 3; ++st) issue_a(st, st);
+  for (int st = 0; st < 4; ++st) issue_b(st);
+  xbarrier<0>();
+  expand(0, 0);
+  expand(1, 1);
+  xbarrier<0>();
+  read(ex_const<0>{}, ex_const<0>{});
+  auto stage = [&](auto SL, int st) {
+    constexpr int sl = decltype(SL)::value;
+    xbarrier<kGPer>();
+    issue_a(st + 3, (sl + 3) & 3);
+    issue_b(st + 4);
+    __builtin_amdgcn_sched_barrier(0);
+    read(SL, ex_const<1>{});
+    expand(st + 2, (sl + 2) & 3);
+    multiply(ex_const<0>{});
+    xinterleave<8, 11, 6>();
+    __builtin_amdgcn_sched_barrier(0);
+    read(ex_const<(sl + 1) & 3>{}, ex_const<0>{});
+    multiply(ex_const<1>{});
+    xinterleave<8, 8, 1>();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int st = 0;
+  for (; st + 4 <= nst; st += 4) {
+    stage(ex_const<0>{}, st);
+    stage(ex_const<1>{}, st + 1);
+    stage(ex_const<2>{}, st + 2);
+    stage(ex_const<3>{}, st + 3);
+  }
+  if (st < nst) stage(ex_const<0>{}, st);
+  if (st + 1 < nst) stage(ex_const<1>{}, st + 1);
+  if (st + 2 < nst) stage(ex_const<2>{}, st + 2);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // no DMA into LDS that is no longer owned
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) {
+    const int64_t c = c0 + 64 * wn + 32 * ni + li;
+    if (c >= p.n) continue;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int orow = sg.row0 + 128 * wm + 32 * mi + 8 * (r >> 2) + 4 * h + (r & 3);
+        if (orow < sg.hi) store_out(p.Y, p.ybf16, (int64_t)orow * p.ldy + c, acc[mi][ni][r]);
+      }
+  }
+}
+
 // ---- weight gradient: K = a segment's rows. Both operands have K down their
 // rows. The kept values have at most 7 significant bits, so they are exact in
 // bf16, products are exact and the sums fp32. A segment's rows are split over
@@ -977,19 +1375,27 @@ static bool bf16_rows_vec(const void* p, int64_t ld, int64_t cols) {
   return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && cols % 8 == 0;
 }
 
-// Rows of a tile: 16 is the matrix-vector form.
+// The ring kernels: 4 bits, whole blocks (forward) or stages and a bf16 result
+// (gradient), and offsets from the bases that fit 32 bits.
+static bool ring_fits(const ExpertArgs& a, int grad) {
+  const int64_t lim = (int64_t)1 << 32;
+  if (a.bits != 4 || a.d_out * (a.n / 2) >= lim || a.T * a.lda * 2 >= lim) return false;
+  return grad ? a.y_bf16 && a.d_out % 32 == 0 : a.group % 128 == 0;
+}
+
+// Rows of a tile: 16 is the matrix-vector form, 256 the ring kernel.
 static int expert_bm(const ExpertArgs& a, int grad) {
   const int64_t avg = ceil_div(a.R, a.E);
   if (!bf16_rows_vec(a.A, a.lda, grad ? a.d_out : a.n)) return 64;
   if (!grad && avg <= 16) return 16;
-  if (!grad || !a.y_bf16) return avg <= 64 ? 64 : 128;
-  return avg <= 64 ? 64 : (avg <= 512 ? 128 : 256);
+  if (avg <= 64) return 64;
+  return avg > 512 && ring_fits(a, grad) ? 256 : 128;
 }
 
 int64_t expert_grid(const ExpertArgs& a, int grad) {
   const int bm = expert_bm(a, grad);
   const int64_t cols = grad ? a.n : a.d_out;
-  return row_tiles(a.R, a.E, bm) * ceil_div(cols, bm == 16 ? 32 : 128) + 8;
+  return row_tiles(a.R, a.E, bm) * ceil_div(cols, bm == 16 ? 32 : (bm == 256 ? 256 : 128)) + 8;
 }
 
 template <int BITS>
@@ -1052,11 +1458,17 @@ static void grad_go(hipStream_t s, const ExpertArgs& a) {
   hipLaunchKernelGGL((k_expert_mm_grad<BITS, NP, TL, VEC>), tile_grid(p.nrt, p.nct), dim3(TL::THREADS), 0, s, p);
 }
 
+static void ring_go(hipStream_t s, const ExpertArgs& a, int grad) {
+  const ExArgs p = ex_args(a, 256, 256, grad ? a.n : a.d_out);
+  hipLaunchKernelGGL(grad ? k_expert_ring_grad : k_expert_ring, tile_grid(p.nrt, p.nct), dim3(512), 0, s, p);
+}
+
 template <int BITS>
 static void fwd_bits(hipStream_t s, const ExpertArgs& a) {
   if (!bf16_rows_vec(a.A, a.lda, a.n)) return mm_go<BITS, ExTile64, 0, false>(s, a);
   const int bm = expert_bm(a, 0);
   if (bm == 16) mv_go<BITS>(s, a);
+  else if (bm == 256) ring_go(s, a, 0);
   else if (bm == 64) mm_group<BITS, ExTile64>(s, a);
   else mm_group<BITS, ExTile128>(s, a);
 }
@@ -1070,7 +1482,7 @@ static void grad_bits(hipStream_t s, const ExpertArgs& a) {
   } else if (a.y_bf16) {
     if (bm == 64) grad_go<BITS, 1, ExTile64, true>(s, a);
     else if (bm == 128) grad_go<BITS, 1, ExTile128, true>(s, a);
-    else grad_go<BITS, 1, ExTileX, true>(s, a);
+    else ring_go(s, a, 1);
   } else {
     if (bm == 64) grad_go<BITS, 3, ExTile64, true>(s, a);
     else grad_go<BITS, 3, ExTile128, true>(s, a);

@@ -195,9 +195,12 @@ def test_nonfinite_rows_stay_in_their_tokens():
 
 
 # ---------------------------------------------------------------- packed products
-def product_bound(X, off, rows, qw, sc, zr, bits, group, n, R, few):
+def product_bound(X, off, rows, qw, sc, zr, bits, group, n, R, E):
     """Bound on the fp32 error of the forward product. Tiles: a group's sum
-    takes `group` additions, its scaling one, the groups n / group. Few rows at
+    takes `group` additions, its scaling one, the groups n / group. Many rows
+    at 4 bits (R > 512 E): one running sum of n additions, carried from unit to
+    unit by n / group ratios, each of three roundings (quotient, product, and
+    the last scaling). Few rows at
     4 bits and groups of 128 codes: a piece of 128 sums x (16 + q) and x, each
     with 128 additions of magnitudes up to 31 |x|, and takes their difference
     in one more rounding; the two sums' magnitudes together are at most
@@ -209,7 +212,9 @@ def product_bound(X, off, rows, qw, sc, zr, bits, group, n, R, few):
         lo, hi = off[e], off[e + 1]
         x = np.abs(X[lo:hi] if rows is None else X[rows[lo:hi]])
         mag[lo:hi] = (group + n // group + 1) * (x @ W.T)
-        if few and bits == 4 and group % 128 == 0:
+        if R > 512 * E and bits == 4:
+            mag[lo:hi] = (n + 3 * (n // group) + 1) * (x @ W.T)
+        if R <= 16 * E and bits == 4 and group % 128 == 0:
             mag[lo:hi] = (128 + 2) * 62 * (x @ S.T) + (n // 128 + 1) * (x @ W.T)
     return U32 * mag
 
@@ -225,7 +230,10 @@ PRODUCTS = [   # T, k, E, d, n, group, drop, only, gathered
     (100, 2, 4, 257, 640, 32, 0.3, None, True),      # 64-row tiles, ragged both ways, a group per chunk
     (300, 1, 2, 129, 512, 128, 0.0, None, False),    # 128-row tiles
     (257, 2, 3, 96, 320, 160, 0.0, [0, 2], True),    # an empty expert between two
-    (700, 1, 1, 200, 256, 256, 0.1, None, True),
+    (700, 1, 1, 200, 256, 256, 0.1, None, True),     # 256-row tiles from here on (4 bits)
+    (1200, 1, 2, 300, 160, 32, 0.1, None, True),     # five stages, a group per stage
+    (1100, 1, 2, 257, 1152, 128, 0.0, None, False),
+    (1600, 2, 3, 40, 32, 32, 0.0, [0, 1], True),     # one stage, an empty expert at the end
 ]
 
 
@@ -243,15 +251,44 @@ def test_expert_matmul(T, k, E, d, n, group, drop, only, gathered, bits):
         before = arr(out)
         Y = arr(G.expert_matmul(X, *args, rows=rt, out=out))
         ref = X64.expert_matmul(arr(X), off, qw, sc, zr, bits, group, n, rows if gathered else None, before)
-        e = product_bound(arr(X), off, rows if gathered else None, qw, sc, zr, bits, group, n, R, R <= 16 * E)
+        e = product_bound(arr(X), off, rows if gathered else None, qw, sc, zr, bits, group, n, R, E)
         tol = e + (UBF * (np.abs(ref) + e) if ydt == BF16 else 0)
         assert np.all(np.abs(Y - ref)[:off[-1]] <= tol[:off[-1]])
         assert np.array_equal(Y[off[-1]:], before[off[-1]:])
 
 
+def test_scales_of_any_size():
+    """Zero, negative, tiny and huge scales, in tiles of every size: exact
+    zeros for zero scales, and where a unit cannot be carried (outside
+    2^-40 .. 2^40, many rows) the group's weights rounded to bf16 once."""
+    n, d, group = 256, 96, 64
+    for R in (5, 60, 200, 700):
+        qw, sc, zr = layers(R, 1, d, n, 4, group)
+        sc[0, 0] = 0.0
+        sc[0, 1, 1] = 0.0
+        sc[0, 2] *= -1.0
+        sc[0, 3] *= 1e-20
+        sc[0, 4, 2:] *= 1e20
+        sc[0, 5] = [1e-15, 1.0, 1e15, 1e-3]
+        X = values(R, R, n)
+        Y = arr(G.expert_matmul(X, None, *cuda_layers(qw, sc, zr), 4, group))
+        W = dequantize(qw[0], sc[0], zr[0], 4, group, n)
+        ref, mag = arr(X) @ W.T, np.abs(arr(X)) @ np.abs(W).T
+        e = U32 * (n + 3 * (n // group) + 1) * mag
+        if R <= 16:
+            S = np.repeat(np.abs(sc[0].astype(np.float64)), group, axis=1)
+            e = U32 * (130 * 62 * (np.abs(arr(X)) @ S.T) + 3 * mag)
+        if R > 512:
+            odd = np.repeat((np.abs(sc[0]) < 2.0 ** -40) | (np.abs(sc[0]) > 2.0 ** 40), group, axis=1)
+            e = e + (UBF + U32) * (np.abs(arr(X)) @ (np.abs(W) * odd).T)
+        assert np.all(np.abs(Y - ref) <= e)
+        assert np.all(Y[:, 0] == 0)
+
+
 GRADS = [   # R, E, d, n, group, cuts (None: one layer without offsets)
     (1, 1, 32, 64, 32, None), (3, 2, 70, 128, 128, [1, 3]), (50, 3, 130, 96, 96, [20, 20, 45]),
     (130, 1, 64, 160, 32, None), (400, 2, 257, 320, 64, [129, 400]), (300, 2, 100, 256, 256, [0, 290]),
+    (1100, 2, 96, 320, 64, [500, 1090]), (600, 1, 32, 96, 32, None), (1300, 2, 224, 544, 32, [513, 513]),
 ]
 
 
