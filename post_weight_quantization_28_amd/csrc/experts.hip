@@ -854,8 +854,19 @@ __device__ __forceinline__ uint64_t lds_u64(uint32_t at) { return *reinterpret_c
 // Piece c of row r of a [row][32] tile (64 bytes a row).
 __device__ __forceinline__ uint32_t xrow_piece(int r, int c) { return (uint32_t)r * 64u + 16u * (c ^ ((r >> 2) & 3)); }
 
+// 16 codes of one output row on their way from LDS to LDS. They are read half
+// a stage before they are expanded, so that the expansion does not hold up the
+// products it stands between.
+struct XCodes {
+  uint64_t w;
+  uint32_t z, s;
+};
+
 // The 8 codes of w times f, minus z f, rounded once: codes - z + 128 as
 // bytes (one addition per four), then (t - 128) f in one fma.
+__device__ __forceinline__ uint32_t xbias(uint32_t z) {
+  return __builtin_amdgcn_perm(0u, 0x80u - z, 0u);    // its low byte four times
+}
 __device__ __forceinline__ ex_u32x4_t xexpand(uint32_t w, uint32_t bias, float f) {
   const uint32_t lo = (w & 0x0F0F0F0Fu) + bias, hi = ((w >> 4) & 0x0F0F0F0Fu) + bias;
   const float m = -128.f * f;
@@ -942,14 +953,15 @@ k_expert_ring(ExArgs p) {
   const uint32_t xd0 = lds + kFB + xrow_piece(xr, 2 * xh), xd1 = lds + kFB + xrow_piece(xr, 2 * xh + 1);
   const uint32_t xz = lds + kFZero + 4 * xr, xs = lds + kFScale + 4 * xr;
   auto unit_ok = [](float s) { return fabsf(s) >= 0x1p-40f && fabsf(s) <= 0x1p40f; };
-  auto expand = [&](int b, int i, uint32_t slot) {
-    const uint64_t w = lds_u64(xq + (b & 1) * 16384 + 16 * (i ^ ((xr >> 2) & 3)));
-    const uint32_t bias = (0x80u - lds_u32(xz + (b & 1) * 1024)) * 0x01010101u;
-    const float s = __uint_as_float(lds_u32(xs + (b & 1) * 1024));
-    const float f = unit_ok(s) ? 1.f : s;
-    lds_write(xd0 + slot, xexpand((uint32_t)w, bias, f));
-    lds_write(xd1 + slot, xexpand((uint32_t)(w >> 32), bias, f));
+  XCodes xw;
+  auto fetch = [&](int b, int i) {
+    xw.w = lds_u64(xq + (b & 1) * 16384 + 16 * (i ^ ((xr >> 2) & 3)));
+    xw.z = lds_u32(xz + (b & 1) * 1024);
+    xw.s = lds_u32(xs + (b & 1) * 1024);
   };
+  auto factor = [&]() { return unit_ok(__uint_as_float(xw.s)) ? 1.f : __uint_as_float(xw.s); };
+  auto expand0 = [&](uint32_t slot) { lds_write(xd0 + slot, xexpand((uint32_t)xw.w, xbias(xw.z), factor())); };
+  auto expand1 = [&](uint32_t slot) { lds_write(xd1 + slot, xexpand((uint32_t)(xw.w >> 32), xbias(xw.z), factor())); };
   uint32_t af[2], bf[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -975,14 +987,20 @@ k_expert_ring(ExArgs p) {
   };
 
   for (int st = 0; st < 3; ++st) issue_a(st, st);
-  issue_q(0, 0);
-  issue_q(0, 1);
-  issue_g(0);
-  issue_q(1, 0);
+  for (int b = 0; b < 2; ++b) {
+    issue_q(b, 0);
+    issue_q(b, 1);
+    issue_g(b);
+  }
   xbarrier<0>();
   uint32_t b0 = 0, b1 = 16384, b2 = 2 * 16384;        // B's slots of stages st, st + 1, st + 2
-  expand(0, 0, b0);
-  expand(0, 1, b1);
+  fetch(0, 0);
+  expand0(b0);
+  expand1(b0);
+  fetch(0, 1);
+  expand0(b1);
+  expand1(b1);
+  fetch(0, 2);
   const uint32_t su = lds + kFScale + 4 * (64 * wn + li);
   float unit[NI];                                      // the current unit of each of the lane's columns
 #pragma unroll
@@ -993,26 +1011,30 @@ k_expert_ring(ExArgs p) {
   xbarrier<0>();
   read(ex_const<0>{}, ex_const<0>{}, b0);
   // DMA instructions of a wave in stage i of a block: A 2; codes of the next
-  // block but one in stages 3 and 0, scales or zero points in stage 0
+  // block but one in stages 2 and 3, scales or zero points in stage 3 (their
+  // buffers' last readers were stages 0 and, for the units, the end of the
+  // block before)
   int left = bpg;                                      // blocks left of the group
   auto stage = [&](auto I, int blk) {
     constexpr int i = decltype(I)::value;
-    xbarrier<i == 0 ? 3 : (i == 1 ? 4 : 2)>();         // what stage i - 1 issued may still fly
+    xbarrier<i == 0 ? 4 : (i == 3 ? 3 : 2)>();         // what stage i - 1 issued may still fly
     issue_a(4 * blk + i + 3, (i + 3) & 3);
-    if constexpr (i == 0) {
-      issue_q(blk + 1, 1);
-      issue_g(blk + 1);
+    if constexpr (i == 2) issue_q(blk + 2, 0);
+    if constexpr (i == 3) {
+      issue_q(blk + 2, 1);
+      issue_g(blk + 2);
     }
-    if constexpr (i == 3) issue_q(blk + 2, 0);
     __builtin_amdgcn_sched_barrier(0);
     read(I, ex_const<1>{}, b0);
-    expand(i < 2 ? blk : blk + 1, (i + 2) & 3, b2);
+    expand0(b2);
     multiply(ex_const<0>{});
-    xinterleave<8, 9, 6>();
+    xinterleave<8, 6, 4>();
     __builtin_amdgcn_sched_barrier(0);
     read(ex_const<(i + 1) & 3>{}, ex_const<0>{}, b1);
+    expand1(b2);
+    fetch(i == 0 ? blk : blk + 1, (i + 3) & 3);
     multiply(ex_const<1>{});
-    xinterleave<8, 6, 1>();
+    xinterleave<8, 9, 4>();
     __builtin_amdgcn_sched_barrier(0);
     const uint32_t t = b0;
     b0 = b1;
@@ -1054,7 +1076,7 @@ k_expert_ring(ExArgs p) {
 
 // Gradient: the rows of a stage's 32 outputs hold 128 contiguous bytes of
 // codes each, so codes, scales and zero points (one of each per row and
-// 32-column chunk, whatever the group) come stage by stage, four ahead.
+// 32-column chunk, whatever the group) come stage by stage, five ahead.
 constexpr int kGPer = 4;                               // DMA instructions per wave and stage
 constexpr uint32_t kGSlot = 32768, kGRaw = 4 * kGSlot, kGScale = kGRaw + 4 * 4096, kGZero = kGScale + 4 * 1024,
                    kGDump = kGZero + 4 * 1024, kGLds = kGDump + 256;   // kGDump: never read
@@ -1118,12 +1140,17 @@ k_expert_ring_grad(ExArgs p) {
   const uint32_t xq = lds + kGRaw + xr * 128 + xc * 8;
   const uint32_t xz = lds + kGZero + 4 * (xr * 8 + (xc >> 1)), xs = lds + kGScale + 4 * (xr * 8 + (xc >> 1));
   const uint32_t xd0 = lds + 16384 + col_piece<256>(xr, 2 * xc), xd1 = lds + 16384 + col_piece<256>(xr, 2 * xc + 1);
-  auto expand = [&](int st, int slot) {
-    const uint64_t w = lds_u64(xq + (st & 3) * 4096);
-    const uint32_t bias = (0x80u - lds_u32(xz + (st & 3) * 1024)) * 0x01010101u;
-    const float s = __uint_as_float(lds_u32(xs + (st & 3) * 1024));
-    lds_write(xd0 + slot * kGSlot, xexpand((uint32_t)w, bias, s));
-    lds_write(xd1 + slot * kGSlot, xexpand((uint32_t)(w >> 32), bias, s));
+  XCodes xw;
+  auto fetch = [&](int st) {
+    xw.w = lds_u64(xq + (st & 3) * 4096);
+    xw.z = lds_u32(xz + (st & 3) * 1024);
+    xw.s = lds_u32(xs + (st & 3) * 1024);
+  };
+  auto expand0 = [&](int slot) {
+    lds_write(xd0 + slot * kGSlot, xexpand((uint32_t)xw.w, xbias(xw.z), __uint_as_float(xw.s)));
+  };
+  auto expand1 = [&](int slot) {
+    lds_write(xd1 + slot * kGSlot, xexpand((uint32_t)(xw.w >> 32), xbias(xw.z), __uint_as_float(xw.s)));
   };
   // fragment addresses (slots 2 and 3 are past the offset field of 0)
   uint32_t af[2][2], bf[2][2];                        // [slot / 2][kk], [slot / 2][ni]
@@ -1156,24 +1183,31 @@ k_expert_ring_grad(ExArgs p) {
   for (int st = 0; st < 3; ++st) issue_a(st, st);
   for (int st = 0; st < 4; ++st) issue_b(st);
   xbarrier<0>();
-  expand(0, 0);
-  expand(1, 1);
+  for (int st = 0; st < 2; ++st) {
+    fetch(st);
+    expand0(st);
+    expand1(st);
+  }
+  fetch(2);
   xbarrier<0>();
+  issue_b(4);                                          // into the codes of stage 0, read above
   read(ex_const<0>{}, ex_const<0>{});
   auto stage = [&](auto SL, int st) {
     constexpr int sl = decltype(SL)::value;
     xbarrier<kGPer>();
     issue_a(st + 3, (sl + 3) & 3);
-    issue_b(st + 4);
+    issue_b(st + 5);                                   // over the codes of st + 1, read in stage st - 2
     __builtin_amdgcn_sched_barrier(0);
     read(SL, ex_const<1>{});
-    expand(st + 2, (sl + 2) & 3);
+    expand0((sl + 2) & 3);
     multiply(ex_const<0>{});
-    xinterleave<8, 11, 6>();
+    xinterleave<8, 8, 4>();
     __builtin_amdgcn_sched_barrier(0);
     read(ex_const<(sl + 1) & 3>{}, ex_const<0>{});
+    expand1((sl + 2) & 3);
+    fetch(st + 3);
     multiply(ex_const<1>{});
-    xinterleave<8, 8, 1>();
+    xinterleave<8, 11, 4>();
     __builtin_amdgcn_sched_barrier(0);
   };
   int st = 0;
