@@ -342,8 +342,8 @@ k_expert_mv(const uint16_t* __restrict__ X, int T, int64_t n, int64_t ldx, const
 //
 // A BM x 128 tile per workgroup (v_mfma_f32_32x32x16_bf16; wave (wm, wn) holds
 // MI x NI blocks of 32 x 32). K advances in stages of 64 through two LDS
-// buffers. The operands of stage st + 2 are on their way into registers and
-// those of stage st + 1 are written into the other buffer, the packed one
+// buffers. The operands of the next DA and DB stages are on their way into
+// registers and those of stage st + 1 are written into the other buffer, the packed one
 // expanded to bf16 on its way, in between the products of stage st: one
 // barrier per stage, and the expansion (once per workgroup, about three
 // operations per code) runs beside the matrix cores. Operand layouts in LDS
@@ -356,17 +356,20 @@ k_expert_mv(const uint16_t* __restrict__ X, int T, int64_t n, int64_t ldx, const
 //    keeps the writes of wide column runs off each other's banks.
 constexpr int kExBK = 64;
 
-template <int MI_, int NI_, int WM_, int WN_>
+// DA, DB: stages of A and B on their way into registers (the loads of stage
+// st + D leave at the start of stage st).
+template <int MI_, int NI_, int WM_, int WN_, int DA_, int DB_>
 struct ExTile {
+  static constexpr int DA = DA_, DB = DB_, U = DA_ > 2 || DB_ > 2 ? 4 : 2;   // stages per loop body
   static constexpr int MI = MI_, NI = NI_, WM = WM_, WN = WN_;
   static constexpr int BM = 32 * MI * WM, BN = 32 * NI * WN, THREADS = 64 * WM * WN;
   static constexpr int PA = BM * 8 / THREADS;   // 16-byte pieces of A per thread and stage
   static constexpr int NB = BN * 8 / THREADS;   // 8-code units of B per thread and stage
 };
-using ExTileX = ExTile<4, 2, 2, 4>;      // 256 x 256, 8 waves
-using ExTile128 = ExTile<2, 2, 2, 2>;    // 128 x 128
-using ExTile64 = ExTile<2, 1, 1, 4>;     // 64 x 128
-using ExTile32 = ExTile<1, 1, 1, 4>;     // 32 x 128
+using ExTileX = ExTile<4, 2, 2, 4, 1, 2>;      // 256 x 256, 8 waves
+using ExTile128 = ExTile<2, 2, 2, 2, 1, 2>;    // 128 x 128
+using ExTile64 = ExTile<2, 1, 1, 4, 4, 4>;     // 64 x 128: little work per stage to hide a load behind
+using ExTile32 = ExTile<1, 1, 1, 4, 4, 4>;     // 32 x 128
 
 typedef __attribute__((address_space(3))) ex_u32x4_t lds_piece_t;
 typedef __attribute__((address_space(3))) const ex_bf16x8_t lds_frag_t;
@@ -495,6 +498,25 @@ __device__ __forceinline__ void for_four(F&& f) {
   f(ex_const<3>{});
 }
 
+// stage(index modulo U, index) for all stages, U per loop body.
+template <int U, class F>
+__device__ __forceinline__ void run_stages(int nst, F&& stage) {
+  int st = 0;
+  for (; st + U <= nst; st += U) {
+    stage(ex_const<0>{}, st);
+    stage(ex_const<1>{}, st + 1);
+    if constexpr (U == 4) {
+      stage(ex_const<2>{}, st + 2);
+      stage(ex_const<3>{}, st + 3);
+    }
+  }
+  if (st < nst) stage(ex_const<0>{}, st);
+  if constexpr (U == 4) {
+    if (st + 1 < nst) stage(ex_const<1>{}, st + 1);
+    if (st + 2 < nst) stage(ex_const<2>{}, st + 2);
+  }
+}
+
 // ---- forward: K = n. The codes minus the zero point are exact in bf16, the
 // group's sum is scaled once in fp32 (tot += s acc), as in the one-layer
 // product. GS: stages per group when fixed (groups of 64 and 128: the first
@@ -533,33 +555,34 @@ k_expert_mm(ExArgs p) {
 #pragma unroll
   for (int e = 0; e < NB; ++e) bw[e] = lds + ASZ + row_piece(br, bu + e);
 
-  ex_u32x4_t ra[PA];
-  UnitWords<BITS, NB> rb[2];
-  uint32_t rz[2];
-  auto aload = [&](int st) {
+  constexpr int DA = TL::DA, DB = TL::DB, U = TL::U;
+  ex_u32x4_t ra[DA][PA];
+  UnitWords<BITS, NB> rb[DB];
+  uint32_t rz[DB];
+  auto aload = [&](auto S, int st) {
 #pragma unroll
-    for (int i = 0; i < PA; ++i) ra[i] = load_piece<VEC>(arow[i], (int64_t)st * kExBK + 8 * ac, p.n);
+    for (int i = 0; i < PA; ++i) ra[S % DA][i] = load_piece<VEC>(arow[i], (int64_t)st * kExBK + 8 * ac, p.n);
   };
-  auto bload = [&](auto B, int st) {
+  auto bload = [&](auto S, int st) {
     const int c = min(2 * st + bu / 4, nchunks - 1);      // a chunk past the end meets zeros of A
-    rb[B].load(qrow, 4 * c + bu % 4);
+    rb[S % DB].load(qrow, 4 * c + bu % 4);
     const int g = GS == 1 ? st : (GS == 2 ? st >> 1 : c / cpg);
-    rz[B] = zrow[g];
+    rz[S % DB] = zrow[g];
   };
-  auto awrite = [&](auto B) {
+  auto awrite = [&](auto S) {
 #pragma unroll
-    for (int i = 0; i < PA; ++i) lds_write(aw + B * BUF + i * (AR * 128), ra[i]);
+    for (int i = 0; i < PA; ++i) lds_write(aw + (S % 2) * BUF + i * (AR * 128), ra[S % DA][i]);
   };
   // part kk of the four that a stage's products interleave with
-  auto bwrite = [&](auto B, auto KK) {
-    constexpr int kk = decltype(KK)::value;
+  auto bwrite = [&](auto S, auto KK) {
+    constexpr int kk = decltype(KK)::value, B = decltype(S)::value % DB;
 #pragma unroll
     for (int e = 0; e < NB; ++e)
       if (e * 4 / NB == kk) {
         float f[8];
         rb[B].get(e, (float)rz[B], f);
-        lds_write(bw[e] + B * BUF, (ex_u32x4_t){pack_exact(f[0], f[1]), pack_exact(f[2], f[3]),
-                                                 pack_exact(f[4], f[5]), pack_exact(f[6], f[7])});
+        lds_write(bw[e] + (S % 2) * BUF, (ex_u32x4_t){pack_exact(f[0], f[1]), pack_exact(f[2], f[3]),
+                                                       pack_exact(f[4], f[5]), pack_exact(f[6], f[7])});
       }
   };
   const float* srow[NI];
@@ -592,11 +615,12 @@ k_expert_mm(ExArgs p) {
       sc[ni] = srow[ni][min(g, ngroups - 1)];
     }
   };
-  auto stage = [&](auto B, int st) {
-    constexpr int b = decltype(B)::value;
+  auto stage = [&](auto S, int st) {
+    constexpr int i = decltype(S)::value, b = i % 2;    // i: st modulo U
+    const ex_const<i + 1> next{};
     __syncthreads();
-    aload(min(st + 1, nst - 1));
-    bload(B, min(st + 2, nst - 1));
+    aload(ex_const<i + DA>{}, min(st + DA, nst - 1));
+    bload(ex_const<i + DB>{}, min(st + DB, nst - 1));
     __builtin_amdgcn_sched_barrier(0);    // the loads leave before the stage's products
     ex_bf16x8_t fa[2][MI], fb[2][NI];
     auto frags = [&](auto KK) {
@@ -616,7 +640,7 @@ k_expert_mm(ExArgs p) {
         for (int ni = 0; ni < NI; ++ni)
           acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
               fa[kk & 1][mi], fb[kk & 1][ni], (GS == 1 || (GS == 2 && b == 0)) && kk == 0 ? zero : acc[mi][ni], 0, 0, 0);
-      bwrite(ex_const<1 - b>{}, KK);
+      bwrite(next, KK);
       if (GS == 0 && (kk & 1) == 1 && ++cin == cpg && g < ngroups) {   // the group is complete
         flush();
 #pragma unroll
@@ -626,20 +650,16 @@ k_expert_mm(ExArgs p) {
         cin = 0;
       }
     });
-    awrite(ex_const<1 - b>{});
+    awrite(next);
     if (GS == 1 || (GS == 2 && b == 1)) flush();
   };
-  aload(0);
-  bload(ex_const<0>{}, 0);
-  bload(ex_const<1>{}, min(1, nst - 1));
+  for_four([&](auto S) {
+    if constexpr (S < DA) aload(S, min((int)S, nst - 1));
+    if constexpr (S < DB) bload(S, min((int)S, nst - 1));
+  });
   awrite(ex_const<0>{});
   for_four([&](auto KK) { bwrite(ex_const<0>{}, KK); });
-  int st = 0;
-  for (; st + 1 < nst; st += 2) {
-    stage(ex_const<0>{}, st);
-    stage(ex_const<1>{}, st + 1);
-  }
-  if (st < nst) stage(ex_const<0>{}, st);
+  run_stages<U>(nst, stage);
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) {
     const int64_t o = o0 + 32 * (NI * wn + ni) + li;
@@ -696,16 +716,18 @@ k_expert_mm_grad(ExArgs p) {
 #pragma unroll
   for (int e = 0; e < NB; ++e) bw[e] = lds + ASZ + col_piece<BN>(br, bu + e);
 
-  ex_u32x4_t ra[PA];
-  UnitWords<BITS, NB> rb[2];
-  float rs[2];
-  uint32_t rz[2];
-  bool rv[2];
-  auto aload = [&](int st) {
+  constexpr int DA = TL::DA, DB = TL::DB, U = TL::U;
+  ex_u32x4_t ra[DA][PA];
+  UnitWords<BITS, NB> rb[DB];
+  float rs[DB];
+  uint32_t rz[DB];
+  bool rv[DB];
+  auto aload = [&](auto S, int st) {
 #pragma unroll
-    for (int i = 0; i < PA; ++i) ra[i] = load_piece<VEC>(arow[i], (int64_t)st * kExBK + 8 * ac, p.d_out);
+    for (int i = 0; i < PA; ++i) ra[S % DA][i] = load_piece<VEC>(arow[i], (int64_t)st * kExBK + 8 * ac, p.d_out);
   };
-  auto bload = [&](auto B, int st) {
+  auto bload = [&](auto S, int st) {
+    constexpr int B = decltype(S)::value % DB;
     const int64_t o = (int64_t)st * kExBK + br;
     const int64_t oc = ebase + min(o, p.d_out - 1);
     rb[B].load(p.qw + oc * nchunks * BITS, uc);
@@ -713,12 +735,12 @@ k_expert_mm_grad(ExArgs p) {
     rz[B] = p.zeros[oc * ngroups + gi];
     rv[B] = cok && o < p.d_out;                              // outputs past d_out: weights of 0
   };
-  auto awrite = [&](auto B) {
+  auto awrite = [&](auto S) {
 #pragma unroll
-    for (int i = 0; i < PA; ++i) lds_write(aw + B * BUF + i * (AR * 128), ra[i]);
+    for (int i = 0; i < PA; ++i) lds_write(aw + (S % 2) * BUF + i * (AR * 128), ra[S % DA][i]);
   };
-  auto bwrite = [&](auto B, auto KK) {
-    constexpr int kk = decltype(KK)::value;
+  auto bwrite = [&](auto S, auto KK) {
+    constexpr int kk = decltype(KK)::value, B = decltype(S)::value % DB;
     const float scale = rv[B] ? rs[B] : 0.f;
 #pragma unroll
     for (int e = 0; e < NB; ++e)
@@ -738,7 +760,7 @@ k_expert_mm_grad(ExArgs p) {
               f[2 * i + 1] -= __uint_as_float(v[i] & 0xFFFF0000u);
             }
           }
-          lds_write(bw[e] + B * BUF + q * BSZ, v);
+          lds_write(bw[e] + (S % 2) * BUF + q * BSZ, v);
         }
       }
   };
@@ -749,11 +771,12 @@ k_expert_mm_grad(ExArgs p) {
   for (int ni = 0; ni < NI; ++ni) bf[ni] = lds + ASZ + col_frag_at<BN>(32 * (NI * wn + ni), lane);
 
   ex_f32x16_t acc[MI][NI] = {};
-  auto stage = [&](auto B, int st) {
-    constexpr int b = decltype(B)::value;
+  auto stage = [&](auto S, int st) {
+    constexpr int i = decltype(S)::value, b = i % 2;    // i: st modulo U
+    const ex_const<i + 1> next{};
     __syncthreads();
-    aload(min(st + 1, nst - 1));
-    bload(B, min(st + 2, nst - 1));
+    aload(ex_const<i + DA>{}, min(st + DA, nst - 1));
+    bload(ex_const<i + DB>{}, min(st + DB, nst - 1));
     __builtin_amdgcn_sched_barrier(0);
     ex_bf16x8_t fa[2][MI], fb[2][NP][NI];
     auto frags = [&](auto KK) {
@@ -777,21 +800,17 @@ k_expert_mm_grad(ExArgs p) {
 #pragma unroll
           for (int ni = 0; ni < NI; ++ni)
             acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk & 1][mi], fb[kk & 1][q][ni], acc[mi][ni], 0, 0, 0);
-      bwrite(ex_const<1 - b>{}, KK);
+      bwrite(next, KK);
     });
-    awrite(ex_const<1 - b>{});
+    awrite(next);
   };
-  aload(0);
-  bload(ex_const<0>{}, 0);
-  bload(ex_const<1>{}, min(1, nst - 1));
+  for_four([&](auto S) {
+    if constexpr (S < DA) aload(S, min((int)S, nst - 1));
+    if constexpr (S < DB) bload(S, min((int)S, nst - 1));
+  });
   awrite(ex_const<0>{});
   for_four([&](auto KK) { bwrite(ex_const<0>{}, KK); });
-  int st = 0;
-  for (; st + 1 < nst; st += 2) {
-    stage(ex_const<0>{}, st);
-    stage(ex_const<1>{}, st + 1);
-  }
-  if (st < nst) stage(ex_const<0>{}, st);
+  run_stages<U>(nst, stage);
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) {
     const int64_t c = c0 + 32 * (NI * wn + ni) + li;
@@ -1283,21 +1302,23 @@ k_keep_grad(KgArgs p) {
   uint32_t bw[NB];
 #pragma unroll
   for (int u = 0; u < NB; ++u) bw[u] = lds + ASZ + col_piece<BN>(br, bu + u);
-  ex_u32x4_t ra[PA], rb[2][NB / 2];
-  uint32_t rx[2];
-  bool rv[2];
+  constexpr int DA = TL::DA, DB = TL::DB, U = TL::U;
+  ex_u32x4_t ra[DA][PA], rb[DB][NB / 2];
+  uint32_t rx[DB];
+  bool rv[DB];
   const int64_t bc = bok ? bcol : 0;
   // the source row of a stage is looked up one stage before its loads
   auto lookup = [&](int st) { return (int)source_row(p.rows, min(k0 + st * kExBK + br, k1 - 1), p.T); };
   int src = 0;
-  auto aload = [&](int st) {
+  auto aload = [&](auto S, int st) {
 #pragma unroll
     for (int i = 0; i < PA; ++i) {
       const int r = k0 + st * kExBK + ar + AR * i;        // rows past the part: zeros on both sides
-      ra[i] = load_piece<VEC>(p.P + (int64_t)min(r, k1 - 1) * p.ldp, m0 + 8 * ap, r < k1 ? p.m : 0);
+      ra[S % DA][i] = load_piece<VEC>(p.P + (int64_t)min(r, k1 - 1) * p.ldp, m0 + 8 * ap, r < k1 ? p.m : 0);
     }
   };
-  auto bload = [&](auto B, int st) {
+  auto bload = [&](auto S, int st) {
+    constexpr int B = decltype(S)::value % DB;
     const ex_u32x4_t* c = reinterpret_cast<const ex_u32x4_t*>(p.codes + src * p.pitch + bc);
 #pragma unroll
     for (int i = 0; i < NB / 2; ++i) rb[B][i] = c[i];
@@ -1305,12 +1326,12 @@ k_keep_grad(KgArgs p) {
     rv[B] = k0 + st * kExBK + br < k1 && bok;
     src = lookup(min(st + 1, nst - 1));
   };
-  auto awrite = [&](auto B) {
+  auto awrite = [&](auto S) {
 #pragma unroll
-    for (int i = 0; i < PA; ++i) lds_write(aw + B * BUF + i * (AR * 2 * AW), ra[i]);
+    for (int i = 0; i < PA; ++i) lds_write(aw + (S % 2) * BUF + i * (AR * 2 * AW), ra[S % DA][i]);
   };
-  auto bwrite = [&](auto B, auto KK) {
-    constexpr int kk = decltype(KK)::value;
+  auto bwrite = [&](auto S, auto KK) {
+    constexpr int kk = decltype(KK)::value, B = decltype(S)::value % DB;
     const float step = rv[B] ? __uint_as_float(rx[B] == 255u ? 0x7FC00000u : rx[B] << 23) : 0.f;
 #pragma unroll
     for (int q = 0; q < NB; ++q)
@@ -1326,7 +1347,7 @@ k_keep_grad(KgArgs p) {
           o[2 * w] = pack_exact(f[0], f[1]);
           o[2 * w + 1] = pack_exact(f[2], f[3]);
         }
-        lds_write(bw[q] + B * BUF, o);
+        lds_write(bw[q] + (S % 2) * BUF, o);
       }
   };
   uint32_t af[MI], bf[NI];
@@ -1336,11 +1357,12 @@ k_keep_grad(KgArgs p) {
   for (int ni = 0; ni < NI; ++ni) bf[ni] = lds + ASZ + col_frag_at<BN>(32 * (NI * wn + ni), lane);
 
   ex_f32x16_t acc[MI][NI] = {};
-  auto stage = [&](auto B, int st) {
-    constexpr int b = decltype(B)::value;
+  auto stage = [&](auto S, int st) {
+    constexpr int i = decltype(S)::value, b = i % 2;    // i: st modulo U
+    const ex_const<i + 1> next{};
     __syncthreads();
-    aload(min(st + 1, nst - 1));
-    bload(B, min(st + 2, nst - 1));
+    aload(ex_const<i + DA>{}, min(st + DA, nst - 1));
+    bload(ex_const<i + DB>{}, min(st + DB, nst - 1));
     __builtin_amdgcn_sched_barrier(0);
     ex_bf16x8_t fa[2][MI], fb[2][NI];
     auto frags = [&](auto KK) {
@@ -1359,24 +1381,20 @@ k_keep_grad(KgArgs p) {
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni)
           acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk & 1][mi], fb[kk & 1][ni], acc[mi][ni], 0, 0, 0);
-      bwrite(ex_const<1 - b>{}, KK);
+      bwrite(next, KK);
     });
-    awrite(ex_const<1 - b>{});
+    awrite(next);
   };
   if (nst > 0) {
     src = lookup(0);
-    aload(0);
-    bload(ex_const<0>{}, 0);
-    bload(ex_const<1>{}, min(1, nst - 1));
+    for_four([&](auto S) {
+      if constexpr (S < DA) aload(S, min((int)S, nst - 1));
+      if constexpr (S < DB) bload(S, min((int)S, nst - 1));
+    });
     awrite(ex_const<0>{});
     for_four([&](auto KK) { bwrite(ex_const<0>{}, KK); });
   }
-  int st = 0;
-  for (; st + 1 < nst; st += 2) {
-    stage(ex_const<0>{}, st);
-    stage(ex_const<1>{}, st + 1);
-  }
-  if (st < nst) stage(ex_const<0>{}, st);
+  run_stages<U>(nst, stage);
   const int h = lane >> 5, li = lane & 31;
   float* __restrict__ out = p.out + (int64_t)sp * p.split_stride + (int64_t)e * p.m * p.n;
 #pragma unroll
