@@ -46,33 +46,48 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
+// The segments of up to 64 experts from e0 on, one per lane, and the
+// inclusive sums of their row tiles.
+struct SegScan {
+  int lo, hi, nt, inc;
+};
+__device__ __forceinline__ SegScan scan_segments(const int32_t* __restrict__ offsets, int E, int R, int BM, int e0) {
+  const int e = e0 + (threadIdx.x & 63);
+  SegScan s = {0, 0, 0, 0};
+  if (e < E) {
+    s.lo = min(max(offsets[e], 0), R);
+    s.hi = min(max(offsets[e + 1], s.lo), R);
+  }
+  s.nt = (s.hi - s.lo + BM - 1) / BM;
+  s.inc = wave_scan(s.nt);
+  return s;
+}
+
+// Row tile rt, if it is among the 64 experts of s (`before` tiles precede them).
+__device__ __forceinline__ bool pick_segment(const SegScan& s, int e0, int before, int BM, int rt, Seg& sg) {
+  const uint64_t past = __ballot(before + s.inc > rt);
+  if (!past) return false;
+  const int l = __ffsll((long long)past) - 1;
+  const int lo = __builtin_amdgcn_readlane(s.lo, l), hi = __builtin_amdgcn_readlane(s.hi, l);
+  const int first = before + __builtin_amdgcn_readlane(s.inc - s.nt, l);
+  sg = Seg{e0 + l, lo, hi, lo + (rt - first) * BM};
+  return true;
+}
+
 // Row tile rt of BM rows (every wave of the workgroup finds it for itself).
 __device__ __forceinline__ Seg find_tile(const int32_t* __restrict__ offsets, int E, int R, int BM, int rt) {
-  const int lane = threadIdx.x & 63;
+  Seg sg = {-1, 0, 0, 0};
   if (offsets == nullptr) {
-    const bool in = (int64_t)rt * BM < R;
-    return Seg{in ? 0 : -1, 0, R, rt * BM};
+    if ((int64_t)rt * BM < R) sg = Seg{0, 0, R, rt * BM};
+    return sg;
   }
   int before = 0;
   for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = e0 + lane;
-    int lo = 0, hi = 0;
-    if (e < E) {
-      lo = min(max(offsets[e], 0), R);
-      hi = min(max(offsets[e + 1], lo), R);
-    }
-    const int nt = (hi - lo + BM - 1) / BM;
-    const int inc = wave_scan(nt);
-    const uint64_t past = __ballot(before + inc > rt);
-    if (past) {
-      const int l = __ffsll((long long)past) - 1;
-      const int slo = __builtin_amdgcn_readlane(lo, l), shi = __builtin_amdgcn_readlane(hi, l);
-      const int first = before + __builtin_amdgcn_readlane(inc - nt, l);
-      return Seg{e0 + l, slo, shi, slo + (rt - first) * BM};
-    }
-    before += __builtin_amdgcn_readlane(inc, 63);
+    const SegScan s = scan_segments(offsets, E, R, BM, e0);
+    if (pick_segment(s, e0, before, BM, rt, sg)) break;
+    before += __builtin_amdgcn_readlane(s.inc, 63);
   }
-  return Seg{-1, 0, 0, 0};
+  return sg;
 }
 
 // Source row of sorted row p (rows == nullptr: p itself).
@@ -366,7 +381,6 @@ struct ExTile {
   static constexpr int PA = BM * 8 / THREADS;   // 16-byte pieces of A per thread and stage
   static constexpr int NB = BN * 8 / THREADS;   // 8-code units of B per thread and stage
 };
-using ExTileX = ExTile<4, 2, 2, 4, 1, 2>;      // 256 x 256, 8 waves
 using ExTile128 = ExTile<2, 2, 2, 2, 1, 2>;    // 128 x 128
 using ExTile64 = ExTile<2, 1, 1, 4, 4, 4>;     // 64 x 128: little work per stage to hide a load behind
 using ExTile32 = ExTile<1, 1, 1, 4, 4, 4>;     // 32 x 128
@@ -415,6 +429,21 @@ __device__ __forceinline__ ex_u32x4_t load_piece(const uint16_t* __restrict__ ro
     for (int i = 0; i < 8; ++i) v[i] = c + i < limit ? row[c + i] : 0u;
     return (ex_u32x4_t){v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
   }
+}
+
+// The 8 codes of w times f, minus z f, rounded once: codes - z + 128 as
+// bytes (one addition per four), then (t - 128) f in one fma.
+__device__ __forceinline__ uint32_t xbias(uint32_t z) {
+  return __builtin_amdgcn_perm(0u, 0x80u - z, 0u);    // its low byte four times
+}
+__device__ __forceinline__ ex_u32x4_t xexpand(uint32_t w, uint32_t bias, float f) {
+  const uint32_t lo = (w & 0x0F0F0F0Fu) + bias, hi = ((w >> 4) & 0x0F0F0F0Fu) + bias;
+  const float m = -128.f * f;
+  ex_u32x4_t o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = ex_pack2(fmaf((float)((lo >> (8 * i)) & 0xFFu), f, m), fmaf((float)((hi >> (8 * i)) & 0xFFu), f, m));
+  return o;
 }
 
 // The words of NB units of 8 codes, unit u0 (a multiple of NB) of a packed
@@ -477,6 +506,29 @@ __device__ __forceinline__ bool tile_of(int64_t b, int nr, int nc, int& rt, int&
   return true;
 }
 
+// The tile of workgroup b. The list holds the tiles that there are, not the
+// launch's upper bound, so that the XCDs' parts are equal (with the bound the
+// last XCDs' parts were empty: 57 against TTT us for 2036 rows over 32 experts).
+__device__ __forceinline__ bool locate(const int32_t* __restrict__ offsets, int E, int R, int BM, int64_t b, int nc,
+                                       int& ct, Seg& sg) {
+  int rt;
+  if (offsets == nullptr) {
+    if (!tile_of(b, (int)ceil_div(R, BM), nc, rt, ct)) return false;
+    sg = Seg{0, 0, R, rt * BM};
+    return true;
+  }
+  if (E <= 64) {
+    const SegScan s = scan_segments(offsets, E, R, BM, 0);
+    return tile_of(b, __builtin_amdgcn_readlane(s.inc, 63), nc, rt, ct) && pick_segment(s, 0, 0, BM, rt, sg);
+  }
+  int total = 0;
+  for (int e0 = 0; e0 < E; e0 += 64)
+    total += __builtin_amdgcn_readlane(scan_segments(offsets, E, R, BM, e0).inc, 63);
+  if (!tile_of(b, total, nc, rt, ct)) return false;
+  sg = find_tile(offsets, E, R, BM, rt);
+  return sg.e >= 0;
+}
+
 struct ExArgs {
   const uint16_t* A; int64_t lda;             // X or dY
   const int32_t* rows; int T;
@@ -528,10 +580,9 @@ k_expert_mm(ExArgs p) {
   constexpr int MI = TL::MI, NI = TL::NI, BM = TL::BM, PA = TL::PA, NB = TL::NB, THREADS = TL::THREADS;
   constexpr uint32_t ASZ = BM * 128, BSZ = TL::BN * 128, BUF = ASZ + BSZ;
   __shared__ __align__(16) uint8_t smem[2 * BUF];
-  int rt, ct;
-  if (!tile_of(blockIdx.x, p.nrt, p.nct, rt, ct)) return;
-  const Seg sg = find_tile(p.offsets, p.E, p.R, BM, rt);
-  if (sg.e < 0) return;
+  int ct;
+  Seg sg;
+  if (!locate(p.offsets, p.E, p.R, BM, blockIdx.x, p.nct, ct, sg)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave % TL::WM, wn = wave / TL::WM, h = lane >> 5, li = lane & 31;
   const int64_t o0 = (int64_t)ct * TL::BN;
@@ -686,10 +737,9 @@ k_expert_mm_grad(ExArgs p) {
   constexpr int MI = TL::MI, NI = TL::NI, BM = TL::BM, BN = TL::BN, PA = TL::PA, NB = TL::NB, THREADS = TL::THREADS;
   constexpr uint32_t ASZ = BM * 128, BSZ = kExBK * 2 * BN, BUF = ASZ + NP * BSZ;
   __shared__ __align__(16) uint8_t smem[2 * BUF];
-  int rt, ct;
-  if (!tile_of(blockIdx.x, p.nrt, p.nct, rt, ct)) return;
-  const Seg sg = find_tile(p.offsets, p.E, p.R, BM, rt);
-  if (sg.e < 0) return;
+  int ct;
+  Seg sg;
+  if (!locate(p.offsets, p.E, p.R, BM, blockIdx.x, p.nct, ct, sg)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave % TL::WM, wn = wave / TL::WM, h = lane >> 5, li = lane & 31;
   const int64_t c0 = (int64_t)ct * TL::BN;
@@ -745,6 +795,10 @@ k_expert_mm_grad(ExArgs p) {
 #pragma unroll
     for (int e = 0; e < NB; ++e)
       if (e * 4 / NB == kk) {
+        if constexpr (BITS == 4 && NP == 1) {
+          lds_write(bw[e] + (S % 2) * BUF, xexpand(rb[B].w[e], xbias(rz[B]), scale));
+          continue;
+        }
         float f[8];
         rb[B].get(e, (float)rz[B], f);
 #pragma unroll
@@ -881,21 +935,6 @@ struct XCodes {
   uint32_t z, s;
 };
 
-// The 8 codes of w times f, minus z f, rounded once: codes - z + 128 as
-// bytes (one addition per four), then (t - 128) f in one fma.
-__device__ __forceinline__ uint32_t xbias(uint32_t z) {
-  return __builtin_amdgcn_perm(0u, 0x80u - z, 0u);    // its low byte four times
-}
-__device__ __forceinline__ ex_u32x4_t xexpand(uint32_t w, uint32_t bias, float f) {
-  const uint32_t lo = (w & 0x0F0F0F0Fu) + bias, hi = ((w >> 4) & 0x0F0F0F0Fu) + bias;
-  const float m = -128.f * f;
-  ex_u32x4_t o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = ex_pack2(fmaf((float)((lo >> (8 * i)) & 0xFFu), f, m), fmaf((float)((hi >> (8 * i)) & 0xFFu), f, m));
-  return o;
-}
-
 // One MFMA, then VALU operations and LDS reads of its share, N times.
 template <int N, int READS, int VALUS, int I = 0>
 __device__ __forceinline__ void xinterleave() {
@@ -919,10 +958,9 @@ __global__ void __launch_bounds__(512, 2)
 k_expert_ring(ExArgs p) {
   constexpr int MI = 4, NI = 2;
   __shared__ __align__(16) uint8_t smem[kFLds];
-  int rt, ct;
-  if (!tile_of(blockIdx.x, p.nrt, p.nct, rt, ct)) return;
-  const Seg sg = find_tile(p.offsets, p.E, p.R, 256, rt);
-  if (sg.e < 0) return;
+  int ct;
+  Seg sg;
+  if (!locate(p.offsets, p.E, p.R, 256, blockIdx.x, p.nct, ct, sg)) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, li = lane & 31;
@@ -1103,10 +1141,9 @@ __global__ void __launch_bounds__(512, 2)
 k_expert_ring_grad(ExArgs p) {
   constexpr int MI = 4, NI = 2;
   __shared__ __align__(16) uint8_t smem[kGLds];
-  int rt, ct;
-  if (!tile_of(blockIdx.x, p.nrt, p.nct, rt, ct)) return;
-  const Seg sg = find_tile(p.offsets, p.E, p.R, 256, rt);
-  if (sg.e < 0) return;
+  int ct;
+  Seg sg;
+  if (!locate(p.offsets, p.E, p.R, 256, blockIdx.x, p.nct, ct, sg)) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, li = lane & 31;
@@ -1411,6 +1448,182 @@ k_keep_grad(KgArgs p) {
   }
 }
 
+// Wide gradients (m > 128): the ring of the expert products. 256 x 256 x 32
+// stages, 8 waves of 128 x 64; P, the kept codes and their steps come by
+// LDS-DMA (P three stages ahead, the others five), four instructions per wave
+// and stage. A wave fetches the codes of the four rows it expands, so their
+// source rows are the same for 16 lanes each and are read as scalars.
+constexpr int kKPer = 4;
+constexpr uint32_t kKB = 4 * 16384, kKRaw = kKB + 3 * 16384, kKExp = kKRaw + 4 * 8192, kKLds = kKExp + 4 * 2048;
+__global__ void __launch_bounds__(512, 2)
+k_keep_ring(KgArgs p) {
+  constexpr int MI = 4, NI = 2;
+  __shared__ __align__(16) uint8_t smem[kKLds];
+  int rt, ct;
+  if (!tile_of(blockIdx.x, p.nmt, p.nnt, rt, ct)) return;
+  const int e = blockIdx.y, sp = blockIdx.z;
+  int lo = 0, hi = p.R;
+  if (p.offsets) {
+    lo = min(max(p.offsets[e], 0), p.R);
+    hi = min(max(p.offsets[e + 1], lo), p.R);
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+  const int per = (int)(ceil_div(ceil_div(hi - lo, p.splits), kExBK) * kExBK);
+  const int k0 = (int)min((int64_t)hi, lo + (int64_t)sp * per), k1 = (int)min((int64_t)hi, k0 + (int64_t)per);
+  const int nst = (k1 - k0 + 31) / 32;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, li = lane & 31;
+  const int64_t m0 = (int64_t)rt * 256, c0 = (int64_t)ct * 256;
+  const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+
+  // P: instruction 2 wave + i moves rows 2 (2 wave + i) + lane / 32 of a stage
+  int ta[2];
+  const uint16_t* pa[2];
+  bool pok[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    ta[i] = 2 * (2 * wave + i) + (lane >> 5);
+    const int pos = lane & 31, c = pos ^ dma_swz(ta[i]) ^ (pos >> 4);
+    pok[i] = m0 + 8 * c < p.m;
+    pa[i] = p.P + (int64_t)(k0 + ta[i]) * p.ldp + m0 + 8 * c;
+  }
+  auto issue_a = [&](int st, int slot) {
+    const int c = min(st, nst - 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // rows past the part and columns past m: zeros
+      const bool ok = pok[i] && k0 + 32 * c + ta[i] < k1;
+      const void* src = ok ? static_cast<const void*>(pa[i] + (int64_t)c * 32 * p.ldp) : kZeroChunk;
+      dma16(src, __builtin_amdgcn_readfirstlane(lds + slot * 16384 + (2 * wave + i) * 1024));
+    }
+  };
+  // codes: 16 columns lane % 16 of row 4 wave + lane / 16; their steps
+  typedef __attribute__((address_space(4))) const int32_t const_i32;
+  const const_i32* rows = (const const_i32*)(uintptr_t)p.rows;
+  const uint32_t vcol = (uint32_t)min(c0 + 16 * (lane & 15), p.pitch - 16);
+  const uint32_t vgrp = (uint32_t)min(c0 / 32 + (lane & 7), p.pitch / 32 - 1);
+  auto issue_b = [&](int st) {
+    const int r = k0 + 32 * min(st, nst - 1) + 4 * wave;
+    int src[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = min(r + i, k1 - 1);
+      src[i] = min(max(p.rows ? rows[q] : q, 0), p.T - 1);
+    }
+    const int a = lane & 16 ? src[1] : src[0], b = lane & 16 ? src[3] : src[2];
+    const uint32_t row = (uint32_t)(lane & 32 ? b : a);
+    xdma16(row * (uint32_t)p.pitch + vcol, p.codes, __builtin_amdgcn_readfirstlane(lds + kKRaw + (st & 3) * 8192 + wave * 1024));
+    xdma1(row * (uint32_t)(p.pitch / 32) + vgrp, p.exps,
+          __builtin_amdgcn_readfirstlane(lds + kKExp + (st & 3) * 2048 + wave * 256));
+  };
+  // expansion: columns 16 (tid % 16) .. of the stage's row tid / 16
+  const int xr = tid >> 4, xc = tid & 15;
+  const uint32_t xq = lds + kKRaw + tid * 16;
+  const uint32_t xe = lds + kKExp + wave * 256 + 4 * (16 * (xr & 3) + (xc >> 1));
+  const uint32_t xd0 = lds + kKB + col_piece<256>(xr, 2 * xc), xd1 = lds + kKB + col_piece<256>(xr, 2 * xc + 1);
+  typedef __attribute__((address_space(3))) const ex_u32x4_t lds_quad_t;
+  ex_u32x4_t xw;
+  uint32_t xx = 0;
+  auto fetch = [&](int st) {
+    xw = *reinterpret_cast<lds_quad_t*>(xq + (st & 3) * 8192);
+    xx = lds_u32(xe + (st & 3) * 2048);
+  };
+  auto step_of = [&](int st) {
+    return k0 + 32 * st + xr < k1 ? __uint_as_float(xx == 255u ? 0x7FC00000u : xx << 23) : 0.f;
+  };
+  auto convert = [&](uint32_t w0, uint32_t w1, float step) {
+    ex_u32x4_t o;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const uint32_t u = (w ? w1 : w0) ^ 0x80808080u;
+      float f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = ((float)((u >> (8 * i)) & 0xFFu) - 128.f) * step;
+      o[2 * w] = pack_exact(f[0], f[1]);
+      o[2 * w + 1] = pack_exact(f[2], f[3]);
+    }
+    return o;
+  };
+  uint32_t af[MI], bf[NI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) af[mi] = lds + col_frag_at<256>(128 * wm + 32 * mi, lane);
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) bf[ni] = lds + kKB + col_frag_at<256>(64 * wn + 32 * ni, lane);
+  ex_bf16x8_t fa[2][MI], fb[2][NI];
+  auto read = [&](uint32_t aslot, uint32_t bslot, auto KK) {
+    constexpr int kk = decltype(KK)::value;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) fa[kk][mi] = lds_col_frag<256>(af[mi] + aslot + kk * 8192);
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) fb[kk][ni] = lds_col_frag<256>(bf[ni] + bslot + kk * 8192);
+  };
+  ex_f32x16_t acc[MI][NI] = {};
+  auto multiply = [&](auto KK) {
+    constexpr int kk = decltype(KK)::value;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni)
+        acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk][mi], fb[kk][ni], acc[mi][ni], 0, 0, 0);
+  };
+  if (nst > 0) {
+    for (int st = 0; st < 3; ++st) issue_a(st, st);
+    for (int st = 0; st < 4; ++st) issue_b(st);
+    xbarrier<0>();
+    uint32_t b0 = 0, b1 = 16384, b2 = 2 * 16384;       // B's slots of stages st, st + 1, st + 2
+    for (int st = 0; st < 2; ++st) {
+      fetch(st);
+      const float f = step_of(st);
+      lds_write(xd0 + st * 16384, convert(xw[0], xw[1], f));
+      lds_write(xd1 + st * 16384, convert(xw[2], xw[3], f));
+    }
+    fetch(2);
+    xbarrier<0>();
+    issue_b(4);                                         // over the codes of stage 0, read above
+    read(0, b0, ex_const<0>{});
+    auto stage = [&](auto SL, int st) {
+      constexpr int sl = decltype(SL)::value;
+      xbarrier<kKPer>();
+      issue_a(st + 3, (sl + 3) & 3);
+      issue_b(st + 5);                                  // over the codes of st + 1, read in stage st - 2
+      __builtin_amdgcn_sched_barrier(0);
+      const float f = step_of(st + 2);
+      read(sl * 16384, b0, ex_const<1>{});
+      lds_write(xd0 + b2, convert(xw[0], xw[1], f));
+      multiply(ex_const<0>{});
+      xinterleave<8, 12, 5>();
+      __builtin_amdgcn_sched_barrier(0);
+      read(((sl + 1) & 3) * 16384, b1, ex_const<0>{});
+      lds_write(xd1 + b2, convert(xw[2], xw[3], f));
+      fetch(st + 3);
+      multiply(ex_const<1>{});
+      xinterleave<8, 14, 5>();
+      __builtin_amdgcn_sched_barrier(0);
+      const uint32_t t = b0;
+      b0 = b1;
+      b1 = b2;
+      b2 = t;
+    };
+    run_stages<4>(nst, stage);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no DMA into LDS that is no longer owned
+  }
+  float* __restrict__ out = p.out + (int64_t)sp * p.split_stride + (int64_t)e * p.m * p.n;
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) {
+    const int64_t c = c0 + 64 * wn + 32 * ni + li;
+    if (c >= p.n) continue;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int64_t row = m0 + 128 * wm + 32 * mi + 8 * (r >> 2) + 4 * h + (r & 3);
+        if (row < p.m) out[row * p.n + c] = acc[mi][ni][r];
+      }
+  }
+}
+
 __global__ void __launch_bounds__(256)
 k_keep_grad_sum(const float* __restrict__ part, int splits, int64_t count, float* __restrict__ out) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -1593,16 +1806,20 @@ hipError_t launch_keep_grad(hipStream_t s, const KeepGradPlan& pl, const uint16_
   p.offsets = offsets;
   p.E = E;
   p.R = (int)R;
-  p.nmt = (int)ceil_div(m, pl.bm);
-  p.nnt = (int)ceil_div(n, pl.bm == 256 ? 256 : 128);
   p.splits = pl.splits;
   p.out = pl.splits > 1 ? part : G;
   p.split_stride = (int64_t)E * m * n;
   const bool vec = bf16_rows_vec(P, ldp, m);
-  if (pl.bm == 32) kg_go<ExTile32>(s, p, vec);
-  else if (pl.bm == 64) kg_go<ExTile64>(s, p, vec);
-  else if (pl.bm == 128) kg_go<ExTile128>(s, p, vec);
-  else kg_go<ExTileX>(s, p, vec);
+  // the ring's offsets into the codes are 32 bits
+  const int bm = pl.bm == 256 && !(vec && T * p.pitch < ((int64_t)1 << 32)) ? 128 : pl.bm;
+  p.nmt = (int)ceil_div(m, bm);
+  p.nnt = (int)ceil_div(n, bm == 256 ? 256 : 128);
+  if (bm == 32) kg_go<ExTile32>(s, p, vec);
+  else if (bm == 64) kg_go<ExTile64>(s, p, vec);
+  else if (bm == 128) kg_go<ExTile128>(s, p, vec);
+  else
+    hipLaunchKernelGGL(k_keep_ring, dim3((unsigned)(8 * ceil_div((int64_t)p.nmt * p.nnt, 8)), (unsigned)E,
+                                         (unsigned)pl.splits), dim3(512), 0, s, p);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || pl.splits <= 1) return err;
   const int64_t count = (int64_t)E * m * n;
