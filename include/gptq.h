@@ -276,7 +276,7 @@ gptq_status gptq_repack_act_order(void *stream, const uint32_t *qweight,
  * place. inverse (R int32, slot order): each slot's place. Ids outside
  * [0, E) (padding, dropped tokens) hold no place: their inverse is -1, and
  * rows is -1 from offsets[E] on. 1 <= E <= GPTQ_MAX_EXPERTS, k >= 1,
- * T k < 2^31; T == 0 writes zero offsets. The order does not depend on
+ * T k <= 2^31 - 65536; T == 0 writes zero offsets. The order does not depend on
  * timing. Workspace: gptq_route_workspace_bytes (0 for up to 4096 slots). */
 #define GPTQ_MAX_EXPERTS 1024
 gptq_status gptq_route_workspace_bytes(int64_t T, int64_t k, int64_t E, size_t *bytes);
@@ -326,10 +326,12 @@ gptq_status gptq_combine_grad(void *stream, const void *dY, int32_t dydt, int64_
  * ldx). rows (R int32, as gptq_route writes them; clamped to [0, T)) spares
  * the copy of gptq_dispatch; NULL: X holds the R sorted rows (T >= R).
  * Products of activations and integers are exact in fp32, sums are fp32 in a
- * fixed order, and every group's sum is scaled in fp32: the weights are never
- * rounded. Results are bitwise reproducible. Few rows per expert (R <= 16 E)
- * take a matrix-vector form, in which an infinite activation may give NaN
- * where the sum is infinite.
+ * fixed order, and groups are scaled in fp32: the weights are not rounded.
+ * Results are bitwise reproducible. Few rows per expert (R <= 16 E) take a
+ * matrix-vector form, in which an infinite activation may give NaN where the
+ * sum is infinite. Many (R > 512 E, 4 bits, groups that are multiples of 128)
+ * keep one running sum in units of the current group's scale; there the
+ * weights of a group whose scale is outside 2^-40 .. 2^40 are rounded to bf16.
  *
  * gptq_expert_matmul_grad: dX[p] = dY[p] W_hat_e (dX: R x n, dxdt; dY: R x
  * d_out bf16, row pitch ldy). The scale changes along this sum: with a bf16

@@ -1303,6 +1303,7 @@ struct KgArgs {
   const int32_t* rows; const int32_t* offsets; int E, R;
   int nmt, nnt, splits;
   float* out; int64_t split_stride;   // out[split][e][m][n]
+  int stream;                         // a large G is stored past the caches (268 MB: 230 against 241 us)
 };
 
 template <class TL, bool VEC>
@@ -1344,9 +1345,11 @@ k_keep_grad(KgArgs p) {
   uint32_t rx[DB];
   bool rv[DB];
   const int64_t bc = bok ? bcol : 0;
-  // the source row of a stage is looked up one stage before its loads
-  auto lookup = [&](int st) { return (int)source_row(p.rows, min(k0 + st * kExBK + br, k1 - 1), p.T); };
-  int src = 0;
+  // the source row of a stage is looked up U stages before its loads: loads
+  // return in order, so waiting for a recent one would wait for all of them
+  // (one stage ahead: 34 against 30 us for 16384 rows, 64 x 4096)
+  auto lookup = [&](int st) { return (int)source_row(p.rows, min(k0 + min(st, nst) * kExBK + br, k1 - 1), p.T); };
+  int src[U];
   auto aload = [&](auto S, int st) {
 #pragma unroll
     for (int i = 0; i < PA; ++i) {
@@ -1355,13 +1358,14 @@ k_keep_grad(KgArgs p) {
     }
   };
   auto bload = [&](auto S, int st) {
-    constexpr int B = decltype(S)::value % DB;
-    const ex_u32x4_t* c = reinterpret_cast<const ex_u32x4_t*>(p.codes + src * p.pitch + bc);
+    constexpr int B = decltype(S)::value % DB, Q = decltype(S)::value % U;
+    const int64_t row = src[Q];
+    src[Q] = lookup(st + U);
+    const ex_u32x4_t* c = reinterpret_cast<const ex_u32x4_t*>(p.codes + row * p.pitch + bc);
 #pragma unroll
     for (int i = 0; i < NB / 2; ++i) rb[B][i] = c[i];
-    rx[B] = p.exps[src * (p.pitch / 32) + bc / 32];
+    rx[B] = p.exps[row * (p.pitch / 32) + bc / 32];
     rv[B] = k0 + st * kExBK + br < k1 && bok;
-    src = lookup(min(st + 1, nst - 1));
   };
   auto awrite = [&](auto S) {
 #pragma unroll
@@ -1423,7 +1427,8 @@ k_keep_grad(KgArgs p) {
     awrite(next);
   };
   if (nst > 0) {
-    src = lookup(0);
+#pragma unroll
+    for (int i = 0; i < U; ++i) src[i] = lookup(i);
     for_four([&](auto S) {
       if constexpr (S < DA) aload(S, min((int)S, nst - 1));
       if constexpr (S < DB) bload(S, min((int)S, nst - 1));
@@ -1619,7 +1624,10 @@ k_keep_ring(KgArgs p) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int64_t row = m0 + 128 * wm + 32 * mi + 8 * (r >> 2) + 4 * h + (r & 3);
-        if (row < p.m) out[row * p.n + c] = acc[mi][ni][r];
+        if (row < p.m) {
+          if (p.stream) __builtin_nontemporal_store(acc[mi][ni][r], out + row * p.n + c);
+          else out[row * p.n + c] = acc[mi][ni][r];
+        }
       }
   }
 }
@@ -1809,6 +1817,7 @@ hipError_t launch_keep_grad(hipStream_t s, const KeepGradPlan& pl, const uint16_
   p.splits = pl.splits;
   p.out = pl.splits > 1 ? part : G;
   p.split_stride = (int64_t)E * m * n;
+  p.stream = pl.splits == 1 && p.split_stride * 4 > kStreamBytes;
   const bool vec = bf16_rows_vec(P, ldp, m);
   // the ring's offsets into the codes are 32 bits
   const int bm = pl.bm == 256 && !(vec && T * p.pitch < ((int64_t)1 << 32)) ? 128 : pl.bm;

@@ -1029,7 +1029,7 @@ gptq_status gptq_dequant_matmul_noalloc(void* stream, const void* X, int32_t xdt
 
 namespace {
 
-constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;       // places are int32
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 65536;   // places are int32, and kernels round rows up to tiles
 constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 512;  // of one launch
 
 gptq_status dt_check(int32_t dt) {
@@ -1042,7 +1042,7 @@ bool mis(const void* p, int32_t dt) { return ((uintptr_t)p & (dt == GPTQ_BF16 ? 
 gptq_status slots_check(int64_t T, int64_t n, int64_t k, int64_t R) {
   if (T < 0 || n < 0 || R < 0) return fail(GPTQ_EINVAL, "negative size");
   if (k < 1) return fail(GPTQ_EINVAL, "k must be at least 1");
-  if (T > kMaxRows / k || R > kMaxRows) return fail(GPTQ_EINVAL, "too many slots (T k must be below 2^31)");
+  if (T > kMaxRows / k || R > kMaxRows) return fail(GPTQ_EINVAL, "too many slots (T k may be at most 2^31 - 65536)");
   if (n > 0 && T > kMaxThreads / n) return fail(GPTQ_EINVAL, "T n is too large for one launch");
   if (T > kMaxThreads / 256) return fail(GPTQ_EINVAL, "T is too large for one launch");
   return GPTQ_OK;
@@ -1163,7 +1163,7 @@ gptq_status gptq_expert_matmul(void* stream, const void* X, int32_t xdt, int64_t
   if (st != GPTQ_OK || (st = experts_check(E, offsets)) != GPTQ_OK || (st = dt_check(ydt)) != GPTQ_OK) return st;
   if (xdt != GPTQ_BF16) return fail(GPTQ_EINVAL, "expert_matmul takes bf16 activations");
   if (n < 1 || d_out < 1) return fail(GPTQ_EINVAL, "need n >= 1 and d_out >= 1");
-  if (T < 0 || T > kMaxRows || R > kMaxRows) return fail(GPTQ_EINVAL, "T and R must be in [0, 2^31)");
+  if (T < 0 || T > kMaxRows || R > kMaxRows) return fail(GPTQ_EINVAL, "T and R must be in [0, 2^31 - 65536]");
   if (R == 0) return GPTQ_OK;
   if (rows ? T < 1 : T < R) return fail(GPTQ_EINVAL, "X has too few rows");
   if (ldx < n) return fail(GPTQ_EINVAL, "ldx < n");
@@ -1183,7 +1183,7 @@ gptq_status gptq_expert_matmul_grad(void* stream, const void* dY, int32_t dydt, 
   if (st != GPTQ_OK || (st = experts_check(E, offsets)) != GPTQ_OK || (st = dt_check(dxdt)) != GPTQ_OK) return st;
   if (dydt != GPTQ_BF16) return fail(GPTQ_EINVAL, "expert_matmul_grad takes a bf16 gradient");
   if (n < 1 || d_out < 1) return fail(GPTQ_EINVAL, "need n >= 1 and d_out >= 1");
-  if (R > kMaxRows) return fail(GPTQ_EINVAL, "R must be in [0, 2^31)");
+  if (R > kMaxRows) return fail(GPTQ_EINVAL, "R must be in [0, 2^31 - 65536]");
   if (R == 0) return GPTQ_OK;
   if (ldy < d_out) return fail(GPTQ_EINVAL, "ldy < d_out");
   if (ldx < n) return fail(GPTQ_EINVAL, "ldx < n");
@@ -1229,7 +1229,7 @@ gptq_status gptq_checkpoint_weight_grad(void* stream, const void* P, int32_t pdt
   gptq_status st = gptq_checkpoint_weight_grad_workspace_bytes(R, E, m, n, &need);
   if (st != GPTQ_OK || (st = experts_check(E, offsets)) != GPTQ_OK) return st;
   if (pdt != GPTQ_BF16) return fail(GPTQ_EINVAL, "checkpoint_weight_grad takes a bf16 P");
-  if (T < 0 || T > kMaxRows) return fail(GPTQ_EINVAL, "T must be in [0, 2^31)");
+  if (T < 0 || T > kMaxRows) return fail(GPTQ_EINVAL, "T must be in [0, 2^31 - 65536]");
   if (m == 0 || n == 0) return GPTQ_OK;
   if (!G) return fail(GPTQ_EINVAL, "NULL pointer");
   if (R > 0) {

@@ -403,14 +403,20 @@ def _dense(t, name, dtype, device, shape):
     return t.data_ptr()
 
 
+# The current stream's handle without the Python object around it, where this
+# torch has it (0.1 against 1.1 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _call(device, f, *args):
     """One call on the tensors' device, on its current stream."""
     i = device.index
     if i == torch.cuda.current_device():
-        st = f(torch.cuda.current_stream(i).cuda_stream, *args)
+        st = f(_raw_stream(i), *args)
     else:
         with torch.cuda.device(i):
-            st = f(torch.cuda.current_stream(i).cuda_stream, *args)
+            st = f(_raw_stream(i), *args)
     if st != OK:
         _check(st)
 
