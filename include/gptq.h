@@ -341,17 +341,24 @@ gptq_status gptq_combine_grad(void *stream, const void *dY, int32_t dydt, int64_
  * order.
  *
  * d_out >= 1, n >= 1; R == 0 enqueues nothing. Rows of X and dY may have any
- * alignment (16-byte aligned rows are faster). Asynchronous, no workspace.
+ * alignment (16-byte aligned rows are faster). Asynchronous. Workspace:
+ * gptq_expert_matmul_workspace_bytes / gptq_expert_matmul_grad_workspace_bytes
+ * (fp32 partial results when few tiles split the sum; 0 for most sizes).
  * ("El balance de errores de la inferencia de pocos bits", section 6: decode
  * and prefill are separate regimes of one dequantising product.) */
+gptq_status gptq_expert_matmul_workspace_bytes(int64_t R, int64_t n, int64_t d_out, int64_t E, int32_t bits,
+                                               int32_t group, size_t *bytes);
 gptq_status gptq_expert_matmul(void *stream, const void *X, int32_t xdt, int64_t T, int64_t n, int64_t ldx,
                                const int32_t *rows, int64_t R, const int32_t *offsets, int64_t E,
                                const uint32_t *qweight, const float *scales, const uint8_t *zeros, int64_t d_out,
-                               int32_t bits, int32_t group, void *Y, int32_t ydt, int64_t ldy);
+                               int32_t bits, int32_t group, void *Y, int32_t ydt, int64_t ldy, void *workspace,
+                               size_t ws_bytes);
+gptq_status gptq_expert_matmul_grad_workspace_bytes(int64_t R, int64_t n, int64_t d_out, int64_t E, int32_t bits,
+                                                    int32_t group, size_t *bytes);
 gptq_status gptq_expert_matmul_grad(void *stream, const void *dY, int32_t dydt, int64_t R, int64_t ldy,
                                     const int32_t *offsets, int64_t E, const uint32_t *qweight, const float *scales,
                                     const uint8_t *zeros, int64_t d_out, int64_t n, int32_t bits, int32_t group,
-                                    void *dX, int32_t dxdt, int64_t ldx);
+                                    void *dX, int32_t dxdt, int64_t ldx, void *workspace, size_t ws_bytes);
 
 /* ---- Activations kept in 8 bits for the backward pass -------------------------
  * X (T x n, bf16 or fp32, row pitch ldx) is kept as codes (T x 32 ceil(n / 32)

@@ -27,6 +27,7 @@ typedef __bf16 ex_bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float ex_f32x16_t __attribute__((ext_vector_type(16)));
 typedef float ex_f32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int ex_u32x4_t __attribute__((ext_vector_type(4)));
+typedef ex_u32x4_t ex_u32x4_any_t __attribute__((aligned(2)));
 
 struct Seg {
   int e;        // expert, -1: no such tile
@@ -416,19 +417,32 @@ __device__ __forceinline__ ex_bf16x8_t lds_col_frag(uint32_t at) {
   return __builtin_bit_cast(ex_bf16x8_t, f);
 }
 
-// 8 elements of a bf16 row from column c (limit: the row's length). VEC:
-// 16-byte aligned rows and limit % 8 == 0.
-template <bool VEC>
+// 8 elements of a bf16 row from column c (limit: the row's length). WIDE, at
+// least 8 columns: one 16-byte load at any alignment, moved back to end with
+// the row (end_piece puts that right); otherwise element by element.
+template <bool WIDE>
 __device__ __forceinline__ ex_u32x4_t load_piece(const uint16_t* __restrict__ row, int64_t c, int64_t limit) {
-  if constexpr (VEC) {   // one load in any case, so that the loads of a stage can be counted
-    const void* src = c < limit ? static_cast<const void*>(row + c) : kZeroChunk;
-    return *reinterpret_cast<const ex_u32x4_t*>(src);
+  if constexpr (WIDE) {
+    return *reinterpret_cast<const ex_u32x4_any_t*>(row + min(c, limit - 8));
   } else {
     uint32_t v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = c + i < limit ? row[c + i] : 0u;
     return (ex_u32x4_t){v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
   }
+}
+
+// A piece that was loaded `over` columns early: those columns off, zeros
+// behind (over <= 0: as it is).
+__device__ __forceinline__ ex_u32x4_t end_piece(ex_u32x4_t v, int64_t over) {
+  if (over <= 0) return v;
+  if (over >= 8) return (ex_u32x4_t){0u, 0u, 0u, 0u};
+  const int o = (int)over;
+  if (o & 4) v = (ex_u32x4_t){v[2], v[3], 0u, 0u};
+  if (o & 2) v = (ex_u32x4_t){v[1], v[2], v[3], 0u};
+  if (o & 1)
+    v = (ex_u32x4_t){v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+  return v;
 }
 
 // The 8 codes of w times f, minus z f, rounded once: codes - z + 128 as
@@ -537,6 +551,8 @@ struct ExArgs {
   int64_t d_out, n; int group;
   void* Y; int ybf16; int64_t ldy;
   int nrt, nct;
+  int per_split;                              // stages of one of the gridDim.y parts of K
+  int64_t split_stride;                       // bytes from part to part of Y (fp32 then)
 };
 
 template <int B>
@@ -571,10 +587,10 @@ __device__ __forceinline__ void run_stages(int nst, F&& stage) {
 
 // ---- forward: K = n. The codes minus the zero point are exact in bf16, the
 // group's sum is scaled once in fp32 (tot += s acc), as in the one-layer
-// product. GS: stages per group when fixed (groups of 64 and 128: the first
-// product of a group starts from zero, no test inside a stage), 0: groups
-// of any number of 32-code chunks, tested after every chunk.
-template <int BITS, class TL, int GS, bool VEC>
+// product. G128: groups of 128, two stages each (the first product of a group
+// starts from zero, no test inside a stage); otherwise groups of any number of
+// 32-code chunks, tested after every chunk.
+template <int BITS, class TL, bool G128, bool WIDE>
 __global__ void __launch_bounds__(TL::THREADS, 512 / TL::THREADS)
 k_expert_mm(ExArgs p) {
   constexpr int MI = TL::MI, NI = TL::NI, BM = TL::BM, PA = TL::PA, NB = TL::NB, THREADS = TL::THREADS;
@@ -587,7 +603,8 @@ k_expert_mm(ExArgs p) {
   const int wm = wave % TL::WM, wn = wave / TL::WM, h = lane >> 5, li = lane & 31;
   const int64_t o0 = (int64_t)ct * TL::BN;
   const int64_t ngroups = p.n / p.group;
-  const int cpg = p.group / 32, nchunks = (int)(p.n / 32), nst = (nchunks + 1) / 2;
+  const int cpg = p.group / 32, nchunks = (int)(p.n / 32);
+  const int s0 = blockIdx.y * p.per_split, nst = min((nchunks + 1) / 2 - s0, p.per_split);   // this part's stages
   const uint32_t lds = lds_addr(smem);
 
   // staging: piece tid % 8 of rows tid / 8 + (THREADS / 8) i of A; units
@@ -612,15 +629,20 @@ k_expert_mm(ExArgs p) {
   uint32_t rz[DB];
   auto aload = [&](auto S, int st) {
 #pragma unroll
-    for (int i = 0; i < PA; ++i) ra[S % DA][i] = load_piece<VEC>(arow[i], (int64_t)st * kExBK + 8 * ac, p.n);
+    for (int i = 0; i < PA; ++i) ra[S % DA][i] = load_piece<WIDE>(arow[i], (int64_t)(s0 + st) * kExBK + 8 * ac, p.n);
   };
   auto bload = [&](auto S, int st) {
-    const int c = min(2 * st + bu / 4, nchunks - 1);      // a chunk past the end meets zeros of A
+    const int c = min(2 * (s0 + st) + bu / 4, nchunks - 1);      // a chunk past the end meets zeros of A
     rb[S % DB].load(qrow, 4 * c + bu % 4);
-    const int g = GS == 1 ? st : (GS == 2 ? st >> 1 : c / cpg);
+    const int g = G128 ? (s0 + st) >> 1 : c / cpg;
     rz[S % DB] = zrow[g];
   };
-  auto awrite = [&](auto S) {
+  auto awrite = [&](auto S, int st) {
+    if (WIDE && (int64_t)(s0 + st + 1) * kExBK > p.n) {
+      const int64_t over = (int64_t)(s0 + st) * kExBK + 8 * ac - (p.n - 8);
+#pragma unroll
+      for (int i = 0; i < PA; ++i) ra[S % DA][i] = end_piece(ra[S % DA][i], over);
+    }
 #pragma unroll
     for (int i = 0; i < PA; ++i) lds_write(aw + (S % 2) * BUF + i * (AR * 128), ra[S % DA][i]);
   };
@@ -651,10 +673,10 @@ k_expert_mm(ExArgs p) {
   ex_f32x16_t acc[MI][NI] = {}, tot[MI][NI] = {};
   const ex_f32x16_t zero = {};
   float sc[NI];
-#pragma unroll
-  for (int ni = 0; ni < NI; ++ni) sc[ni] = srow[ni][0];
   int cin = 0;
-  int64_t g = 0;
+  int64_t g = (int64_t)s0 * kExBK / p.group;               // a part starts with a group
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) sc[ni] = srow[ni][g];
   auto flush = [&]() {
     ++g;
 #pragma unroll
@@ -690,9 +712,9 @@ k_expert_mm(ExArgs p) {
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni)
           acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              fa[kk & 1][mi], fb[kk & 1][ni], (GS == 1 || (GS == 2 && b == 0)) && kk == 0 ? zero : acc[mi][ni], 0, 0, 0);
+              fa[kk & 1][mi], fb[kk & 1][ni], G128 && b == 0 && kk == 0 ? zero : acc[mi][ni], 0, 0, 0);
       bwrite(next, KK);
-      if (GS == 0 && (kk & 1) == 1 && ++cin == cpg && g < ngroups) {   // the group is complete
+      if (!G128 && (kk & 1) == 1 && ++cin == cpg && g < ngroups) {   // the group is complete
         flush();
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi)
@@ -701,16 +723,17 @@ k_expert_mm(ExArgs p) {
         cin = 0;
       }
     });
-    awrite(next);
-    if (GS == 1 || (GS == 2 && b == 1)) flush();
+    awrite(next, st + 1);
+    if (G128 && b == 1) flush();
   };
   for_four([&](auto S) {
     if constexpr (S < DA) aload(S, min((int)S, nst - 1));
     if constexpr (S < DB) bload(S, min((int)S, nst - 1));
   });
-  awrite(ex_const<0>{});
+  awrite(ex_const<0>{}, 0);
   for_four([&](auto KK) { bwrite(ex_const<0>{}, KK); });
   run_stages<U>(nst, stage);
+  void* Y = static_cast<char*>(p.Y) + blockIdx.y * p.split_stride;
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) {
     const int64_t o = o0 + 32 * (NI * wn + ni) + li;
@@ -720,7 +743,7 @@ k_expert_mm(ExArgs p) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int row = sg.row0 + 32 * (MI * wm + mi) + 8 * (r >> 2) + 4 * h + (r & 3);
-        if (row < sg.hi) store_out(p.Y, p.ybf16, (int64_t)row * p.ldy + o, tot[mi][ni][r]);
+        if (row < sg.hi) store_out(Y, p.ybf16, (int64_t)row * p.ldy + o, tot[mi][ni][r]);
       }
   }
 }
@@ -731,7 +754,7 @@ k_expert_mm(ExArgs p) {
 // weight, which adds to the sum's error what the bf16 rounding of the result
 // adds again). For results kept in fp32 the weight goes as NP = 3 bf16 pieces
 // and three products: 24 bits, what its fp32 value holds.
-template <int BITS, int NP, class TL, bool VEC>
+template <int BITS, int NP, class TL, bool WIDE>
 __global__ void __launch_bounds__(TL::THREADS, NP > 1 ? 1 : 512 / TL::THREADS)
 k_expert_mm_grad(ExArgs p) {
   constexpr int MI = TL::MI, NI = TL::NI, BM = TL::BM, BN = TL::BN, PA = TL::PA, NB = TL::NB, THREADS = TL::THREADS;
@@ -745,7 +768,7 @@ k_expert_mm_grad(ExArgs p) {
   const int64_t c0 = (int64_t)ct * TL::BN;
   const int64_t ngroups = p.n / p.group;
   const int nchunks = (int)(p.n / 32);
-  const int nst = (int)ceil_div(p.d_out, kExBK);
+  const int s0 = blockIdx.y * p.per_split, nst = min((int)ceil_div(p.d_out, kExBK) - s0, p.per_split);
   const uint32_t lds = lds_addr(smem);
 
   // staging: A as in the forward product; units NB (tid % BU) .. of output
@@ -774,18 +797,23 @@ k_expert_mm_grad(ExArgs p) {
   bool rv[DB];
   auto aload = [&](auto S, int st) {
 #pragma unroll
-    for (int i = 0; i < PA; ++i) ra[S % DA][i] = load_piece<VEC>(arow[i], (int64_t)st * kExBK + 8 * ac, p.d_out);
+    for (int i = 0; i < PA; ++i) ra[S % DA][i] = load_piece<WIDE>(arow[i], (int64_t)(s0 + st) * kExBK + 8 * ac, p.d_out);
   };
   auto bload = [&](auto S, int st) {
     constexpr int B = decltype(S)::value % DB;
-    const int64_t o = (int64_t)st * kExBK + br;
+    const int64_t o = (int64_t)(s0 + st) * kExBK + br;
     const int64_t oc = ebase + min(o, p.d_out - 1);
     rb[B].load(p.qw + oc * nchunks * BITS, uc);
     rs[B] = p.scales[oc * ngroups + gi];
     rz[B] = p.zeros[oc * ngroups + gi];
     rv[B] = cok && o < p.d_out;                              // outputs past d_out: weights of 0
   };
-  auto awrite = [&](auto S) {
+  auto awrite = [&](auto S, int st) {
+    if (WIDE && (int64_t)(s0 + st + 1) * kExBK > p.d_out) {
+      const int64_t over = (int64_t)(s0 + st) * kExBK + 8 * ac - (p.d_out - 8);
+#pragma unroll
+      for (int i = 0; i < PA; ++i) ra[S % DA][i] = end_piece(ra[S % DA][i], over);
+    }
 #pragma unroll
     for (int i = 0; i < PA; ++i) lds_write(aw + (S % 2) * BUF + i * (AR * 128), ra[S % DA][i]);
   };
@@ -856,15 +884,16 @@ k_expert_mm_grad(ExArgs p) {
             acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk & 1][mi], fb[kk & 1][q][ni], acc[mi][ni], 0, 0, 0);
       bwrite(next, KK);
     });
-    awrite(next);
+    awrite(next, st + 1);
   };
   for_four([&](auto S) {
     if constexpr (S < DA) aload(S, min((int)S, nst - 1));
     if constexpr (S < DB) bload(S, min((int)S, nst - 1));
   });
-  awrite(ex_const<0>{});
+  awrite(ex_const<0>{}, 0);
   for_four([&](auto KK) { bwrite(ex_const<0>{}, KK); });
   run_stages<U>(nst, stage);
+  void* Y = static_cast<char*>(p.Y) + blockIdx.y * p.split_stride;
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) {
     const int64_t c = c0 + 32 * (NI * wn + ni) + li;
@@ -874,7 +903,7 @@ k_expert_mm_grad(ExArgs p) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int row = sg.row0 + 32 * (MI * wm + mi) + 8 * (r >> 2) + 4 * h + (r & 3);
-        if (row < sg.hi) store_out(p.Y, p.ybf16, (int64_t)row * p.ldy + c, acc[mi][ni][r]);
+        if (row < sg.hi) store_out(Y, p.ybf16, (int64_t)row * p.ldy + c, acc[mi][ni][r]);
       }
   }
 }
@@ -1291,6 +1320,19 @@ k_expert_ring_grad(ExArgs p) {
   }
 }
 
+// Y[row][c] = the parts' sum, in order, for the rows of the segments.
+__global__ void __launch_bounds__(256)
+k_expert_sum(const float* __restrict__ part, int splits, int R, uint32_t cols, const int32_t* __restrict__ offsets, int E,
+             void* __restrict__ Y, int ybf16, int64_t ldy) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, count = (int64_t)R * cols;
+  if (i >= count) return;
+  const int64_t row = i / cols;
+  if (offsets && (row < offsets[0] || row >= offsets[E])) return;
+  float v = part[i];
+  for (int s = 1; s < splits; ++s) v += part[s * count + i];
+  store_out(Y, ybf16, row * ldy + (i - row * cols), v);
+}
+
 // ---- weight gradient: K = a segment's rows. Both operands have K down their
 // rows. The kept values have at most 7 significant bits, so they are exact in
 // bf16, products are exact and the sums fp32. A segment's rows are split over
@@ -1306,7 +1348,7 @@ struct KgArgs {
   int stream;                         // a large G is stored past the caches (268 MB: 230 against 241 us)
 };
 
-template <class TL, bool VEC>
+template <class TL, bool WIDE>
 __global__ void __launch_bounds__(TL::THREADS, 512 / TL::THREADS)
 k_keep_grad(KgArgs p) {
   constexpr int MI = TL::MI, NI = TL::NI, BM = TL::BM, BN = TL::BN, PA = TL::PA, NB = TL::NB, THREADS = TL::THREADS;
@@ -1350,11 +1392,20 @@ k_keep_grad(KgArgs p) {
   // (one stage ahead: 34 against 30 us for 16384 rows, 64 x 4096)
   auto lookup = [&](int st) { return (int)source_row(p.rows, min(k0 + min(st, nst) * kExBK + br, k1 - 1), p.T); };
   int src[U];
+  // Columns past m are read along with a row where they are in bounds (their
+  // results are not stored); at the end of P the piece is moved back.
+  const int64_t pend = (int64_t)(p.R - 1) * p.ldp + p.m - 8;
   auto aload = [&](auto S, int st) {
 #pragma unroll
     for (int i = 0; i < PA; ++i) {
       const int r = k0 + st * kExBK + ar + AR * i;        // rows past the part: zeros on both sides
-      ra[S % DA][i] = load_piece<VEC>(p.P + (int64_t)min(r, k1 - 1) * p.ldp, m0 + 8 * ap, r < k1 ? p.m : 0);
+      if constexpr (WIDE) {
+        const int64_t at = min((int64_t)r * p.ldp + m0 + 8 * ap, pend);
+        const void* src = r < k1 ? static_cast<const void*>(p.P + at) : kZeroChunk;
+        ra[S % DA][i] = *static_cast<const ex_u32x4_any_t*>(src);
+      } else {
+        ra[S % DA][i] = load_piece<false>(p.P + (int64_t)min(r, k1 - 1) * p.ldp, m0 + 8 * ap, r < k1 ? p.m : 0);
+      }
     }
   };
   auto bload = [&](auto S, int st) {
@@ -1367,7 +1418,14 @@ k_keep_grad(KgArgs p) {
     rx[B] = p.exps[row * (p.pitch / 32) + bc / 32];
     rv[B] = k0 + st * kExBK + br < k1 && bok;
   };
-  auto awrite = [&](auto S) {
+  auto awrite = [&](auto S, int st) {
+    if (WIDE && k0 + (st + 1) * kExBK >= p.R) {           // the stage may hold the last row
+#pragma unroll
+      for (int i = 0; i < PA; ++i) {
+        const int r = k0 + st * kExBK + ar + AR * i;
+        if (r < k1) ra[S % DA][i] = end_piece(ra[S % DA][i], (int64_t)r * p.ldp + m0 + 8 * ap - pend);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < PA; ++i) lds_write(aw + (S % 2) * BUF + i * (AR * 2 * AW), ra[S % DA][i]);
   };
@@ -1424,7 +1482,7 @@ k_keep_grad(KgArgs p) {
           acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk & 1][mi], fb[kk & 1][ni], acc[mi][ni], 0, 0, 0);
       bwrite(next, KK);
     });
-    awrite(next);
+    awrite(next, st + 1);
   };
   if (nst > 0) {
 #pragma unroll
@@ -1433,7 +1491,7 @@ k_keep_grad(KgArgs p) {
       if constexpr (S < DA) aload(S, min((int)S, nst - 1));
       if constexpr (S < DB) bload(S, min((int)S, nst - 1));
     });
-    awrite(ex_const<0>{});
+    awrite(ex_const<0>{}, 0);
     for_four([&](auto KK) { bwrite(ex_const<0>{}, KK); });
   }
   run_stages<U>(nst, stage);
@@ -1649,20 +1707,48 @@ static bool bf16_rows_vec(const void* p, int64_t ld, int64_t cols) {
 }
 
 // The ring kernels: 4 bits, whole blocks (forward) or stages and a bf16 result
-// (gradient), and offsets from the bases that fit 32 bits.
+// (gradient), offsets from the bases that fit 32 bits, and tiles for half of
+// the chip at least (fewer are better split along K).
 static bool ring_fits(const ExpertArgs& a, int grad) {
   const int64_t lim = (int64_t)1 << 32;
   if (a.bits != 4 || a.d_out * (a.n / 2) >= lim || a.T * a.lda * 2 >= lim) return false;
-  return grad ? a.y_bf16 && a.d_out % 32 == 0 : a.group % 128 == 0;
+  if (!(grad ? a.y_bf16 && a.d_out % 32 == 0 : a.group % 128 == 0)) return false;
+  return ceil_div(a.R, 256) * ceil_div(grad ? a.n : a.d_out, 256) >= 128;
 }
 
 // Rows of a tile: 16 is the matrix-vector form, 256 the ring kernel.
 static int expert_bm(const ExpertArgs& a, int grad) {
   const int64_t avg = ceil_div(a.R, a.E);
-  if (!bf16_rows_vec(a.A, a.lda, grad ? a.d_out : a.n)) return 64;
-  if (!grad && avg <= 16) return 16;
-  if (avg <= 64) return 64;
-  return avg > 512 && ring_fits(a, grad) ? 256 : 128;
+  const bool vec = bf16_rows_vec(a.A, a.lda, grad ? a.d_out : a.n);
+  if (!grad && avg <= 16 && vec) return 16;
+  if (avg <= 64 || (grad && a.d_out < 8)) return 64;
+  return vec && avg > 512 && ring_fits(a, grad) ? 256 : 128;
+}
+
+// Parts of K. Few tiles leave most of the chip idle and make every workgroup
+// walk all of K: then K is split until there are two workgroups per CU, at
+// least four stages each (24 rows of 5612 outputs, gradient of 512 columns:
+// 185 us in one part, SSS in parts). The parts meet in fp32 in the workspace.
+// From the sizes alone, so that the workspace's size is known before the call.
+ExpertSplit expert_split(int64_t R, int E, int64_t n, int64_t d_out, int group, int grad) {
+  ExpertSplit sp = {1, 0, 0};
+  const int64_t K = grad ? d_out : n, cols = grad ? n : d_out;
+  const int64_t nst = ceil_div(K, kExBK);
+  sp.per = (int)nst;
+  const int64_t avg = ceil_div(R, E);
+  if (R <= 0 || (!grad && avg <= 16)) return sp;           // the matrix-vector form splits inside
+  const int bm = avg <= 64 ? 64 : 128;
+  const int64_t tiles = std::min<int64_t>(R, ceil_div(R, bm) + (E - 1) / 2) * ceil_div(cols, 128);
+  int64_t unit = 1;                                        // stages between starts of a group
+  if (!grad)
+    while (unit * kExBK % group != 0) ++unit;
+  int64_t s = std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), nst / 4);
+  if (s <= 1) return sp;
+  const int64_t per = ceil_div(ceil_div(nst, s), unit) * unit;
+  sp.per = (int)per;
+  sp.splits = (int)ceil_div(nst, per);
+  sp.part_bytes = sp.splits > 1 ? (size_t)sp.splits * R * cols * sizeof(float) : 0;
+  return sp;
 }
 
 int64_t expert_grid(const ExpertArgs& a, int grad) {
@@ -1684,6 +1770,8 @@ static void mv_go(hipStream_t s, const ExpertArgs& a) {
                        a.offsets, a.E, a.R, a.qw, a.scales, a.zeros, a.d_out, a.group, a.Y, a.y_bf16, a.ldy);
 }
 
+static dim3 tile_grid(int nr, int nc) { return dim3((unsigned)(8 * ceil_div((int64_t)nr * nc, 8))); }
+
 static ExArgs ex_args(const ExpertArgs& a, int BM, int BN, int64_t cols) {
   ExArgs p;
   p.A = static_cast<const uint16_t*>(a.A);
@@ -1704,31 +1792,52 @@ static ExArgs ex_args(const ExpertArgs& a, int BM, int BN, int64_t cols) {
   p.ldy = a.ldy;
   p.nrt = (int)row_tiles(a.R, a.E, BM);
   p.nct = (int)ceil_div(cols, BN);
+  p.per_split = 0;
+  p.split_stride = 0;
   return p;
 }
 
-static dim3 tile_grid(int nr, int nc) { return dim3((unsigned)(8 * ceil_div((int64_t)nr * nc, 8))); }
-
-template <int BITS, class TL, int GS, bool VEC>
-static void mm_go(hipStream_t s, const ExpertArgs& a) {
-  const ExArgs p = ex_args(a, TL::BM, TL::BN, a.d_out);
-  hipLaunchKernelGGL((k_expert_mm<BITS, TL, GS, VEC>), tile_grid(p.nrt, p.nct), dim3(TL::THREADS), 0, s, p);
+// The tile kernels write their parts of K into the workspace when there are several.
+template <class F>
+static void split_go(hipStream_t s, const ExpertArgs& a, ExArgs p, int64_t cols, int grad, F&& launch) {
+  const ExpertSplit sp = expert_split(a.R, a.E, a.n, a.d_out, a.group, grad);
+  p.per_split = sp.per;
+  dim3 grid = tile_grid(p.nrt, p.nct);
+  grid.y = (unsigned)sp.splits;
+  if (sp.splits > 1) {
+    p.Y = a.part;
+    p.ybf16 = 0;
+    p.ldy = cols;
+    p.split_stride = (int64_t)a.R * cols * (int64_t)sizeof(float);
+  }
+  launch(grid, p);
+  if (sp.splits > 1)
+    hipLaunchKernelGGL(k_expert_sum, dim3((unsigned)ceil_div((int64_t)a.R * cols, 256)), dim3(256), 0, s,
+                       static_cast<const float*>(a.part), sp.splits, a.R, (uint32_t)cols, a.offsets, a.E, a.Y, a.y_bf16,
+                       a.ldy);
 }
 
-// Fixed group lengths are worth their own code at 4 bits, the common width.
+template <int BITS, class TL, bool G128>
+static void mm_go(hipStream_t s, const ExpertArgs& a) {
+  split_go(s, a, ex_args(a, TL::BM, TL::BN, a.d_out), a.d_out, 0, [&](dim3 grid, const ExArgs& p) {
+    hipLaunchKernelGGL((k_expert_mm<BITS, TL, G128, true>), grid, dim3(TL::THREADS), 0, s, p);
+  });
+}
+
+// Groups of 128 are worth their own code at 4 bits, the common layer.
 template <int BITS, class TL>
 static void mm_group(hipStream_t s, const ExpertArgs& a) {
   if constexpr (BITS == 4) {
-    if (a.group == 64) return mm_go<4, TL, 1, true>(s, a);
-    if (a.group == 128) return mm_go<4, TL, 2, true>(s, a);
+    if (a.group == 128) return mm_go<4, TL, true>(s, a);
   }
-  mm_go<BITS, TL, 0, true>(s, a);
+  mm_go<BITS, TL, false>(s, a);
 }
 
-template <int BITS, int NP, class TL, bool VEC>
+template <int BITS, int NP, class TL, bool WIDE>
 static void grad_go(hipStream_t s, const ExpertArgs& a) {
-  const ExArgs p = ex_args(a, TL::BM, TL::BN, a.n);
-  hipLaunchKernelGGL((k_expert_mm_grad<BITS, NP, TL, VEC>), tile_grid(p.nrt, p.nct), dim3(TL::THREADS), 0, s, p);
+  split_go(s, a, ex_args(a, TL::BM, TL::BN, a.n), a.n, 1, [&](dim3 grid, const ExArgs& p) {
+    hipLaunchKernelGGL((k_expert_mm_grad<BITS, NP, TL, WIDE>), grid, dim3(TL::THREADS), 0, s, p);
+  });
 }
 
 static void ring_go(hipStream_t s, const ExpertArgs& a, int grad) {
@@ -1738,7 +1847,6 @@ static void ring_go(hipStream_t s, const ExpertArgs& a, int grad) {
 
 template <int BITS>
 static void fwd_bits(hipStream_t s, const ExpertArgs& a) {
-  if (!bf16_rows_vec(a.A, a.lda, a.n)) return mm_go<BITS, ExTile64, 0, false>(s, a);
   const int bm = expert_bm(a, 0);
   if (bm == 16) mv_go<BITS>(s, a);
   else if (bm == 256) ring_go(s, a, 0);
@@ -1749,7 +1857,7 @@ static void fwd_bits(hipStream_t s, const ExpertArgs& a) {
 template <int BITS>
 static void grad_bits(hipStream_t s, const ExpertArgs& a) {
   const int bm = expert_bm(a, 1);
-  if (!bf16_rows_vec(a.A, a.lda, a.d_out)) {
+  if (a.d_out < 8) {
     if (a.y_bf16) grad_go<BITS, 1, ExTile64, false>(s, a);
     else grad_go<BITS, 3, ExTile64, false>(s, a);
   } else if (a.y_bf16) {
@@ -1791,9 +1899,9 @@ KeepGradPlan keep_grad_plan(int64_t R, int E, int64_t m, int64_t n) {
 }
 
 template <class TL>
-static void kg_go(hipStream_t s, const KgArgs& p, bool vec) {
+static void kg_go(hipStream_t s, const KgArgs& p) {
   const dim3 grid((unsigned)(8 * ceil_div((int64_t)p.nmt * p.nnt, 8)), (unsigned)p.E, (unsigned)p.splits);
-  if (vec) hipLaunchKernelGGL((k_keep_grad<TL, true>), grid, dim3(TL::THREADS), 0, s, p);
+  if (p.m >= 8) hipLaunchKernelGGL((k_keep_grad<TL, true>), grid, dim3(TL::THREADS), 0, s, p);
   else hipLaunchKernelGGL((k_keep_grad<TL, false>), grid, dim3(TL::THREADS), 0, s, p);
 }
 
@@ -1823,9 +1931,9 @@ hipError_t launch_keep_grad(hipStream_t s, const KeepGradPlan& pl, const uint16_
   const int bm = pl.bm == 256 && !(vec && T * p.pitch < ((int64_t)1 << 32)) ? 128 : pl.bm;
   p.nmt = (int)ceil_div(m, bm);
   p.nnt = (int)ceil_div(n, bm == 256 ? 256 : 128);
-  if (bm == 32) kg_go<ExTile32>(s, p, vec);
-  else if (bm == 64) kg_go<ExTile64>(s, p, vec);
-  else if (bm == 128) kg_go<ExTile128>(s, p, vec);
+  if (bm == 32) kg_go<ExTile32>(s, p);
+  else if (bm == 64) kg_go<ExTile64>(s, p);
+  else if (bm == 128) kg_go<ExTile128>(s, p);
   else
     hipLaunchKernelGGL(k_keep_ring, dim3((unsigned)(8 * ceil_div((int64_t)p.nmt * p.nnt, 8)), (unsigned)E,
                                          (unsigned)pl.splits), dim3(512), 0, s, p);

@@ -1060,8 +1060,7 @@ gptq_status expert_weights_check(const ExpertArgs& a, int grad) {
   if (mis(a.A, GPTQ_BF16) || mis(a.Y, a.y_bf16 ? GPTQ_BF16 : GPTQ_F32))
     return fail(GPTQ_EINVAL, "a matrix is not aligned to its elements");
   if (((uintptr_t)a.qw & 15) != 0) return fail(GPTQ_EINVAL, "qweight must be 16-byte aligned");
-  if (a.d_out > kMaxRows || a.n > kMaxRows) return fail(GPTQ_EINVAL, "d_out or n too large");
-  if (expert_grid(a, grad) > kMaxThreads / 256) return fail(GPTQ_EINVAL, "product too large for one launch");
+  if (expert_grid(a, grad) > kMaxThreads / 512) return fail(GPTQ_EINVAL, "product too large for one launch");
   return GPTQ_OK;
 }
 
@@ -1155,22 +1154,51 @@ gptq_status gptq_combine_grad(void* stream, const void* dY, int32_t dydt, int64_
   return GPTQ_OK;
 }
 
+static gptq_status expert_sizes(int64_t R, int64_t n, int64_t d_out, int64_t E, int32_t bits, int32_t group) {
+  const gptq_status st = dq_check(R, n, d_out, bits, group);
+  if (st != GPTQ_OK) return st;
+  if (E < 1 || E > GPTQ_MAX_EXPERTS) return fail(GPTQ_EINVAL, "need 1 <= E <= GPTQ_MAX_EXPERTS");
+  if (n < 1 || d_out < 1) return fail(GPTQ_EINVAL, "need n >= 1 and d_out >= 1");
+  if (R > kMaxRows || n > kMaxRows || d_out > kMaxRows) return fail(GPTQ_EINVAL, "R, n and d_out may be at most 2^31 - 65536");
+  return GPTQ_OK;
+}
+
+static gptq_status expert_workspace(int64_t R, int64_t n, int64_t d_out, int64_t E, int32_t bits, int32_t group,
+                                    int grad, size_t* bytes) {
+  if (!bytes) return fail(GPTQ_EINVAL, "bytes is NULL");
+  const gptq_status st = expert_sizes(R, n, d_out, E, bits, group);
+  if (st != GPTQ_OK) return st;
+  *bytes = (expert_split(R, (int)E, n, d_out, group, grad).part_bytes + 255) / 256 * 256;
+  return GPTQ_OK;
+}
+
+gptq_status gptq_expert_matmul_workspace_bytes(int64_t R, int64_t n, int64_t d_out, int64_t E, int32_t bits,
+                                               int32_t group, size_t* bytes) {
+  return expert_workspace(R, n, d_out, E, bits, group, 0, bytes);
+}
+
+gptq_status gptq_expert_matmul_grad_workspace_bytes(int64_t R, int64_t n, int64_t d_out, int64_t E, int32_t bits,
+                                                    int32_t group, size_t* bytes) {
+  return expert_workspace(R, n, d_out, E, bits, group, 1, bytes);
+}
+
 gptq_status gptq_expert_matmul(void* stream, const void* X, int32_t xdt, int64_t T, int64_t n, int64_t ldx,
                                const int32_t* rows, int64_t R, const int32_t* offsets, int64_t E,
                                const uint32_t* qweight, const float* scales, const uint8_t* zeros, int64_t d_out,
-                               int32_t bits, int32_t group, void* Y, int32_t ydt, int64_t ldy) {
-  gptq_status st = dq_check(R, n, d_out, bits, group);
+                               int32_t bits, int32_t group, void* Y, int32_t ydt, int64_t ldy, void* workspace,
+                               size_t ws_bytes) {
+  gptq_status st = expert_sizes(R, n, d_out, E, bits, group);
   if (st != GPTQ_OK || (st = experts_check(E, offsets)) != GPTQ_OK || (st = dt_check(ydt)) != GPTQ_OK) return st;
   if (xdt != GPTQ_BF16) return fail(GPTQ_EINVAL, "expert_matmul takes bf16 activations");
-  if (n < 1 || d_out < 1) return fail(GPTQ_EINVAL, "need n >= 1 and d_out >= 1");
-  if (T < 0 || T > kMaxRows || R > kMaxRows) return fail(GPTQ_EINVAL, "T and R must be in [0, 2^31 - 65536]");
+  if (T < 0 || T > kMaxRows) return fail(GPTQ_EINVAL, "T must be in [0, 2^31 - 65536]");
   if (R == 0) return GPTQ_OK;
   if (rows ? T < 1 : T < R) return fail(GPTQ_EINVAL, "X has too few rows");
   if (ldx < n) return fail(GPTQ_EINVAL, "ldx < n");
   if (ldy < d_out) return fail(GPTQ_EINVAL, "ldy < d_out");
   const ExpertArgs a = {X, ldx, rows, (int)T, offsets, (int)E, (int)R, qweight, scales, zeros,
-                        d_out, n, bits, group, Y, ydt == GPTQ_BF16, ldy};
+                        d_out, n, bits, group, Y, ydt == GPTQ_BF16, ldy, workspace};
   if ((st = expert_weights_check(a, 0)) != GPTQ_OK) return st;
+  if ((st = check_ws(workspace, ws_bytes, expert_split(R, (int)E, n, d_out, group, 0).part_bytes)) != GPTQ_OK) return st;
   HIP_TRY(launch_expert_mm((hipStream_t)stream, a), "expert_matmul");
   return GPTQ_OK;
 }
@@ -1178,18 +1206,17 @@ gptq_status gptq_expert_matmul(void* stream, const void* X, int32_t xdt, int64_t
 gptq_status gptq_expert_matmul_grad(void* stream, const void* dY, int32_t dydt, int64_t R, int64_t ldy,
                                     const int32_t* offsets, int64_t E, const uint32_t* qweight, const float* scales,
                                     const uint8_t* zeros, int64_t d_out, int64_t n, int32_t bits, int32_t group,
-                                    void* dX, int32_t dxdt, int64_t ldx) {
-  gptq_status st = dq_check(R, n, d_out, bits, group);
+                                    void* dX, int32_t dxdt, int64_t ldx, void* workspace, size_t ws_bytes) {
+  gptq_status st = expert_sizes(R, n, d_out, E, bits, group);
   if (st != GPTQ_OK || (st = experts_check(E, offsets)) != GPTQ_OK || (st = dt_check(dxdt)) != GPTQ_OK) return st;
   if (dydt != GPTQ_BF16) return fail(GPTQ_EINVAL, "expert_matmul_grad takes a bf16 gradient");
-  if (n < 1 || d_out < 1) return fail(GPTQ_EINVAL, "need n >= 1 and d_out >= 1");
-  if (R > kMaxRows) return fail(GPTQ_EINVAL, "R must be in [0, 2^31 - 65536]");
   if (R == 0) return GPTQ_OK;
   if (ldy < d_out) return fail(GPTQ_EINVAL, "ldy < d_out");
   if (ldx < n) return fail(GPTQ_EINVAL, "ldx < n");
   const ExpertArgs a = {dY, ldy, nullptr, (int)R, offsets, (int)E, (int)R, qweight, scales, zeros,
-                        d_out, n, bits, group, dX, dxdt == GPTQ_BF16, ldx};
+                        d_out, n, bits, group, dX, dxdt == GPTQ_BF16, ldx, workspace};
   if ((st = expert_weights_check(a, 1)) != GPTQ_OK) return st;
+  if ((st = check_ws(workspace, ws_bytes, expert_split(R, (int)E, n, d_out, group, 1).part_bytes)) != GPTQ_OK) return st;
   HIP_TRY(launch_expert_mm_grad((hipStream_t)stream, a), "expert_matmul_grad");
   return GPTQ_OK;
 }

@@ -86,9 +86,13 @@ def load():
         "gptq_combine_grad": [c_vp, c_vp, ctypes.c_int32, c_i64, c_vp, ctypes.c_int32, c_i64, c_i64, c_vp, c_vp,
                               c_i64, c_i64, c_i64, c_vp, ctypes.c_int32, c_i64, c_vp],
         "gptq_expert_matmul": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp,
-                               c_vp, c_i64, ctypes.c_int32, ctypes.c_int32, c_vp, ctypes.c_int32, c_i64],
+                               c_vp, c_i64, ctypes.c_int32, ctypes.c_int32, c_vp, ctypes.c_int32, c_i64, c_vp, c_sz],
+        "gptq_expert_matmul_workspace_bytes": [c_i64, c_i64, c_i64, c_i64, ctypes.c_int32, ctypes.c_int32,
+                                               ctypes.POINTER(c_sz)],
         "gptq_expert_matmul_grad": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_i64,
-                                    c_i64, ctypes.c_int32, ctypes.c_int32, c_vp, ctypes.c_int32, c_i64],
+                                    c_i64, ctypes.c_int32, ctypes.c_int32, c_vp, ctypes.c_int32, c_i64, c_vp, c_sz],
+        "gptq_expert_matmul_grad_workspace_bytes": [c_i64, c_i64, c_i64, c_i64, ctypes.c_int32, ctypes.c_int32,
+                                                    ctypes.POINTER(c_sz)],
         "gptq_checkpoint_save": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_vp],
         "gptq_checkpoint_restore": [c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, ctypes.c_int32, c_i64],
         "gptq_checkpoint_weight_grad_workspace_bytes": [c_i64, c_i64, c_i64, c_i64, ctypes.POINTER(c_sz)],
@@ -548,7 +552,8 @@ def _segments(offsets, rows, E, device, R):
             None if rows is None else _dense(rows, "rows", torch.int32, device, (R,)))
 
 
-def expert_matmul(X, offsets, qweight, scales, zeros, bits, group, rows=None, out=None, out_dtype=torch.float32):
+def expert_matmul(X, offsets, qweight, scales, zeros, bits, group, rows=None, out=None, out_dtype=torch.float32,
+                  workspace=None):
     """Y[p] = X[rows[p]] W_hat_e^T for the rows p of expert e (offsets, rows:
     from route). X bf16 (T x n); qweight E x d_out x n*bits/32, scales and
     zeros E x d_out x n/group: E layers as quantize_layer packs them, without
@@ -566,12 +571,15 @@ def expert_matmul(X, offsets, qweight, scales, zeros, bits, group, rows=None, ou
     yp, ldy = _rows2d(out, "out", _FLOATS, dev)
     if out.shape != (R, d_out):
         raise ValueError(f"out must have the shape {(R, d_out)}")
+    need = _bytes("gptq_expert_matmul_workspace_bytes", R, n, d_out, E, bits, group)
+    ws, wsp = _scratch(need, dev, workspace)
     _call(dev, lib.gptq_expert_matmul, xp, BF16, T, n, ldx, rp, R, op, E, qp, sp, zp, d_out, bits, group, yp,
-          _DTYPE_CODES[out.dtype], ldy)
+          _DTYPE_CODES[out.dtype], ldy, wsp, need)
     return out
 
 
-def expert_matmul_grad(dY, offsets, qweight, scales, zeros, bits, group, n, out=None, out_dtype=torch.bfloat16):
+def expert_matmul_grad(dY, offsets, qweight, scales, zeros, bits, group, n, out=None, out_dtype=torch.bfloat16,
+                       workspace=None):
     """dX[p] = dY[p] W_hat_e, the gradient of expert_matmul for its sorted
     rows (dY: R x d_out bf16). A bf16 result rounds each weight to bf16 once;
     an fp32 result takes it in three pieces at three times the work."""
@@ -588,8 +596,10 @@ def expert_matmul_grad(dY, offsets, qweight, scales, zeros, bits, group, n, out=
     xp, ldx = _rows2d(out, "out", _FLOATS, dev)
     if out.shape != (R, n):
         raise ValueError(f"out must have the shape {(R, n)}")
+    need = _bytes("gptq_expert_matmul_grad_workspace_bytes", R, n, d_out, E, bits, group)
+    ws, wsp = _scratch(need, dev, workspace)
     _call(dev, lib.gptq_expert_matmul_grad, gp, BF16, R, ldy, op, E, qp, sp, zp, d_out, n, bits, group, xp,
-          _DTYPE_CODES[out.dtype], ldx)
+          _DTYPE_CODES[out.dtype], ldx, wsp, need)
     return out
 
 

@@ -129,11 +129,13 @@ def test_expert_product_refusals():
 
     def fwd(X=FAKE, xdt=0, T=8, n=128, ldx=128, rows=FAKE, R=16, off=FAKE, E=4, qw=FAKE, sc=FAKE, zr=FAKE, d=64,
             bits=4, group=128, Y=FAKE, ydt=1, ldy=64):
-        return lib.gptq_expert_matmul(None, X, xdt, T, n, ldx, rows, R, off, E, qw, sc, zr, d, bits, group, Y, ydt, ldy)
+        return lib.gptq_expert_matmul(None, X, xdt, T, n, ldx, rows, R, off, E, qw, sc, zr, d, bits, group, Y, ydt, ldy,
+                                      None, 0)
 
     def bwd(dY=FAKE, dt=0, R=16, ldy=64, off=FAKE, E=4, qw=FAKE, sc=FAKE, zr=FAKE, d=64, n=128, bits=4, group=128,
             dX=FAKE, xdt=0, ldx=128):
-        return lib.gptq_expert_matmul_grad(None, dY, dt, R, ldy, off, E, qw, sc, zr, d, n, bits, group, dX, xdt, ldx)
+        return lib.gptq_expert_matmul_grad(None, dY, dt, R, ldy, off, E, qw, sc, zr, d, n, bits, group, dX, xdt, ldx,
+                                           None, 0)
     odd = ctypes.c_void_p((1 << 20) + 4)
     for bad in (dict(xdt=1), dict(ydt=2), dict(n=0), dict(d=0), dict(bits=5), dict(group=48), dict(group=96),
                 dict(E=0), dict(E=1025), dict(off=NULL), dict(T=0), dict(rows=NULL), dict(ldx=127), dict(ldy=63),
@@ -145,6 +147,22 @@ def test_expert_product_refusals():
                 dict(ldy=63), dict(ldx=127), dict(dY=NULL), dict(dX=NULL), dict(qw=odd), dict(R=-1), dict(R=2 ** 31)):
         assert bwd(**bad) == -1, bad
     assert bwd(R=0, dY=NULL, dX=NULL) == 0
+    # few tiles with a long sum: partial results need a workspace
+    out = ctypes.c_size_t(0)
+    assert lib.gptq_expert_matmul_workspace_bytes(16, 4096, 64, 4, 4, 128, ctypes.byref(out)) == 0 and out.value == 0
+    assert lib.gptq_expert_matmul_workspace_bytes(8192, 4096, 11008, 8, 4, 128, ctypes.byref(out)) == 0
+    assert out.value == 0
+    assert lib.gptq_expert_matmul_workspace_bytes(128, 4096, 64, 4, 4, 128, ctypes.byref(out)) == 0
+    assert out.value > 0 and out.value % (128 * 64 * 4) == 0
+    assert fwd(R=128, n=4096, ldx=4096) == -5
+    assert lib.gptq_expert_matmul_grad_workspace_bytes(16, 128, 4096, 4, 4, 128, ctypes.byref(out)) == 0
+    assert out.value > 0 and out.value % (16 * 128 * 4) == 0
+    assert bwd(d=4096, ldy=4096) == -5
+    for bad in ((-1, 128, 64, 4, 4, 128), (16, 0, 64, 4, 4, 128), (16, 128, 0, 4, 4, 128), (16, 128, 64, 0, 4, 128),
+                (16, 128, 64, 4, 7, 128), (16, 128, 64, 4, 4, 48)):
+        assert lib.gptq_expert_matmul_workspace_bytes(*bad, ctypes.byref(out)) == -1
+        assert lib.gptq_expert_matmul_grad_workspace_bytes(*bad, ctypes.byref(out)) == -1
+    assert lib.gptq_expert_matmul_workspace_bytes(16, 128, 64, 4, 4, 128, None) == -1
 
 
 def test_checkpoint_refusals():

@@ -197,8 +197,9 @@ def test_nonfinite_rows_stay_in_their_tokens():
 # ---------------------------------------------------------------- packed products
 def product_bound(X, off, rows, qw, sc, zr, bits, group, n, R, E):
     """Bound on the fp32 error of the forward product. Tiles: a group's sum
-    takes `group` additions, its scaling one, the groups n / group. Many rows
-    at 4 bits (R > 512 E): one running sum of n additions, carried from unit to
+    takes `group` additions, its scaling one, the groups (and the parts K may be
+    split into, at most one per group) n / group + 1. Large products (4 bits,
+    R > 512 E, groups that are multiples of 128, 128 tiles of 256 x 256): one running sum of n additions, carried from unit to
     unit by n / group ratios, each of three roundings (quotient, product, and
     the last scaling). Few rows at
     4 bits and groups of 128 codes: a piece of 128 sums x (16 + q) and x, each
@@ -211,8 +212,8 @@ def product_bound(X, off, rows, qw, sc, zr, bits, group, n, R, E):
         S = np.repeat(np.abs(sc[e].astype(np.float64)), group, axis=1)
         lo, hi = off[e], off[e + 1]
         x = np.abs(X[lo:hi] if rows is None else X[rows[lo:hi]])
-        mag[lo:hi] = (group + n // group + 1) * (x @ W.T)
-        if R > 512 * E and bits == 4:
+        mag[lo:hi] = (group + n // group + 2) * (x @ W.T)
+        if R > 512 * E and bits == 4 and group % 128 == 0 and -(-R // 256) * -(-sc.shape[1] // 256) >= 128:
             mag[lo:hi] = (n + 3 * (n // group) + 1) * (x @ W.T)
         if R <= 16 * E and bits == 4 and group % 128 == 0:
             mag[lo:hi] = (128 + 2) * 62 * (x @ S.T) + (n // 128 + 1) * (x @ W.T)
@@ -230,10 +231,16 @@ PRODUCTS = [   # T, k, E, d, n, group, drop, only, gathered
     (100, 2, 4, 257, 640, 32, 0.3, None, True),      # 64-row tiles, ragged both ways, a group per chunk
     (300, 1, 2, 129, 512, 128, 0.0, None, False),    # 128-row tiles
     (257, 2, 3, 96, 320, 160, 0.0, [0, 2], True),    # an empty expert between two
-    (700, 1, 1, 200, 256, 256, 0.1, None, True),     # 256-row tiles from here on (4 bits)
-    (1200, 1, 2, 300, 160, 32, 0.1, None, True),     # five stages, a group per stage
-    (1100, 1, 2, 257, 1152, 128, 0.0, None, False),
-    (1600, 2, 3, 40, 32, 32, 0.0, [0, 1], True),     # one stage, an empty expert at the end
+    (700, 1, 1, 200, 256, 256, 0.1, None, True),
+    (1200, 1, 2, 300, 160, 32, 0.1, None, True),     # five chunks, a group each
+    (1600, 2, 3, 40, 32, 32, 0.0, [0, 1], True),     # one chunk, an empty expert at the end
+    (30, 4, 2, 70, 2048, 128, 0.1, None, True),      # few tiles, long sums: parts of K
+    (200, 1, 1, 130, 1920, 96, 0.0, None, False),    # parts that start with a group of 96 codes
+    (90, 1, 1, 33, 4128, 32, 0.0, None, True),       # parts, half a stage at the end
+    (1200, 1, 2, 6550, 128, 128, 0.1, None, True),   # 256-row tiles from here on (4 bits): one block of codes
+    (1100, 1, 2, 6401, 384, 128, 0.0, None, False),  # ragged both ways
+    (1600, 2, 3, 2400, 640, 128, 0.0, [0, 1], True),
+    (700, 1, 1, 10753, 512, 256, 0.2, None, True),   # two blocks a group
 ]
 
 
@@ -261,15 +268,16 @@ def test_scales_of_any_size():
     """Zero, negative, tiny and huge scales, in tiles of every size: exact
     zeros for zero scales, and where a unit cannot be carried (outside
     2^-40 .. 2^40, many rows) the group's weights rounded to bf16 once."""
-    n, d, group = 256, 96, 64
-    for R in (5, 60, 200, 700):
+    n, group = 256, 128
+    for R, d in ((5, 96), (60, 96), (200, 96), (700, 10800)):
         qw, sc, zr = layers(R, 1, d, n, 4, group)
         sc[0, 0] = 0.0
         sc[0, 1, 1] = 0.0
         sc[0, 2] *= -1.0
         sc[0, 3] *= 1e-20
-        sc[0, 4, 2:] *= 1e20
-        sc[0, 5] = [1e-15, 1.0, 1e15, 1e-3]
+        sc[0, 4, 1:] *= 1e20
+        sc[0, 5] = [1e-15, 1.0]
+        sc[0, 6] = [1e15, 1e-3]
         X = values(R, R, n)
         Y = arr(G.expert_matmul(X, None, *cuda_layers(qw, sc, zr), 4, group))
         W = dequantize(qw[0], sc[0], zr[0], 4, group, n)
@@ -289,6 +297,10 @@ GRADS = [   # R, E, d, n, group, cuts (None: one layer without offsets)
     (1, 1, 32, 64, 32, None), (3, 2, 70, 128, 128, [1, 3]), (50, 3, 130, 96, 96, [20, 20, 45]),
     (130, 1, 64, 160, 32, None), (400, 2, 257, 320, 64, [129, 400]), (300, 2, 100, 256, 256, [0, 290]),
     (1100, 2, 96, 320, 64, [500, 1090]), (600, 1, 32, 96, 32, None), (1300, 2, 224, 544, 32, [513, 513]),
+    (24, 4, 1500, 128, 32, [3, 3, 10, 23]), (20, 1, 1501, 96, 32, None), (300, 2, 1283, 64, 64, [100, 290]),  # parts of K
+    (9, 1, 5, 64, 32, None),                         # fewer outputs than a piece
+    (1100, 2, 96, 6432, 32, [500, 1090]), (700, 1, 32, 10784, 32, None),      # 256-row tiles (4 bits)
+    (1300, 2, 224, 5632, 128, [513, 513]), (1100, 2, 352, 6528, 96, [600, 1100]),
 ]
 
 
