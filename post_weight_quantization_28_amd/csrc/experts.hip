@@ -160,8 +160,10 @@ __device__ __forceinline__ uint32_t pack_exact(float a, float b) {
 //    32 j + 8 i .. + 7 of every lane. The order of K inside a product is
 //    free as long as X's fragment follows it.
 //  * Other groups: a product must not mix groups, so step i takes chunk i of
-//    the piece and lane j its codes 8 j .. + 7 (one word at 4 bits), and the
-//    sum is scaled after every chunk.
+//    the piece and lane j its codes 8 j .. + 7, and the sum is scaled after
+//    every chunk. At 4 bits a lane still loads a chunk in one go and four lane
+//    swaps hand out its words (360 rows over 64 experts, 322 x 4608 in groups
+//    of 32: 73 us with a word per load, 36 us so).
 //  * 4 bits: a code in bits 3..6 of the bf16 pattern of 16 is the number
 //    16 + q, so one shift and one and-or give two codes (pairs i, i + 4: X's
 //    fragment is permuted alike), one operation per code against three with
@@ -213,6 +215,24 @@ __device__ __forceinline__ ex_bf16x8_t mv_order(ex_u32x4_t x) {
   const ex_u32x4_t u = {__builtin_amdgcn_perm(x[2], x[0], 0x05040100u), __builtin_amdgcn_perm(x[2], x[0], 0x07060302u),
                         __builtin_amdgcn_perm(x[3], x[1], 0x05040100u), __builtin_amdgcn_perm(x[3], x[1], 0x07060302u)};
   return __builtin_bit_cast(ex_bf16x8_t, u);
+}
+
+// w[i] of lane group j (16 lanes) <-> w[j] of lane group i.
+__device__ __forceinline__ void mv_transpose(uint32_t (&w)[4]) {
+  auto swap32 = [](uint32_t& a, uint32_t& b) {   // a's upper 32 lanes with b's lower
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+  };
+  auto swap16 = [](uint32_t& a, uint32_t& b) {   // a's odd rows of 16 with b's even ones
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+  };
+  swap32(w[0], w[2]);
+  swap32(w[1], w[3]);
+  swap16(w[0], w[1]);
+  swap16(w[2], w[3]);
 }
 
 template <int BITS, bool WIDE, int WAVES, int OB, int S>
@@ -314,6 +334,64 @@ k_expert_mv(const uint16_t* __restrict__ X, int T, int64_t n, int64_t ldx, const
             const float v = BITS == 4 ? fmaf(-(16.f + zu[b]), xs[r], acc[b][r]) : acc[b][r];
             tot[b][r] = fmaf(su[b], v, tot[b][r]);
           }
+      }
+    }
+  } else if constexpr (BITS == 4) {
+    // lane j loads chunk j of a piece (16 bytes) and the four words of each
+    // chunk then change lanes, so that step i has chunk i: word j in lane j
+    const int per = (npieces + WAVES - 1) / WAVES;
+    const int pbeg = wave * per, pend = min(npieces, pbeg + per);
+    for (int p0 = pbeg; p0 < pend; p0 += S) {
+      uint32_t w[S][OB][4];
+      ex_u32x4_t x[S][4];
+      float s[S][OB];
+      uint32_t z[S][OB];
+#pragma unroll
+      for (int u = 0; u < S; ++u) {
+        const int c = min(4 * min(p0 + u, pend - 1) + j, nchunks - 1);
+        const int64_t g = (int64_t)c * 32 / group;
+#pragma unroll
+        for (int b = 0; b < OB; ++b) {
+          load_chunk<4>(qrow[b] + (int64_t)c * 4, w[u][b]);
+          s[u][b] = srow[b][g];
+          z[u][b] = zrow[b][g];
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" : "+v"(srcrow));
+      const uint16_t* __restrict__ xrow = X + (int64_t)min(max(srcrow, 0), T - 1) * ldx;
+#pragma unroll
+      for (int u = 0; u < S; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("" : "=v"(x[u][i]));   // any value
+      if (xok) {
+#pragma unroll
+        for (int u = 0; u < S; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = min(4 * min(p0 + u, pend - 1) + i, nchunks - 1);
+            x[u][i] = *reinterpret_cast<const ex_u32x4_t*>(xrow + (int64_t)c * 32 + 8 * j);
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < S; ++u) {
+        if (p0 + u >= pend) break;
+#pragma unroll
+        for (int b = 0; b < OB; ++b) mv_transpose(w[u][b]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (4 * (p0 + u) + i >= nchunks) break;
+          const ex_bf16x8_t a = mv_order(x[u][i]);
+          const ex_f32x4_t none = {0.f, 0.f, 0.f, 0.f};
+          const ex_f32x4_t xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, ones, none, 0, 0, 0);
+#pragma unroll
+          for (int b = 0; b < OB; ++b) {
+            const ex_f32x4_t acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, mv_codes<4>(w[u][b], i, 0.f), none, 0, 0, 0);
+            const float si = __shfl(s[u][b], 16 * i + li), zi = 16.f + (float)__shfl((int)z[u][b], 16 * i + li);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) tot[b][r] = fmaf(si, fmaf(-zi, xs[r], acc[r]), tot[b][r]);
+          }
+        }
       }
     }
   } else {
@@ -522,7 +600,7 @@ __device__ __forceinline__ bool tile_of(int64_t b, int nr, int nc, int& rt, int&
 
 // The tile of workgroup b. The list holds the tiles that there are, not the
 // launch's upper bound, so that the XCDs' parts are equal (with the bound the
-// last XCDs' parts were empty: 57 against TTT us for 2036 rows over 32 experts).
+// last XCDs' parts were empty: 61 against 51 us for 2036 rows over 32 experts).
 __device__ __forceinline__ bool locate(const int32_t* __restrict__ offsets, int E, int R, int BM, int64_t b, int nc,
                                        int& ct, Seg& sg) {
   int rt;
@@ -1728,7 +1806,7 @@ static int expert_bm(const ExpertArgs& a, int grad) {
 // Parts of K. Few tiles leave most of the chip idle and make every workgroup
 // walk all of K: then K is split until there are two workgroups per CU, at
 // least four stages each (24 rows of 5612 outputs, gradient of 512 columns:
-// 185 us in one part, SSS in parts). The parts meet in fp32 in the workspace.
+// 185 us in one part, 38 us in parts). The parts meet in fp32 in the workspace.
 // From the sizes alone, so that the workspace's size is known before the call.
 ExpertSplit expert_split(int64_t R, int E, int64_t n, int64_t d_out, int group, int grad) {
   ExpertSplit sp = {1, 0, 0};

@@ -370,11 +370,12 @@ k_combine(const void* __restrict__ Ys, int64_t lds, int R, const int32_t* __rest
 }
 
 // dYs[inverse[t k + j]] = w[t][j] dY[t], dw[t][j] = <dY[t], Ys[inverse[t k + j]]>.
-// One workgroup per token; kCgSlots slots per pass over the columns, so dY
-// is read once for up to that many. The dot products are fp32: a thread's
+// One workgroup per token; kCgSlots slots per pass over the columns, whose rows
+// of Ys are all loaded before the first is used, so dY is read once for up to
+// that many. The dot products are fp32: a thread's
 // columns in order, then the lanes and the waves in a fixed tree. A dropped
 // slot has dw = 0 and writes no row.
-constexpr int kCgSlots = 8;
+constexpr int kCgSlots = 4;
 template <bool DYBF, bool YSBF, bool OBF, bool VEC>
 __global__ void __launch_bounds__(256)
 k_combine_grad(const void* __restrict__ dY, int64_t ldy, const void* __restrict__ Ys, int64_t lds, int64_t R,
@@ -399,14 +400,17 @@ k_combine_grad(const void* __restrict__ dY, int64_t ldy, const void* __restrict_
       const int nc = (int)min((int64_t)8, n - c);
       float g[8];
       rt_load8<DYBF, VEC>(dY, t * ldy + c, nc, g);
+      float y[kCgSlots][8];
+#pragma unroll
+      for (int u = 0; u < kCgSlots; ++u)
+        if (p[u] >= 0) rt_load8<YSBF, VEC>(Ys, (int64_t)p[u] * lds + c, nc, y[u]);
 #pragma unroll
       for (int u = 0; u < kCgSlots; ++u) {
         if (p[u] < 0) continue;
-        float y[8], o[8];
-        rt_load8<YSBF, VEC>(Ys, (int64_t)p[u] * lds + c, nc, y);
+        float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          dot[u] = fmaf(g[e], y[e], dot[u]);
+          dot[u] = fmaf(g[e], y[u][e], dot[u]);
           o[e] = wj[u] * g[e];
         }
         rt_store8<OBF, VEC>(dYs, (int64_t)p[u] * ldo + c, nc, o);
