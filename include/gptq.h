@@ -275,7 +275,7 @@ gptq_status gptq_repack_act_order(void *stream, const uint32_t *qweight,
  * places offsets[e] .. offsets[e + 1] - 1. rows (R int32): the token of each
  * place. inverse (R int32, slot order): each slot's place. Ids outside
  * [0, E) (padding, dropped tokens) hold no place: their inverse is -1, and
- * rows is -1 from offsets[E] on. 1 <= E <= GPTQ_MAX_EXPERTS, k >= 1,
+ * rows is -1 from offsets[E] on. 1 <= E <= GPTQ_MAX_EXPERTS, 1 <= k,
  * T k <= 2^31 - 65536; T == 0 writes zero offsets. The order does not depend on
  * timing. Workspace: gptq_route_workspace_bytes (0 for up to 4096 slots). */
 #define GPTQ_MAX_EXPERTS 1024
@@ -327,11 +327,13 @@ gptq_status gptq_combine_grad(void *stream, const void *dY, int32_t dydt, int64_
  * the copy of gptq_dispatch; NULL: X holds the R sorted rows (T >= R).
  * Products of activations and integers are exact in fp32, sums are fp32 in a
  * fixed order, and groups are scaled in fp32: the weights are not rounded.
- * Results are bitwise reproducible. Few rows per expert (R <= 16 E) take a
- * matrix-vector form, in which an infinite activation may give NaN where the
- * sum is infinite. Many (R > 512 E, 4 bits, groups that are multiples of 128)
- * keep one running sum in units of the current group's scale; there the
- * weights of a group whose scale is outside 2^-40 .. 2^40 are rounded to bf16.
+ * Results are bitwise reproducible. Few rows per expert (R <= 16 E, 16-byte
+ * aligned) take a matrix-vector form, in which an infinite activation, or one
+ * above 2^123, may give NaN or an infinity where the sum is infinite or still
+ * finite. Many (R > 512 E, 4 bits, groups that are multiples of 128, tiles for
+ * half of the GPU) keep one running sum in units of the current group's scale;
+ * there the weights of a group whose scale is outside 2^-40 .. 2^40 are
+ * rounded to bf16.
  *
  * gptq_expert_matmul_grad: dX[p] = dY[p] W_hat_e (dX: R x n, dxdt; dY: R x
  * d_out bf16, row pitch ldy). The scale changes along this sum: with a bf16

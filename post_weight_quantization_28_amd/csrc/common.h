@@ -304,7 +304,7 @@ int64_t expert_grid(const ExpertArgs& a, int grad);   // an upper bound on the w
 hipError_t launch_expert_mm(hipStream_t s, const ExpertArgs& a);
 hipError_t launch_expert_mm_grad(hipStream_t s, const ExpertArgs& a);
 struct KeepGradPlan {
-  int bm;               // rows of a tile of G: 32, 64 or 128
+  int bm;               // rows of a tile of G: 32, 64, 128 or 256
   int splits;           // parts a segment's rows are split into
   size_t part_bytes;    // fp32 partials when splits > 1
 };

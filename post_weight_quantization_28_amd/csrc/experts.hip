@@ -668,7 +668,7 @@ __device__ __forceinline__ void run_stages(int nst, F&& stage) {
 // product. G128: groups of 128, two stages each (the first product of a group
 // starts from zero, no test inside a stage); otherwise groups of any number of
 // 32-code chunks, tested after every chunk.
-template <int BITS, class TL, bool G128, bool WIDE>
+template <int BITS, class TL, bool G128>
 __global__ void __launch_bounds__(TL::THREADS, 512 / TL::THREADS)
 k_expert_mm(ExArgs p) {
   constexpr int MI = TL::MI, NI = TL::NI, BM = TL::BM, PA = TL::PA, NB = TL::NB, THREADS = TL::THREADS;
@@ -707,7 +707,7 @@ k_expert_mm(ExArgs p) {
   uint32_t rz[DB];
   auto aload = [&](auto S, int st) {
 #pragma unroll
-    for (int i = 0; i < PA; ++i) ra[S % DA][i] = load_piece<WIDE>(arow[i], (int64_t)(s0 + st) * kExBK + 8 * ac, p.n);
+    for (int i = 0; i < PA; ++i) ra[S % DA][i] = load_piece<true>(arow[i], (int64_t)(s0 + st) * kExBK + 8 * ac, p.n);
   };
   auto bload = [&](auto S, int st) {
     const int c = min(2 * (s0 + st) + bu / 4, nchunks - 1);      // a chunk past the end meets zeros of A
@@ -716,7 +716,7 @@ k_expert_mm(ExArgs p) {
     rz[S % DB] = zrow[g];
   };
   auto awrite = [&](auto S, int st) {
-    if (WIDE && (int64_t)(s0 + st + 1) * kExBK > p.n) {
+    if ((int64_t)(s0 + st + 1) * kExBK > p.n) {
       const int64_t over = (int64_t)(s0 + st) * kExBK + 8 * ac - (p.n - 8);
 #pragma unroll
       for (int i = 0; i < PA; ++i) ra[S % DA][i] = end_piece(ra[S % DA][i], over);
@@ -1785,13 +1785,16 @@ static bool bf16_rows_vec(const void* p, int64_t ld, int64_t cols) {
 }
 
 // The ring kernels: 4 bits, whole blocks (forward) or stages and a bf16 result
-// (gradient), offsets from the bases that fit 32 bits, and tiles for half of
-// the chip at least (fewer are better split along K).
+// (gradient), offsets from the bases that fit 32 bits, tiles for half of the
+// chip at least (fewer are better split along K), and more columns than the
+// smaller tile has (65536 rows, 128 outputs of 4096: 157 us here, 105 us in
+// 128 x 128 tiles; gradient 173 and 134 us).
 static bool ring_fits(const ExpertArgs& a, int grad) {
   const int64_t lim = (int64_t)1 << 32;
-  if (a.bits != 4 || a.d_out * (a.n / 2) >= lim || a.T * a.lda * 2 >= lim) return false;
+  if (a.bits != 4 || a.d_out * (a.n / 2) >= lim || a.lda >= lim / 2 / std::max(a.T, 1)) return false;
   if (!(grad ? a.y_bf16 && a.d_out % 32 == 0 : a.group % 128 == 0)) return false;
-  return ceil_div(a.R, 256) * ceil_div(grad ? a.n : a.d_out, 256) >= 128;
+  const int64_t cols = grad ? a.n : a.d_out;
+  return cols > 128 && ceil_div(a.R, 256) * ceil_div(cols, 256) >= 128;
 }
 
 // Rows of a tile: 16 is the matrix-vector form, 256 the ring kernel.
@@ -1898,7 +1901,7 @@ static void split_go(hipStream_t s, const ExpertArgs& a, ExArgs p, int64_t cols,
 template <int BITS, class TL, bool G128>
 static void mm_go(hipStream_t s, const ExpertArgs& a) {
   split_go(s, a, ex_args(a, TL::BM, TL::BN, a.d_out), a.d_out, 0, [&](dim3 grid, const ExArgs& p) {
-    hipLaunchKernelGGL((k_expert_mm<BITS, TL, G128, true>), grid, dim3(TL::THREADS), 0, s, p);
+    hipLaunchKernelGGL((k_expert_mm<BITS, TL, G128>), grid, dim3(TL::THREADS), 0, s, p);
   });
 }
 

@@ -1041,7 +1041,7 @@ bool mis(const void* p, int32_t dt) { return ((uintptr_t)p & (dt == GPTQ_BF16 ? 
 // Sizes of a call over slots: T tokens, k slots each, n columns.
 gptq_status slots_check(int64_t T, int64_t n, int64_t k, int64_t R) {
   if (T < 0 || n < 0 || R < 0) return fail(GPTQ_EINVAL, "negative size");
-  if (k < 1) return fail(GPTQ_EINVAL, "k must be at least 1");
+  if (k < 1 || k > kMaxRows) return fail(GPTQ_EINVAL, "k must be in [1, 2^31 - 65536]");
   if (T > kMaxRows / k || R > kMaxRows) return fail(GPTQ_EINVAL, "too many slots (T k may be at most 2^31 - 65536)");
   if (n > 0 && T > kMaxThreads / n) return fail(GPTQ_EINVAL, "T n is too large for one launch");
   if (T > kMaxThreads / 256) return fail(GPTQ_EINVAL, "T is too large for one launch");

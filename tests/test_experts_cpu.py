@@ -104,6 +104,20 @@ def test_route_refusals():
     assert lib.gptq_route(None, FAKE, 2, 4096, 2, 8, FAKE, FAKE, FAKE, FAKE, 8) == -5
 
 
+def test_slots_per_token_refusals():
+    """k is a 32-bit number in the kernels: larger ones are refused, also
+    where there is no token."""
+    G, lib = _lib()
+    out = ctypes.c_size_t(0)
+    for k in (-1, 0, 2 ** 31, 2 ** 32 + 2, 2 ** 40):
+        for T in (0, 1):
+            assert lib.gptq_route_workspace_bytes(T, k, 8, ctypes.byref(out)) == -1
+            assert lib.gptq_route(None, FAKE, k, T, k, 8, FAKE, FAKE, FAKE, None, 0) == -1
+            assert lib.gptq_dispatch(None, FAKE, 0, T, 8, 8, k, FAKE, 8, FAKE, 8) == -1
+            assert lib.gptq_combine(None, FAKE, 0, 8, 8, FAKE, NULL, T, 8, k, FAKE, 0, 8) == -1
+            assert lib.gptq_combine_grad(None, FAKE, 0, 8, FAKE, 0, 8, 8, FAKE, FAKE, T, 8, k, FAKE, 0, 8, FAKE) == -1
+
+
 def test_row_call_refusals():
     G, lib = _lib()
     odd = ctypes.c_void_p((1 << 20) + 1)

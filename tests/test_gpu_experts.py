@@ -199,13 +199,14 @@ def product_bound(X, off, rows, qw, sc, zr, bits, group, n, R, E):
     """Bound on the fp32 error of the forward product. Tiles: a group's sum
     takes `group` additions, its scaling one, the groups (and the parts K may be
     split into, at most one per group) n / group + 1. Large products (4 bits,
-    R > 512 E, groups that are multiples of 128, 128 tiles of 256 x 256): one running sum of n additions, carried from unit to
+    R > 512 E, groups that are multiples of 128, 128 tiles of 256 x 256 in more
+    than 128 columns): one running sum of n additions, carried from unit to
     unit by n / group ratios, each of three roundings (quotient, product, and
-    the last scaling). Few rows at
-    4 bits and groups of 128 codes: a piece of 128 sums x (16 + q) and x, each
-    with 128 additions of magnitudes up to 31 |x|, and takes their difference
-    in one more rounding; the two sums' magnitudes together are at most
-    62 sum |x|, scaled once; the n / 128 pieces add."""
+    the last scaling). Few rows at 4 bits: a piece of 128 codes (a chunk of 32
+    in other groups than multiples of 128) sums x (16 + q) and x, each with as
+    many additions of magnitudes up to 31 |x|, and takes their difference in
+    one more rounding; the two sums' magnitudes together are at most
+    62 sum |x|, scaled once; the pieces add."""
     mag = np.zeros((R, sc.shape[1]))
     for e in range(len(off) - 1):
         W = np.abs(dequantize(qw[e], sc[e], zr[e], bits, group, n))
@@ -213,10 +214,11 @@ def product_bound(X, off, rows, qw, sc, zr, bits, group, n, R, E):
         lo, hi = off[e], off[e + 1]
         x = np.abs(X[lo:hi] if rows is None else X[rows[lo:hi]])
         mag[lo:hi] = (group + n // group + 2) * (x @ W.T)
-        if R > 512 * E and bits == 4 and group % 128 == 0 and -(-R // 256) * -(-sc.shape[1] // 256) >= 128:
+        if R > 512 * E and bits == 4 and group % 128 == 0 and sc.shape[1] > 128 and -(-R // 256) * -(-sc.shape[1] // 256) >= 128:
             mag[lo:hi] = (n + 3 * (n // group) + 1) * (x @ W.T)
-        if R <= 16 * E and bits == 4 and group % 128 == 0:
-            mag[lo:hi] = (128 + 2) * 62 * (x @ S.T) + (n // 128 + 1) * (x @ W.T)
+        if R <= 16 * E and bits == 4:
+            piece = 128 if group % 128 == 0 else 32
+            mag[lo:hi] = (piece + 2) * 62 * (x @ S.T) + (n // piece + 1) * (x @ W.T)
     return U32 * mag
 
 
@@ -241,6 +243,9 @@ PRODUCTS = [   # T, k, E, d, n, group, drop, only, gathered
     (1100, 1, 2, 6401, 384, 128, 0.0, None, False),  # ragged both ways
     (1600, 2, 3, 2400, 640, 128, 0.0, [0, 1], True),
     (700, 1, 1, 10753, 512, 256, 0.2, None, True),   # two blocks a group
+    (20, 2, 8, 50, 1312, 32, 0.1, None, True),       # few rows in small groups: 41 chunks of codes, 11 pieces
+    (45, 4, 64, 35, 672, 96, 0.0, None, True),       # a piece with two groups of 96
+    (33000, 1, 1, 40, 128, 128, 0.1, None, True),    # many rows of few columns
 ]
 
 
@@ -301,6 +306,7 @@ GRADS = [   # R, E, d, n, group, cuts (None: one layer without offsets)
     (9, 1, 5, 64, 32, None),                         # fewer outputs than a piece
     (1100, 2, 96, 6432, 32, [500, 1090]), (700, 1, 32, 10784, 32, None),      # 256-row tiles (4 bits)
     (1300, 2, 224, 5632, 128, [513, 513]), (1100, 2, 352, 6528, 96, [600, 1100]),
+    (33000, 1, 64, 128, 64, [32999]),                # many rows of few columns
 ]
 
 
