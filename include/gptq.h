@@ -314,7 +314,8 @@ gptq_status gptq_combine_grad(void *stream, const void *dY, int32_t dydt, int64_
  * E layers of the same shape in the packed layout of gptq_dequant_matmul, one
  * after another: qweight E x d_out x n*bits/32 words (16-byte aligned base),
  * scales and zeros E x d_out x n/group; group a positive multiple of 32 that
- * divides n, groups contiguous (layers quantized without act-order). offsets
+ * divides n, groups contiguous (layers quantized without act-order); zero
+ * points in 0 .. 2^bits - 1, as gptq_quantize_layer writes them. offsets
  * (E + 1 int32 on the device, as gptq_route writes them) split the R rows
  * into the experts' segments; NULL with E = 1 gives all rows to the one
  * layer. Rows from offsets[E] on are not read, and their outputs keep what

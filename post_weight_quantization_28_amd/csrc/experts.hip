@@ -1179,7 +1179,7 @@ k_expert_ring(ExArgs p) {
   // buffers' last readers were stages 0 and, for the units, the end of the
   // block before)
   int left = bpg;                                      // blocks left of the group
-  auto stage = [&](auto I, int blk) {
+  auto stage = [&](auto ON, auto I, int blk) {
     constexpr int i = decltype(I)::value;
     xbarrier<i == 0 ? 4 : (i == 3 ? 3 : 2)>();         // what stage i - 1 issued may still fly
     issue_a(4 * blk + i + 3, (i + 3) & 3);
@@ -1189,38 +1189,47 @@ k_expert_ring(ExArgs p) {
       issue_g(blk + 2);
     }
     __builtin_amdgcn_sched_barrier(0);
-    read(I, ex_const<1>{}, b0);
+    if constexpr (ON) read(I, ex_const<1>{}, b0);
     expand0(b2);
-    multiply(ex_const<0>{});
-    xinterleave<8, 6, 4>();
-    __builtin_amdgcn_sched_barrier(0);
-    read(ex_const<(i + 1) & 3>{}, ex_const<0>{}, b1);
+    if constexpr (ON) {
+      multiply(ex_const<0>{});
+      xinterleave<8, 6, 4>();
+      __builtin_amdgcn_sched_barrier(0);
+      read(ex_const<(i + 1) & 3>{}, ex_const<0>{}, b1);
+    }
     expand1(b2);
     fetch(i == 0 ? blk : blk + 1, (i + 3) & 3);
-    multiply(ex_const<1>{});
-    xinterleave<8, 9, 4>();
-    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (ON) {
+      multiply(ex_const<1>{});
+      xinterleave<8, 9, 4>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
     const uint32_t t = b0;
     b0 = b1;
     b1 = b2;
     b2 = t;
   };
-  for (int blk = 0; blk < nblk; ++blk) {
-    for_four([&](auto I) { stage(I, blk); });
-    if (--left == 0 && blk + 1 < nblk) {               // the group is complete: into the next one's unit
-      left = bpg;
+  if (__builtin_amdgcn_readfirstlane(sg.row0 + 128 * wm < sg.hi)) {
+    for (int blk = 0; blk < nblk; ++blk) {
+      for_four([&](auto I) { stage(std::true_type{}, I, blk); });
+      if (--left == 0 && blk + 1 < nblk) {             // the group is complete: into the next one's unit
+        left = bpg;
 #pragma unroll
-      for (int ni = 0; ni < NI; ++ni) {
-        const float s = __uint_as_float(lds_u32(su + ((blk + 1) & 1) * 1024 + 128 * ni));
-        const float next = unit_ok(s) ? s : 1.f;
-        const float r = unit[ni] / next;
-        unit[ni] = next;
+        for (int ni = 0; ni < NI; ++ni) {
+          const float s = __uint_as_float(lds_u32(su + ((blk + 1) & 1) * 1024 + 128 * ni));
+          const float next = unit_ok(s) ? s : 1.f;
+          const float r = unit[ni] / next;
+          unit[ni] = next;
 #pragma unroll
-        for (int mi = 0; mi < MI; ++mi)
+          for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-          for (int q = 0; q < 16; ++q) acc[mi][ni][q] *= r;
+            for (int q = 0; q < 16; ++q) acc[mi][ni][q] *= r;
+        }
       }
     }
+  } else {
+    // no row of these waves' half exists: they expand codes for the others
+    for (int blk = 0; blk < nblk; ++blk) for_four([&](auto I) { stage(std::false_type{}, I, blk); });
   }
   // no DMA may land in LDS that this workgroup no longer owns
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -1355,34 +1364,32 @@ k_expert_ring_grad(ExArgs p) {
   xbarrier<0>();
   issue_b(4);                                          // into the codes of stage 0, read above
   read(ex_const<0>{}, ex_const<0>{});
-  auto stage = [&](auto SL, int st) {
+  auto stage = [&](auto ON, auto SL, int st) {
     constexpr int sl = decltype(SL)::value;
     xbarrier<kGPer>();
     issue_a(st + 3, (sl + 3) & 3);
     issue_b(st + 5);                                   // over the codes of st + 1, read in stage st - 2
     __builtin_amdgcn_sched_barrier(0);
-    read(SL, ex_const<1>{});
+    if constexpr (ON) read(SL, ex_const<1>{});
     expand0((sl + 2) & 3);
-    multiply(ex_const<0>{});
-    xinterleave<8, 8, 4>();
-    __builtin_amdgcn_sched_barrier(0);
-    read(ex_const<(sl + 1) & 3>{}, ex_const<0>{});
+    if constexpr (ON) {
+      multiply(ex_const<0>{});
+      xinterleave<8, 8, 4>();
+      __builtin_amdgcn_sched_barrier(0);
+      read(ex_const<(sl + 1) & 3>{}, ex_const<0>{});
+    }
     expand1((sl + 2) & 3);
     fetch(st + 3);
-    multiply(ex_const<1>{});
-    xinterleave<8, 11, 4>();
-    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (ON) {
+      multiply(ex_const<1>{});
+      xinterleave<8, 11, 4>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
-  int st = 0;
-  for (; st + 4 <= nst; st += 4) {
-    stage(ex_const<0>{}, st);
-    stage(ex_const<1>{}, st + 1);
-    stage(ex_const<2>{}, st + 2);
-    stage(ex_const<3>{}, st + 3);
-  }
-  if (st < nst) stage(ex_const<0>{}, st);
-  if (st + 1 < nst) stage(ex_const<1>{}, st + 1);
-  if (st + 2 < nst) stage(ex_const<2>{}, st + 2);
+  if (__builtin_amdgcn_readfirstlane(sg.row0 + 128 * wm < sg.hi))
+    run_stages<4>(nst, [&](auto SL, int st) { stage(std::true_type{}, SL, st); });
+  else                                                 // no row of these waves' half exists
+    run_stages<4>(nst, [&](auto SL, int st) { stage(std::false_type{}, SL, st); });
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // no DMA into LDS that is no longer owned
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) {
@@ -1797,13 +1804,25 @@ static bool ring_fits(const ExpertArgs& a, int grad) {
   return cols > 128 && ceil_div(a.R, 256) * ceil_div(cols, 256) >= 128;
 }
 
+// 64 or 128 rows of a tile: the small ones while all of them run at once, two
+// (gradient: nearly three) workgroups per CU, or while most segments fit one;
+// beyond, the large ones expand each weight for twice the rows. 64 against 128
+// rows, 4 bits: 96 rows for each of 8 experts of 4096 x 4096 (512 tiles) 89 and
+// 111 us, gradient 74 and 88; 96 for each of 32 of 1408 x 2048 (704 tiles) 82
+// and 72, gradient 55 and 53; 29 for each of 64 of 1272 x 5120 154 and 184.
+static int small_bm(int64_t R, int E, int64_t cols, int grad) {
+  const int64_t tiles = std::min<int64_t>(R, ceil_div(R, 64) + (E - 1) / 2) * ceil_div(cols, 128);
+  return ceil_div(R, E) <= 48 || tiles <= (grad ? 640 : 512) ? 64 : 128;
+}
+
 // Rows of a tile: 16 is the matrix-vector form, 256 the ring kernel.
 static int expert_bm(const ExpertArgs& a, int grad) {
   const int64_t avg = ceil_div(a.R, a.E);
   const bool vec = bf16_rows_vec(a.A, a.lda, grad ? a.d_out : a.n);
   if (!grad && avg <= 16 && vec) return 16;
-  if (avg <= 64 || (grad && a.d_out < 8)) return 64;
-  return vec && avg > 512 && ring_fits(a, grad) ? 256 : 128;
+  if (grad && a.d_out < 8) return 64;
+  if (vec && avg > 512 && ring_fits(a, grad)) return 256;
+  return small_bm(a.R, a.E, grad ? a.n : a.d_out, grad);
 }
 
 // Parts of K. Few tiles leave most of the chip idle and make every workgroup
@@ -1818,7 +1837,7 @@ ExpertSplit expert_split(int64_t R, int E, int64_t n, int64_t d_out, int group, 
   sp.per = (int)nst;
   const int64_t avg = ceil_div(R, E);
   if (R <= 0 || (!grad && avg <= 16)) return sp;           // the matrix-vector form splits inside
-  const int bm = avg <= 64 ? 64 : 128;
+  const int bm = small_bm(R, E, cols, grad);
   const int64_t tiles = std::min<int64_t>(R, ceil_div(R, bm) + (E - 1) / 2) * ceil_div(cols, 128);
   int64_t unit = 1;                                        // stages between starts of a group
   if (!grad)

@@ -231,7 +231,9 @@ PRODUCTS = [   # T, k, E, d, n, group, drop, only, gathered
     (17, 1, 2, 64, 128, 128, 0.0, [1], True),        # every row at one expert, the other empty
     (40, 2, 4, 100, 96, 96, 0.0, None, True),        # 64-row tiles, half a stage at the end
     (100, 2, 4, 257, 640, 32, 0.3, None, True),      # 64-row tiles, ragged both ways, a group per chunk
-    (300, 1, 2, 129, 512, 128, 0.0, None, False),    # 128-row tiles
+    (300, 1, 2, 129, 512, 128, 0.0, None, False),
+    (600, 1, 2, 7001, 256, 128, 0.1, None, True),    # more than 512 tiles of 64 rows: 128-row tiles
+    (600, 1, 2, 7001, 96, 32, 0.0, None, False),
     (257, 2, 3, 96, 320, 160, 0.0, [0, 2], True),    # an empty expert between two
     (700, 1, 1, 200, 256, 256, 0.1, None, True),
     (1200, 1, 2, 300, 160, 32, 0.1, None, True),     # five chunks, a group each
@@ -307,6 +309,7 @@ GRADS = [   # R, E, d, n, group, cuts (None: one layer without offsets)
     (1100, 2, 96, 6432, 32, [500, 1090]), (700, 1, 32, 10784, 32, None),      # 256-row tiles (4 bits)
     (1300, 2, 224, 5632, 128, [513, 513]), (1100, 2, 352, 6528, 96, [600, 1100]),
     (33000, 1, 64, 128, 64, [32999]),                # many rows of few columns
+    (600, 2, 70, 8320, 32, [250, 590]),              # more than 640 tiles of 64 rows: 128-row tiles
 ]
 
 
