@@ -255,23 +255,41 @@ hipError_t launch_route(hipStream_t s, const int32_t* ids, int64_t ldi, int64_t 
 // ---------------------------------------------------------------- rows there and back
 // The rows of Ys and dY are read once, so they are loaded past the caches
 // (268 MB of Ys: 80 against 94 us).
-// A unit is 8 columns: 16 bytes of bf16, 32 of fp32. VEC: every row of both
-// sides is 16-byte aligned and n % 8 == 0, so units move as whole 16-byte
-// pieces; otherwise columns past n are guarded one by one.
-template <bool BF, bool VEC>
+// A unit is 8 columns: 16 bytes of bf16, 32 of fp32.
+//   kAligned: every row of both sides is 16-byte aligned and n % 8 == 0, so
+//     units move as whole 16-byte pieces;
+//   kAnywhere: n >= 8; pieces of any alignment, a row's last unit moved back to
+//     end with the row (the columns that two units share get the same value
+//     from both);
+//   kSingly: columns one by one, for rows of less than a unit.
+// 4096 tokens, 8 slots each, rows of 1915: the way there, the way back and its
+// gradient 28, 38 and 78 us with kAnywhere, 67, 79 and 193 column by column.
+enum { kSingly, kAnywhere, kAligned };
+typedef rt_u32x4_t rt_u32x4_any_t __attribute__((aligned(2)));
+typedef rt_f32x4_t rt_f32x4_any_t __attribute__((aligned(4)));
+
+template <bool BF, int MODE>
 __device__ __forceinline__ void rt_load8(const void* base, int64_t off, int ncols, float (&v)[8]) {
-  if constexpr (VEC && BF) {
-    const rt_u32x4_t u =
-        __builtin_nontemporal_load(reinterpret_cast<const rt_u32x4_t*>(static_cast<const uint16_t*>(base) + off));
+  if constexpr (MODE != kSingly && BF) {
+    rt_u32x4_t u;
+    if constexpr (MODE == kAligned)
+      u = __builtin_nontemporal_load(reinterpret_cast<const rt_u32x4_t*>(static_cast<const uint16_t*>(base) + off));
+    else u = *reinterpret_cast<const rt_u32x4_any_t*>(static_cast<const uint16_t*>(base) + off);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = __uint_as_float(u[i] << 16);
       v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
     }
-  } else if constexpr (VEC) {
+  } else if constexpr (MODE != kSingly) {
     const float* p = static_cast<const float*>(base) + off;
-    const rt_f32x4_t a = __builtin_nontemporal_load(reinterpret_cast<const rt_f32x4_t*>(p));
-    const rt_f32x4_t b = __builtin_nontemporal_load(reinterpret_cast<const rt_f32x4_t*>(p + 4));
+    rt_f32x4_t a, b;
+    if constexpr (MODE == kAligned) {
+      a = __builtin_nontemporal_load(reinterpret_cast<const rt_f32x4_t*>(p));
+      b = __builtin_nontemporal_load(reinterpret_cast<const rt_f32x4_t*>(p + 4));
+    } else {
+      a = *reinterpret_cast<const rt_f32x4_any_t*>(p);
+      b = *reinterpret_cast<const rt_f32x4_any_t*>(p + 4);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[i] = a[i];
@@ -293,15 +311,23 @@ __device__ __forceinline__ uint32_t rt_pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, p);
 }
 
-template <bool BF, bool VEC>
+template <bool BF, int MODE>
 __device__ __forceinline__ void rt_store8(void* base, int64_t off, int ncols, const float (&v)[8]) {
-  if constexpr (VEC && BF) {
+  if constexpr (MODE != kSingly && BF) {
     const rt_u32x4_t u = {rt_pack2(v[0], v[1]), rt_pack2(v[2], v[3]), rt_pack2(v[4], v[5]), rt_pack2(v[6], v[7])};
-    *reinterpret_cast<rt_u32x4_t*>(static_cast<uint16_t*>(base) + off) = u;
-  } else if constexpr (VEC) {
+    uint16_t* p = static_cast<uint16_t*>(base) + off;
+    if constexpr (MODE == kAligned) *reinterpret_cast<rt_u32x4_t*>(p) = u;
+    else *reinterpret_cast<rt_u32x4_any_t*>(p) = u;
+  } else if constexpr (MODE != kSingly) {
+    const rt_f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
     float* p = static_cast<float*>(base) + off;
-    *reinterpret_cast<rt_f32x4_t*>(p) = (rt_f32x4_t){v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<rt_f32x4_t*>(p + 4) = (rt_f32x4_t){v[4], v[5], v[6], v[7]};
+    if constexpr (MODE == kAligned) {
+      *reinterpret_cast<rt_f32x4_t*>(p) = a;
+      *reinterpret_cast<rt_f32x4_t*>(p + 4) = b;
+    } else {
+      *reinterpret_cast<rt_f32x4_any_t*>(p) = a;
+      *reinterpret_cast<rt_f32x4_any_t*>(p + 4) = b;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -312,24 +338,31 @@ __device__ __forceinline__ void rt_store8(void* base, int64_t off, int ncols, co
   }
 }
 
-// Xs[inverse[t k + j]] = X[t]: rows of `width` elements of U (16 bytes, or
-// one element when the rows are not aligned), copied bit by bit. One thread
-// per element of X's rows. STREAM: non-temporal stores (268 MB of copies, 8
-// per row: 37 against 51 us).
-template <typename U, bool STREAM>
+// Xs[inverse[t k + j]] = X[t], copied bit by bit: one thread per piece (a U) of
+// X's rows, `width` pieces a row. The pitches are in bytes, and a row's last
+// piece is moved back to end with it (bytes: its length). ANY: 16-byte pieces
+// of any alignment. STREAM: non-temporal stores (268 MB of copies, 8 per row:
+// 37 against 51 us).
+template <typename U, bool STREAM, bool ANY>
 __global__ void __launch_bounds__(256)
-k_dispatch(const U* __restrict__ X, int64_t ldx, uint32_t T, uint32_t width, int k,
-           const int32_t* __restrict__ inverse, int R, U* __restrict__ Xs, int64_t lds) {
+k_dispatch(const char* __restrict__ X, int64_t ldx, uint32_t T, uint32_t width, int64_t bytes, int k,
+           const int32_t* __restrict__ inverse, int R, char* __restrict__ Xs, int64_t lds) {
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  const uint32_t t = i / width, c = i - t * width;
+  const uint32_t t = i / width;
   if (t >= T) return;
-  const U v = X[(int64_t)t * ldx + c];
+  const int64_t c = min((int64_t)(i - t * width) * (int64_t)sizeof(U), bytes - (int64_t)sizeof(U));
+  const char* in = X + (int64_t)t * ldx + c;
+  U v;
+  if constexpr (ANY) v = *reinterpret_cast<const rt_u32x4_any_t*>(in);
+  else v = *reinterpret_cast<const U*>(in);
   const int32_t* __restrict__ inv = inverse + (int64_t)t * k;
   for (int j = 0; j < k; ++j) {
     const int p = inv[j];
     if ((unsigned)p < (unsigned)R) {
-      if constexpr (STREAM) __builtin_nontemporal_store(v, Xs + (int64_t)p * lds + c);
-      else Xs[(int64_t)p * lds + c] = v;
+      char* out = Xs + (int64_t)p * lds + c;
+      if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<U*>(out));
+      else if constexpr (ANY) *reinterpret_cast<rt_u32x4_any_t*>(out) = v;
+      else *reinterpret_cast<U*>(out) = v;
     }
   }
 }
@@ -337,13 +370,15 @@ k_dispatch(const U* __restrict__ X, int64_t ldx, uint32_t T, uint32_t width, int
 // Y[t] = sum_j w[t][j] Ys[inverse[t k + j]]. KB rows (1, 2, 4 or 8: the
 // smallest that covers k, at most 8) are loaded before the first is added,
 // so a thread has up to 128 bytes of bf16 in flight.
-template <bool YSBF, bool YBF, bool VEC, int KB>
+template <bool YSBF, bool YBF, int MODE, int KB>
 __global__ void __launch_bounds__(256)
 k_combine(const void* __restrict__ Ys, int64_t lds, int R, const int32_t* __restrict__ inverse,
           const float* __restrict__ w, uint32_t T, uint32_t n, uint32_t units, int k, void* __restrict__ Y, int64_t ldy) {
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  const uint32_t t = i / units, c = 8u * (i - t * units);
+  const uint32_t t = i / units;
   if (t >= T) return;
+  uint32_t c = 8u * (i - t * units);
+  if constexpr (MODE == kAnywhere) c = min(c, n - 8u);
   const int nc = (int)min(8u, n - c);
   const int64_t s0 = (int64_t)t * k;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -358,7 +393,7 @@ k_combine(const void* __restrict__ Ys, int64_t lds, int R, const int32_t* __rest
     }
 #pragma unroll
     for (int u = 0; u < KB; ++u)
-      if ((unsigned)p[u] < (unsigned)R) rt_load8<YSBF, VEC>(Ys, (int64_t)p[u] * lds + c, nc, v[u]);
+      if ((unsigned)p[u] < (unsigned)R) rt_load8<YSBF, MODE>(Ys, (int64_t)p[u] * lds + c, nc, v[u]);
 #pragma unroll
     for (int u = 0; u < KB; ++u)
       if ((unsigned)p[u] < (unsigned)R) {
@@ -366,17 +401,18 @@ k_combine(const void* __restrict__ Ys, int64_t lds, int R, const int32_t* __rest
         for (int e = 0; e < 8; ++e) sum[e] = fmaf(wj[u], v[u][e], sum[e]);
       }
   }
-  rt_store8<YBF, VEC>(Y, (int64_t)t * ldy + c, nc, sum);
+  rt_store8<YBF, MODE>(Y, (int64_t)t * ldy + c, nc, sum);
 }
 
 // dYs[inverse[t k + j]] = w[t][j] dY[t], dw[t][j] = <dY[t], Ys[inverse[t k + j]]>.
-// One workgroup per token; kCgSlots slots per pass over the columns, whose rows
-// of Ys are all loaded before the first is used, so dY is read once for up to
-// that many. The dot products are fp32: a thread's
-// columns in order, then the lanes and the waves in a fixed tree. A dropped
-// slot has dw = 0 and writes no row.
+// kCgSlots slots per pass over the columns, whose rows of Ys are all loaded
+// before the first is used, so dY is read once for up to that many. One
+// workgroup per token makes its passes; with few tokens each pass has a
+// workgroup (64 tokens, 8 slots, 2048 columns: 4.8 against 6.8 us). The dot products are fp32: a thread's columns in order, then
+// the lanes and the waves in a fixed tree. A dropped slot has dw = 0 and writes
+// no row.
 constexpr int kCgSlots = 4;
-template <bool DYBF, bool YSBF, bool OBF, bool VEC>
+template <bool DYBF, bool YSBF, bool OBF, int MODE>
 __global__ void __launch_bounds__(256)
 k_combine_grad(const void* __restrict__ dY, int64_t ldy, const void* __restrict__ Ys, int64_t lds, int64_t R,
                const int32_t* __restrict__ inverse, const float* __restrict__ w, int64_t n, int64_t units, int k,
@@ -384,7 +420,7 @@ k_combine_grad(const void* __restrict__ dY, int64_t ldy, const void* __restrict_
   __shared__ float red[4][kCgSlots];
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int j0 = 0; j0 < k; j0 += kCgSlots) {
+  for (int j0 = blockIdx.y * kCgSlots; j0 < k; j0 += gridDim.y * kCgSlots) {
     float dot[kCgSlots], wj[kCgSlots];
     int p[kCgSlots];
 #pragma unroll
@@ -396,24 +432,25 @@ k_combine_grad(const void* __restrict__ dY, int64_t ldy, const void* __restrict_
       dot[u] = 0.f;
     }
     for (int64_t i = threadIdx.x; i < units; i += 256) {
-      const int64_t c = 8 * i;
-      const int nc = (int)min((int64_t)8, n - c);
+      const int64_t c = MODE == kAnywhere ? min(8 * i, n - 8) : 8 * i;
+      const int nc = (int)min((int64_t)8, n - c), seen = (int)(8 * i - c);   // columns of the unit before
       float g[8];
-      rt_load8<DYBF, VEC>(dY, t * ldy + c, nc, g);
+      rt_load8<DYBF, MODE>(dY, t * ldy + c, nc, g);
       float y[kCgSlots][8];
 #pragma unroll
       for (int u = 0; u < kCgSlots; ++u)
-        if (p[u] >= 0) rt_load8<YSBF, VEC>(Ys, (int64_t)p[u] * lds + c, nc, y[u]);
+        if (p[u] >= 0) rt_load8<YSBF, MODE>(Ys, (int64_t)p[u] * lds + c, nc, y[u]);
 #pragma unroll
       for (int u = 0; u < kCgSlots; ++u) {
         if (p[u] < 0) continue;
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          dot[u] = fmaf(g[e], y[u][e], dot[u]);
+          const float d = fmaf(g[e], y[u][e], dot[u]);
+          dot[u] = MODE == kAnywhere && e < seen ? dot[u] : d;
           o[e] = wj[u] * g[e];
         }
-        rt_store8<OBF, VEC>(dYs, (int64_t)p[u] * ldo + c, nc, o);
+        rt_store8<OBF, MODE>(dYs, (int64_t)p[u] * ldo + c, nc, o);
       }
     }
 #pragma unroll
@@ -434,84 +471,88 @@ static bool rows_aligned(const void* p, int64_t ld, int esize) {
   return ((uintptr_t)p & 15) == 0 && (ld * esize) % 16 == 0;
 }
 
+template <typename U, bool STREAM, bool ANY>
+static void dispatch_go(hipStream_t s, const void* X, int64_t ldx, int64_t T, int64_t bytes, int k,
+                        const int32_t* inverse, int64_t R, void* Xs, int64_t lds) {
+  const int64_t width = ceil_div(bytes, (int64_t)sizeof(U));
+  hipLaunchKernelGGL((k_dispatch<U, STREAM, ANY>), dim3((unsigned)ceil_div(T * width, 256)), dim3(256), 0, s,
+                     static_cast<const char*>(X), ldx, (uint32_t)T, (uint32_t)width, bytes, k, inverse, (int)R,
+                     static_cast<char*>(Xs), lds);
+}
+
 hipError_t launch_dispatch(hipStream_t s, const void* X, int esize, int64_t T, int64_t n, int64_t ldx, int k,
                            const int32_t* inverse, int64_t R, void* Xs, int64_t lds) {
   if (T <= 0 || n <= 0 || k <= 0) return hipSuccess;
-  if (rows_aligned(X, ldx, esize) && rows_aligned(Xs, lds, esize) && (n * esize) % 16 == 0) {
-    const int per = 16 / esize;
-    const int64_t width = n / per;
-    const auto kernel = T * k * n * esize > kStreamBytes ? k_dispatch<rt_u32x4_t, true> : k_dispatch<rt_u32x4_t, false>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)ceil_div(T * width, 256)), dim3(256), 0, s,
-                       static_cast<const rt_u32x4_t*>(X), ldx / per, (uint32_t)T, (uint32_t)width, k, inverse, (int)R,
-                       static_cast<rt_u32x4_t*>(Xs), lds / per);
-  } else if (esize == 2) {
-    hipLaunchKernelGGL((k_dispatch<uint16_t, false>), dim3((unsigned)ceil_div(T * n, 256)), dim3(256), 0, s,
-                       static_cast<const uint16_t*>(X), ldx, (uint32_t)T, (uint32_t)n, k, inverse, (int)R, static_cast<uint16_t*>(Xs), lds);
-  } else {
-    hipLaunchKernelGGL((k_dispatch<uint32_t, false>), dim3((unsigned)ceil_div(T * n, 256)), dim3(256), 0, s,
-                       static_cast<const uint32_t*>(X), ldx, (uint32_t)T, (uint32_t)n, k, inverse, (int)R, static_cast<uint32_t*>(Xs), lds);
-  }
+  const bool aligned = rows_aligned(X, ldx, esize) && rows_aligned(Xs, lds, esize) && (n * esize) % 16 == 0;
+  const int64_t bytes = n * esize;
+  const auto go = !aligned ? (bytes >= 16 ? dispatch_go<rt_u32x4_t, false, true>
+                              : esize == 2 ? dispatch_go<uint16_t, false, false> : dispatch_go<uint32_t, false, false>)
+                  : T * k * bytes > kStreamBytes ? dispatch_go<rt_u32x4_t, true, false>
+                                                 : dispatch_go<rt_u32x4_t, false, false>;
+  go(s, X, ldx * esize, T, bytes, k, inverse, R, Xs, lds * esize);
   return hipGetLastError();
 }
 
-template <bool YSBF, bool YBF, bool VEC, int KB>
+template <bool YSBF, bool YBF, int MODE, int KB>
 static void combine_kb(hipStream_t s, const CombineArgs& a) {
   const int64_t units = ceil_div(a.n, 8);
-  hipLaunchKernelGGL((k_combine<YSBF, YBF, VEC, KB>), dim3((unsigned)ceil_div(a.T * units, 256)), dim3(256), 0, s, a.Ys,
+  hipLaunchKernelGGL((k_combine<YSBF, YBF, MODE, KB>), dim3((unsigned)ceil_div(a.T * units, 256)), dim3(256), 0, s, a.Ys,
                      a.lds, (int)a.R, a.inverse, a.w, (uint32_t)a.T, (uint32_t)a.n, (uint32_t)units, a.k, a.Y, a.ldy);
 }
 
-template <bool YSBF, bool YBF, bool VEC>
-static void combine_go(hipStream_t s, const CombineArgs& a) {
-  if constexpr (VEC) {
-    if (a.k == 1) return combine_kb<YSBF, YBF, true, 1>(s, a);
-    if (a.k == 2) return combine_kb<YSBF, YBF, true, 2>(s, a);
-    if (a.k > 4) return combine_kb<YSBF, YBF, true, 8>(s, a);
+template <bool YSBF, bool YBF, int MODE>
+static void combine_mode(hipStream_t s, const CombineArgs& a) {
+  if constexpr (MODE != kSingly) {
+    if (a.k == 1) return combine_kb<YSBF, YBF, MODE, 1>(s, a);
+    if (a.k == 2) return combine_kb<YSBF, YBF, MODE, 2>(s, a);
+    if (a.k > 4) return combine_kb<YSBF, YBF, MODE, 8>(s, a);
   }
-  combine_kb<YSBF, YBF, VEC, 4>(s, a);
+  combine_kb<YSBF, YBF, MODE, 4>(s, a);
+}
+
+template <bool YSBF, bool YBF>
+static void combine_go(hipStream_t s, const CombineArgs& a) {
+  if (a.n % 8 == 0 && rows_aligned(a.Ys, a.lds, YSBF ? 2 : 4) && rows_aligned(a.Y, a.ldy, YBF ? 2 : 4))
+    combine_mode<YSBF, YBF, kAligned>(s, a);
+  else if (a.n >= 8) combine_mode<YSBF, YBF, kAnywhere>(s, a);
+  else combine_mode<YSBF, YBF, kSingly>(s, a);
 }
 
 hipError_t launch_combine(hipStream_t s, const CombineArgs& a) {
   if (a.T <= 0 || a.n <= 0) return hipSuccess;
-  const bool vec = a.n % 8 == 0 && rows_aligned(a.Ys, a.lds, a.ys_bf16 ? 2 : 4) &&
-                   rows_aligned(a.Y, a.ldy, a.y_bf16 ? 2 : 4);
-  switch ((a.ys_bf16 ? 4 : 0) | (a.y_bf16 ? 2 : 0) | (vec ? 1 : 0)) {
-    case 0: combine_go<false, false, false>(s, a); break;
-    case 1: combine_go<false, false, true>(s, a); break;
-    case 2: combine_go<false, true, false>(s, a); break;
-    case 3: combine_go<false, true, true>(s, a); break;
-    case 4: combine_go<true, false, false>(s, a); break;
-    case 5: combine_go<true, false, true>(s, a); break;
-    case 6: combine_go<true, true, false>(s, a); break;
-    default: combine_go<true, true, true>(s, a); break;
-  }
+  if (a.ys_bf16) a.y_bf16 ? combine_go<true, true>(s, a) : combine_go<true, false>(s, a);
+  else a.y_bf16 ? combine_go<false, true>(s, a) : combine_go<false, false>(s, a);
   return hipGetLastError();
 }
 
+template <bool DYBF, bool YSBF, bool OBF, int MODE>
+static void combine_grad_mode(hipStream_t s, const CombineGradArgs& a) {
+  const int64_t passes = ceil_div(a.k, kCgSlots);
+  const dim3 grid((unsigned)a.T, (unsigned)(a.T * passes <= 1024 ? passes : 1));
+  hipLaunchKernelGGL((k_combine_grad<DYBF, YSBF, OBF, MODE>), grid, dim3(256), 0, s, a.dY, a.ldy, a.Ys, a.lds, a.R,
+                     a.inverse, a.w, a.n, ceil_div(a.n, 8), a.k, a.dYs, a.ldo, a.dw);
+}
+
 template <bool DYBF, bool YSBF, bool OBF>
-static void combine_grad_go(hipStream_t s, const CombineGradArgs& a, bool vec) {
-  const int64_t units = ceil_div(a.n, 8);
-  if (vec)
-    hipLaunchKernelGGL((k_combine_grad<DYBF, YSBF, OBF, true>), dim3((unsigned)a.T), dim3(256), 0, s, a.dY, a.ldy,
-                       a.Ys, a.lds, a.R, a.inverse, a.w, a.n, units, a.k, a.dYs, a.ldo, a.dw);
-  else
-    hipLaunchKernelGGL((k_combine_grad<DYBF, YSBF, OBF, false>), dim3((unsigned)a.T), dim3(256), 0, s, a.dY, a.ldy,
-                       a.Ys, a.lds, a.R, a.inverse, a.w, a.n, units, a.k, a.dYs, a.ldo, a.dw);
+static void combine_grad_go(hipStream_t s, const CombineGradArgs& a) {
+  if (a.n % 8 == 0 && rows_aligned(a.dY, a.ldy, DYBF ? 2 : 4) && rows_aligned(a.Ys, a.lds, YSBF ? 2 : 4) &&
+      rows_aligned(a.dYs, a.ldo, OBF ? 2 : 4))
+    combine_grad_mode<DYBF, YSBF, OBF, kAligned>(s, a);
+  else if (a.n >= 8) combine_grad_mode<DYBF, YSBF, OBF, kAnywhere>(s, a);
+  else combine_grad_mode<DYBF, YSBF, OBF, kSingly>(s, a);
 }
 
 hipError_t launch_combine_grad(hipStream_t s, const CombineGradArgs& a) {
   if (a.T <= 0 || a.k <= 0) return hipSuccess;
-  const bool vec = a.n % 8 == 0 && rows_aligned(a.dY, a.ldy, a.dy_bf16 ? 2 : 4) &&
-                   rows_aligned(a.Ys, a.lds, a.ys_bf16 ? 2 : 4) && rows_aligned(a.dYs, a.ldo, a.out_bf16 ? 2 : 4);
   switch ((a.dy_bf16 ? 4 : 0) | (a.ys_bf16 ? 2 : 0) | (a.out_bf16 ? 1 : 0)) {
-    case 0: combine_grad_go<false, false, false>(s, a, vec); break;
-    case 1: combine_grad_go<false, false, true>(s, a, vec); break;
-    case 2: combine_grad_go<false, true, false>(s, a, vec); break;
-    case 3: combine_grad_go<false, true, true>(s, a, vec); break;
-    case 4: combine_grad_go<true, false, false>(s, a, vec); break;
-    case 5: combine_grad_go<true, false, true>(s, a, vec); break;
-    case 6: combine_grad_go<true, true, false>(s, a, vec); break;
-    default: combine_grad_go<true, true, true>(s, a, vec); break;
+    case 0: combine_grad_go<false, false, false>(s, a); break;
+    case 1: combine_grad_go<false, false, true>(s, a); break;
+    case 2: combine_grad_go<false, true, false>(s, a); break;
+    case 3: combine_grad_go<false, true, true>(s, a); break;
+    case 4: combine_grad_go<true, false, false>(s, a); break;
+    case 5: combine_grad_go<true, false, true>(s, a); break;
+    case 6: combine_grad_go<true, true, false>(s, a); break;
+    default: combine_grad_go<true, true, true>(s, a); break;
   }
   return hipGetLastError();
 }

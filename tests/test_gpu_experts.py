@@ -99,6 +99,7 @@ def test_route_pitch_and_no_tokens():
 SLOTS = [   # T, k, E, n, drop
     (1, 1, 1, 8, 0.0), (5, 2, 4, 33, 0.3), (16, 8, 8, 512, 0.0), (33, 5, 9, 1000, 0.5), (130, 2, 300, 72, 0.1),
     (3, 9, 16, 4104, 0.2), (12, 2, 4, 1, 0.0), (9, 3, 4, 256, 1.0),
+    (600, 6, 8, 1003, 0.1), (7, 4, 4, 5, 0.2), (11, 1, 4, 9, 0.0), (6, 12, 16, 2055, 0.1),
 ]
 
 
@@ -147,6 +148,18 @@ def test_combine_grad(T, k, E, n, drop, gdt, ysdt, odt):
     assert np.all(np.abs(arr(dw) - rw) <= (n + 8) * U32 * mag)
     untouched = np.setdiff1d(np.arange(T * k), inv[inv >= 0])
     assert np.array_equal(arr(dYs)[untouched], before[untouched])
+
+
+def test_shared_columns_count_once():
+    """Rows of 11 columns: the last unit moves back over columns 3 to 7, whose
+    infinities must enter the dot product from one side only."""
+    inv = torch.arange(4, dtype=torch.int32).reshape(4, 1).cuda()
+    dY = torch.ones(4, 11, dtype=BF16, device="cuda")
+    Ys = torch.ones(4, 11, dtype=BF16, device="cuda")
+    dY[0, 5], Ys[1, 4], dY[2, 6] = float("inf"), float("-inf"), float("nan")
+    dYs, dw = G.combine_grad(dY, Ys, inv, torch.ones(4, 1, device="cuda"))
+    assert arr(dw).reshape(-1)[[0, 1, 3]].tolist() == [np.inf, -np.inf, 11.0] and np.isnan(arr(dw)[2, 0])
+    assert torch.equal(torch.nan_to_num(dYs, nan=7.0), torch.nan_to_num(dY, nan=7.0))
 
 
 def test_unaligned_rows_and_pitches():
