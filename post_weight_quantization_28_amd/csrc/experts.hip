@@ -1822,6 +1822,9 @@ static int expert_bm(const ExpertArgs& a, int grad) {
   if (!grad && avg <= 16 && vec) return 16;
   if (grad && a.d_out < 8) return 64;
   if (vec && avg > 512 && ring_fits(a, grad)) return 256;
+  // three pieces fill a CU's LDS with one workgroup, small or large: 100 rows for
+  // each of 4 experts of 2048 x 2048 40 and 49 us, 450 rows 99 and 69
+  if (grad && !a.y_bf16) return avg <= 128 ? 64 : 128;
   return small_bm(a.R, a.E, grad ? a.n : a.d_out, grad);
 }
 
