@@ -299,7 +299,8 @@ struct ExpertSplit {
   int splits, per;      // parts of K, stages of a part
   size_t part_bytes;    // fp32 partial results when splits > 1
 };
-ExpertSplit expert_split(int64_t R, int E, int64_t n, int64_t d_out, int group, int grad);
+// pieces: the gradient with an fp32 result
+ExpertSplit expert_split(int64_t R, int E, int64_t n, int64_t d_out, int group, int grad, bool pieces);
 int64_t expert_grid(const ExpertArgs& a, int grad);   // an upper bound on the workgroups of a launch
 hipError_t launch_expert_mm(hipStream_t s, const ExpertArgs& a);
 hipError_t launch_expert_mm_grad(hipStream_t s, const ExpertArgs& a);

@@ -1810,7 +1810,11 @@ static bool ring_fits(const ExpertArgs& a, int grad) {
 // rows, 4 bits: 96 rows for each of 8 experts of 4096 x 4096 (512 tiles) 89 and
 // 111 us, gradient 74 and 88; 96 for each of 32 of 1408 x 2048 (704 tiles) 82
 // and 72, gradient 55 and 53; 29 for each of 64 of 1272 x 5120 154 and 184.
-static int small_bm(int64_t R, int E, int64_t cols, int grad) {
+// Three pieces (fp32 gradient) fill a CU's LDS with one workgroup, small or
+// large: 100 rows for each of 4 experts of 2048 x 2048 40 and 49 us, 450 rows
+// 99 and 69.
+static int small_bm(int64_t R, int E, int64_t cols, int grad, bool pieces) {
+  if (pieces) return ceil_div(R, E) <= 128 ? 64 : 128;
   const int64_t tiles = std::min<int64_t>(R, ceil_div(R, 64) + (E - 1) / 2) * ceil_div(cols, 128);
   return ceil_div(R, E) <= 48 || tiles <= (grad ? 640 : 512) ? 64 : 128;
 }
@@ -1822,30 +1826,28 @@ static int expert_bm(const ExpertArgs& a, int grad) {
   if (!grad && avg <= 16 && vec) return 16;
   if (grad && a.d_out < 8) return 64;
   if (vec && avg > 512 && ring_fits(a, grad)) return 256;
-  // three pieces fill a CU's LDS with one workgroup, small or large: 100 rows for
-  // each of 4 experts of 2048 x 2048 40 and 49 us, 450 rows 99 and 69
-  if (grad && !a.y_bf16) return avg <= 128 ? 64 : 128;
-  return small_bm(a.R, a.E, grad ? a.n : a.d_out, grad);
+  return small_bm(a.R, a.E, grad ? a.n : a.d_out, grad, grad && !a.y_bf16);
 }
 
 // Parts of K. Few tiles leave most of the chip idle and make every workgroup
-// walk all of K: then K is split until there are two workgroups per CU, at
-// least four stages each (24 rows of 5612 outputs, gradient of 512 columns:
+// walk all of K: then K is split until there are two workgroups per CU (one
+// with three pieces; 150 rows of 4096 outputs, K 2048, in 320 workgroups 43 us,
+// in 256 31 us), at least four stages each (24 rows of 5612 outputs, gradient of 512 columns:
 // 185 us in one part, 38 us in parts). The parts meet in fp32 in the workspace.
 // From the sizes alone, so that the workspace's size is known before the call.
-ExpertSplit expert_split(int64_t R, int E, int64_t n, int64_t d_out, int group, int grad) {
+ExpertSplit expert_split(int64_t R, int E, int64_t n, int64_t d_out, int group, int grad, bool pieces) {
   ExpertSplit sp = {1, 0, 0};
   const int64_t K = grad ? d_out : n, cols = grad ? n : d_out;
   const int64_t nst = ceil_div(K, kExBK);
   sp.per = (int)nst;
   const int64_t avg = ceil_div(R, E);
   if (R <= 0 || (!grad && avg <= 16)) return sp;           // the matrix-vector form splits inside
-  const int bm = small_bm(R, E, cols, grad);
+  const int bm = small_bm(R, E, cols, grad, pieces);
   const int64_t tiles = std::min<int64_t>(R, ceil_div(R, bm) + (E - 1) / 2) * ceil_div(cols, 128);
   int64_t unit = 1;                                        // stages between starts of a group
   if (!grad)
     while (unit * kExBK % group != 0) ++unit;
-  int64_t s = std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), nst / 4);
+  int64_t s = std::min<int64_t>((pieces ? 256 : 512) / std::max<int64_t>(tiles, 1), nst / 4);
   if (s <= 1) return sp;
   const int64_t per = ceil_div(ceil_div(nst, s), unit) * unit;
   sp.per = (int)per;
@@ -1903,7 +1905,7 @@ static ExArgs ex_args(const ExpertArgs& a, int BM, int BN, int64_t cols) {
 // The tile kernels write their parts of K into the workspace when there are several.
 template <class F>
 static void split_go(hipStream_t s, const ExpertArgs& a, ExArgs p, int64_t cols, int grad, F&& launch) {
-  const ExpertSplit sp = expert_split(a.R, a.E, a.n, a.d_out, a.group, grad);
+  const ExpertSplit sp = expert_split(a.R, a.E, a.n, a.d_out, a.group, grad, grad && !a.y_bf16);
   p.per_split = sp.per;
   dim3 grid = tile_grid(p.nrt, p.nct);
   grid.y = (unsigned)sp.splits;

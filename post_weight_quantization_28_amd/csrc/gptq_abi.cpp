@@ -1168,7 +1168,9 @@ static gptq_status expert_workspace(int64_t R, int64_t n, int64_t d_out, int64_t
   if (!bytes) return fail(GPTQ_EINVAL, "bytes is NULL");
   const gptq_status st = expert_sizes(R, n, d_out, E, bits, group);
   if (st != GPTQ_OK) return st;
-  *bytes = (expert_split(R, (int)E, n, d_out, group, grad).part_bytes + 255) / 256 * 256;
+  size_t need = expert_split(R, (int)E, n, d_out, group, grad, false).part_bytes;
+  if (grad) need = std::max(need, expert_split(R, (int)E, n, d_out, group, 1, true).part_bytes);   // of either result
+  *bytes = (need + 255) / 256 * 256;
   return GPTQ_OK;
 }
 
@@ -1198,7 +1200,7 @@ gptq_status gptq_expert_matmul(void* stream, const void* X, int32_t xdt, int64_t
   const ExpertArgs a = {X, ldx, rows, (int)T, offsets, (int)E, (int)R, qweight, scales, zeros,
                         d_out, n, bits, group, Y, ydt == GPTQ_BF16, ldy, workspace};
   if ((st = expert_weights_check(a, 0)) != GPTQ_OK) return st;
-  if ((st = check_ws(workspace, ws_bytes, expert_split(R, (int)E, n, d_out, group, 0).part_bytes)) != GPTQ_OK) return st;
+  if ((st = check_ws(workspace, ws_bytes, expert_split(R, (int)E, n, d_out, group, 0, false).part_bytes)) != GPTQ_OK) return st;
   HIP_TRY(launch_expert_mm((hipStream_t)stream, a), "expert_matmul");
   return GPTQ_OK;
 }
@@ -1216,7 +1218,7 @@ gptq_status gptq_expert_matmul_grad(void* stream, const void* dY, int32_t dydt, 
   const ExpertArgs a = {dY, ldy, nullptr, (int)R, offsets, (int)E, (int)R, qweight, scales, zeros,
                         d_out, n, bits, group, dX, dxdt == GPTQ_BF16, ldx, workspace};
   if ((st = expert_weights_check(a, 1)) != GPTQ_OK) return st;
-  if ((st = check_ws(workspace, ws_bytes, expert_split(R, (int)E, n, d_out, group, 1).part_bytes)) != GPTQ_OK) return st;
+  if ((st = check_ws(workspace, ws_bytes, expert_split(R, (int)E, n, d_out, group, 1, dxdt == GPTQ_F32).part_bytes)) != GPTQ_OK) return st;
   HIP_TRY(launch_expert_mm_grad((hipStream_t)stream, a), "expert_matmul_grad");
   return GPTQ_OK;
 }
