@@ -436,6 +436,9 @@ WGRADS = [   # T, k, E, m, n, drop, only, gathered
     (3000, 1, 1, 16, 96, 0.0, None, True),       # parts of the rows summed in order
     (700, 4, 2, 72, 256, 0.3, None, True), (90, 1, 4, 257, 64, 1.0, None, True),
     (4000, 1, 2, 128, 32, 0.0, [1], True),       # a whole batch at one expert, split
+    (3000, 1, 2, 136, 300, 0.1, None, True),     # 256 x 256 tiles from here on: parts of the rows
+    (700, 2, 3, 264, 520, 0.2, [0, 2], True),    # ragged both ways, an empty expert
+    (40, 1, 2, 512, 64, 0.0, [1], False), (1, 1, 1, 256, 32, 0.0, None, False), (90, 1, 4, 256, 33, 1.0, None, True),
 ]
 
 
