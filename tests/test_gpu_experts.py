@@ -618,3 +618,32 @@ def test_unaligned_activations():
                            G.expert_matmul_grad(dY, None, *wl, 4, 64, 256))
         kept = G.checkpoint_save(X)
         assert torch.equal(G.checkpoint_weight_grad(dYo[:, 1:73], kept), G.checkpoint_weight_grad(dY, kept))
+
+
+def test_fewer_rows_than_slots():
+    """Ys with fewer rows than there are slots (a capacity): weights and
+    dweights have T k entries all the same, slots whose place is past the rows
+    count as dropped, and nothing behind the rows or behind dweights is
+    written. Called as a C program calls it."""
+    lib = G.load()
+    for T, k, E, n, R in ((9, 3, 4, 40, 15), (130, 2, 8, 33, 100), (6, 12, 16, 5, 1), (40, 5, 4, 256, 0)):
+        inv = X64.route(expert_ids(T + n, T, k, E, 0.1), E)[2]
+        it = torch.from_numpy(inv).cuda()
+        Ys, dY = values(1, T * k, n), values(2, T, n, scale=1e-3)
+        w = torch.rand(T, k, generator=torch.Generator().manual_seed(T)).cuda()
+        Y = arr(G.combine(Ys[:R], it, w, out_dtype=F32))
+        ref, mag = X64.combine(arr(Ys[:R]), inv, arr(w)), X64.combine(np.abs(arr(Ys[:R])), inv, arr(w))
+        assert np.all(np.abs(Y - ref) <= k * U32 * mag * 1.01 + U32 * np.abs(ref))
+        dYs = values(9, T * k, n, dtype=F32)
+        before = arr(dYs)
+        dw = torch.full((T * k + 64,), 7.0, device="cuda")
+        st = lib.gptq_combine_grad(torch.cuda.current_stream().cuda_stream, dY.data_ptr(), G.BF16, n, Ys.data_ptr(),
+                                   G.BF16, R, n, it.data_ptr(), w.data_ptr(), T, n, k, dYs.data_ptr(), G.F32, n,
+                                   dw.data_ptr())
+        assert st == 0
+        rYs, rw = X64.combine_grad(arr(dY), arr(Ys[:R]), inv, arr(w), before[:R])
+        _, m = X64.combine_grad(np.abs(arr(dY)), np.abs(arr(Ys[:R])), inv, arr(w), before[:R])
+        assert np.all(np.abs(arr(dYs)[:R] - rYs) <= U32 * 1.01 * np.abs(rYs))
+        assert np.array_equal(arr(dYs)[R:], before[R:])
+        assert np.all(np.abs(arr(dw)[:T * k].reshape(T, k) - rw) <= (n + 8) * U32 * m)
+        assert np.all(arr(dw)[:T * k].reshape(T, k)[(inv < 0) | (inv >= R)] == 0) and torch.all(dw[T * k:] == 7.0)
