@@ -283,21 +283,26 @@ gptq_status gptq_route_workspace_bytes(int64_t T, int64_t k, int64_t E, size_t *
 gptq_status gptq_route(void *stream, const int32_t *expert_ids, int64_t ldi, int64_t T, int64_t k, int64_t E,
                        int32_t *offsets, int32_t *rows, int32_t *inverse, void *workspace, size_t ws_bytes);
 
-/* gptq_dispatch: Xs[inverse[t k + j]] = X[t] (bits copied; X: T x n, Xs: R x
- * n, dtype dt, row pitches ldx, lds >= n). R is the number of rows of Xs:
- * slots whose place is outside [0, R) are skipped, and rows of Xs that no
- * slot names keep what they held. Places must be distinct.
+/* From here on R is the number of rows of Xs, Ys and dYs: T k, or any other
+ * number (a capacity). inverse, weights and dweights are in slot order and
+ * have T k entries whatever R is.
+ *
+ * gptq_dispatch: Xs[inverse[t k + j]] = X[t] (bits copied; X: T x n, Xs: R x
+ * n, dtype dt, row pitches ldx, lds >= n). Slots whose place is outside
+ * [0, R) are skipped, and rows of Xs that no slot names keep what they held.
+ * Places inside [0, R) must be distinct.
  *
  * gptq_combine: Y[t] = sum_j weights[t k + j] Ys[inverse[t k + j]], summed in
  * the order of j in fp32 and rounded once (Y: T x n, ydt; Ys: R x n, ysdt;
- * weights: R fp32, or NULL for weights of one, which makes it the gradient of
- * gptq_dispatch). Slots whose place is outside [0, R) add nothing; a token
+ * weights: T k fp32, or NULL for weights of one, which makes it the gradient
+ * of gptq_dispatch). Slots whose place is outside [0, R) add nothing; a token
  * with none gets zeros.
  *
  * gptq_combine_grad: the gradients of gptq_combine for dY (T x n, dydt):
  * dYs[inverse[i]] = weights[i] dY[t] (R x n, odt; rows that no slot names
- * keep what they held) and dweights[i] = <dY[t], Ys[inverse[i]]> (R fp32, 0
- * for a slot without a place; fp32 sums in a fixed order).
+ * keep what they held; places inside [0, R) must be distinct) and dweights[i]
+ * = <dY[t], Ys[inverse[i]]> (T k fp32, all of them written: 0 for a slot whose
+ * place is outside [0, R); fp32 sums in a fixed order).
  *
  * dtypes are GPTQ_BF16 or GPTQ_F32, each argument its own; any alignment and
  * pitch (16-byte aligned rows move in 16-byte pieces). No output may overlap
