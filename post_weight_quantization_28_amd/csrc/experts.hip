@@ -523,18 +523,19 @@ __device__ __forceinline__ ex_u32x4_t end_piece(ex_u32x4_t v, int64_t over) {
   return v;
 }
 
-// The 8 codes of w times f, minus z f, rounded once: codes - z + 128 as
-// bytes (one addition per four), then (t - 128) f in one fma.
+// The 8 codes of w minus z, times f: codes - z + 128 as bytes (one addition
+// per four, no borrow from byte to byte), the top bit of each turned to make
+// them signed, then one conversion and one product per code. The product is
+// finite wherever f (q - z) is.
 __device__ __forceinline__ uint32_t xbias(uint32_t z) {
   return __builtin_amdgcn_perm(0u, 0x80u - z, 0u);    // its low byte four times
 }
 __device__ __forceinline__ ex_u32x4_t xexpand(uint32_t w, uint32_t bias, float f) {
-  const uint32_t lo = (w & 0x0F0F0F0Fu) + bias, hi = ((w >> 4) & 0x0F0F0F0Fu) + bias;
-  const float m = -128.f * f;
+  const uint32_t lo = ((w & 0x0F0F0F0Fu) + bias) ^ 0x80808080u, hi = (((w >> 4) & 0x0F0F0F0Fu) + bias) ^ 0x80808080u;
   ex_u32x4_t o;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    o[i] = ex_pack2(fmaf((float)((lo >> (8 * i)) & 0xFFu), f, m), fmaf((float)((hi >> (8 * i)) & 0xFFu), f, m));
+    o[i] = ex_pack2((float)(int8_t)(lo >> (8 * i)) * f, (float)(int8_t)(hi >> (8 * i)) * f);
   return o;
 }
 

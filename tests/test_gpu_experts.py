@@ -647,3 +647,35 @@ def test_fewer_rows_than_slots():
         assert np.array_equal(arr(dYs)[R:], before[R:])
         assert np.all(np.abs(arr(dw)[:T * k].reshape(T, k) - rw) <= (n + 8) * U32 * m)
         assert np.all(arr(dw)[:T * k].reshape(T, k)[(inv < 0) | (inv >= R)] == 0) and torch.all(dw[T * k:] == 7.0)
+
+
+@pytest.mark.parametrize("bits", [4, 3, 2])
+def test_scales_near_the_largest(bits):
+    """Scales of 2^122 to 2^123, whose weights s (q - z) are still finite (at
+    most 15 2^123), with activations and gradients small enough for the
+    results: the products of every tile size are finite and as exact as with
+    any other scale (4 bits and many rows: the weights rounded to bf16 once)."""
+    n, group = 256, 128
+    for R, d in ((5, 96), (60, 96), (200, 96), (700, 10800)):
+        qw, sc, zr = layers(R, 1, d, n, bits, group)
+        sc = (2.0 ** 122 * (1.0 + sc / 0.05)).astype(np.float32)
+        X = values(R, R, n, scale=2.0 ** -100)
+        Y = arr(G.expert_matmul(X, None, *cuda_layers(qw, sc, zr), bits, group))
+        W = dequantize(qw[0], sc[0], zr[0], bits, group, n)
+        ref, mag = arr(X) @ W.T, np.abs(arr(X)) @ np.abs(W).T
+        e = U32 * (n + 3 * (n // group) + 1) * mag
+        if R <= 16 and bits == 4:
+            e = U32 * (130 * 62 * (np.abs(arr(X)) @ np.repeat(sc[0].astype(np.float64), group, axis=1).T) + 3 * mag)
+        if R > 512 and bits == 4:
+            e = e + (UBF + U32) * 1.01 * mag
+        assert np.all(np.abs(Y - ref) <= e)
+    for R, d, n in ((40, 70, 160), (300, 130, 160), (1100, 64, 6432)):
+        qw, sc, zr = layers(R, 1, d, n, bits, 32)
+        sc = (2.0 ** 122 * (1.0 + sc / 0.05)).astype(np.float32)
+        dY = values(R, R, d, scale=2.0 ** -110)
+        W = dequantize(qw[0], sc[0], zr[0], bits, 32, n)
+        ref, mag = arr(dY) @ W, np.abs(arr(dY)) @ np.abs(W)
+        for odt in (BF16, F32):
+            dX = arr(G.expert_matmul_grad(dY, None, *cuda_layers(qw, sc, zr), bits, 32, n, out_dtype=odt))
+            err = ((UBF + U32 + d * U32) if odt == BF16 else (UBF ** 3 + U32 + 3 * d * U32)) * 1.01 * mag
+            assert np.all(np.abs(dX - ref) <= err + (UBF * (np.abs(ref) + err) if odt == BF16 else 0))
