@@ -305,8 +305,10 @@ gptq_status gptq_route(void *stream, const int32_t *expert_ids, int64_t ldi, int
  * place is outside [0, R); fp32 sums in a fixed order).
  *
  * dtypes are GPTQ_BF16 or GPTQ_F32, each argument its own; any alignment and
- * pitch (16-byte aligned rows move in 16-byte pieces). No output may overlap
- * an input. All asynchronous, no workspace. */
+ * pitch. No output may overlap an input. At most 2^32 - 512 threads start at
+ * once: T ceil(n / 8) of them in gptq_combine and gptq_dispatch (fp32: T
+ * ceil(n / 4); T n where a row has less than 16 bytes), 256 T in
+ * gptq_combine_grad. All asynchronous, no workspace. */
 gptq_status gptq_dispatch(void *stream, const void *X, int32_t dt, int64_t T, int64_t n, int64_t ldx, int64_t k,
                           const int32_t *inverse, int64_t R, void *Xs, int64_t lds);
 gptq_status gptq_combine(void *stream, const void *Ys, int32_t ysdt, int64_t R, int64_t lds, const int32_t *inverse,

@@ -1043,9 +1043,13 @@ gptq_status slots_check(int64_t T, int64_t n, int64_t k, int64_t R) {
   if (T < 0 || n < 0 || R < 0) return fail(GPTQ_EINVAL, "negative size");
   if (k < 1 || k > kMaxRows) return fail(GPTQ_EINVAL, "k must be in [1, 2^31 - 65536]");
   if (T > kMaxRows / k || R > kMaxRows) return fail(GPTQ_EINVAL, "too many slots (T k may be at most 2^31 - 65536)");
-  if (n > 0 && T > kMaxThreads / n) return fail(GPTQ_EINVAL, "T n is too large for one launch");
-  if (T > kMaxThreads / 256) return fail(GPTQ_EINVAL, "T is too large for one launch");
+  if (n > kMaxThreads) return fail(GPTQ_EINVAL, "n may be at most 2^32 - 512");   // columns are counted in 32 bits
   return GPTQ_OK;
+}
+
+// A launch with `per` threads for each of T tokens.
+gptq_status launch_check(int64_t T, int64_t per) {
+  return T > kMaxThreads / per ? fail(GPTQ_EINVAL, "T n is too large for one launch") : GPTQ_OK;
 }
 
 gptq_status experts_check(int64_t E, const int32_t* offsets) {
@@ -1112,6 +1116,8 @@ gptq_status gptq_dispatch(void* stream, const void* X, int32_t dt, int64_t T, in
   gptq_status st = dt_check(dt);
   if (st != GPTQ_OK || (st = slots_check(T, n, k, R)) != GPTQ_OK) return st;
   if (T == 0 || n == 0 || R == 0) return GPTQ_OK;
+  const int64_t bytes = n * (dt == GPTQ_BF16 ? 2 : 4);          // of a row: 16 a thread, or an element where there are fewer
+  if ((st = launch_check(T, bytes >= 16 ? ceil_div(bytes, 16) : n)) != GPTQ_OK) return st;
   if (ldx < n || lds < n) return fail(GPTQ_EINVAL, "row pitch below n");
   if (!X || !inverse || !Xs) return fail(GPTQ_EINVAL, "NULL pointer");
   if (mis(X, dt) || mis(Xs, dt)) return fail(GPTQ_EINVAL, "a matrix is not aligned to its elements");
@@ -1125,6 +1131,7 @@ gptq_status gptq_combine(void* stream, const void* Ys, int32_t ysdt, int64_t R, 
   gptq_status st = dt_check(ysdt);
   if (st != GPTQ_OK || (st = dt_check(ydt)) != GPTQ_OK || (st = slots_check(T, n, k, R)) != GPTQ_OK) return st;
   if (T == 0 || n == 0) return GPTQ_OK;
+  if ((st = launch_check(T, ceil_div(n, 8))) != GPTQ_OK) return st;
   if (ldy < n || (R > 0 && lds < n)) return fail(GPTQ_EINVAL, "row pitch below n");
   if ((R > 0 && !Ys) || !inverse || !Y) return fail(GPTQ_EINVAL, "NULL pointer");
   if (mis(Ys, ysdt) || mis(Y, ydt)) return fail(GPTQ_EINVAL, "a matrix is not aligned to its elements");
@@ -1138,7 +1145,7 @@ gptq_status gptq_combine_grad(void* stream, const void* dY, int32_t dydt, int64_
                               int64_t n, int64_t k, void* dYs, int32_t odt, int64_t ldo, float* dweights) {
   gptq_status st = dt_check(dydt);
   if (st != GPTQ_OK || (st = dt_check(ysdt)) != GPTQ_OK || (st = dt_check(odt)) != GPTQ_OK ||
-      (st = slots_check(T, n, k, R)) != GPTQ_OK)
+      (st = slots_check(T, n, k, R)) != GPTQ_OK || (st = launch_check(T, 256)) != GPTQ_OK)
     return st;
   if (T == 0) return GPTQ_OK;
   if (!inverse || !weights || !dweights) return fail(GPTQ_EINVAL, "NULL pointer");

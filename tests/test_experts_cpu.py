@@ -217,3 +217,36 @@ def test_binding_refuses_host_tensors():
                  lambda: G.checkpoint_weight_grad(x, None)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_row_calls_are_refused_by_their_launch_alone():
+    """What limits the way there and back is the threads of a launch (one per
+    8 columns, or 256 per token), not the number of elements: larger calls
+    come as far as the test of their pointers."""
+    G, lib = _lib()
+
+    def why(st):
+        assert st == -1
+        return lib.gptq_last_error().decode()
+
+    def dispatch(T, n, dt=0):
+        return why(lib.gptq_dispatch(None, NULL, dt, T, n, n, 1, FAKE, T, FAKE, n))
+
+    def combine(T, n):
+        return why(lib.gptq_combine(None, NULL, 0, T, n, FAKE, NULL, T, n, 1, FAKE, 0, n))
+
+    def grad(T, n):
+        return why(lib.gptq_combine_grad(None, NULL, 0, n, FAKE, 0, T, n, FAKE, FAKE, T, n, 1, FAKE, 0, n, FAKE))
+    for T, n in ((2 ** 20 + 3, 4104), (2 ** 24 + 5, 8), (2 ** 31 - 65536, 8), (2 ** 21, 16368), (1, 2 ** 32 - 512)):
+        assert "NULL pointer" in dispatch(T, n) and "NULL pointer" in combine(T, n)
+    assert "NULL pointer" in dispatch(2 ** 20, 16368, 1) and "NULL pointer" in dispatch(2 ** 30, 3)
+    assert "NULL pointer" in grad(2 ** 20 + 3, 4104) and "NULL pointer" in grad(2 ** 24 - 2, 2 ** 20)
+    for T, n in ((2 ** 21, 16384), (2 ** 31 - 65536, 17), (1, 2 ** 32 - 511)):
+        assert "too large" in dispatch(T, n) or "at most" in dispatch(T, n)
+        assert "too large" in combine(T, n) or "at most" in combine(T, n)
+    assert "too large" in dispatch(2 ** 30, 4, 0) and "too large" in dispatch(2 ** 20, 16384, 1)
+    assert "too large" in grad(2 ** 24, 8)
+    out = ctypes.c_size_t(0)
+    for T in (2 ** 24 + 5, 2 ** 31 - 65536):
+        assert lib.gptq_route_workspace_bytes(T, 1, 8, ctypes.byref(out)) == 0
+        assert out.value == (9 * (-(-T // 1024) + 1) * 4 + 255) // 256 * 256

@@ -679,3 +679,49 @@ def test_scales_near_the_largest(bits):
             dX = arr(G.expert_matmul_grad(dY, None, *cuda_layers(qw, sc, zr), bits, 32, n, out_dtype=odt))
             err = ((UBF + U32 + d * U32) if odt == BF16 else (UBF ** 3 + U32 + 3 * d * U32)) * 1.01 * mag
             assert np.all(np.abs(dX - ref) <= err + (UBF * (np.abs(ref) + err) if odt == BF16 else 0))
+
+
+def test_rows_beyond_32_bits():
+    """More than 2^32 elements on each side (2^20 + 3 rows of 4104): the way
+    there, the way back and its gradient."""
+    T, n = 2 ** 20 + 3, 4104
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.randint(-1, 3, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    r = G.route(ids, 3)
+    place = r.inverse[:, 0].long()
+    kept = (place >= 0).nonzero()[:, 0]
+    X = torch.randn(T, n, generator=g, device="cuda", dtype=BF16)
+    w = torch.rand(T, 1, generator=g, device="cuda")
+    Xs = torch.zeros(T, n, dtype=BF16, device="cuda")
+    G.dispatch(X, r.inverse, out=Xs)
+    Y = G.combine(Xs, r.inverse, w)
+    dYs = torch.zeros(T, n, dtype=BF16, device="cuda")
+    _, dw = G.combine_grad(X, Xs, r.inverse, w, out=dYs)
+    last = int(r.offsets[-1])
+    assert last == kept.numel() and torch.count_nonzero(Xs[last:]) == 0 and torch.count_nonzero(dYs[last:]) == 0
+    for part in kept.split(1 << 17):
+        x, at = X[part], place[part]
+        assert torch.equal(Xs[at], x)
+        # one product in fp32, rounded to bf16
+        scaled = (w[part] * x.float()).to(BF16)
+        assert torch.equal(Y[part], scaled) and torch.equal(dYs[at], scaled)
+        sq = (x.float().double() ** 2).sum(1)
+        assert torch.all((dw[part, 0].double() - sq).abs() <= (n + 8) * U32 * sq)
+    gone = (place < 0).nonzero()[:, 0]
+    assert torch.count_nonzero(Y[gone]) == 0 and torch.count_nonzero(dw[gone]) == 0
+
+
+def test_route_of_many_tokens():
+    """More tokens than a launch of one workgroup per token could take."""
+    T, E = 2 ** 24 + 5, 1024
+    ids = torch.randint(-1, E + 1, (T, 1), generator=torch.Generator(device="cuda").manual_seed(2), device="cuda",
+                        dtype=torch.int32)
+    r = G.route(ids, E)
+    key = torch.where((ids >= 0) & (ids < E), ids, E)[:, 0].long()
+    order = torch.sort(key, stable=True)[1]
+    counts = torch.bincount(key, minlength=E + 1)
+    kept = int(counts[:E].sum())
+    assert torch.equal(r.offsets[1:].long(), counts[:E].cumsum(0)) and int(r.offsets[0]) == 0
+    assert torch.equal(r.rows[:kept].long(), order[:kept]) and torch.all(r.rows[kept:] == -1)
+    assert torch.equal(r.inverse[order[:kept], 0].long(), torch.arange(kept, device="cuda"))
+    assert torch.all(r.inverse[order[kept:], 0] == -1)
