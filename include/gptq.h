@@ -387,7 +387,9 @@ gptq_status gptq_expert_matmul_grad(void *stream, const void *dY, int32_t dydt, 
  * bf16, row pitch ldp): the weight gradient of a linear layer (P = dY), or of
  * an adapter's input factor (P = dY B), from the kept input. offsets, rows
  * and E as above (one kept row per token serves its k places); an empty
- * segment's G is zero. Products are exact, sums fp32 in a fixed order.
+ * segment's G is zero. Products are exact, sums fp32 in a fixed order. At
+ * most 2^32 - 512 threads start at once: 256 for each 128 columns of 128 rows
+ * of one G (of 32 or 64 where m is no more).
  * Workspace: gptq_checkpoint_weight_grad_workspace_bytes (fp32 partial sums
  * when few tiles split the rows). All asynchronous.
  * ("Resumen Técnico: GPTQ-intrinsic LoRA", "Declaración del Problema": the

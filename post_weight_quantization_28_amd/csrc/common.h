@@ -310,6 +310,7 @@ struct KeepGradPlan {
   size_t part_bytes;    // fp32 partials when splits > 1
 };
 KeepGradPlan keep_grad_plan(int64_t R, int E, int64_t m, int64_t n);
+int64_t keep_grad_threads(int64_t m, int64_t n);   // an upper bound on the threads of a launch's first dimension
 hipError_t launch_keep_grad(hipStream_t s, const KeepGradPlan& pl, const uint16_t* P, int64_t ldp, int64_t R, int64_t m,
                             const int8_t* codes, const uint8_t* exps, int64_t T, int64_t n, const int32_t* rows,
                             const int32_t* offsets, int E, float* G, float* part);

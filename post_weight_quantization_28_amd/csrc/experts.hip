@@ -2013,6 +2013,14 @@ KeepGradPlan keep_grad_plan(int64_t R, int E, int64_t m, int64_t n) {
   return p;
 }
 
+// Of the smallest tiles that m may get (256 threads each); the 256 x 256 ones,
+// of 512, have no more for the same G. G's parts are at most 2^24 values
+// (fewer tiles than workgroups fit the chip), so their sum is never larger.
+int64_t keep_grad_threads(int64_t m, int64_t n) {
+  const int bm = m <= 32 ? 32 : (m <= 64 ? 64 : 128);
+  return (ceil_div(m, bm) * ceil_div(n, 128) + 8) * 256;
+}
+
 template <class TL>
 static void kg_go(hipStream_t s, const KgArgs& p) {
   const dim3 grid((unsigned)(8 * ceil_div((int64_t)p.nmt * p.nnt, 8)), (unsigned)p.E, (unsigned)p.splits);

@@ -1251,7 +1251,7 @@ gptq_status gptq_checkpoint_weight_grad_workspace_bytes(int64_t R, int64_t E, in
   if (!bytes) return fail(GPTQ_EINVAL, "bytes is NULL");
   if (R < 0 || m < 0 || n < 0) return fail(GPTQ_EINVAL, "negative size");
   if (E < 1 || E > GPTQ_MAX_EXPERTS) return fail(GPTQ_EINVAL, "need 1 <= E <= GPTQ_MAX_EXPERTS");
-  if (R > kMaxRows || m > kMaxRows || n > kMaxRows || (m > 0 && n > 0 && E * m > kMaxThreads / n))
+  if (R > kMaxRows || m > kMaxRows || n > kMaxRows || keep_grad_threads(m, n) > kMaxThreads)
     return fail(GPTQ_EINVAL, "gradient too large for one launch");
   *bytes = (keep_grad_plan(R, (int)E, m, n).part_bytes + 255) / 256 * 256;
   return GPTQ_OK;

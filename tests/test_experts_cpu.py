@@ -250,3 +250,16 @@ def test_row_calls_are_refused_by_their_launch_alone():
     for T in (2 ** 24 + 5, 2 ** 31 - 65536):
         assert lib.gptq_route_workspace_bytes(T, 1, 8, ctypes.byref(out)) == 0
         assert out.value == (9 * (-(-T // 1024) + 1) * 4 + 255) // 256 * 256
+
+
+def test_weight_gradient_is_refused_by_its_launch_alone():
+    """More than 2^32 values in all the experts' gradients are allowed; what
+    counts is the tiles of one of them."""
+    G, lib = _lib()
+    out = ctypes.c_size_t(0)
+    need = lib.gptq_checkpoint_weight_grad_workspace_bytes
+    for R, E, m, n in ((16384, 128, 6144, 6144), (64, 1024, 28672, 8192), (5, 2, 33000, 65600), (1, 1, 1, 2 ** 31 - 65536),
+                       (1, 1, 2 ** 31 - 65536, 1)):
+        assert need(R, E, m, n, ctypes.byref(out)) == 0 and out.value == 0
+    for m, n in ((2 ** 20, 2 ** 20), (2 ** 31 - 65536, 129), (32, 2 ** 31)):
+        assert need(100, 1, m, n, ctypes.byref(out)) == -1

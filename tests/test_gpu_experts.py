@@ -725,3 +725,20 @@ def test_route_of_many_tokens():
     assert torch.equal(r.rows[:kept].long(), order[:kept]) and torch.all(r.rows[kept:] == -1)
     assert torch.equal(r.inverse[order[:kept], 0].long(), torch.arange(kept, device="cuda"))
     assert torch.all(r.inverse[order[kept:], 0] == -1)
+
+
+@pytest.mark.parametrize("m", [33000, 33001])
+def test_weight_gradient_beyond_32_bits(m):
+    """A gradient of more than 2^32 elements (2 experts of m x 65600): every
+    column of some rows against the formula."""
+    E, n, T = 2, 65600, 5
+    P_, X = values(m, T, m), values(3, T, n)
+    kept = G.checkpoint_save(X)
+    x = G.checkpoint_restore(kept, F32).double()
+    off = torch.tensor([0, 2, 5], dtype=torch.int32).cuda()
+    g = G.checkpoint_weight_grad(P_, kept, offsets=off)
+    for e, (lo, hi) in enumerate(((0, 2), (2, 5))):
+        for rows in (slice(0, 300), slice(m // 2, m // 2 + 300), slice(m - 300, m)):
+            p = P_[lo:hi, rows].double()
+            ref, mag = p.t().contiguous() @ x[lo:hi], p.abs().t().contiguous() @ x[lo:hi].abs()
+            assert torch.all((g[e, rows].double() - ref).abs() <= (hi - lo + 64) * U32 * mag)
