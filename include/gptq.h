@@ -351,7 +351,8 @@ gptq_status gptq_combine_grad(void *stream, const void *dY, int32_t dydt, int64_
  * order.
  *
  * d_out >= 1, n >= 1; R == 0 enqueues nothing. Rows of X and dY may have any
- * alignment (16-byte aligned rows are faster). Asynchronous. Workspace:
+ * alignment (16-byte aligned rows are faster). Fewer than 2^24 - 16 tiles of 64
+ * or 128 rows x 128 columns, E - 1 rows of tiles more than R needs. Asynchronous. Workspace:
  * gptq_expert_matmul_workspace_bytes / gptq_expert_matmul_grad_workspace_bytes
  * (fp32 partial results when few tiles split the sum; 0 for most sizes).
  * ("El balance de errores de la inferencia de pocos bits", section 6: decode
@@ -380,7 +381,7 @@ gptq_status gptq_expert_matmul_grad(void *stream, const void *dY, int32_t dydt, 
  * With 2^p <= max|x| < 2^(p + 1) the step is 2^(p - 6): errors are at most
  * half a step, up to a whole one within half a step of 2^(p + 1). x_hat is
  * exact in bf16. A group with an infinity or NaN has exps = 255 and codes 0
- * and comes back as NaN.
+ * and comes back as NaN. T ceil(n / 32) is at most 2^30 - 128.
  *
  * gptq_checkpoint_weight_grad: G (E x m x n fp32, contiguous) with
  * G[e] = sum over the rows p of segment e of P[p]^T x_hat[rows[p]] (P: R x m

@@ -301,7 +301,7 @@ struct ExpertSplit {
 };
 // pieces: the gradient with an fp32 result
 ExpertSplit expert_split(int64_t R, int E, int64_t n, int64_t d_out, int group, int grad, bool pieces);
-int64_t expert_grid(const ExpertArgs& a, int grad);   // an upper bound on the workgroups of a launch
+int64_t expert_threads(const ExpertArgs& a, int grad);   // an upper bound on the threads of a launch's first dimension
 hipError_t launch_expert_mm(hipStream_t s, const ExpertArgs& a);
 hipError_t launch_expert_mm_grad(hipStream_t s, const ExpertArgs& a);
 struct KeepGradPlan {

@@ -1864,10 +1864,12 @@ ExpertSplit expert_split(int64_t R, int E, int64_t n, int64_t d_out, int group, 
   return sp;
 }
 
-int64_t expert_grid(const ExpertArgs& a, int grad) {
+int64_t expert_threads(const ExpertArgs& a, int grad) {
   const int bm = expert_bm(a, grad);
   const int64_t cols = grad ? a.n : a.d_out;
-  return row_tiles(a.R, a.E, bm) * ceil_div(cols, bm == 16 ? 32 : (bm == 256 ? 256 : 128)) + 8;
+  if (bm == 16) return ceil_div(cols, 32) * 256;           // the row tiles are the second dimension
+  return bm == 256 ? (row_tiles(a.R, a.E, 256) * ceil_div(cols, 256) + 8) * 512
+                   : (row_tiles(a.R, a.E, bm) * ceil_div(cols, 128) + 8) * 256;
 }
 
 template <int BITS>

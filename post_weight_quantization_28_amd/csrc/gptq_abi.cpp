@@ -1060,11 +1060,11 @@ gptq_status experts_check(int64_t E, const int32_t* offsets) {
 
 // The checks that both expert products share (R > 0).
 gptq_status expert_weights_check(const ExpertArgs& a, int grad) {
+  if (expert_threads(a, grad) > kMaxThreads) return fail(GPTQ_EINVAL, "product too large for one launch");
   if (!a.A || !a.qw || !a.scales || !a.zeros || !a.Y) return fail(GPTQ_EINVAL, "NULL pointer");
   if (mis(a.A, GPTQ_BF16) || mis(a.Y, a.y_bf16 ? GPTQ_BF16 : GPTQ_F32))
     return fail(GPTQ_EINVAL, "a matrix is not aligned to its elements");
   if (((uintptr_t)a.qw & 15) != 0) return fail(GPTQ_EINVAL, "qweight must be 16-byte aligned");
-  if (expert_grid(a, grad) > kMaxThreads / 512) return fail(GPTQ_EINVAL, "product too large for one launch");
   return GPTQ_OK;
 }
 

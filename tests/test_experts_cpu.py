@@ -263,3 +263,23 @@ def test_weight_gradient_is_refused_by_its_launch_alone():
         assert need(R, E, m, n, ctypes.byref(out)) == 0 and out.value == 0
     for m, n in ((2 ** 20, 2 ** 20), (2 ** 31 - 65536, 129), (32, 2 ** 31)):
         assert need(100, 1, m, n, ctypes.byref(out)) == -1
+
+
+def test_products_are_refused_by_their_launch_alone():
+    G, lib = _lib()
+
+    def why(R, E, d, n, grad):
+        if grad:
+            st = lib.gptq_expert_matmul_grad(None, NULL, 0, R, d, FAKE, E, FAKE, FAKE, FAKE, d, n, 4, 32, FAKE, 0, n, None, 0)
+        else:
+            st = lib.gptq_expert_matmul(None, NULL, 0, R, n, n, NULL, R, FAKE, E, FAKE, FAKE, FAKE, d, 4, 32, FAKE, 0, d,
+                                        None, 0)
+        assert st == -1
+        return lib.gptq_last_error().decode()
+    # 256 threads a tile: 2^17 x 127 tiles of 128 x 128 fit, 2^17 x 128 (2^32 threads) do not
+    for R, E, wide in ((16384, 1024, 2 ** 20), (2 ** 23, 8, 2 ** 14), (2 ** 24, 1, 2 ** 14 - 128)):
+        assert "NULL pointer" in why(R, E, wide, 32, False)
+        if R > 16 * E:
+            assert "NULL pointer" in why(R, E, 32, wide, True)
+    for R, E, wide in ((2 ** 24, 1, 2 ** 14 + 128), (2 ** 30, 1, 2 ** 20)):
+        assert "too large" in why(R, E, wide, 32, False) and "too large" in why(R, E, 32, wide, True)
