@@ -282,4 +282,6 @@ def test_products_are_refused_by_their_launch_alone():
         if R > 16 * E:
             assert "NULL pointer" in why(R, E, 32, wide, True)
     for R, E, wide in ((2 ** 24, 1, 2 ** 14 + 128), (2 ** 30, 1, 2 ** 20)):
-        assert "too large" in why(R, E, wide, 32, False) and "too large" in why(R, E, 32, wide, True)
+        assert "too large" in why(R, E, wide, 32, False)
+    # (the gradient of the first of them goes in 256 x 256 tiles, of which 2^16 x 65 fit)
+    assert "NULL pointer" in why(2 ** 24, 1, 32, 2 ** 14 + 128, True) and "too large" in why(2 ** 30, 1, 32, 2 ** 20, True)
