@@ -336,9 +336,9 @@ gptq_status gptq_combine_grad(void *stream, const void *dY, int32_t dydt, int64_
  * Products of activations and integers are exact in fp32, sums are fp32 in a
  * fixed order, and groups are scaled in fp32: the weights are not rounded.
  * Results are bitwise reproducible. Few rows per expert (R <= 16 E, 16-byte
- * aligned) take a matrix-vector form, in which an infinite activation, or one
- * above 2^123, may give NaN or an infinity where the sum is infinite or still
- * finite. Many (R > 512 E, 4 bits, groups that are multiples of 128, tiles for
+ * aligned) take a matrix-vector form, which at 4 bits sums x (16 + q) over 128
+ * codes: an infinite activation, or one above 2^116, may give NaN or an
+ * infinity there where the sum is infinite or still finite. Many (R > 512 E, 4 bits, groups that are multiples of 128, tiles for
  * half of the GPU) keep one running sum in units of the current group's scale;
  * there the weights of a group whose scale is outside 2^-40 .. 2^40 are
  * rounded to bf16.

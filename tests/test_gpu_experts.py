@@ -742,3 +742,23 @@ def test_weight_gradient_beyond_32_bits(m):
             p = P_[lo:hi, rows].double()
             ref, mag = p.t().contiguous() @ x[lo:hi], p.abs().t().contiguous() @ x[lo:hi].abs()
             assert torch.all((g[e, rows].double() - ref).abs() <= (hi - lo + 64) * U32 * mag)
+
+
+def test_large_activations():
+    """Few rows at 4 bits sum x (16 + q) over 128 codes (32 in small groups):
+    activations up to 2^116 keep that in range, of one sign all of them, as
+    the sum of x (q - z) may be in any form."""
+    for n, group in ((256, 128), (384, 64)):
+        qw, sc, zr = layers(1, 1, 96, n, 4, group)
+        sc = (sc * 2.0 ** -60).astype(np.float32)
+        W = dequantize(qw[0], sc[0], zr[0], 4, group, n)
+        S = np.repeat(np.abs(sc[0].astype(np.float64)), group, axis=1)
+        for R in (5, 16, 60, 200):
+            X = torch.full((R, n), 2.0 ** 116, dtype=BF16, device="cuda")
+            X[1], X[2, 7], X[3, ::2] = -2.0 ** 116, 1.0, 0.0
+            Y = arr(G.expert_matmul(X, None, *cuda_layers(qw, sc, zr), 4, group))
+            ref, mag = arr(X) @ W.T, np.abs(arr(X)) @ np.abs(W).T
+            e = U32 * (n + n // group + 2) * mag
+            if R <= 16:
+                e = U32 * (130 * 62 * (np.abs(arr(X)) @ S.T) + (n // 32 + 1) * mag)
+            assert np.all(np.abs(Y - ref) <= e)
