@@ -341,7 +341,8 @@ gptq_status gptq_combine_grad(void *stream, const void *dY, int32_t dydt, int64_
  * infinity there where the sum is infinite or still finite. Many (R > 512 E, 4 bits, groups that are multiples of 128, tiles for
  * half of the GPU) keep one running sum in units of the current group's scale;
  * there the weights of a group whose scale is outside 2^-40 .. 2^40 are
- * rounded to bf16.
+ * rounded to bf16, a partial sum above 2^88 may become infinite (in a group of
+ * scale 2^-40), and what is below 2^-109 may be lost (scale 2^40).
  *
  * gptq_expert_matmul_grad: dX[p] = dY[p] W_hat_e (dX: R x n, dxdt; dY: R x
  * d_out bf16, row pitch ldy). The scale changes along this sum: with a bf16

@@ -762,3 +762,29 @@ def test_large_activations():
             if R <= 16:
                 e = U32 * (130 * 62 * (np.abs(arr(X)) @ S.T) + (n // 32 + 1) * mag)
             assert np.all(np.abs(Y - ref) <= e)
+
+
+def test_units_carried_from_end_to_end():
+    """Many rows at 4 bits keep the running sum in units of the current
+    group's scale: neighbouring groups whose scales are next to the two ends
+    of the range in which it is carried (2^-40 .. 2^40), and beside them,
+    rising, falling and in turn."""
+    n, group, R, d = 512, 128, 700, 10760
+    lo, hi = 2.0 ** -40, 2.0 ** 40
+    under, over = float(np.nextafter(np.float32(lo), np.float32(0))), float(np.nextafter(np.float32(hi), np.float32(np.inf)))
+    rows = [[lo, hi, lo, hi], [hi, lo, hi, lo], [lo, lo, hi, hi], [hi, hi, lo, lo], [lo, 1.0, hi, -lo], [-hi, lo, -lo, hi],
+            [under, hi, over, lo], [hi, under, lo, over], [over, lo, under, hi], [1.5 * lo, hi / 1.5, 1.5 * lo, hi / 1.5]]
+    qw, sc, zr = layers(1, 1, d, n, 4, group)
+    sc[0, :len(rows)] = np.array(rows, np.float32)
+    sc[0, d - len(rows):] = np.array(rows, np.float32)[::-1]
+    X = values(R, R, n)
+    X[1, 256:] = 0                                      # rows that end with zeros keep what came before
+    X[2, 384:] = 0
+    X[3, :384] = 0
+    W = dequantize(qw[0], sc[0], zr[0], 4, group, n)
+    ref, mag = arr(X) @ W.T, np.abs(arr(X)) @ np.abs(W).T
+    odd = np.repeat((np.abs(sc[0]) < lo) | (np.abs(sc[0]) > hi), group, axis=1)
+    e = U32 * (n + 3 * (n // group) + 1) * mag + (UBF + U32) * 1.01 * (np.abs(arr(X)) @ (np.abs(W) * odd).T)
+    for odt in (F32, BF16):
+        Y = arr(G.expert_matmul(X, None, *cuda_layers(qw, sc, zr), 4, group, out_dtype=odt))
+        assert np.all(np.abs(Y - ref) <= e + (UBF * (np.abs(ref) + e) if odt == BF16 else 0))
