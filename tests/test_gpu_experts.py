@@ -788,3 +788,61 @@ def test_units_carried_from_end_to_end():
     for odt in (F32, BF16):
         Y = arr(G.expert_matmul(X, None, *cuda_layers(qw, sc, zr), 4, group, out_dtype=odt))
         assert np.all(np.abs(Y - ref) <= e + (UBF * (np.abs(ref) + e) if odt == BF16 else 0))
+
+
+MANY = [   # T, k, E, d, n, group, only (experts beside the borders of 64, others empty)
+    (70, 2, 130, 40, 256, 128, [0, 63, 64, 66, 127, 128, 129]),     # matrix-vector form
+    (33, 2, 65, 33, 96, 32, [62, 64]),
+    (50, 4, 1024, 24, 128, 64, None),
+    (600, 2, 65, 40, 192, 64, [0, 60, 63, 64]),                     # 64-row tiles
+    (1100, 2, 130, 70, 128, 128, [1, 62, 63, 65, 129]),
+    (4200, 4, 1024, 24, 32, 32, None),
+    (300, 4, 65, 33, 2048, 128, [3, 64]),                           # parts of K
+    (1950, 2, 65, 700, 64, 32, None),                               # 128-row tiles
+    (33400, 1, 65, 160, 128, 128, [0, 1, 63, 64]),                  # 256-row tiles (4 bits)
+]
+
+
+@pytest.mark.parametrize("bits", [4, 3])
+@pytest.mark.parametrize("T,k,E,d,n,group,only", MANY)
+def test_more_than_64_experts(T, k, E, d, n, group, only, bits):
+    """The product, its gradient in both types and the weight gradient where
+    the look-up of a tile's expert goes beyond 64 of them."""
+    off, rows, _ = X64.route(expert_ids(T + d, T, k, E, 0.05, only), E)
+    R = T * k
+    X, dY = values(n + T, T, n), values(R + d, R, d, scale=1e-3)
+    qw, sc, zr = layers(d + bits, E, d, n, bits, group)
+    ot, rt, wl = torch.from_numpy(off).cuda(), torch.from_numpy(rows).cuda(), cuda_layers(qw, sc, zr)
+    out = values(8, R, d, dtype=F32)
+    before = arr(out)
+    Y = arr(G.expert_matmul(X, ot, *wl, bits, group, rows=rt, out=out))
+    ref = X64.expert_matmul(arr(X), off, qw, sc, zr, bits, group, n, rows, before)
+    tol = product_bound(arr(X), off, rows, qw, sc, zr, bits, group, n, R, E)
+    assert np.all(np.abs(Y - ref)[:off[-1]] <= tol[:off[-1]])
+    assert np.array_equal(Y[off[-1]:], before[off[-1]:])
+    mag = np.zeros((R, n))
+    for e in range(E):
+        if off[e] < off[e + 1]:
+            mag[off[e]:off[e + 1]] = np.abs(arr(dY)[off[e]:off[e + 1]]) @ np.abs(dequantize(qw[e], sc[e], zr[e], bits, group, n))
+    for odt in (BF16, F32):
+        out = values(8, R, n, dtype=odt)
+        before = arr(out)
+        dX = arr(G.expert_matmul_grad(dY, ot, *wl, bits, group, n, out=out))
+        ref = X64.expert_matmul_grad(arr(dY), off, qw, sc, zr, bits, group, n, before)
+        err = ((UBF + U32 + d * U32) if odt == BF16 else (UBF ** 3 + U32 + 3 * d * U32)) * 1.01 * mag
+        tol = err + (UBF * (np.abs(ref) + err) if odt == BF16 else 0)
+        assert np.all(np.abs(dX - ref)[:off[-1]] <= tol[:off[-1]])
+        assert np.array_equal(dX[off[-1]:], before[off[-1]:])
+
+
+@pytest.mark.parametrize("T,k,E,m,n,only", [(300, 2, 130, 24, 64, [0, 63, 64, 127, 128, 129]), (900, 2, 65, 136, 70, [63, 64]),
+                                            (2100, 2, 1024, 40, 33, None)])
+def test_weight_gradient_of_more_than_64_experts(T, k, E, m, n, only):
+    off, rows, _ = X64.route(expert_ids(T + m, T, k, E, 0.05, only), E)
+    X, Pm = values(T + n, T, n), values(T + m, T * k, m, scale=1e-3)
+    kept = G.checkpoint_save(X)
+    vals = arr(G.checkpoint_restore(kept, F32))
+    g = arr(G.checkpoint_weight_grad(Pm, kept, offsets=torch.from_numpy(off).cuda(), rows=torch.from_numpy(rows).cuda()))
+    ref = X64.weight_grad(arr(Pm), vals, off, rows)
+    mag = X64.weight_grad(np.abs(arr(Pm)), np.abs(vals), off, rows)
+    assert np.all(np.abs(g - ref) <= (T * k + 64) * U32 * mag)
