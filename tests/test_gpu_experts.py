@@ -846,3 +846,37 @@ def test_weight_gradient_of_more_than_64_experts(T, k, E, m, n, only):
     ref = X64.weight_grad(arr(Pm), vals, off, rows)
     mag = X64.weight_grad(np.abs(arr(Pm)), np.abs(vals), off, rows)
     assert np.all(np.abs(g - ref) <= (T * k + 64) * U32 * mag)
+
+
+def test_results_above_128_mb():
+    """Results that are stored past the caches: the way there, the 8-bit
+    copy's values and the wide weight gradient, against calls on parts."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+
+    def normal(rows, cols, dtype=BF16):
+        return torch.randn(rows, cols, generator=gen, device="cuda").to(dtype)
+    T, k, E, n = 4100, 4, 8, 4104                       # 134.6 MB
+    r = G.route(torch.from_numpy(expert_ids(1, T, k, E, 0.01)).cuda(), E)
+    X = normal(T, n)
+    last = int(r.offsets[-1])
+    Xs = torch.zeros(T * k, n, dtype=BF16, device="cuda")
+    G.dispatch(X, r.inverse, out=Xs)
+    assert torch.equal(Xs[:last], X[r.rows[:last].long()]) and torch.count_nonzero(Xs[last:]) == 0
+    for T, dtype in ((16500, BF16), (8250, F32)):       # 135.4 MB
+        kept = G.checkpoint_save(normal(T, n, dtype))
+        whole = G.checkpoint_restore(kept, dtype)
+        for a in range(0, T, 4000):
+            part = G.Checkpoint(kept.codes[a:a + 4000], kept.exps[a:a + 4000], n)
+            assert torch.equal(whole[a:a + 4000], G.checkpoint_restore(part, dtype))
+    E, m, n, T = 4, 2048, 4104, 300                     # 134.5 MB
+    off, rows, _ = X64.route(expert_ids(5, T, 2, E, 0.1), E)
+    Pm = 1e-3 * normal(2 * T, m)
+    kept = G.checkpoint_save(normal(T, n))
+    rt = torch.from_numpy(rows).cuda()
+    g = G.checkpoint_weight_grad(Pm, kept, offsets=torch.from_numpy(off).cuda(), rows=rt)
+    x = G.checkpoint_restore(kept, F32)
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        p, v = Pm[lo:hi].double().t().contiguous(), x[rt[lo:hi].long()].double()
+        assert torch.all((g[e].double() - p @ v).abs() <= (hi - lo + 64) * U32 * (p.abs() @ v.abs()))
+        assert torch.equal(g[e], G.checkpoint_weight_grad(Pm[lo:hi], kept, rows=rt[lo:hi])[0])
