@@ -120,27 +120,19 @@ __device__ __forceinline__ void load_chunk(const uint32_t* __restrict__ p, uint3
   }
 }
 
-// Codes 8 j .. 8 j + 7 of a chunk, minus z, as floats (exact).
+// Codes 8 j .. 8 j + 7 of a chunk of 2- or 3-bit codes, minus z, as floats
+// (exact).
 template <int BITS>
 __device__ __forceinline__ void codes8(const uint32_t (&w)[BITS], int j, float z, float (&f)[8]) {
-  if constexpr (BITS == 4) {
-    // byte i of lo / hi holds code 2 i / 2 i + 1: one conversion per code
-    const uint32_t lo = w[j] & 0x0F0F0F0Fu, hi = (w[j] >> 4) & 0x0F0F0F0Fu;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = (float)((lo >> (8 * i)) & 0xFFu) - z;
-      f[2 * i + 1] = (float)((hi >> (8 * i)) & 0xFFu) - z;
-    }
-  } else {
-    const int base = 8 * BITS * j, wi = base >> 5, sh = base & 31;
-    uint64_t v = w[wi];
-    if constexpr (BITS == 3) {
-      if (wi + 1 < BITS) v |= (uint64_t)w[wi + 1] << 32;
-    }
-    v >>= sh;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = (float)(uint32_t)((v >> (BITS * i)) & ((1u << BITS) - 1u)) - z;
+  static_assert(BITS < 4, "4-bit codes go by mv_codes<4>");
+  const int base = 8 * BITS * j, wi = base >> 5, sh = base & 31;
+  uint64_t v = w[wi];
+  if constexpr (BITS == 3) {
+    if (wi + 1 < BITS) v |= (uint64_t)w[wi + 1] << 32;
   }
+  v >>= sh;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = (float)(uint32_t)((v >> (BITS * i)) & ((1u << BITS) - 1u)) - z;
 }
 
 // Two floats whose low halves are zero (small integers, kept values) as bf16.
@@ -540,29 +532,13 @@ __device__ __forceinline__ ex_u32x4_t xexpand(uint32_t w, uint32_t bias, float f
   return o;
 }
 
-// The words of NB units of 8 codes, unit u0 (a multiple of NB) of a packed
-// row, and unit e of them minus z as floats.
-template <int BITS, int NB>
+// The words of 4 units of 8 codes (a chunk), unit u0 (a multiple of 4) of a
+// packed row, and unit e of them minus z as floats.
+template <int BITS>
 struct UnitWords {
-  static constexpr int N = (BITS * NB * 8 + 31) / 32;
-  uint32_t w[N];
-  int sh;
+  uint32_t w[BITS];
   __device__ __forceinline__ void load(const uint32_t* __restrict__ row, int64_t u0) {
-    const int64_t bit = u0 * (8 * BITS);
-    const uint32_t* __restrict__ p = row + (bit >> 5);
-    sh = BITS == 3 && NB == 2 ? (int)(bit & 31) : 0;     // 48 bits from bit 0 or 16
-    if constexpr (BITS == 4 && NB == 4) {
-      const ex_u32x4_t v = *reinterpret_cast<const ex_u32x4_t*>(p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = v[i];
-    } else if constexpr (BITS == 4 && NB == 2) {
-      const uint64_t v = *reinterpret_cast<const uint64_t*>(p);
-      w[0] = (uint32_t)v;
-      w[1] = (uint32_t)(v >> 32);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = p[i];
-    }
+    load_chunk<BITS>(row + (u0 * (8 * BITS) >> 5), w);
   }
   __device__ __forceinline__ void get(int e, float z, float (&f)[8]) const {
     if constexpr (BITS == 4) {
@@ -576,8 +552,8 @@ struct UnitWords {
     } else {
       const int base = 8 * BITS * e, wi = base >> 5;
       uint64_t v = w[wi];
-      if (BITS == 3 && wi + 1 < N) v |= (uint64_t)w[wi + 1] << 32;
-      v >>= (base & 31) + sh;
+      if (BITS == 3 && wi + 1 < BITS) v |= (uint64_t)w[wi + 1] << 32;
+      v >>= base & 31;
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = (float)(uint32_t)((v >> (BITS * i)) & ((1u << BITS) - 1u)) - z;
     }
@@ -705,7 +681,8 @@ k_expert_mm(ExArgs p) {
 
   constexpr int DA = TL::DA, DB = TL::DB, U = TL::U;
   ex_u32x4_t ra[DA][PA];
-  UnitWords<BITS, NB> rb[DB];
+  static_assert(NB == 4, "a chunk per load");
+  UnitWords<BITS> rb[DB];
   uint32_t rz[DB];
   auto aload = [&](auto S, int st) {
 #pragma unroll
@@ -871,7 +848,8 @@ k_expert_mm_grad(ExArgs p) {
 
   constexpr int DA = TL::DA, DB = TL::DB, U = TL::U;
   ex_u32x4_t ra[DA][PA];
-  UnitWords<BITS, NB> rb[DB];
+  static_assert(NB == 4, "a chunk per load");
+  UnitWords<BITS> rb[DB];
   float rs[DB];
   uint32_t rz[DB];
   bool rv[DB];
