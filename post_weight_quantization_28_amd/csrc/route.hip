@@ -16,9 +16,9 @@
 // The order is a counting sort whose ranks come from ballots, never from
 // atomics that return a place, so it does not depend on timing. Everything
 // here is bound by memory (or, for a few tokens, by the launches): the
-// copies are organised by token, so each row of X and dY is read once and
-// its k copies leave from registers, and the way back adds the k rows in
-// the order of j in fp32 and rounds once.
+// copies are organised by token, so each row of X is read once (dY: once for
+// four slots) and its copies leave from registers, and the way back adds the
+// k rows in the order of j in fp32 and rounds once.
 #include "common.h"
 #include "dma.h"
 
@@ -253,8 +253,9 @@ hipError_t launch_route(hipStream_t s, const int32_t* ids, int64_t ldi, int64_t 
 }
 
 // ---------------------------------------------------------------- rows there and back
-// The rows of Ys and dY are read once, so they are loaded past the caches
-// (268 MB of Ys: 80 against 94 us).
+// The rows of Ys are read once, so where they are aligned they are loaded past
+// the caches, whatever their number (268 MB of Ys: 80 against 94 us), and dY
+// with them, which the gradient reads once for each four slots of a token.
 // A unit is 8 columns: 16 bytes of bf16, 32 of fp32.
 //   kAligned: every row of both sides is 16-byte aligned and n % 8 == 0, so
 //     units move as whole 16-byte pieces;
