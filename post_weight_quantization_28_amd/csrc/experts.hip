@@ -1419,7 +1419,6 @@ struct KgArgs {
   const int32_t* rows; const int32_t* offsets; int E, R;
   int nmt, nnt, splits;
   float* out; int64_t split_stride;   // out[split][e][m][n]
-  int stream;                         // a large G is stored past the caches (268 MB: 230 against 241 us)
 };
 
 template <class TL, bool WIDE>
@@ -1756,10 +1755,7 @@ k_keep_ring(KgArgs p) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int64_t row = m0 + 128 * wm + 32 * mi + 8 * (r >> 2) + 4 * h + (r & 3);
-        if (row < p.m) {
-          if (p.stream) __builtin_nontemporal_store(acc[mi][ni][r], out + row * p.n + c);
-          else out[row * p.n + c] = acc[mi][ni][r];
-        }
+        if (row < p.m) out[row * p.n + c] = acc[mi][ni][r];
       }
   }
 }
@@ -2031,7 +2027,6 @@ hipError_t launch_keep_grad(hipStream_t s, const KeepGradPlan& pl, const uint16_
   p.splits = pl.splits;
   p.out = pl.splits > 1 ? part : G;
   p.split_stride = (int64_t)E * m * n;
-  p.stream = pl.splits == 1 && p.split_stride * 4 > kStreamBytes;
   const bool vec = bf16_rows_vec(P, ldp, m);
   // the ring's offsets into the codes are 32 bits
   const int bm = pl.bm == 256 && !(vec && T * p.pitch < ((int64_t)1 << 32)) ? 128 : pl.bm;
