@@ -246,15 +246,23 @@ hipError_t launch_dequant_mm(hipStream_t s, const DqPlan& p, const uint16_t* X, 
                              int64_t ldx, const uint32_t* qw, const float* scales, const uint8_t* zeros,
                              int64_t d_out, int bits, int group, float* Y, int64_t ldy, float* part);
 
-// Outputs above this many bytes are stored past the caches (non-temporal):
-// they do not fit beside the inputs in the 256 MB last-level cache, and the
-// next reader finds nothing of them there either way. Smaller ones stay
-// cached for it.
+// Copies of aligned rows (the way there, the 8-bit copy's values) above this
+// many bytes are stored past the caches (non-temporal). The copy alone is
+// faster so at every size; what reads the result next loses up to about the
+// 256 MB of the last-level cache. Captured calls, us past the caches / through
+// them: the way there alone 34 MB 7.3 / 9.0, 101 MB 18.9 / 21.5, 134 MB 28 /
+// 28, 268 MB 57 / 64, 403 MB 73 / 92; with the way back after it 18 / 18, 44 /
+// 41, 58 / 52, 113 / 101, 154 / 160. The values of the 8-bit copy alone 134 MB
+// 30 / 37, 268 MB 67 / 71; saved again after it 101 MB 57 / 57, 134 MB 74 / 72,
+// 201 MB 107 / 112, 268 MB 141 / 147.
 constexpr int64_t kStreamBytes = (int64_t)128 << 20;
 
 // ---- route.hip: tokens in the order of their experts, and back
 constexpr int kRouteMaxExperts = 1024;
-constexpr int64_t kRouteOneBlock = 4096;    // slots up to which one workgroup does it all
+// Slots up to which one workgroup does it all, the most that its 16 waves hold.
+// 512 and 4096 slots of 8 experts 7.2 and 9.9 us (of 1024 experts 9.3 and 12.8),
+// in three launches 11.6 and 12.5 (15.8 and 17.7).
+constexpr int64_t kRouteOneBlock = 4096;
 constexpr int64_t kRouteBlockSlots = 1024;  // slots per workgroup beyond
 size_t route_workspace(int64_t R, int64_t E);
 hipError_t launch_route(hipStream_t s, const int32_t* ids, int64_t ldi, int64_t T, int k, int E, int32_t* offsets,

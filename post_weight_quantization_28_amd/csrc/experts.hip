@@ -173,7 +173,8 @@ __device__ __forceinline__ uint32_t pack_exact(float a, float b) {
 // the rest the weights' way from memory. One load per scale and piece instead
 // of one per S pieces: 22.9 / 42.5; 8 waves per workgroup 22.0 / 67;
 // 16 outputs per wave 19.8 / 40; 64 outputs 23.5 / 32.6; the weights loaded
-// past the caches 20.9 / 32.9.
+// past the caches 20.9 / 32.9. In captured calls, which take 20.3 / 32.5: four
+// pieces asked for at a time 19.6 / 33.0, one 24.6 / 38.0.
 template <int BITS>
 __device__ __forceinline__ ex_bf16x8_t mv_window(const uint32_t* __restrict__ chunk, int j, float z) {
   const int base = 8 * BITS * j, wi = base >> 5;
@@ -1780,7 +1781,11 @@ static bool bf16_rows_vec(const void* p, int64_t ld, int64_t cols) {
 // (gradient), offsets from the bases that fit 32 bits, tiles for half of the
 // chip at least (fewer are better split along K), and more columns than the
 // smaller tile has (65536 rows, 128 outputs of 4096: 157 us here, 105 us in
-// 128 x 128 tiles; gradient 173 and 134 us).
+// 128 x 128 tiles; gradient 173 and 134 us). One expert, K 4096, ring and
+// smaller tiles: 64 tiles (2048 x 2048) 122 and 69 us, gradient 107 and 66; 128
+// tiles (1024 x 8192) 121 and 95, 106 and 96; 172 tiles (1024 x 11008) 122 and
+// 136, 112 and 137; 256 tiles (2048 x 8192) 144 and 183, 131 and 180. Between
+// 128 and about 160 tiles the smaller ones are still ahead.
 static bool ring_fits(const ExpertArgs& a, int grad) {
   const int64_t lim = (int64_t)1 << 32;
   if (a.bits != 4 || a.d_out * (a.n / 2) >= lim || a.lda >= lim / 2 / std::max(a.T, 1)) return false;
@@ -1805,6 +1810,16 @@ static int small_bm(int64_t R, int E, int64_t cols, int grad, bool pieces) {
 }
 
 // Rows of a tile: 16 is the matrix-vector form, 256 the ring kernel.
+//  * Matrix-vector form and 64-row tiles, 4 bits: 8 experts of 4096 x 4096 with
+//    4, 16, 20 and 32 rows each 26, 45, 54, 71 and 42, 46, 44, 49 us; 64 of
+//    1408 x 2048 with 4, 16, 20 and 24 rows 29, 57, 65, 74 and 53, 58, 59, 63;
+//    groups of 64 with 16 rows 58 and 57, 77 and 74. (3 bits stay ahead longer:
+//    24 rows 58 and 74, 74 and 108.)
+//  * Ring and 128-row tiles: 8 experts of 4096 x 4096 with 512, 640 and 1024
+//    rows each 247, 251, 381 and 219, 258, 392 us, gradient 222, 228, 348 and
+//    219, 257, 391; 8 of 11008 x 4096 506, 562, 901 and 568, 661, 1030. Fewer
+//    rows go either way with how full the last tiles are (256 rows: 125 and 136,
+//    but 372 and 343).
 static int expert_bm(const ExpertArgs& a, int grad) {
   const int64_t avg = ceil_div(a.R, a.E);
   const bool vec = bf16_rows_vec(a.A, a.lda, grad ? a.d_out : a.n);
