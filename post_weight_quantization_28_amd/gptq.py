@@ -4,6 +4,9 @@ Every step of the computation runs in the HIP kernels of libgptq.so; PyTorch
 provides device memory and the current stream. There is no fallback: if the
 library is not built, or a tensor is not on the GPU, the calls raise.
 The names mirror include/gptq.h.
+Tensors are memory here: no call records anything for autograd, and outputs
+require no gradient whatever the inputs do. Gradients are calls of their own
+(combine_grad, expert_matmul_grad, checkpoint_weight_grad).
 """
 import ctypes
 import functools
@@ -475,11 +478,22 @@ def route(expert_ids, n_experts, workspace=None):
     return r
 
 
-def _slots(inverse, device, T):
-    if not isinstance(inverse, torch.Tensor) or inverse.dim() != 2:
+def _slots(inverse, device, T=None):
+    """Pointer of the places (T x k), T and k."""
+    if not isinstance(inverse, torch.Tensor):
+        raise TypeError("inverse must be a CUDA (HIP) tensor")
+    if inverse.dim() != 2:
         raise ValueError("inverse must have two dimensions")
-    k = inverse.shape[1]
-    return _dense(inverse, "inverse", torch.int32, device, (T, k)), k
+    rows, k = inverse.shape
+    T = rows if T is None else T
+    return _dense(inverse, "inverse", torch.int32, device, (T, k)), T, k
+
+
+def _length(t, name):
+    """Entries of a list of places or rows, before the rest of it is looked over."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    return t.numel()
 
 
 def dispatch(X, inverse, out=None):
@@ -489,7 +503,7 @@ def dispatch(X, inverse, out=None):
     xp, ldx = _rows2d(X, "X", _FLOATS)
     T, n = X.shape
     dev = X.device
-    ip, k = _slots(inverse, dev, T)
+    ip, T, k = _slots(inverse, dev, T)
     out, sp, lds = _result(out, (T * k if out is None else out.shape[0], n), X.dtype, dev, (X.dtype,))
     R = out.shape[0]
     _call(dev, lib.gptq_dispatch, xp, _DTYPE_CODES[X.dtype], T, n, ldx, k, ip, R, sp, lds)
@@ -504,8 +518,7 @@ def combine(Ys, inverse, weights=None, out=None, out_dtype=None):
     sp, lds = _rows2d(Ys, "Ys", _FLOATS)
     R, n = Ys.shape
     dev = Ys.device
-    T = inverse.shape[0]
-    ip, k = _slots(inverse, dev, T)
+    ip, T, k = _slots(inverse, dev)
     wp = None if weights is None else _dense(weights, "weights", torch.float32, dev, (T, k))
     out, yp, ldy = _result(out, (T, n), out_dtype or Ys.dtype, dev)
     _call(dev, lib.gptq_combine, sp, _DTYPE_CODES[Ys.dtype], R, lds, ip, wp, T, n, k, yp, _DTYPE_CODES[out.dtype], ldy)
@@ -524,7 +537,7 @@ def combine_grad(dY, Ys, inverse, weights, out=None, out_dtype=None):
     R, cols = Ys.shape
     if cols != n:
         raise ValueError(f"Ys must have {n} columns")
-    ip, k = _slots(inverse, dev, T)
+    ip, T, k = _slots(inverse, dev, T)
     wp = _dense(weights, "weights", torch.float32, dev, (T, k))
     out, op, ldo = _result(out, (R, n), out_dtype or dY.dtype, dev)
     dw = torch.empty_strided((T, k), (k, 1), dtype=torch.float32, device=dev)
@@ -567,7 +580,7 @@ def expert_matmul(X, offsets, qweight, scales, zeros, bits, group, rows=None, ou
     T, n = X.shape
     dev = X.device
     E, d_out, qp, sp, zp = _expert_layers(qweight, scales, zeros, bits, group, n, dev)
-    R = T if rows is None else rows.numel()
+    R = T if rows is None else _length(rows, "rows")
     op, rp = _segments(offsets, rows, E, dev, R)
     out, yp, ldy = _result(out, (R, d_out), out_dtype, dev)
     need = _bytes("gptq_expert_matmul_workspace_bytes", R, n, d_out, E, bits, group)
@@ -619,9 +632,15 @@ def checkpoint_save(X, out=None):
     return out
 
 
+def _codes(c):
+    codes = getattr(c, "codes", None)
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise TypeError("a Checkpoint is wanted, with two dimensions of codes")
+    return codes
+
+
 def _kept(c, device):
-    groups = (c.n + 31) // 32
-    T = c.codes.shape[0]
+    T, groups = _codes(c).shape[0], (c.n + 31) // 32
     return (_dense(c.codes, "codes", torch.int8, device, (T, 32 * groups)),
             _dense(c.exps, "exps", torch.uint8, device, (T, groups)))
 
@@ -629,7 +648,7 @@ def _kept(c, device):
 def checkpoint_restore(kept, dtype=torch.bfloat16, out=None):
     """The kept values (T x n), exact in bf16 and in fp32."""
     lib = load()
-    dev = kept.codes.device
+    dev = _codes(kept).device
     cp, ep = _kept(kept, dev)
     T, n = kept.codes.shape[0], kept.n
     out, xp, ldx = _result(out, (T, n), dtype, dev)
@@ -647,7 +666,7 @@ def checkpoint_weight_grad(P, kept, offsets=None, rows=None, out=None, workspace
     dev = P.device
     cp, ep = _kept(kept, dev)
     T, n = kept.codes.shape[0], kept.n
-    E = 1 if offsets is None else offsets.numel() - 1
+    E = 1 if offsets is None else _length(offsets, "offsets") - 1
     op, rp = _segments(offsets, rows, E, dev, R)
     need = _bytes("gptq_checkpoint_weight_grad_workspace_bytes", R, E, m, n)
     if out is None:

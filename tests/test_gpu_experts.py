@@ -880,3 +880,34 @@ def test_results_above_128_mb():
         p, v = Pm[lo:hi].double().t().contiguous(), x[rt[lo:hi].long()].double()
         assert torch.all((g[e].double() - p @ v).abs() <= (hi - lo + 64) * U32 * (p.abs() @ v.abs()))
         assert torch.equal(g[e], G.checkpoint_weight_grad(Pm[lo:hi], kept, rows=rt[lo:hi])[0])
+
+
+def test_binding_refuses_what_is_no_tensor():
+    """Lists, None and the like in the place of a tensor are told apart from
+    tensors before anything is read from them."""
+    X, w = values(1, 4, 128), torch.ones(4, 1, device="cuda")
+    inv = torch.arange(4, dtype=torch.int32).reshape(4, 1).cuda()
+    off = torch.tensor([0, 4], dtype=torch.int32).cuda()
+    wl = cuda_layers(*layers(1, 1, 32, 128, 4, 128))
+    kept = G.checkpoint_save(X)
+    for bad in (None, [[0], [1], [2], [3]], inv.cpu()):
+        for call in (lambda: G.dispatch(X, bad), lambda: G.combine(X, bad, w), lambda: G.combine_grad(X, X, bad, w)):
+            with pytest.raises(TypeError):
+                call()
+    for bad in ([0, 4], off.cpu()):
+        for call in (lambda: G.expert_matmul(X, bad, *wl, 4, 128), lambda: G.expert_matmul(X, off, *wl, 4, 128, rows=bad),
+                     lambda: G.expert_matmul_grad(values(2, 4, 32), bad, *wl, 4, 128, 128),
+                     lambda: G.checkpoint_weight_grad(X, kept, offsets=bad), lambda: G.checkpoint_weight_grad(X, kept, rows=bad)):
+            with pytest.raises(TypeError):
+                call()
+    for bad in (None, X):
+        with pytest.raises(TypeError):
+            G.checkpoint_weight_grad(X, bad)
+        with pytest.raises(TypeError):
+            G.checkpoint_restore(bad)
+    with pytest.raises(ValueError):
+        G.combine(X, inv[:, 0], w)
+    with pytest.raises(ValueError):
+        G.dispatch(X, inv[:3])
+    with pytest.raises(TypeError):
+        G.checkpoint_save(X, out=X)
