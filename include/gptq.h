@@ -346,10 +346,11 @@ gptq_status gptq_combine_grad(void *stream, const void *dY, int32_t dydt, int64_
  *
  * gptq_expert_matmul_grad: dX[p] = dY[p] W_hat_e (dX: R x n, dxdt; dY: R x
  * d_out bf16, row pitch ldy). The scale changes along this sum: with a bf16
- * result each weight s (q - z) is rounded to bf16 once (relative 2^-8 at
- * most); with an fp32 result it is taken in three bf16 pieces, which hold
- * its fp32 value, at three times the matrix work. Sums are fp32 in a fixed
- * order.
+ * result each weight's fp32 value s (q - z) is rounded to bf16 once (relative
+ * 2^-8 at most; the result's error is about 1.4 times what its own rounding
+ * gives); with an fp32 result it is taken in three bf16 pieces, which hold
+ * its fp32 value (below 2^-110 to within 2^-134), at three times the matrix
+ * work. Sums are fp32 in a fixed order.
  *
  * d_out >= 1, n >= 1; R == 0 enqueues nothing. Rows of X and dY may have any
  * alignment (16-byte aligned rows are faster). Fewer than 2^24 - 16 tiles of 64

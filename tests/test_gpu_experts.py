@@ -911,3 +911,21 @@ def test_binding_refuses_what_is_no_tensor():
         G.dispatch(X, inv[:3])
     with pytest.raises(TypeError):
         G.checkpoint_save(X, out=X)
+
+
+@pytest.mark.parametrize("R,d,n", [(40, 64, 128), (300, 70, 160), (1100, 64, 6400)])
+def test_gradient_of_tiny_weights(R, d, n):
+    """Three bf16 pieces hold a weight's fp32 value as long as its last bit is
+    not below bf16's smallest step of 2^-133, and what is below that to within
+    half of it; the bf16 result's weights stay within 2^-8 down to 2^-126."""
+    for k in (100, 109, 116, 122):
+        qw, sc, zr = layers(R + k, 1, d, n, 4, 32)
+        sc = (2.0 ** -k * (1.0 + sc)).astype(np.float32)
+        dY = values(R, R, d, scale=2.0 ** 60)
+        W = dequantize(qw[0], sc[0], zr[0], 4, 32, n)
+        ref, mag = arr(dY) @ W, np.abs(arr(dY)) @ np.abs(W)
+        small = np.abs(arr(dY)).sum(1, keepdims=True) * 2.0 ** -134
+        for odt in (BF16, F32):
+            dX = arr(G.expert_matmul_grad(dY, None, *cuda_layers(qw, sc, zr), 4, 32, n, out_dtype=odt))
+            err = ((UBF + U32 + d * U32) * mag if odt == BF16 else (UBF ** 3 + U32 + 3 * d * U32) * mag + small) * 1.01
+            assert np.all(np.abs(dX - ref) <= err + (UBF * (np.abs(ref) + err) if odt == BF16 else 0))
