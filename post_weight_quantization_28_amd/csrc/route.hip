@@ -372,10 +372,12 @@ k_dispatch(const char* __restrict__ X, int64_t ldx, uint32_t T, uint32_t width, 
   }
 }
 
-// Y[t] = sum_j w[t][j] Ys[inverse[t k + j]]. KB rows (1, 2, 4 or 8: the
-// smallest that covers k, at most 8) are loaded before the first is added,
-// so a thread has up to 128 bytes of bf16 in flight.
-template <bool YSBF, bool YBF, int MODE, int KB>
+// Y[t] = sum_j w[t][j] Ys[inverse[t k + j]]. Four rows are loaded before the
+// first is added, so a thread has up to 64 bytes of bf16 in flight (8192 tokens,
+// 8 slots, 2048 columns: 55 us, with eight rows 66; kernels of their own for one
+// and two slots are within 3 % of this one).
+constexpr int kCombineRows = 4;
+template <bool YSBF, bool YBF, int MODE>
 __global__ void __launch_bounds__(256)
 k_combine(const void* __restrict__ Ys, int64_t lds, int R, const int32_t* __restrict__ inverse,
           const float* __restrict__ w, uint32_t T, uint32_t n, uint32_t units, int k, void* __restrict__ Y, int64_t ldy) {
@@ -386,6 +388,7 @@ k_combine(const void* __restrict__ Ys, int64_t lds, int R, const int32_t* __rest
   if constexpr (MODE == kAnywhere) c = min(c, n - 8u);
   const int nc = (int)min(8u, n - c);
   const int64_t s0 = (int64_t)t * k;
+  constexpr int KB = kCombineRows;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int j0 = 0; j0 < k; j0 += KB) {
     float v[KB][8], wj[KB];
@@ -413,7 +416,9 @@ k_combine(const void* __restrict__ Ys, int64_t lds, int R, const int32_t* __rest
 // kCgSlots slots per pass over the columns, whose rows of Ys are all loaded
 // before the first is used, so dY is read once for up to that many. One
 // workgroup per token makes its passes; with few tokens each pass has a
-// workgroup (64 tokens, 8 slots, 2048 columns: 4.8 against 6.8 us). The dot products are fp32: a thread's columns in order, then
+// workgroup (8 slots, 2048 columns: 64 tokens 4.6 against 6.5 us, 512 9.6 and
+// 12.9, 1024 17.4 and 17.7, 2048 30.5 and 32.6: beyond it matters little). The
+// dot products are fp32: a thread's columns in order, then
 // the lanes and the waves in a fixed tree. A dropped slot has dw = 0 and writes
 // no row.
 constexpr int kCgSlots = 4;
@@ -498,21 +503,11 @@ hipError_t launch_dispatch(hipStream_t s, const void* X, int esize, int64_t T, i
   return hipGetLastError();
 }
 
-template <bool YSBF, bool YBF, int MODE, int KB>
-static void combine_kb(hipStream_t s, const CombineArgs& a) {
-  const int64_t units = ceil_div(a.n, 8);
-  hipLaunchKernelGGL((k_combine<YSBF, YBF, MODE, KB>), dim3((unsigned)ceil_div(a.T * units, 256)), dim3(256), 0, s, a.Ys,
-                     a.lds, (int)a.R, a.inverse, a.w, (uint32_t)a.T, (uint32_t)a.n, (uint32_t)units, a.k, a.Y, a.ldy);
-}
-
 template <bool YSBF, bool YBF, int MODE>
 static void combine_mode(hipStream_t s, const CombineArgs& a) {
-  if constexpr (MODE != kSingly) {
-    if (a.k == 1) return combine_kb<YSBF, YBF, MODE, 1>(s, a);
-    if (a.k == 2) return combine_kb<YSBF, YBF, MODE, 2>(s, a);
-    if (a.k > 4) return combine_kb<YSBF, YBF, MODE, 8>(s, a);
-  }
-  combine_kb<YSBF, YBF, MODE, 4>(s, a);
+  const int64_t units = ceil_div(a.n, 8);
+  hipLaunchKernelGGL((k_combine<YSBF, YBF, MODE>), dim3((unsigned)ceil_div(a.T * units, 256)), dim3(256), 0, s, a.Ys,
+                     a.lds, (int)a.R, a.inverse, a.w, (uint32_t)a.T, (uint32_t)a.n, (uint32_t)units, a.k, a.Y, a.ldy);
 }
 
 template <bool YSBF, bool YBF>
