@@ -991,9 +991,9 @@ k_expert_mm_grad(ExArgs p) {
 // use the unit 1 and have their weights s (q - z) rounded to bf16 instead. A
 // sum below 2^88 is in fp32's range in any of these units, and fp32's smallest
 // step in the largest unit is 2^-149 2^40.
-// Measured: 8192 rows over 8 experts of 11008 x 4096 860 to 930 us (0.79 to 0.86
-// PFLOP/s; 1128 in 128 x 128 tiles, a library product of expanded weights
-// 530), gradient of 4096 x 4096 349 to 370 us (0.74 to 0.79 PFLOP/s; 399, 197).
+// Measured: 8192 rows over 8 experts of 11008 x 4096 880 to 950 us (0.78 to 0.84
+// PFLOP/s; 1030 in 128 x 128 tiles, a library product of expanded weights
+// 530), gradient of 4096 x 4096 344 to 376 us (0.73 to 0.80 PFLOP/s; 391, 197).
 // The products keep the matrix cores busy half of the time and the expansion
 // the vector units the other half; the two waves of a SIMD meet at the
 // barriers too often to fill each other's gaps. Waves whose half of the tile
@@ -1797,7 +1797,7 @@ static bool ring_fits(const ExpertArgs& a, int grad) {
 // 64 or 128 rows of a tile: the small ones while all of them run at once, two
 // (gradient: nearly three) workgroups per CU, or while most segments fit one;
 // beyond, the large ones expand each weight for twice the rows. 64 against 128
-// rows, 4 bits: 96 rows for each of 8 experts of 4096 x 4096 (512 tiles) 89 and
+// rows, 4 bits, groups of 64: 96 rows for each of 8 experts of 4096 x 4096 (512 tiles) 89 and
 // 111 us, gradient 74 and 88; 96 for each of 32 of 1408 x 2048 (704 tiles) 82
 // and 72, gradient 55 and 53; 29 for each of 64 of 1272 x 5120 154 and 184.
 // Three pieces (fp32 gradient) fill a CU's LDS with one workgroup, small or

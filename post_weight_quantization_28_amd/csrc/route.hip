@@ -255,11 +255,11 @@ hipError_t launch_route(hipStream_t s, const int32_t* ids, int64_t ldi, int64_t 
 // ---------------------------------------------------------------- rows there and back
 // The rows of Ys are read once, so where they are aligned they are loaded past
 // the caches, whatever their number, and dY with them, which the gradient reads
-// once for each four slots of a token. Past the caches and through them: 268 MB
-// of Ys 80 and 94 us; the gradient of 8192 tokens, 8 slots, 2048 columns 99 and
-// 122, of 2048 tokens 34 and 29.5, of 512 tokens 9.7 and 9.2; fewer make no
-// difference, nor does a way back right after the way there up to 2048 tokens
-// (8192 tokens 125 and 129 for both).
+// once for each four slots of a token. Past the caches and through them, 2048
+// columns, 8 slots: the way back of 8192 tokens (268 MB of Ys) 55 and 58 us, its
+// gradient 99 and 122, of 2048 tokens 33 and 31, of 512 tokens 9.7 and 9.2; the
+// way back right after the way there is alike up to 2048 tokens (8192: 115 and
+// 120 for both). One slot of 4096 tokens of 4096 columns: 14.7 and 12.4.
 // A unit is 8 columns: 16 bytes of bf16, 32 of fp32.
 //   kAligned: every row of both sides is 16-byte aligned and n % 8 == 0, so
 //     units move as whole 16-byte pieces;
