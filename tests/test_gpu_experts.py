@@ -929,3 +929,92 @@ def test_gradient_of_tiny_weights(R, d, n):
             dX = arr(G.expert_matmul_grad(dY, None, *cuda_layers(qw, sc, zr), 4, 32, n, out_dtype=odt))
             err = ((UBF + U32 + d * U32) * mag if odt == BF16 else (UBF ** 3 + U32 + 3 * d * U32) * mag + small) * 1.01
             assert np.all(np.abs(dX - ref) <= err + (UBF * (np.abs(ref) + err) if odt == BF16 else 0))
+
+
+def weights64(qw, sc, zr, bits, group, n):
+    """Dequantised weights of one layer in 64 bits, on the GPU."""
+    at = torch.arange(n, device="cuda") * bits
+    j, sh = at // 32, at % 32
+    words = qw.to(torch.int64) & 0xFFFFFFFF
+    q = words[:, j] >> sh
+    if 32 % bits:
+        q = torch.where(sh + bits > 32, q | words[:, torch.clamp(j + 1, max=words.shape[1] - 1)] << (32 - sh), q)
+    g = torch.arange(n, device="cuda") // group
+    return ((q & (2 ** bits - 1)).double() - zr.double()[:, g]) * sc.double()[:, g]
+
+
+def random_layers(gen, E, d, n, bits, group):
+    """Random packed layers, made on the GPU."""
+    qw = torch.randint(-2 ** 31, 2 ** 31, (E, d, n // 32 * bits), generator=gen, device="cuda", dtype=torch.int64).int()
+    sc = 0.002 + 0.05 * torch.rand(E, d, n // group, generator=gen, device="cuda")
+    zr = torch.randint(0, 2 ** bits, (E, d, n // group), generator=gen, device="cuda", dtype=torch.int32).to(torch.uint8)
+    return qw, sc, zr
+
+
+def test_activations_beyond_32_bits():
+    """X of more than 4 GB (no ring: its offsets are 32 bits), gathered from
+    both ends: the product, and the weight gradient from the 8-bit copy of it
+    (more than 4 GB of codes)."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    T, n = 2 ** 20 + 3, 4224
+    X = torch.randn(T, n, generator=gen, device="cuda", dtype=BF16)
+    kept = G.checkpoint_save(X)
+    for E, R, d in ((2, 1200, 6550), (4, 30, 40), (2, 90, 40)):
+        qw, sc, zr = random_layers(gen, E, d, n, 4, 128)
+        rows = torch.randint(0, 1000, (R,), generator=gen, device="cuda")
+        rows[::2] = T - 1 - rows[::2]
+        off = torch.tensor([0] + [R * (e + 1) // E for e in range(E)], dtype=torch.int32)
+        Y = G.expert_matmul(X, off.cuda(), qw, sc, zr, 4, 128, rows=rows.int())
+        for e in range(E):
+            x, W = X[rows[off[e]:off[e + 1]]].double(), weights64(qw[e], sc[e], zr[e], 4, 128, n).t().contiguous()
+            tol = (128 + n // 128 + 2) * U32 * (x.abs() @ W.abs())
+            if R <= 16 * E:
+                S = sc[e].double().repeat_interleave(128, 1).t().contiguous()
+                tol = 130 * 62 * U32 * (x.abs() @ S) + (n // 128 + 1) * U32 * (x.abs() @ W.abs())
+            assert torch.all((Y[off[e]:off[e + 1]].double() - x @ W).abs() <= tol)
+    for m, R in ((136, 3000), (24, 500)):
+        rows = torch.randint(0, 1000, (R,), generator=gen, device="cuda")
+        rows[::2] = T - 1 - rows[::2]
+        Pm = torch.randn(R, m, generator=gen, device="cuda").to(BF16)
+        off = torch.tensor([0, R // 3, R], dtype=torch.int32)
+        g = G.checkpoint_weight_grad(Pm, kept, offsets=off.cuda(), rows=rows.int())
+        for e in range(2):
+            at = rows[off[e]:off[e + 1]]
+            part = G.Checkpoint(kept.codes[at].contiguous(), kept.exps[at].contiguous(), n)
+            x, p = G.checkpoint_restore(part, F32).double(), Pm[off[e]:off[e + 1]].double().t().contiguous()
+            assert torch.all((x - X[at].double()).abs() <= X[at].double().abs().amax(1, keepdim=True) / 64)
+            assert torch.all((g[e].double() - p @ x).abs() <= (R + 64) * U32 * (p.abs() @ x.abs()))
+
+
+@pytest.mark.parametrize("E,d,n,R", [(520, 1024, 16384, 40), (520, 1024, 16384, 9000), (1, 524416, 16384, 20), (1, 524416, 16384, 600)])
+def test_packed_weights_beyond_32_bits(E, d, n, R):
+    """More than 4 GB of codes, of all the experts or of one: the first and
+    last expert's rows, the first and last outputs, and the gradient."""
+    gen = torch.Generator(device="cuda").manual_seed(E + R)
+    qw, sc, zr = random_layers(gen, E, d, n, 4, 128)
+    X = torch.randn(R, n, generator=gen, device="cuda").to(BF16)
+    dY = (1e-3 * torch.randn(R, d, generator=gen, device="cuda")).to(BF16)
+    half = R // 2 if E > 1 else R
+    off = torch.full((E + 1,), half, dtype=torch.int32)
+    off[0], off[E] = 0, R
+    ot = off.cuda()
+    Y = G.expert_matmul(X, ot, qw, sc, zr, 4, 128)
+    dX = G.expert_matmul_grad(dY, ot, qw, sc, zr, 4, 128, n, out_dtype=F32)
+    for e, lo, hi in ((0, 0, half), (E - 1, half, R)):
+        if lo == hi:
+            continue
+        x, g = X[lo:hi].double(), dY[lo:hi].double()
+        ref, mag = torch.zeros(hi - lo, n, dtype=torch.float64, device="cuda"), torch.zeros(hi - lo, n, dtype=torch.float64, device="cuda")
+        for c in range(0, d, 16384):
+            cut = slice(c, min(d, c + 16384))
+            W = weights64(qw[e, cut], sc[e, cut], zr[e, cut], 4, 128, n)
+            ref += g[:, cut].contiguous() @ W
+            mag += g[:, cut].abs().contiguous() @ W.abs()
+            if c == 0 or c + 16384 >= d:
+                Wt = W.t().contiguous()
+                tol = (128 + n // 128 + 2) * U32 * (x.abs() @ Wt.abs())
+                if R <= 16 * E:
+                    S = sc[e, cut].double().repeat_interleave(128, 1).t().contiguous()
+                    tol = 130 * 62 * U32 * (x.abs() @ S) + (n // 128 + 1) * U32 * (x.abs() @ Wt.abs())
+                assert torch.all((Y[lo:hi, cut].double() - x @ Wt).abs() <= tol)
+        assert torch.all((dX[lo:hi].double() - ref).abs() <= (UBF ** 3 + U32 + 3 * d * U32) * 1.01 * mag)
