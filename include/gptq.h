@@ -338,11 +338,12 @@ gptq_status gptq_combine_grad(void *stream, const void *dY, int32_t dydt, int64_
  * Results are bitwise reproducible. Few rows per expert (R <= 16 E, 16-byte
  * aligned) take a matrix-vector form, which at 4 bits sums x (16 + q) over 128
  * codes: an infinite activation, or one above 2^116, may give NaN or an
- * infinity there where the sum is infinite or still finite. Many (R > 512 E, 4 bits, groups that are multiples of 128, tiles for
- * half of the GPU) keep one running sum in units of the current group's scale;
- * there the weights of a group whose scale is outside 2^-40 .. 2^40 are
- * rounded to bf16, a partial sum above 2^88 may become infinite (in a group of
- * scale 2^-40), and what is below 2^-109 may be lost (scale 2^40).
+ * infinity there where the sum is infinite or still finite. Many (R > 512 E,
+ * 4 bits, groups that are multiples of 128, tiles for half of the GPU) keep
+ * one running sum in units of the current group's scale; there the weights of
+ * a group whose scale is outside 2^-40 .. 2^40 are rounded to bf16, a partial
+ * sum above 2^88 may become infinite (in a group of scale 2^-40), and what is
+ * below 2^-109 may be lost (scale 2^40).
  *
  * gptq_expert_matmul_grad: dX[p] = dY[p] W_hat_e (dX: R x n, dxdt; dY: R x
  * d_out bf16, row pitch ldy). The scale changes along this sum: with a bf16
@@ -353,8 +354,9 @@ gptq_status gptq_combine_grad(void *stream, const void *dY, int32_t dydt, int64_
  * work. Sums are fp32 in a fixed order.
  *
  * d_out >= 1, n >= 1; R == 0 enqueues nothing. Rows of X and dY may have any
- * alignment (16-byte aligned rows are faster). Fewer than 2^24 - 16 tiles of 64
- * or 128 rows x 128 columns, E - 1 rows of tiles more than R needs. Asynchronous. Workspace:
+ * alignment (16-byte aligned rows are faster). Fewer than 2^24 - 16 tiles of
+ * 64 or 128 rows x 128 columns, E - 1 rows of tiles more than R needs.
+ * Asynchronous. Workspace:
  * gptq_expert_matmul_workspace_bytes / gptq_expert_matmul_grad_workspace_bytes
  * (fp32 partial results when few tiles split the sum; 0 for most sizes).
  * ("El balance de errores de la inferencia de pocos bits", section 6: decode
