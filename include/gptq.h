@@ -409,6 +409,105 @@ gptq_status gptq_checkpoint_weight_grad(void *stream, const void *P, int32_t pdt
                                         const int32_t *rows, const int32_t *offsets, int64_t E, float *G,
                                         void *workspace, size_t ws_bytes);
 
+/* ---- Packed layers with bias, activation, gate and residual ---------------------
+ * gptq_linear: the product of gptq_expert_matmul with what stands behind it in
+ * a model, in the same launch: for the rows p of expert e
+ *   z = X[rows[p]] W_hat_e^T + bias[e]                 (fp32)
+ *   plain:  Y[p] = act(z) + residual[p]
+ *   gated:  Y[p] = act(z[0 .. d)) * z[d .. 2 d) + residual[p]
+ * d: columns of Y. A gated layer has 2 d packed rows an expert: those of the
+ * gate, then those of the other factor (two layers quantized against the same
+ * Hessian, one after the other, are one layer of 2 d rows). With m = d (2 d when
+ * gated): qweight E x m x n*bits/32, scales and zeros E x m x n/group, bias
+ * E x m fp32 or NULL, residual R x d (rdt, row pitch ldr) or NULL, Y R x d (ydt,
+ * row pitch ldy), Z R x m (zdt, row pitch ldz) or NULL: where z is kept for
+ * gptq_linear_grad. X, rows, offsets, E, R, bits, group and the kernels' numbers
+ * are those of gptq_expert_matmul; the epilogue is computed in fp32 and rounded
+ * once. E = 1 and offsets NULL: one dense layer. Rows from offsets[E] on are
+ * neither read nor written in any matrix. Y may be the residual (same type and
+ * pitch); no other output may overlap an input.
+ *   act: GPTQ_ACT_NONE z; _RELU max(z, 0) (NaN stays NaN); _GELU z Phi(z);
+ * _GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2; _SILU z / (1 +
+ * exp(-z)). Of minus infinity the last three are NaN.
+ * Workspace: gptq_linear_workspace_bytes (fp32 partial results; 0 for most
+ * sizes). m <= 2^31 - 65536. Asynchronous.
+ *
+ * gptq_linear_grad: from dY (R x d, dydt bf16 or fp32, row pitch ldy) and Z as
+ * gptq_linear kept it (bf16 or fp32),
+ *   plain:  dZ[p] = dY[p] act'(z);  gated:  dZ[p] = (dY u act'(g), dY act(g))
+ *   dbias[e] = sum over the rows p of segment e of dZ[p]     (fp32, 0 if empty)
+ *   dX[p] = dZ[p] W_hat_e                                    (R x n, dxdt)
+ * dZ (R x m bf16, row pitch lddz) is rounded to bf16 once, which is what the
+ * matrix product takes, and is also P of gptq_checkpoint_weight_grad; dbias sums
+ * its values before that rounding, in a fixed order. NULL dbias: not wanted. With
+ * GPTQ_ACT_NONE and no gate Z is not read and may be NULL, and if dY is bf16 dZ
+ * may be NULL too (the product then takes dY). The residual's gradient is dY, the
+ * gradient of X by token is gptq_combine of dX. dX takes the weights as
+ * gptq_expert_matmul_grad does. act' of relu is 0 at 0. dZ may be Z or, ungated,
+ * dY (bf16, same pitch). Workspace: gptq_linear_grad_workspace_bytes.
+ * Asynchronous.
+ * ("El balance de errores de la inferencia de pocos bits", section 6: what a
+ * fused kernel saves is the traffic between its parts.) */
+typedef enum {
+  GPTQ_ACT_NONE = 0,
+  GPTQ_ACT_RELU = 1,
+  GPTQ_ACT_GELU = 2,
+  GPTQ_ACT_GELU_TANH = 3,
+  GPTQ_ACT_SILU = 4
+} gptq_act;
+gptq_status gptq_linear_workspace_bytes(int64_t R, int64_t n, int64_t d, int32_t gated, int64_t E, int32_t bits,
+                                        int32_t group, size_t *bytes);
+gptq_status gptq_linear(void *stream, const void *X, int32_t xdt, int64_t T, int64_t n, int64_t ldx,
+                        const int32_t *rows, int64_t R, const int32_t *offsets, int64_t E, const uint32_t *qweight,
+                        const float *scales, const uint8_t *zeros, const float *bias, int64_t d, int32_t bits,
+                        int32_t group, int32_t act, int32_t gated, const void *residual, int32_t rdt, int64_t ldr,
+                        void *Z, int32_t zdt, int64_t ldz, void *Y, int32_t ydt, int64_t ldy, void *workspace,
+                        size_t ws_bytes);
+gptq_status gptq_linear_grad_workspace_bytes(int64_t R, int64_t n, int64_t d, int32_t gated, int64_t E, int32_t bits,
+                                             int32_t group, size_t *bytes);
+gptq_status gptq_linear_grad(void *stream, const void *dY, int32_t dydt, int64_t ldy, const void *Z, int32_t zdt,
+                             int64_t ldz, int64_t R, const int32_t *offsets, int64_t E, const uint32_t *qweight,
+                             const float *scales, const uint8_t *zeros, int64_t d, int64_t n, int32_t bits,
+                             int32_t group, int32_t act, int32_t gated, void *dZ, int64_t lddz, float *dbias, void *dX,
+                             int32_t dxdt, int64_t ldx, void *workspace, size_t ws_bytes);
+
+/* ---- Distillation from a teacher's top logits -----------------------------------
+ * The loss that tuning a quantized model (its adapters, or the layers around
+ * its packed weights) against the model before quantization minimises, from
+ * the K entries per position that were kept of the teacher.
+ *   s = Z[t] / temperature, lse[t] = log sum_v exp(s_v), q_v = exp(s_v - lse)
+ *   p: log_probs == 0: softmax over the entries k of teacher[t] / temperature;
+ *      log_probs == 1: p_k = exp(teacher[t][k]) as it is (their sum M may be
+ *      below 1)
+ *   loss[t] = sum_k p_k (log p_k - log q_{ids[t][k]})
+ * Z: T x V (zdt bf16 or fp32, row pitch ldz); ids, teacher: T x K, int32 and
+ * fp32, contiguous; loss, lse: T fp32. Entries whose id is outside [0, V) do not
+ * count; a row without entries, or whose p are all 0 (padding), has loss 0 and
+ * gradient 0. An entry with p = 0 adds nothing wherever its logit is. Logits of
+ * -infinity (masked entries) have q = 0; a row of nothing else has lse = -infinity
+ * and a loss of NaN, unless it is padding. NaN and +infinity make their row NaN.
+ * 1 <= K <= GPTQ_DISTILL_MAX_K, V <= 2^31 - 65536, temperature positive and
+ * finite. Everything is fp32, in an order that does not depend on timing.
+ * Workspace: gptq_distill_workspace_bytes (0 for many rows).
+ *
+ * gptq_distill_grad: for grad (T fp32: d total / d loss[t]) and lse as
+ * gptq_distill gave it,
+ *   dZ[t][v] = grad[t] / temperature (M q_v - sum over k with ids = v of p_k)
+ * (T x V, dzdt bf16 or fp32, row pitch ldd; an id that stands more than once in
+ * a row counts each time). dZ may be Z (same type and pitch). No workspace. Both
+ * asynchronous; T == 0 enqueues nothing. T may be at most 2^24 - 2.
+ * ("Resumen Técnico: GPTQ-intrinsic LoRA", "Declaración del Problema": the
+ * low-rank factors beside the quantized layer, which tuning moves.) */
+#define GPTQ_DISTILL_MAX_K 1024
+gptq_status gptq_distill_workspace_bytes(int64_t T, int64_t V, size_t *bytes);
+gptq_status gptq_distill(void *stream, const void *Z, int32_t zdt, int64_t T, int64_t V, int64_t ldz,
+                         const int32_t *ids, const float *teacher, int64_t K, float temperature, int32_t log_probs,
+                         float *loss, float *lse, void *workspace, size_t ws_bytes);
+gptq_status gptq_distill_grad(void *stream, const void *Z, int32_t zdt, int64_t T, int64_t V, int64_t ldz,
+                              const int32_t *ids, const float *teacher, int64_t K, float temperature,
+                              int32_t log_probs, const float *lse, const float *grad, void *dZ, int32_t dzdt,
+                              int64_t ldd);
+
 /* ---- EoRA: rank-r compensation of the compression error ----------------------
  * B (d_out x rank fp32, row-major) and A (rank x n fp32, row-major) such that
  * W_hat + B A is the best rank-r correction of W_hat in the layer loss

@@ -323,6 +323,50 @@ hipError_t launch_keep_grad(hipStream_t s, const KeepGradPlan& pl, const uint16_
                             const int8_t* codes, const uint8_t* exps, int64_t T, int64_t n, const int32_t* rows,
                             const int32_t* offsets, int E, float* G, float* part);
 
+// ---- linear.hip: packed products with bias, activation, gate and residual, and
+// their gradient
+struct LinearArgs {
+  ExpertArgs mm;                              // the product: d_out = m outputs (2 d when gated); Y is not used
+  const float* bias;                          // E x m, or null
+  int act, gated;
+  const void* res; int res_bf16; int64_t ldr; // R x d, or null
+  void* Z; int z_bf16; int64_t ldz;           // R x m, or null: the pre-activations are not kept
+  int64_t d;
+  void* Y; int y_bf16; int64_t ldy;           // R x d
+  void* ws;
+};
+size_t linear_workspace(int64_t R, int E, int64_t n, int64_t m, int group);
+hipError_t launch_linear(hipStream_t s, const LinearArgs& a);
+struct LinearGradArgs {
+  ExpertArgs mm;                              // dX = dZ W_hat: A is dZ (or dY itself)
+  const void* dY; int dy_bf16; int64_t ldy;   // R x d
+  const void* Z; int z_bf16; int64_t ldz;     // R x m; null: slope 1
+  int act, gated;
+  int64_t d, m;
+  uint16_t* dZ; int64_t lddz;                 // R x m bf16; null: dY is dZ
+  float* dbias;                               // E x m, or null
+  float* part;                                // linear_bias_parts floats when dbias is wanted
+};
+int64_t linear_bias_parts(int64_t R, int E, int64_t m);
+int64_t linear_grad_threads(int64_t R, int E, int64_t d);   // of the launch that forms dZ
+hipError_t launch_linear_grad(hipStream_t s, const LinearGradArgs& a);
+
+// ---- distill.hip: distillation from a teacher's top logits
+constexpr int kDistillMaxK = 1024;
+struct DistillArgs {
+  const void* Z; int z_bf16; int64_t T, V, ldz;
+  const int32_t* ids; const float* teacher; int K;    // T x K
+  float inv_temp; int log_probs;
+  float *loss, *lse;                          // T (forward)
+  const float *lse_in, *grad;                 // T (gradient)
+  void* dZ; int dz_bf16; int64_t ldd;
+  void* part_sums;                            // distill_parts pairs of floats a row when there are several
+  int parts; int64_t part_cols;               // set by the launch
+};
+int distill_parts(int64_t T, int64_t V);
+hipError_t launch_distill(hipStream_t s, const DistillArgs& a);
+hipError_t launch_distill_grad(hipStream_t s, const DistillArgs& a);
+
 // ---- eora.hip: rank-r compensation of a layer's error
 hipError_t launch_eora_delta(hipStream_t s, const void* W, int wbf16, int64_t ldw, const float* Wh,
                              int64_t d_out, int64_t n, float* D, DevStatus* st);

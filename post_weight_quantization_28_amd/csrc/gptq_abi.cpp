@@ -1230,6 +1230,225 @@ gptq_status gptq_expert_matmul_grad(void* stream, const void* dY, int32_t dydt, 
   return GPTQ_OK;
 }
 
+// ---------------------------------------------------------------- layers with an epilogue
+static gptq_status linear_sizes(int64_t R, int64_t n, int64_t d, int32_t gated, int64_t E, int32_t bits, int32_t group) {
+  if (gated != 0 && gated != 1) return fail(GPTQ_EINVAL, "gated must be 0 or 1");
+  if (gated && d > kMaxRows / 2) return fail(GPTQ_EINVAL, "d of a gated layer may be at most 2^30 - 32768");
+  return expert_sizes(R, n, gated ? 2 * d : d, E, bits, group);
+}
+
+static gptq_status act_check(int32_t act) {
+  return act >= GPTQ_ACT_NONE && act <= GPTQ_ACT_SILU ? GPTQ_OK : fail(GPTQ_EINVAL, "act must be a gptq_act");
+}
+
+gptq_status gptq_linear_workspace_bytes(int64_t R, int64_t n, int64_t d, int32_t gated, int64_t E, int32_t bits,
+                                        int32_t group, size_t* bytes) {
+  if (!bytes) return fail(GPTQ_EINVAL, "bytes is NULL");
+  const gptq_status st = linear_sizes(R, n, d, gated, E, bits, group);
+  if (st != GPTQ_OK) return st;
+  *bytes = (linear_workspace(R, (int)E, n, gated ? 2 * d : d, group) + 255) / 256 * 256;
+  return GPTQ_OK;
+}
+
+gptq_status gptq_linear(void* stream, const void* X, int32_t xdt, int64_t T, int64_t n, int64_t ldx,
+                        const int32_t* rows, int64_t R, const int32_t* offsets, int64_t E, const uint32_t* qweight,
+                        const float* scales, const uint8_t* zeros, const float* bias, int64_t d, int32_t bits,
+                        int32_t group, int32_t act, int32_t gated, const void* residual, int32_t rdt, int64_t ldr,
+                        void* Z, int32_t zdt, int64_t ldz, void* Y, int32_t ydt, int64_t ldy, void* workspace,
+                        size_t ws_bytes) {
+  gptq_status st = linear_sizes(R, n, d, gated, E, bits, group);
+  if (st != GPTQ_OK || (st = experts_check(E, offsets)) != GPTQ_OK || (st = dt_check(ydt)) != GPTQ_OK ||
+      (st = act_check(act)) != GPTQ_OK || (residual && (st = dt_check(rdt)) != GPTQ_OK) ||
+      (Z && (st = dt_check(zdt)) != GPTQ_OK))
+    return st;
+  if (xdt != GPTQ_BF16) return fail(GPTQ_EINVAL, "linear takes bf16 activations");
+  if (T < 0 || T > kMaxRows) return fail(GPTQ_EINVAL, "T must be in [0, 2^31 - 65536]");
+  if (R == 0) return GPTQ_OK;
+  if (rows ? T < 1 : T < R) return fail(GPTQ_EINVAL, "X has too few rows");
+  const int64_t m = gated ? 2 * d : d;
+  if (ldx < n) return fail(GPTQ_EINVAL, "ldx < n");
+  if (ldy < d) return fail(GPTQ_EINVAL, "ldy < d");
+  if (residual && ldr < d) return fail(GPTQ_EINVAL, "ldr < d");
+  if (Z && ldz < m) return fail(GPTQ_EINVAL, "ldz is below the number of packed rows");
+  LinearArgs a = {};
+  a.mm = {X, ldx, rows, (int)T, offsets, (int)E, (int)R, qweight, scales, zeros,
+          m, n, bits, group, Y, ydt == GPTQ_BF16, ldy, workspace};
+  if ((st = expert_weights_check(a.mm, 0)) != GPTQ_OK) return st;
+  if ((residual && mis(residual, rdt)) || (Z && mis(Z, zdt)) || (bias && mis(bias, GPTQ_F32)))
+    return fail(GPTQ_EINVAL, "a matrix is not aligned to its elements");
+  a.bias = bias;
+  a.act = act;
+  a.gated = gated;
+  a.res = residual;
+  a.res_bf16 = rdt == GPTQ_BF16;
+  a.ldr = ldr;
+  a.Z = Z;
+  a.z_bf16 = zdt == GPTQ_BF16;
+  a.ldz = ldz;
+  a.d = d;
+  a.Y = Y;
+  a.y_bf16 = ydt == GPTQ_BF16;
+  a.ldy = ldy;
+  a.ws = workspace;
+  if ((st = check_ws(workspace, ws_bytes, linear_workspace(R, (int)E, n, m, group))) != GPTQ_OK) return st;
+  HIP_TRY(launch_linear((hipStream_t)stream, a), "linear");
+  return GPTQ_OK;
+}
+
+// The gradient's product first (its parts, rounded up), then the partial sums of the bias.
+static size_t linear_grad_product_bytes(int64_t R, int64_t n, int64_t m, int64_t E, int32_t group) {
+  const size_t need = std::max(expert_split(R, (int)E, n, m, group, 1, false).part_bytes,
+                               expert_split(R, (int)E, n, m, group, 1, true).part_bytes);
+  return (need + 255) / 256 * 256;
+}
+
+gptq_status gptq_linear_grad_workspace_bytes(int64_t R, int64_t n, int64_t d, int32_t gated, int64_t E, int32_t bits,
+                                             int32_t group, size_t* bytes) {
+  if (!bytes) return fail(GPTQ_EINVAL, "bytes is NULL");
+  const gptq_status st = linear_sizes(R, n, d, gated, E, bits, group);
+  if (st != GPTQ_OK) return st;
+  const int64_t m = gated ? 2 * d : d;
+  *bytes = linear_grad_product_bytes(R, n, m, E, group) +
+           ((size_t)linear_bias_parts(R, (int)E, m) * sizeof(float) + 255) / 256 * 256;
+  return GPTQ_OK;
+}
+
+gptq_status gptq_linear_grad(void* stream, const void* dY, int32_t dydt, int64_t ldy, const void* Z, int32_t zdt,
+                             int64_t ldz, int64_t R, const int32_t* offsets, int64_t E, const uint32_t* qweight,
+                             const float* scales, const uint8_t* zeros, int64_t d, int64_t n, int32_t bits,
+                             int32_t group, int32_t act, int32_t gated, void* dZ, int64_t lddz, float* dbias, void* dX,
+                             int32_t dxdt, int64_t ldx, void* workspace, size_t ws_bytes) {
+  size_t need = 0;
+  gptq_status st = gptq_linear_grad_workspace_bytes(R, n, d, gated, E, bits, group, &need);
+  if (st != GPTQ_OK || (st = experts_check(E, offsets)) != GPTQ_OK || (st = dt_check(dydt)) != GPTQ_OK ||
+      (st = dt_check(dxdt)) != GPTQ_OK || (st = act_check(act)) != GPTQ_OK)
+    return st;
+  const int64_t m = gated ? 2 * d : d;
+  const bool straight = act == GPTQ_ACT_NONE && !gated;
+  if (R > 0) {
+    if (!dY || (!Z && !straight)) return fail(GPTQ_EINVAL, "NULL pointer");
+    if (!straight && (st = dt_check(zdt)) != GPTQ_OK) return st;
+    if (!dZ && !(straight && dydt == GPTQ_BF16)) return fail(GPTQ_EINVAL, "dZ is NULL and dY cannot stand for it");
+    if (ldy < d) return fail(GPTQ_EINVAL, "ldy < d");
+    if (!straight && ldz < m) return fail(GPTQ_EINVAL, "ldz is below the number of packed rows");
+    if (dZ && lddz < m) return fail(GPTQ_EINVAL, "lddz is below the number of packed rows");
+    if (ldx < n) return fail(GPTQ_EINVAL, "ldx < n");
+    if (mis(dY, dydt) || (!straight && mis(Z, zdt)) || mis(dZ, GPTQ_BF16))
+      return fail(GPTQ_EINVAL, "a matrix is not aligned to its elements");
+  }
+  if (dbias && mis(dbias, GPTQ_F32)) return fail(GPTQ_EINVAL, "a matrix is not aligned to its elements");
+  LinearGradArgs a = {};
+  a.mm = {dZ ? dZ : dY, dZ ? lddz : ldy, nullptr, (int)R, offsets, (int)E, (int)R, qweight, scales, zeros,
+          m, n, bits, group, dX, dxdt == GPTQ_BF16, ldx, workspace};
+  if (R > 0 && (st = expert_weights_check(a.mm, 1)) != GPTQ_OK) return st;
+  if (linear_grad_threads(R, (int)E, d) > kMaxThreads) return fail(GPTQ_EINVAL, "R d is too large for one launch");
+  if ((st = check_ws(workspace, ws_bytes, need)) != GPTQ_OK) return st;
+  a.dY = dY;
+  a.dy_bf16 = dydt == GPTQ_BF16;
+  a.ldy = ldy;
+  a.Z = straight ? nullptr : Z;
+  a.z_bf16 = zdt == GPTQ_BF16;
+  a.ldz = ldz;
+  a.act = act;
+  a.gated = gated;
+  a.d = d;
+  a.m = m;
+  a.dZ = static_cast<uint16_t*>(dZ);
+  a.lddz = lddz;
+  a.dbias = dbias;
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + linear_grad_product_bytes(R, n, m, E, group));
+  HIP_TRY(launch_linear_grad((hipStream_t)stream, a), "linear_grad");
+  return GPTQ_OK;
+}
+
+// ---------------------------------------------------------------- distillation
+static gptq_status distill_sizes(int64_t T, int64_t V) {
+  if (T < 0 || V < 1) return fail(GPTQ_EINVAL, "need T >= 0 and V >= 1");
+  if (T > kMaxThreads / 256) return fail(GPTQ_EINVAL, "T may be at most 2^24 - 2");
+  if (V > kMaxRows) return fail(GPTQ_EINVAL, "V may be at most 2^31 - 65536");
+  return GPTQ_OK;
+}
+
+// What both calls check; the rest of the arguments is filled in by them.
+static gptq_status distill_args(const void* Z, int32_t zdt, int64_t T, int64_t V, int64_t ldz, const int32_t* ids,
+                                const float* teacher, int64_t K, float temperature, int32_t log_probs,
+                                DistillArgs* a) {
+  gptq_status st = dt_check(zdt);
+  if (st != GPTQ_OK || (st = distill_sizes(T, V)) != GPTQ_OK) return st;
+  if (K < 1 || K > GPTQ_DISTILL_MAX_K) return fail(GPTQ_EINVAL, "K must be in [1, GPTQ_DISTILL_MAX_K]");
+  const float inv = 1.f / temperature;
+  if (!(temperature > 0.f) || !(inv > 0.f) || inv - inv != 0.f || temperature - temperature != 0.f)
+    return fail(GPTQ_EINVAL, "temperature must be positive and finite, and its inverse too");
+  if (log_probs != 0 && log_probs != 1) return fail(GPTQ_EINVAL, "log_probs must be 0 or 1");
+  if (T > 0) {
+    if (ldz < V) return fail(GPTQ_EINVAL, "ldz < V");
+    if (!Z || !ids || !teacher) return fail(GPTQ_EINVAL, "NULL pointer");
+    if (mis(Z, zdt)) return fail(GPTQ_EINVAL, "Z is not aligned to its elements");
+  }
+  *a = {};
+  a->Z = Z;
+  a->z_bf16 = zdt == GPTQ_BF16;
+  a->T = T;
+  a->V = V;
+  a->ldz = ldz;
+  a->ids = ids;
+  a->teacher = teacher;
+  a->K = (int)K;
+  a->inv_temp = inv;
+  a->log_probs = log_probs;
+  return GPTQ_OK;
+}
+
+static size_t distill_part_bytes(int64_t T, int64_t V) {
+  const int parts = distill_parts(T, V);
+  return parts > 1 ? ((size_t)T * parts * 2 * sizeof(float) + 255) / 256 * 256 : 0;
+}
+
+gptq_status gptq_distill_workspace_bytes(int64_t T, int64_t V, size_t* bytes) {
+  if (!bytes) return fail(GPTQ_EINVAL, "bytes is NULL");
+  const gptq_status st = distill_sizes(T, V);
+  if (st != GPTQ_OK) return st;
+  *bytes = distill_part_bytes(T, V);
+  return GPTQ_OK;
+}
+
+gptq_status gptq_distill(void* stream, const void* Z, int32_t zdt, int64_t T, int64_t V, int64_t ldz,
+                         const int32_t* ids, const float* teacher, int64_t K, float temperature, int32_t log_probs,
+                         float* loss, float* lse, void* workspace, size_t ws_bytes) {
+  DistillArgs a;
+  gptq_status st = distill_args(Z, zdt, T, V, ldz, ids, teacher, K, temperature, log_probs, &a);
+  if (st != GPTQ_OK || T == 0) return st;
+  if (!loss || !lse) return fail(GPTQ_EINVAL, "NULL pointer");
+  if ((st = check_ws(workspace, ws_bytes, distill_part_bytes(T, V))) != GPTQ_OK) return st;
+  a.loss = loss;
+  a.lse = lse;
+  a.part_sums = workspace;
+  HIP_TRY(launch_distill((hipStream_t)stream, a), "distill");
+  return GPTQ_OK;
+}
+
+gptq_status gptq_distill_grad(void* stream, const void* Z, int32_t zdt, int64_t T, int64_t V, int64_t ldz,
+                              const int32_t* ids, const float* teacher, int64_t K, float temperature,
+                              int32_t log_probs, const float* lse, const float* grad, void* dZ, int32_t dzdt,
+                              int64_t ldd) {
+  DistillArgs a;
+  gptq_status st = dt_check(dzdt);
+  if (st != GPTQ_OK || (st = distill_args(Z, zdt, T, V, ldz, ids, teacher, K, temperature, log_probs, &a)) != GPTQ_OK ||
+      T == 0)
+    return st;
+  if (!lse || !grad || !dZ) return fail(GPTQ_EINVAL, "NULL pointer");
+  if (ldd < V) return fail(GPTQ_EINVAL, "ldd < V");
+  if (mis(dZ, dzdt)) return fail(GPTQ_EINVAL, "dZ is not aligned to its elements");
+  if (dZ == Z && (dzdt != zdt || ldd != ldz)) return fail(GPTQ_EINVAL, "dZ may be Z only with its type and pitch");
+  a.lse_in = lse;
+  a.grad = grad;
+  a.dZ = dZ;
+  a.dz_bf16 = dzdt == GPTQ_BF16;
+  a.ldd = ldd;
+  HIP_TRY(launch_distill_grad((hipStream_t)stream, a), "distill_grad");
+  return GPTQ_OK;
+}
+
 // ---------------------------------------------------------------- kept activations
 gptq_status gptq_checkpoint_save(void* stream, const void* X, int32_t dt, int64_t T, int64_t n, int64_t ldx,
                                  int8_t* codes, uint8_t* exps) {

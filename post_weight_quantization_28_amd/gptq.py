@@ -6,7 +6,8 @@ library is not built, or a tensor is not on the GPU, the calls raise.
 The names mirror include/gptq.h.
 Tensors are memory here: no call records anything for autograd, and outputs
 require no gradient whatever the inputs do. Gradients are calls of their own
-(combine_grad, expert_matmul_grad, checkpoint_weight_grad).
+(combine_grad, expert_matmul_grad, checkpoint_weight_grad, linear_grad,
+distill_grad).
 """
 import ctypes
 import functools
@@ -101,6 +102,21 @@ def load():
         "gptq_checkpoint_weight_grad_workspace_bytes": [c_i64, c_i64, c_i64, c_i64, ctypes.POINTER(c_sz)],
         "gptq_checkpoint_weight_grad": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_i64,
                                         c_vp, c_vp, c_i64, c_vp, c_vp, c_sz],
+        "gptq_linear_workspace_bytes": [c_i64, c_i64, c_i64, ctypes.c_int32, c_i64, ctypes.c_int32, ctypes.c_int32,
+                                        ctypes.POINTER(c_sz)],
+        "gptq_linear": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp,
+                        c_vp, c_i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, c_vp,
+                        ctypes.c_int32, c_i64, c_vp, ctypes.c_int32, c_i64, c_vp, ctypes.c_int32, c_i64, c_vp, c_sz],
+        "gptq_linear_grad_workspace_bytes": [c_i64, c_i64, c_i64, ctypes.c_int32, c_i64, ctypes.c_int32,
+                                             ctypes.c_int32, ctypes.POINTER(c_sz)],
+        "gptq_linear_grad": [c_vp, c_vp, ctypes.c_int32, c_i64, c_vp, ctypes.c_int32, c_i64, c_i64, c_vp, c_i64, c_vp,
+                             c_vp, c_vp, c_i64, c_i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                             c_vp, c_i64, c_vp, c_vp, ctypes.c_int32, c_i64, c_vp, c_sz],
+        "gptq_distill_workspace_bytes": [c_i64, c_i64, ctypes.POINTER(c_sz)],
+        "gptq_distill": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, ctypes.c_float,
+                         ctypes.c_int32, c_vp, c_vp, c_vp, c_sz],
+        "gptq_distill_grad": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, ctypes.c_float,
+                              ctypes.c_int32, c_vp, c_vp, c_vp, ctypes.c_int32, c_i64],
         "gptq_eora_workspace_bytes": [c_i64, c_i64, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(c_sz)],
         "gptq_eora": [c_vp, c_vp, ctypes.c_int, c_vp, c_i64, c_i64, c_i64, c_vp, ctypes.c_int32, ctypes.c_int32,
                       c_vp, c_vp, c_vp, c_vp, c_sz],
@@ -608,6 +624,142 @@ def expert_matmul_grad(dY, offsets, qweight, scales, zeros, bits, group, n, out=
     ws, wsp = _scratch(need, dev, workspace)
     _call(dev, lib.gptq_expert_matmul_grad, gp, BF16, R, ldy, op, E, qp, sp, zp, d_out, n, bits, group, xp,
           _DTYPE_CODES[out.dtype], ldx, wsp, need)
+    return out
+
+
+# ---------------------------------------------------------------- layers with an epilogue
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def _act_code(act):
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError("act must be one of " + ", ".join(ACTIVATIONS))
+    return code
+
+
+def _halves(m, gated):
+    """Columns of the result of m packed rows."""
+    if gated and m % 2:
+        raise ValueError("a gated layer has an even number of packed rows")
+    return m // 2 if gated else m
+
+
+def _matrix(t, name, shape, dtypes, device):
+    """Pointer, type code and row pitch of an optional matrix."""
+    if t is None:
+        return None, BF16, 0
+    p, pitch = _rows2d(t, name, dtypes, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return p, _DTYPE_CODES[t.dtype], pitch
+
+
+def linear(X, qweight, scales, zeros, bits, group, bias=None, act="none", gated=False, residual=None, offsets=None,
+           rows=None, keep=None, out=None, out_dtype=torch.bfloat16, workspace=None):
+    """act(X W_hat^T + bias) + residual of a packed layer, or of E of them with
+    offsets and rows as expert_matmul takes them; gated: the packed rows are
+    those of the gate and, behind them, those of the other factor, and the
+    result is act(gate) * other + residual. bias fp32 (E x) m for m packed rows,
+    residual R x d. keep: a type (bf16 or fp32) or an R x m tensor for the
+    pre-activations that linear_grad takes; the result is then (Y, Z). Rows
+    from offsets[E] on are left as they are."""
+    lib = load()
+    xp, ldx = _rows2d(X, "X", (torch.bfloat16,))
+    T, n = X.shape
+    dev = X.device
+    code, gated = _act_code(act), int(bool(gated))
+    E, m, qp, sp, zp = _expert_layers(qweight, scales, zeros, bits, group, n, dev)
+    d = _halves(m, gated)
+    R = T if rows is None else _length(rows, "rows")
+    op, rp = _segments(offsets, rows, E, dev, R)
+    bp = None if bias is None else _dense(bias, "bias", torch.float32, dev, qweight.shape[:-1])
+    resp, rdt, ldr = _matrix(residual, "residual", (R, d), _FLOATS, dev)
+    if isinstance(keep, torch.dtype):
+        if keep not in _FLOATS:
+            raise _type_error("keep", _FLOATS)
+        keep = torch.empty_strided((R, m), (m or 1, 1), dtype=keep, device=dev)
+    kp, zdt, ldz = _matrix(keep, "keep", (R, m), _FLOATS, dev)
+    out, yp, ldy = _result(out, (R, d), out_dtype, dev)
+    need = _bytes("gptq_linear_workspace_bytes", R, n, d, gated, E, bits, group)
+    ws, wsp = _scratch(need, dev, workspace)
+    _call(dev, lib.gptq_linear, xp, BF16, T, n, ldx, rp, R, op, E, qp, sp, zp, bp, d, bits, group, code, gated, resp,
+          rdt, ldr, kp, zdt, ldz, yp, _DTYPE_CODES[out.dtype], ldy, wsp, need)
+    return out if keep is None else (out, keep)
+
+
+def linear_grad(dY, Z, qweight, scales, zeros, bits, group, n, act="none", gated=False, offsets=None,
+                want_bias=False, dZ=None, out=None, out_dtype=torch.bfloat16, workspace=None):
+    """(dX, dZ, dbias) of linear: dZ (R x m bf16) from dY (R x d, bf16 or fp32)
+    and the kept Z, dX = dZ W_hat (R x n, for the sorted rows), dbias ((E x) m
+    fp32) the sums of dZ over each segment, or None. dZ is also P of
+    checkpoint_weight_grad. Z may be None where act is none and nothing is
+    gated. The residual's gradient is dY."""
+    lib = load()
+    gp, ldy = _rows2d(dY, "dY", _FLOATS)
+    R, d = dY.shape
+    dev = dY.device
+    code, gated = _act_code(act), int(bool(gated))
+    E, m, qp, sp, zp = _expert_layers(qweight, scales, zeros, bits, group, n, dev)
+    if d != _halves(m, gated):
+        raise ValueError(f"dY must have {_halves(m, gated)} columns")
+    op, _ = _segments(offsets, None, E, dev, R)
+    if Z is None and (gated or code):
+        raise ValueError("Z is needed: the pre-activations that linear kept")
+    kp, zdt, ldz = _matrix(Z, "Z", (R, m), _FLOATS, dev)
+    if dZ is None and (gated or code or dY.dtype != torch.bfloat16):
+        dZ = torch.empty_strided((R, m), (m or 1, 1), dtype=torch.bfloat16, device=dev)
+    dzp, _, lddz = _matrix(dZ, "dZ", (R, m), (torch.bfloat16,), dev)
+    db = torch.empty(qweight.shape[:-1], dtype=torch.float32, device=dev) if want_bias else None
+    out, xp, ldx = _result(out, (R, n), out_dtype, dev)
+    need = _bytes("gptq_linear_grad_workspace_bytes", R, n, d, gated, E, bits, group)
+    ws, wsp = _scratch(need, dev, workspace)
+    _call(dev, lib.gptq_linear_grad, gp, _DTYPE_CODES[dY.dtype], ldy, kp, zdt, ldz, R, op, E, qp, sp, zp, d, n, bits,
+          group, code, gated, dzp, lddz, db.data_ptr() if want_bias else None, xp, _DTYPE_CODES[out.dtype], ldx, wsp,
+          need)
+    return out, dY if dZ is None else dZ, db
+
+
+# ---------------------------------------------------------------- distillation
+def _teacher(Z, ids, teacher):
+    p, ldz = _rows2d(Z, "Z", _FLOATS)
+    T, V = Z.shape
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be T x K")
+    K = ids.shape[1]
+    return (p, _DTYPE_CODES[Z.dtype], T, V, ldz, _dense(ids, "ids", torch.int32, Z.device, (T, K)),
+            _dense(teacher, "teacher", torch.float32, Z.device, (T, K)), K)
+
+
+def distill(Z, ids, teacher, temperature=1.0, log_probs=False, workspace=None):
+    """(loss, lse), both T fp32: the divergence of softmax(Z / temperature)
+    (Z: T x V, bf16 or fp32) from the teacher's distribution over the K entries
+    ids (T x K int32; ids outside [0, V) do not count). teacher (T x K fp32):
+    its logits, normalised over these entries, or with log_probs its log
+    probabilities as they are."""
+    lib = load()
+    args = _teacher(Z, ids, teacher)
+    T, V, dev = args[2], args[3], Z.device
+    loss = torch.empty_strided((T,), (1,), dtype=torch.float32, device=dev)
+    lse = torch.empty_strided((T,), (1,), dtype=torch.float32, device=dev)
+    need = _bytes("gptq_distill_workspace_bytes", T, V)
+    ws, wsp = _scratch(need, dev, workspace)
+    _call(dev, lib.gptq_distill, *args, temperature, int(bool(log_probs)), loss.data_ptr(), lse.data_ptr(), wsp, need)
+    return loss, lse
+
+
+def distill_grad(Z, ids, teacher, lse, grad, temperature=1.0, log_probs=False, out=None, out_dtype=None):
+    """dZ (T x V, in out_dtype, default Z's type) of distill for grad (T fp32,
+    the gradient of each row's loss) and the lse that distill gave. ``out`` may
+    be Z."""
+    lib = load()
+    args = _teacher(Z, ids, teacher)
+    T, V, dev = args[2], args[3], Z.device
+    lp = _dense(lse, "lse", torch.float32, dev, (T,))
+    gp = _dense(grad, "grad", torch.float32, dev, (T,))
+    out, dp, ldd = _result(out, (T, V), out_dtype or Z.dtype, dev)
+    _call(dev, lib.gptq_distill_grad, *args, temperature, int(bool(log_probs)), lp, gp, dp, _DTYPE_CODES[out.dtype],
+          ldd)
     return out
 
 

@@ -1,0 +1,408 @@
+"""Packed layers with bias, activation, gate and residual, and their gradient,
+on the GPU against the float64 oracle (oracle/layers.py), through the C ABI.
+
+Tolerances, with u = 2^-24 (half a step of fp32, relative) and 2^-8 for bf16:
+ * z: the product's bound (product_bound of test_gpu_experts.py, counted there),
+   2 u of the magnitudes of a bias, 2^-8 of z where it is kept in bf16.
+ * An activation changes by at most 1.13 of what its argument does (the largest
+   slope, of gelu). Its own evaluation: the argument of an exponential is off by
+   2 u of itself, which the sigmoid's slope turns into at most 2 u 0.23, the
+   exponential, the sum and the reciprocal by 2 u each (erfc by 4 u, its argument
+   by 2 u); all times |z|: 16 u |z| with room.
+ * A gate's product, a residual, a rounding to the type: u, u and 2^-8 (or u).
+ * Slopes: at most 1.13, 24 u for their evaluation (sums of two terms of at most
+   1.2 and 0.5), times |dY| (and |u|).
+ * dX: every dZ is rounded to bf16 once, and so is every weight where dX is bf16,
+   2^-8 each of the sum of magnitudes; sums of m products, at most m u of it
+   (three products per weight in fp32: (3 m + 3) u).
+"""
+import numpy as np
+import pytest
+
+from oracle import experts as X64
+from oracle import layers as L64
+from oracle.dequant import dequantize
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import post_weight_quantization_28_amd as G  # noqa: E402
+from test_gpu_experts import cuda_layers, expert_ids, layers, product_bound, values  # noqa: E402
+
+U32, UBF = 2.0 ** -24, 2.0 ** -8
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def arr(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def last(dtype, x):
+    """The last rounding of values of this size."""
+    return (UBF if dtype == BF16 else U32) * np.abs(x)
+
+
+def value_error(name, z, e):
+    """Bound on act(z)'s error for a z that is off by e."""
+    return (1.13 * e if name != "none" else e) + (0 if name in ("none", "relu") else 16 * U32 * (np.abs(z) + e))
+
+
+def end_error(name, gated, z, e, residual):
+    d = z.shape[1] // 2 if gated else z.shape[1]
+    a = L64.act(name, z[:, :d])[0]
+    ea = value_error(name, z[:, :d], e[:, :d])
+    y, ey = a, ea
+    if gated:
+        u, eu = z[:, d:], e[:, d:]
+        y, ey = a * u, np.abs(u) * ea + np.abs(a) * eu + ea * eu
+        ey = ey + U32 * (np.abs(y) + ey)
+    if residual is not None:
+        ey = ey + U32 * (np.abs(y + residual) + ey)
+    return ey
+
+
+def fast_layers(seed, E, m, n, bits, group):
+    qw, sc, zr = layers(seed, E, m, n, bits, group)
+    return qw, sc / 4, zr
+
+
+LINEARS = [   # T, k, E, d, n, group, drop, only, gathered
+    (1, 1, 1, 33, 32, 32, 0.0, None, False),         # one token, one chunk of codes
+    (1, 2, 8, 96, 512, 128, 0.0, None, True),
+    (3, 1, 1, 128, 1024, 128, 0.0, None, False),     # one dense layer, a few tokens
+    (5, 2, 4, 41, 384, 64, 0.0, None, True),         # odd width: rows of Y at any alignment
+    (30, 2, 7, 65, 1280, 256, 0.2, None, True),      # dropped slots
+    (17, 1, 2, 64, 128, 128, 0.0, [1], True),        # an empty expert
+    (20, 2, 8, 50, 1312, 32, 0.1, None, True),       # few rows, small groups
+    (40, 2, 4, 100, 96, 96, 0.0, None, True),        # 64-row tiles
+    (100, 2, 4, 157, 640, 32, 0.3, None, True),      # ragged both ways
+    (600, 1, 2, 3501, 256, 128, 0.1, None, True),    # more tiles
+    (300, 2, 2, 7001, 96, 32, 0.0, None, True),      # 128-row tiles
+    (257, 2, 3, 96, 320, 160, 0.0, [0, 2], True),    # an empty expert between two
+    (30, 4, 2, 70, 2048, 128, 0.1, None, True),      # parts of K
+    (90, 1, 1, 33, 4128, 32, 0.0, None, False),
+    (1200, 1, 2, 6550, 128, 128, 0.1, None, True),   # 256-row tiles (4 bits), ungated 26 of them wide
+    (1100, 1, 2, 3201, 384, 128, 0.0, None, False),  # and gated
+    (700, 1, 1, 5377, 512, 256, 0.2, None, True),
+]
+
+
+ENDS = [("silu", True), ("gelu", False), ("none", True), ("gelu_tanh", False), ("relu", False), ("none", False)]
+# 4 bits with every end, the other widths (whose ends are the same code) and the largest sizes with some
+LINEAR_CASES = [c + e + (b,) for c in LINEARS for i, e in enumerate(ENDS) for b in (4, 3, 2)
+                if (b == 4 or i < 2) and (c[0] * c[3] < 1000000 or i < 2)]
+
+
+@pytest.mark.parametrize("T,k,E,d,n,group,drop,only,gathered,name,gated,bits", LINEAR_CASES)
+def test_linear(T, k, E, d, n, group, drop, only, gathered, name, gated, bits):
+    off, rows, _ = X64.route(expert_ids(T + d, T, k, E, drop, only), E)
+    R, m = T * k, 2 * d if gated else d
+    X = values(n + T, T if gathered else R, n)
+    qw, sc, zr = fast_layers(d + bits, E, m, n, bits, group)
+    r = np.random.default_rng(d)
+    bias = r.standard_normal((E, m)).astype(np.float32)
+    packed = cuda_layers(qw, sc, zr)
+    rt = torch.from_numpy(rows).cuda() if gathered else None
+    seg = None if E == 1 and drop == 0 else torch.from_numpy(off).cuda()
+    src = rows if gathered else None
+    bound = product_bound(arr(X), off, src, qw, sc, zr, bits, group, n, R, E)
+    live = slice(0, off[-1])
+    for i, (ydt, rdt, zdt) in enumerate([(BF16, BF16, BF16), (F32, F32, F32), (BF16, None, None), (F32, BF16, None)]):
+        if bits != 4 and i > 1:
+            break
+        res = None if rdt is None else values(5, R, d, dtype=rdt)
+        b = None if i == 2 else bias
+        out, kept = values(8, R, d, dtype=ydt), None if zdt is None else values(9, R, m, dtype=zdt)
+        before, zbefore = arr(out), np.zeros((R, m)) if kept is None else arr(kept)
+        got = G.linear(X, *packed, bits, group, bias=None if b is None else torch.from_numpy(b).cuda(), act=name,
+                       gated=gated, residual=res, offsets=seg, rows=rt, keep=kept, out=out)
+        Y, Z = got if kept is not None else (got, None)
+        assert Y is out and (kept is None or Z is kept)
+        ref, zref = L64.linear(arr(X), off, qw, sc, zr, bits, group, name, gated, before, zbefore, b,
+                               None if res is None else arr(res), src)
+        e = bound + (0 if b is None else 2 * U32 * (np.abs(zref) + np.abs(np.repeat(bias, np.diff(off), axis=0)).max()))
+        ey = end_error(name, gated, zref, e, None if res is None else arr(res))
+        ey = ey + last(ydt, np.abs(ref) + ey)
+        assert np.all((np.abs(arr(Y) - ref) <= ey)[live])
+        assert np.array_equal(arr(Y)[off[-1]:], before[off[-1]:])
+        if kept is not None:
+            assert np.all((np.abs(arr(Z) - zref) <= e + last(zdt, np.abs(zref) + e))[live])
+            assert np.array_equal(arr(Z)[off[-1]:], zbefore[off[-1]:])
+
+
+GRADS = [   # R, E, d, n, group, cuts (None: one layer without offsets)
+    (1, 1, 32, 64, 32, None), (1, 1, 1, 32, 32, None), (3, 2, 70, 128, 128, [1, 3]), (50, 3, 65, 96, 96, [20, 20, 45]),
+    (130, 1, 64, 160, 32, None), (400, 2, 257, 320, 64, [129, 400]), (300, 2, 100, 256, 256, [0, 290]),
+    (1100, 2, 96, 320, 64, [500, 1090]), (24, 4, 750, 128, 32, [3, 3, 10, 23]), (20, 1, 1501, 96, 32, None),
+    (700, 70, 40, 64, 32, "many"), (64, 1, 300, 64, 32, [64]), (65, 1, 256, 64, 64, [65]), (1100, 2, 96, 6432, 32, [500, 1090]),
+]
+
+
+def segments(E, R, cuts):
+    if cuts == "many":                                       # more than 64 segments, some empty
+        return np.r_[0, np.sort(np.random.default_rng(E).integers(0, R - 5, E))].astype(np.int32)
+    return np.array([0] + (cuts if cuts is not None else [R]), np.int32)
+
+
+GRAD_ENDS = [("silu", True), ("gelu", False), ("gelu_tanh", True), ("relu", False), ("none", False), ("none", True)]
+GRAD_CASES = [c + e + (b,) for c in GRADS for i, e in enumerate(GRAD_ENDS) for b in (4, 3) if b == 4 or i == 0]
+
+
+@pytest.mark.parametrize("R,E,d,n,group,cuts,name,gated,bits", GRAD_CASES)
+def test_linear_grad(R, E, d, n, group, cuts, name, gated, bits):
+    off = segments(E, R, cuts)
+    m = 2 * d if gated else d
+    qw, sc, zr = layers(d + bits, E, m, n, bits, group)
+    packed = cuda_layers(qw, sc, zr)
+    live = slice(off[0], off[-1])
+    per = np.diff(off).max() if E else 0
+    for dydt, zdt, xdt in ((BF16, BF16, BF16), (F32, F32, F32), (BF16, F32, BF16), (F32, BF16, BF16)):
+        dY, Z = values(1, R, d, dtype=dydt, scale=1e-2), values(2, R, m, dtype=zdt, scale=1.5)
+        dZ, out = values(3, R, m), values(4, R, n, dtype=xdt)
+        zb, xb = arr(dZ), arr(out)
+        dX, dZ2, db = G.linear_grad(dY, Z, *packed, bits, group, n, act=name, gated=gated,
+                                    offsets=None if cuts is None else torch.from_numpy(off).cuda(), want_bias=True, dZ=dZ,
+                                    out=out)
+        assert dX is out and dZ2 is dZ
+        rx, rz, rb = L64.linear_grad(arr(dY), arr(Z), off, qw, sc, zr, bits, group, n, name, gated, zb, xb)
+        g, z = np.abs(arr(dY)), np.abs(arr(Z))
+        if gated:
+            f = np.concatenate([g * z[:, d:], g * z[:, :d]], axis=1)   # what slope or value are multiplied by, or bound by
+        else:
+            f = g
+        ez = (0 if name == "none" and not gated else 32 * U32) * f
+        assert np.all((np.abs(arr(dZ) - rz) <= ez + UBF * (np.abs(rz) + ez) + 2.0 ** -134)[live])
+        assert np.array_equal(arr(dZ)[off[-1]:], zb[off[-1]:])
+        eb = np.zeros_like(rb)
+        for e in range(E):
+            p = slice(off[e], off[e + 1])
+            # at most per / 8 + 8 + per / 64 additions in one chain
+            eb[e] = ez[p].sum(0) if not np.isscalar(ez) else 0
+            eb[e] += U32 * (per / 8 + per / 64 + 12) * np.abs(rz[p]).sum(0)
+        assert np.all(np.abs(arr(db) - rb) <= eb)
+        mag = np.zeros((R, n))
+        ezx = np.zeros((R, n))
+        for e in range(E):
+            p, W = slice(off[e], off[e + 1]), np.abs(dequantize(qw[e], sc[e], zr[e], bits, group, n))
+            mag[p] = np.abs(rz[p]) @ W
+            ezx[p] = (ez[p] if not np.isscalar(ez) else np.zeros_like(rz[p])) @ W
+        ex = 1.01 * (ezx + UBF * mag) + ((UBF + (m + 2) * U32) if xdt == BF16 else (3 * m + 3) * U32) * 1.01 * mag
+        assert np.all((np.abs(arr(dX) - rx) <= ex + last(xdt, np.abs(rx) + ex))[live])
+        assert np.array_equal(arr(dX)[off[-1]:], xb[off[-1]:])
+
+
+def test_linear_grad_of_a_plain_layer_needs_no_copy():
+    """No activation, no gate: dY stands for dZ, Z is not read; an fp32 dY is
+    rounded into a new dZ; an expert without rows has a bias gradient of zero."""
+    qw, sc, zr = layers(1, 3, 70, 128, 4, 64)
+    packed = cuda_layers(qw, sc, zr)
+    off = torch.tensor([0, 40, 40, 90], dtype=torch.int32, device="cuda")
+    dY = values(1, 90, 70)
+    dX, dZ, db = G.linear_grad(dY, None, *packed, 4, 64, 128, offsets=off, want_bias=True)
+    assert dZ is dY and torch.equal(dX, G.expert_matmul_grad(dY, off, *packed, 4, 64, 128))
+    assert torch.count_nonzero(db[1]) == 0 and db.shape == (3, 70)
+    a, b, c = G.linear_grad(dY.float(), None, *packed, 4, 64, 128, offsets=off)
+    assert torch.equal(b, dY) and torch.equal(a, dX) and c is None
+    x, z, db = G.linear_grad(dY[:0], None, *packed, 4, 64, 128, offsets=off * 0, want_bias=True)
+    assert x.shape == (0, 128) and torch.count_nonzero(db) == 0
+
+
+def test_residual_and_gradients_in_place():
+    """Y over the residual, dZ over Z and over dY."""
+    qw, sc, zr = fast_layers(1, 1, 128, 256, 4, 64)
+    packed = cuda_layers(qw, sc, zr)
+    for R in (3, 40, 300):
+        X, res = values(R, R, 256), values(2, R, 64)
+        want = G.linear(X, *packed, 4, 64, act="silu", gated=True, residual=res)
+        got = G.linear(X, *packed, 4, 64, act="silu", gated=True, residual=res, out=res)
+        assert got is res and torch.equal(res, want)
+        dY, Z = values(3, R, 64), values(4, R, 128)
+        want = G.linear_grad(dY, Z, *packed, 4, 64, 256, act="silu", gated=True)
+        got = G.linear_grad(dY, Z, *packed, 4, 64, 256, act="silu", gated=True, dZ=Z)
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], Z)
+        dY, Z = values(3, R, 128), values(4, R, 128)
+        want = G.linear_grad(dY, Z, *packed, 4, 64, 256, act="gelu", want_bias=True)
+        got = G.linear_grad(dY, Z, *packed, 4, 64, 256, act="gelu", dZ=dY, want_bias=True)
+        assert torch.equal(want[1], dY) and torch.equal(want[0], got[0]) and torch.equal(want[2], got[2])
+
+
+def test_linear_at_any_alignment():
+    """Rows apart and at odd addresses: the aligned result within the last
+    rounding's and the sums' bounds, nothing written beside the rows."""
+    n, d, E = 256, 33, 1
+    for R in (5, 50, 300):
+        for gated in (False, True):
+            m = 2 * d if gated else d
+            qw, sc, zr = fast_layers(R, E, m, n, 4, 128)
+            packed = cuda_layers(qw, sc, zr)
+            X, res = values(R, R, n), values(3, R, d)
+            wx, wr = values(4, R, n + 5), values(5, R, d + 3)
+            wx[:, 3:3 + n], wr[:, 1:1 + d] = X, res
+            wy = torch.full((R, d + 9), 7.0, dtype=BF16, device="cuda")
+            wz = torch.full((R, m + 4), 7.0, dtype=F32, device="cuda")
+            Y, Z = G.linear(X, *packed, 4, 128, act="gelu", gated=gated, residual=res, keep=F32)
+            G.linear(wx[:, 3:3 + n], *packed, 4, 128, act="gelu", gated=gated, residual=wr[:, 1:1 + d],
+                     keep=wz[:, 2:2 + m], out=wy[:, 4:4 + d])
+            # (unaligned rows go in tiles, whose bound is the smaller one)
+            e = 2 * product_bound(arr(X), [0, R], None, qw, sc, zr, 4, 128, n, R, 1)
+            assert np.all(np.abs(arr(wz[:, 2:2 + m]) - arr(Z)) <= e)
+            ey = 2 * end_error("gelu", gated, arr(Z), e, arr(res))
+            assert np.all(np.abs(arr(wy[:, 4:4 + d]) - arr(Y)) <= ey + 2 * last(BF16, np.abs(arr(Y)) + ey))
+            assert torch.all(wy[:, :4] == 7) and torch.all(wy[:, 4 + d:] == 7)
+            assert torch.all(wz[:, :2] == 7) and torch.all(wz[:, 2 + m:] == 7)
+
+
+def test_nonfinite_activations_stay_in_their_rows():
+    for R in (6, 60, 400):
+        X = values(R, R, 128)
+        X[2, 5], X[4, 7] = float("nan"), float("inf")
+        qw, sc, zr = fast_layers(1, 1, 96, 128, 4, 32)
+        for name in L64_ACTS:
+            Y = arr(G.linear(X, *cuda_layers(qw, sc, zr), 4, 32, act=name))
+            bad = ~np.isfinite(Y).all(1)
+            assert np.isnan(Y[2]).all() and set(np.nonzero(bad)[0]) <= {2, 4}
+            assert bad[4] or name == "relu"
+
+
+L64_ACTS = ("none", "relu", "gelu", "gelu_tanh", "silu")
+
+
+def test_activations_over_their_range():
+    """Values and slopes from large negative to large positive arguments, through
+    a layer that is the identity (code 1, zero point 0, scale 1)."""
+    n = 32
+    codes = np.eye(n, dtype=np.uint8)
+    from oracle import packing as P
+    packed = cuda_layers(P.pack(codes, 4)[None], np.ones((1, n, 1), np.float32), np.zeros((1, n, 1), np.uint8))
+    z = np.concatenate([np.linspace(-12, 12, 2001), [-3e4, -200.0, -90.0, 0.0, 90.0, 200.0, 3e4], -2.0 ** np.arange(-40, 5.0)])
+    z = np.resize(z, (-(-len(z) // n)) * n).reshape(-1, n)
+    X = torch.from_numpy(z.astype(np.float32)).to(BF16).cuda()
+    zz = arr(X)
+    for name in L64_ACTS:
+        Y, Z = G.linear(X, *packed, 4, 32, act=name, keep=F32, out_dtype=F32)
+        assert np.array_equal(arr(Z), zz)
+        with np.errstate(over="ignore"):
+            a, slope = L64.act(name, zz)
+        assert np.all(np.abs(arr(Y) - a) <= 16 * U32 * np.abs(zz))
+        dY = torch.ones_like(Z)
+        _, dZ, db = G.linear_grad(dY, Z, *packed, 4, 32, n, act=name, want_bias=True)
+        assert np.all(np.abs(arr(dZ) - slope) <= 32 * U32 + UBF * np.abs(slope) + 2.0 ** -134)
+        assert np.all(np.abs(arr(db)[0] - slope.sum(0)) <= (32 + 40) * U32 * (1.2 * len(zz)))
+
+
+def test_gradients_against_differences():
+    """Adjoint: <dY, linear(X + h V) - linear(X - h V)> / 2 h = <dX, V> in the
+    oracle's forward, for a gated layer of two experts."""
+    R, E, d, n, group = 30, 2, 32, 64, 32
+    off = np.array([0, 13, 30], np.int32)
+    qw, sc, zr = fast_layers(3, E, 2 * d, n, 4, group)
+    packed = cuda_layers(qw, sc, zr)
+    X = values(1, R, n)
+    seg = torch.from_numpy(off).cuda()
+    _, Z = G.linear(X, *packed, 4, group, act="silu", gated=True, offsets=seg, keep=F32)
+    dY = values(2, R, d)
+    dX, _, db = G.linear_grad(dY, Z, *packed, 4, group, n, act="silu", gated=True, offsets=seg, want_bias=True,
+                              out_dtype=F32)
+    r = np.random.default_rng(5)
+    V = r.standard_normal((R, n))
+
+    def total(x, bias):
+        return float((L64.linear(x, off, qw, sc, zr, 4, group, "silu", True, np.zeros((R, d)), np.zeros((R, 2 * d)),
+                                 bias)[0] * arr(dY)).sum())
+    h = 1e-4
+    zero = np.zeros((E, 2 * d))
+    diff = (total(arr(X) + h * V, zero) - total(arr(X) - h * V, zero)) / (2 * h)
+    z = arr(Z)
+    W = [np.abs(dequantize(qw[e], sc[e], zr[e], 4, group, n)) for e in range(E)]
+    dz = np.abs(L64.linear_grad(arr(dY), z, off, qw, sc, zr, 4, group, n, "silu", True, np.zeros_like(z), np.zeros((R, n)))[1])
+    mag = sum((dz[off[e]:off[e + 1]] @ W[e] * np.abs(V[off[e]:off[e + 1]])).sum() for e in range(E))
+    # dZ rounded to bf16: 2^-8 of the magnitudes; the difference itself: h^2 of third derivatives, far below
+    assert abs(float((arr(dX) * V).sum()) - diff) <= (UBF + 1e-4) * mag
+    B = r.standard_normal((E, 2 * d))
+    diff = (total(arr(X), h * B) - total(arr(X), -h * B)) / (2 * h)
+    big = sum((dz[off[e]:off[e + 1]] * np.abs(B[e])).sum() for e in range(E))
+    assert abs(float((arr(db) * B).sum()) - diff) <= 1e-4 * big
+
+
+def test_wrong_offsets_stay_in_bounds():
+    """Offsets that fall, pass R or are negative give some result and touch
+    nothing outside the matrices."""
+    qw, sc, zr = fast_layers(1, 4, 64, 64, 4, 32)
+    packed = cuda_layers(qw, sc, zr)
+    for bad in ([0, 30, 10, 90, 40], [-5, 3, 3, 1000, 2000], [50, 40, 30, 20, 10]):
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        rows = torch.tensor([-7, 10 ** 9] * 25, dtype=torch.int32, device="cuda")
+        bias = torch.ones(4, 64, device="cuda")
+        pad = torch.full((60, 40), 3.0, dtype=BF16, device="cuda")
+        out, kept = pad[5:55, :32], torch.full((60, 70), 3.0, dtype=BF16, device="cuda")
+        G.linear(values(1, 9, 64), *packed, 4, 32, bias=bias, act="silu", gated=True, offsets=off, rows=rows, out=out,
+                 keep=kept[5:55, :64])
+        dz = torch.full((60, 70), 3.0, dtype=BF16, device="cuda")
+        G.linear_grad(values(2, 50, 32), values(3, 50, 64), *packed, 4, 32, 64, act="silu", gated=True, offsets=off,
+                      want_bias=True, dZ=dz[5:55, :64])
+        torch.cuda.synchronize()
+        for t, w in ((pad, 32), (kept, 64), (dz, 64)):
+            assert torch.all(t[:5] == 3) and torch.all(t[55:] == 3) and torch.all(t[:, w:] == 3)
+
+
+@pytest.mark.parametrize("T", [4, 600])
+def test_captured_step_replays(T):
+    """Forward and backward in a captured graph, replayed on changing inputs
+    with eager work between: bitwise the eager results."""
+    E, d, n, group = 4, 96, 256, 128
+    qw, sc, zr = fast_layers(1, E, 2 * d, n, 4, group)
+    packed = cuda_layers(qw, sc, zr)
+    off, rows, _ = X64.route(expert_ids(T, T, 2, E), E)
+    seg, src = torch.from_numpy(off).cuda(), torch.from_numpy(rows).cuda()
+    res, dY = values(4, 2 * T, d), values(5, 2 * T, d)
+
+    def step(x):
+        Y, Z = G.linear(x, *packed, 4, group, act="silu", gated=True, residual=res, offsets=seg, rows=src, keep=BF16)
+        return (Y, Z) + G.linear_grad(dY, Z, *packed, 4, group, n, act="silu", gated=True, offsets=seg, want_bias=True)
+    X = [values(10 + i, T, n) for i in range(3)]
+    want = [[t.clone() for t in step(x)] for x in X]
+    live = X[0].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(live)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(live)
+    for i in (0, 1, 2, 0):
+        live.copy_(X[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+        step(X[1])
+
+
+def test_linear_binding_refusals():
+    qw, sc, zr = cuda_layers(*fast_layers(1, 2, 64, 64, 4, 32))
+    X, off = values(1, 6, 64), torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    ok = dict(act="silu", gated=True, offsets=off)
+    G.linear(X, qw, sc, zr, 4, 32, **ok)
+    for bad in (dict(act="tanh"), dict(act=None), dict(bias=torch.zeros(2, 32, device="cuda")), dict(residual=values(1, 6, 64)),
+                dict(keep=values(1, 6, 32)), dict(out=values(1, 6, 64)), dict(offsets=off[:2])):
+        with pytest.raises(ValueError):
+            G.linear(X, qw, sc, zr, 4, 32, **{**ok, **bad})
+    for bad in (dict(bias=torch.zeros(2, 64, dtype=BF16, device="cuda")), dict(residual=values(1, 6, 32).half()),
+                dict(keep=torch.float16), dict(out_dtype=torch.float16), dict(bias=torch.zeros(2, 64))):
+        with pytest.raises(TypeError):
+            G.linear(X, qw, sc, zr, 4, 32, **{**ok, **bad})
+    odd = cuda_layers(*fast_layers(1, 1, 33, 64, 4, 32))
+    with pytest.raises(ValueError):
+        G.linear(X, *odd, 4, 32, act="silu", gated=True)
+    dY = values(1, 6, 32)
+    with pytest.raises(ValueError):
+        G.linear_grad(dY, None, qw, sc, zr, 4, 32, 64, **ok)
+    with pytest.raises(ValueError):
+        G.linear_grad(values(1, 6, 64), values(1, 6, 64), qw, sc, zr, 4, 32, 64, **ok)
+    with pytest.raises(ValueError):
+        G.linear_grad(dY, values(1, 6, 32), qw, sc, zr, 4, 32, 64, **ok)
+    with pytest.raises(TypeError):
+        G.linear_grad(dY, values(1, 6, 64), qw, sc, zr, 4, 32, 64, dZ=torch.zeros(6, 64, device="cuda"), **ok)

@@ -1,0 +1,230 @@
+"""CPU tests of the layer operators: the oracle against worked cases, closed
+forms and differences, and every refusal of the calls on the host."""
+import ctypes
+import math
+import os
+
+import numpy as np
+import pytest
+
+from oracle import layers as L64
+from oracle import packing as P
+
+FAKE, NULL = ctypes.c_void_p(1 << 20), ctypes.c_void_p(0)
+
+
+def _lib():
+    pytest.importorskip("torch")
+    import post_weight_quantization_28_amd as G
+    if not os.path.exists(G.LIB_PATH):
+        pytest.skip("libgptq.so not built")
+    return G, G.load()
+
+
+# ---------------------------------------------------------------- oracle
+def test_activations():
+    z = np.linspace(-6, 6, 241)
+    h = 1e-5
+    for name in ("none", "relu", "gelu", "gelu_tanh", "silu"):
+        a, slope = L64.act(name, z)
+        diff = (L64.act(name, z + h)[0] - L64.act(name, z - h)[0]) / (2 * h)
+        ok = np.abs(z) > 1e-3 if name == "relu" else np.ones_like(z, bool)
+        assert np.all(np.abs(slope - diff)[ok] < 1e-8)
+        assert a[120] == 0
+        if name not in ("none", "relu"):
+            # all three are z times a distribution function: symmetric about one half
+            assert np.allclose(a - L64.act(name, -z)[0], z, atol=1e-12)
+            assert abs(a[-1] - 6) < 0.02 and abs(a[0]) < 0.02
+    assert abs(L64.act("gelu", np.array([1.0]))[0][0] - 0.841344746068543) < 1e-14     # Phi(1)
+    assert abs(L64.act("silu", np.array([1.0]))[0][0] - 1 / (1 + math.exp(-1))) < 1e-15
+    assert abs(L64.act("gelu_tanh", np.array([1.0]))[0][0] - 0.5 * (1 + math.tanh(math.sqrt(2 / math.pi) * 1.044715))) < 1e-15
+
+
+def _tiny(E, m, n, seed=0):
+    r = np.random.default_rng(seed)
+    codes = r.integers(0, 16, (E, m, n)).astype(np.uint8)
+    qw = np.stack([P.pack(c, 4) for c in codes])
+    return qw, r.uniform(0.01, 0.1, (E, m, n // 32)).astype(np.float32), r.integers(0, 16, (E, m, n // 32)).astype(np.uint8)
+
+
+def test_linear_worked_case():
+    """Two codes of weight: z by hand, the gate, the residual, rows behind the
+    segments as they were."""
+    codes = np.zeros((1, 2, 32), np.uint8)
+    codes[0, 0, :2], codes[0, 1, 3] = [3, 1], 5
+    qw = P.pack(codes[0], 4)[None]
+    sc, zr = np.array([[[0.5], [2.0]]], np.float32), np.array([[[1], [0]]], np.uint8)
+    X = np.zeros((3, 32))
+    X[0, 0], X[0, 1], X[1, 3] = 2.0, 7.0, 1.5
+    # row 0: gate 0.5 (2 (3 - 1) + 7 (1 - 1)) = 2, other 0; row 1: gate 0.5 1.5 (0 - 1) = -0.75, other 2 5 1.5 = 15
+    Y, Z = L64.linear(X, [0, 2], qw, sc, zr, 4, 32, "none", True, np.full((3, 1), 9.0), np.full((3, 2), 8.0),
+                      bias=np.array([[1.0, 2.0]]), residual=np.array([[0.5], [0.25], [0.0]]))
+    assert Z.tolist() == [[3.0, 2.0], [0.25, 17.0], [8.0, 8.0]]
+    assert Y.tolist() == [[6.5], [4.5], [9.0]]
+    Y, _ = L64.linear(X, [0, 2], qw, sc, zr, 4, 32, "relu", False, np.full((3, 2), 9.0), np.zeros((3, 2)))
+    assert Y.tolist() == [[2.0, 0.0], [0.0, 15.0], [9.0, 9.0]]
+
+
+def test_linear_grad_is_the_derivative():
+    E, d, n, R = 2, 3, 32, 5
+    r = np.random.default_rng(2)
+    for gated in (False, True):
+        m = 2 * d if gated else d
+        qw, sc, zr = _tiny(E, m, n)
+        X, bias, dY = r.standard_normal((R, n)), r.standard_normal((E, m)), r.standard_normal((R, d))
+        off = [0, 2, 5]
+
+        def total(x, b):
+            return float((L64.linear(x, off, qw, sc, zr, 4, 32, "gelu", gated, np.zeros((R, d)), np.zeros((R, m)), b)[0] * dY).sum())
+        Z = L64.linear(X, off, qw, sc, zr, 4, 32, "gelu", gated, np.zeros((R, d)), np.zeros((R, m)), bias)[1]
+        dX, dZ, db = L64.linear_grad(dY, Z, off, qw, sc, zr, 4, 32, n, "gelu", gated, np.zeros((R, m)), np.zeros((R, n)))
+        h = 1e-6
+        for i in range(R):
+            for j in (0, 7, 31):
+                up, dn = X.copy(), X.copy()
+                up[i, j] += h
+                dn[i, j] -= h
+                assert abs((total(up, bias) - total(dn, bias)) / (2 * h) - dX[i, j]) < 1e-6 * (1 + abs(dX[i, j]))
+        for e in range(E):
+            for j in range(m):
+                up, dn = bias.copy(), bias.copy()
+                up[e, j] += h
+                dn[e, j] -= h
+                assert abs((total(X, up) - total(X, dn)) / (2 * h) - db[e, j]) < 1e-6 * (1 + abs(db[e, j]))
+
+
+def test_expert_layer_is_its_parts():
+    """The whole layer is linear, linear and the weighted sum of them."""
+    r = np.random.default_rng(3)
+    T, k, E, n, d = 4, 2, 3, 32, 32
+    up, down = _tiny(E, 2 * d, n, 1), _tiny(E, n, d, 2)
+    X, w = r.standard_normal((T, n)), r.uniform(0, 1, (T, k))
+    ids = np.array([[0, 2], [1, 1], [-1, 2], [3, -7]], np.int32)
+    b1, b2, res = r.standard_normal((E, 2 * d)), r.standard_normal((E, n)), r.standard_normal((T, n))
+    Y = L64.expert_layer(X, ids, w, up, down, 4, 32, "silu", True, b1, b2, res)
+    want = res.copy()
+    for t in range(T):
+        for j in range(k):
+            e = ids[t, j]
+            if 0 <= e < E:
+                h, _ = L64.linear(X[t:t + 1], [0, 1], *(x[e:e + 1] for x in up), 4, 32, "silu", True, np.zeros((1, d)),
+                                  np.zeros((1, 2 * d)), b1[e:e + 1])
+                o, _ = L64.linear(h, [0, 1], *(x[e:e + 1] for x in down), 4, 32, "none", False, np.zeros((1, n)),
+                                  np.zeros((1, n)), b2[e:e + 1])
+                want[t] += w[t, j] * o[0]
+    assert np.allclose(Y, want, rtol=1e-12, atol=1e-12) and np.array_equal(Y[3], res[3])
+
+
+def test_distill_closed_forms():
+    V = 5
+    Z = np.zeros((2, V))
+    ids, t = np.array([[0, 3], [2, -1]]), np.array([[1.0, 1.0], [4.0, 9.0]])
+    loss, lse, ps = L64.distill(Z, ids, t, 1.0, False)
+    assert np.allclose(lse, math.log(V)) and np.allclose(loss, [math.log(V) - math.log(2), math.log(V)])
+    assert ps == [[(0, 0.5), (3, 0.5)], [(2, 1.0)]]
+    g = L64.distill_grad(Z, lse, ps, np.array([1.0, 2.0]), 1.0)
+    assert np.allclose(g[0], [0.2 - 0.5, 0.2, 0.2, 0.2 - 0.5, 0.2]) and np.allclose(g[1], 2 * np.array([0.2, 0.2, -0.8, 0.2, 0.2]))
+    # the teacher's own logits over all entries: no divergence, no gradient
+    z = np.random.default_rng(1).standard_normal((1, V))
+    loss, lse, ps = L64.distill(z, np.arange(V)[None], z, 3.0, False)
+    assert abs(loss[0]) < 1e-14 and np.abs(L64.distill_grad(z, lse, ps, np.ones(1), 3.0)).max() < 1e-15
+    # log probabilities count as they are: half of the mass, half of the sums
+    loss, lse, ps = L64.distill(z, np.array([[1]]), np.array([[math.log(0.5)]]), 1.0, True)
+    assert abs(loss[0] - 0.5 * (math.log(0.5) - (z[0, 1] - lse[0]))) < 1e-14
+    # nothing to learn
+    loss, _, ps = L64.distill(z, np.array([[-1, V]]), np.zeros((1, 2)), 1.0, False)
+    assert loss[0] == 0 and np.all(L64.distill_grad(z, lse, ps, np.ones(1), 1.0) == 0)
+
+
+def test_distill_grad_is_the_derivative():
+    r = np.random.default_rng(4)
+    Z, ids, t = r.standard_normal((2, 9)), np.array([[1, 4, 4], [8, -1, 0]]), r.standard_normal((2, 3)) - 1
+    for logp in (False, True):
+        loss, lse, ps = L64.distill(Z, ids, t, 1.5, logp)
+        g = L64.distill_grad(Z, lse, ps, np.ones(2), 1.5)
+        for i in range(2):
+            for v in range(9):
+                up, dn = Z.copy(), Z.copy()
+                up[i, v] += 1e-6
+                dn[i, v] -= 1e-6
+                d = (L64.distill(up, ids, t, 1.5, logp)[0][i] - L64.distill(dn, ids, t, 1.5, logp)[0][i]) / 2e-6
+                assert abs(d - g[i, v]) < 1e-8
+
+
+# ---------------------------------------------------------------- refusals
+def test_linear_refusals():
+    G, lib = _lib()
+    odd, one = ctypes.c_void_p((1 << 20) + 4), ctypes.c_void_p((1 << 20) + 1)
+
+    def fwd(X=FAKE, xdt=0, T=8, n=128, ldx=128, rows=FAKE, R=16, off=FAKE, E=4, qw=FAKE, sc=FAKE, zr=FAKE, bias=FAKE,
+            d=64, bits=4, group=64, act=4, gated=1, res=FAKE, rdt=0, ldr=64, Z=FAKE, zdt=1, ldz=128, Y=FAKE, ydt=1, ldy=64,
+            ws=NULL, wsb=0):
+        return lib.gptq_linear(None, X, xdt, T, n, ldx, rows, R, off, E, qw, sc, zr, bias, d, bits, group, act, gated, res,
+                               rdt, ldr, Z, zdt, ldz, Y, ydt, ldy, ws, wsb)
+    for bad in (dict(xdt=1), dict(ydt=2), dict(rdt=3), dict(zdt=-1), dict(n=0), dict(d=0), dict(bits=5), dict(group=48),
+                dict(group=96), dict(E=0), dict(E=1025), dict(off=NULL), dict(T=0), dict(rows=NULL), dict(ldx=127),
+                dict(ldy=63), dict(ldr=63), dict(ldz=127), dict(X=NULL), dict(qw=NULL), dict(sc=NULL), dict(zr=NULL),
+                dict(Y=NULL), dict(qw=odd), dict(R=-1), dict(R=2 ** 31), dict(act=5), dict(act=-1), dict(gated=2),
+                dict(res=one), dict(Z=one), dict(bias=one), dict(Y=one), dict(d=2 ** 30, ldy=2 ** 30),
+                dict(R=2 ** 30, d=2 ** 20, gated=0, ldy=2 ** 20, ldr=2 ** 20, ldz=2 ** 20)):
+        assert fwd(**bad) == -1, bad
+    assert fwd(R=0, X=NULL, Y=NULL) == 0
+
+    def bwd(dY=FAKE, dydt=0, ldy=64, Z=FAKE, zdt=0, ldz=128, R=16, off=FAKE, E=4, qw=FAKE, sc=FAKE, zr=FAKE, d=64, n=128,
+            bits=4, group=64, act=4, gated=1, dZ=FAKE, lddz=128, db=FAKE, dX=FAKE, xdt=0, ldx=128, ws=NULL, wsb=0):
+        return lib.gptq_linear_grad(None, dY, dydt, ldy, Z, zdt, ldz, R, off, E, qw, sc, zr, d, n, bits, group, act, gated,
+                                    dZ, lddz, db, dX, xdt, ldx, ws, wsb)
+    for bad in (dict(dydt=2), dict(zdt=2), dict(xdt=2), dict(n=0), dict(d=0), dict(bits=1), dict(group=48), dict(E=0),
+                dict(off=NULL), dict(ldy=63), dict(ldz=127), dict(lddz=127), dict(ldx=127), dict(dY=NULL), dict(Z=NULL),
+                dict(dZ=NULL), dict(dX=NULL), dict(qw=odd), dict(dY=one), dict(Z=one), dict(dZ=one), dict(db=one),
+                dict(R=-1), dict(R=2 ** 31), dict(act=9), dict(gated=-1), dict(act=0, gated=0, dZ=NULL, dydt=1)):
+        assert bwd(**bad) == -1, bad
+    assert bwd() == -5 and bwd(ws=odd, wsb=1 << 30) == -5         # the bias' partial sums need a workspace
+    out = ctypes.c_size_t(0)
+    for need in (lib.gptq_linear_workspace_bytes, lib.gptq_linear_grad_workspace_bytes):
+        assert need(16, 128, 64, 1, 4, 4, 64, ctypes.byref(out)) == 0 and out.value % 256 == 0
+        for bad in ((-1, 128, 64, 1, 4, 4, 64), (16, 0, 64, 1, 4, 4, 64), (16, 128, 0, 1, 4, 4, 64), (16, 128, 64, 2, 4, 4, 64),
+                    (16, 128, 64, 1, 0, 4, 64), (16, 128, 64, 1, 4, 7, 64), (16, 128, 64, 1, 4, 4, 48)):
+            assert need(*bad, ctypes.byref(out)) == -1
+        assert need(16, 128, 64, 1, 4, 4, 64, None) == -1
+
+
+def test_distill_refusals():
+    G, lib = _lib()
+    one = ctypes.c_void_p((1 << 20) + 1)
+    inf, nan = float("inf"), float("nan")
+
+    def fwd(Z=FAKE, dt=0, T=4, V=100, ldz=100, ids=FAKE, t=FAKE, K=3, temp=1.0, lp=0, loss=FAKE, lse=FAKE, ws=NULL, wsb=0):
+        return lib.gptq_distill(None, Z, dt, T, V, ldz, ids, t, K, temp, lp, loss, lse, ws, wsb)
+
+    def bwd(Z=FAKE, dt=0, T=4, V=100, ldz=100, ids=FAKE, t=FAKE, K=3, temp=1.0, lp=0, lse=FAKE, g=FAKE,
+            dZ=ctypes.c_void_p(1 << 21), odt=0, ldd=100):
+        return lib.gptq_distill_grad(None, Z, dt, T, V, ldz, ids, t, K, temp, lp, lse, g, dZ, odt, ldd)
+    for bad in (dict(dt=2), dict(T=-1), dict(V=0), dict(V=2 ** 31), dict(T=2 ** 24), dict(K=0), dict(K=1025), dict(temp=0.0),
+                dict(temp=-1.0), dict(temp=nan), dict(temp=inf), dict(temp=1e-45), dict(lp=2), dict(ldz=99), dict(Z=NULL),
+                dict(ids=NULL), dict(t=NULL), dict(lse=NULL), dict(Z=one)):
+        assert fwd(**bad) == -1 and bwd(**bad) == -1, bad
+    assert fwd(loss=NULL) == -1
+    for bad in (dict(g=NULL), dict(dZ=NULL), dict(dZ=one), dict(odt=2), dict(ldd=99), dict(dZ=FAKE, odt=1),
+                dict(dZ=FAKE, ldd=101)):
+        assert bwd(**bad) == -1, bad
+    assert fwd(T=0, Z=NULL) == 0 and bwd(T=0, Z=NULL, dZ=NULL) == 0
+    out = ctypes.c_size_t(0)
+    need = lib.gptq_distill_workspace_bytes
+    assert need(4096, 131072, ctypes.byref(out)) == 0 and out.value == 0
+    assert need(4, 131072, ctypes.byref(out)) == 0 and out.value > 0
+    assert fwd(V=131072, ldz=131072) == -5
+    for bad in ((-1, 10), (4, 0), (2 ** 24, 10), (4, 2 ** 31)):
+        assert need(*bad, ctypes.byref(out)) == -1
+    assert need(4, 10, None) == -1
+
+
+def test_binding_refuses_host_tensors():
+    G, _ = _lib()
+    import torch
+    x, q = torch.zeros((2, 32), dtype=torch.bfloat16), torch.zeros((2, 4), dtype=torch.int32)
+    f, i = torch.zeros((2, 1)), torch.zeros((2, 1), dtype=torch.int32)
+    for call in (lambda: G.linear(x, q, f, f, 4, 32), lambda: G.linear_grad(x, x, q, f, f, 4, 32, 32),
+                 lambda: G.distill(x, i, f), lambda: G.distill_grad(x, i, f, f[0], f[0])):
+        with pytest.raises(TypeError):
+            call()
