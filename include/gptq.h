@@ -471,6 +471,43 @@ gptq_status gptq_linear_grad(void *stream, const void *dY, int32_t dydt, int64_t
                              int32_t group, int32_t act, int32_t gated, void *dZ, int64_t lddz, float *dbias, void *dX,
                              int32_t dxdt, int64_t ldx, void *workspace, size_t ws_bytes);
 
+/* ---- A whole layer of experts for a few tokens ----------------------------------
+ * gptq_expert_layer: for T tokens with k slots each, in two launches,
+ *   h = end(up_e x_t + up_bias[e]),  e = expert_ids[t][j]
+ *   Y[t] = residual[t] + sum_j weights[t k + j] (down_e h + down_bias[e])
+ * with end(z) = act(z), or act(z[0 .. d)) * z[d .. 2 d) when gated, as in
+ * gptq_linear. It is gptq_route, gptq_linear for both layers and gptq_combine
+ * (plus the residual), for the tokens of a decoding step. X: T x n bf16, rows
+ * 16-byte aligned (ldx % 8 == 0); expert_ids T x k int32, row pitch ldi; ids
+ * outside [0, E) add nothing, a token without others gets its residual or 0;
+ * an expert may stand more than once in a row. weights: T k fp32, or NULL for
+ * ones. up: E layers of m = d (2 d when gated) rows of n codes, down: E layers
+ * of n rows of d codes, both with `bits` and `group` (which divides n and d) in
+ * the layout of gptq_dequant_matmul, 16-byte aligned; biases fp32 (E x m, E x n)
+ * or NULL; residual T x n (rdt, row pitch ldr) or NULL; Y T x n (ydt, row pitch
+ * ldy), which may be the residual (same type and pitch).
+ * T k <= GPTQ_LAYER_MAX_SLOTS. n and d at most 2^20. More tokens are served by
+ * the calls named above.
+ * Numbers: both products as gptq_expert_matmul's matrix-vector form has them
+ * (at 4 bits activations, and h, up to 2^116). h passes from one launch to the
+ * other rounded to bf16 where Y is bf16 (as a bf16 model keeps it; the result's
+ * error is then about 1.4 times what its own rounding gives), and in three bf16
+ * pieces, which hold its fp32 value, where Y is fp32. Sums are fp32 in a
+ * fixed order: results are bitwise reproducible.
+ * Workspace: gptq_expert_layer_workspace_bytes. Asynchronous; T == 0 enqueues
+ * nothing.
+ * ("El balance de errores de la inferencia de pocos bits", section 6: decoding
+ * pays for the traffic of the packed weights, and for every launch beside it.) */
+#define GPTQ_LAYER_MAX_SLOTS 1024
+gptq_status gptq_expert_layer_workspace_bytes(int64_t T, int64_t k, int64_t d, int32_t ydt, size_t *bytes);
+gptq_status gptq_expert_layer(void *stream, const void *X, int32_t xdt, int64_t T, int64_t n, int64_t ldx,
+                              const int32_t *expert_ids, int64_t ldi, int64_t k, const float *weights, int64_t E,
+                              const uint32_t *up_qweight, const float *up_scales, const uint8_t *up_zeros,
+                              const float *up_bias, const uint32_t *down_qweight, const float *down_scales,
+                              const uint8_t *down_zeros, const float *down_bias, int64_t d, int32_t bits,
+                              int32_t group, int32_t act, int32_t gated, const void *residual, int32_t rdt,
+                              int64_t ldr, void *Y, int32_t ydt, int64_t ldy, void *workspace, size_t ws_bytes);
+
 /* ---- Distillation from a teacher's top logits -----------------------------------
  * The loss that tuning a quantized model (its adapters, or the layers around
  * its packed weights) against the model before quantization minimises, from

@@ -351,6 +351,27 @@ int64_t linear_bias_parts(int64_t R, int E, int64_t m);
 int64_t linear_grad_threads(int64_t R, int E, int64_t d);   // of the launch that forms dZ
 hipError_t launch_linear_grad(hipStream_t s, const LinearGradArgs& a);
 
+// ---- layer.hip: a layer of experts for a few tokens
+constexpr int kLayerMaxSlots = 1024;
+constexpr int64_t kLayerMaxWidth = 1 << 20;     // of n and d
+constexpr int kLayerDownWaves = 16;
+struct PackedLayers {
+  const uint32_t* qw; const float* scales; const uint8_t* zeros;
+};
+struct LayerArgs {
+  const uint16_t* X; int T; int64_t n, ldx;
+  const int32_t* ids; int64_t ldi; int k, slots, E;   // slots = T k
+  const float* w;                             // T x k, or null: ones
+  PackedLayers up, down;                      // E x m x n (m = 2 d when gated), E x n x d
+  const float *b1, *b2;                       // E x m, E x n, or null
+  int64_t d; int bits, group, act, gated;
+  const void* res; int res_bf16; int64_t ldr;
+  void* Y; int y_bf16; int64_t ldy;
+  uint16_t* H; int pieces; int64_t plane;     // `pieces` times slots x d, plane elements apart
+};
+int layer_pieces(int y_bf16);                 // bf16 pieces in which h is kept for a result of this type
+hipError_t launch_layer(hipStream_t s, const LayerArgs& a);
+
 // ---- distill.hip: distillation from a teacher's top logits
 constexpr int kDistillMaxK = 1024;
 struct DistillArgs {

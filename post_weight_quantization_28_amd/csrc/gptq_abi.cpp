@@ -1361,6 +1361,84 @@ gptq_status gptq_linear_grad(void* stream, const void* dY, int32_t dydt, int64_t
   return GPTQ_OK;
 }
 
+// ---------------------------------------------------------------- a layer of experts
+static_assert(GPTQ_LAYER_MAX_SLOTS == kLayerMaxSlots && GPTQ_MAX_EXPERTS == kRouteMaxExperts, "limits of the kernels");
+static_assert(GPTQ_DISTILL_MAX_K == kDistillMaxK, "limits of the kernels");
+
+gptq_status gptq_expert_layer_workspace_bytes(int64_t T, int64_t k, int64_t d, int32_t ydt, size_t* bytes) {
+  if (!bytes) return fail(GPTQ_EINVAL, "bytes is NULL");
+  const gptq_status st = dt_check(ydt);
+  if (st != GPTQ_OK) return st;
+  if (T < 0 || k < 1 || d < 1) return fail(GPTQ_EINVAL, "need T >= 0, k >= 1 and d >= 1");
+  if (k > kLayerMaxSlots || T > kLayerMaxSlots / k)
+    return fail(GPTQ_EINVAL, "T k may be at most GPTQ_LAYER_MAX_SLOTS: route, linear and combine take more");
+  if (d > kLayerMaxWidth) return fail(GPTQ_EINVAL, "n and d may be at most 2^20");
+  *bytes = ((size_t)layer_pieces(ydt == GPTQ_BF16) * T * k * d * sizeof(uint16_t) + 255) / 256 * 256;
+  return GPTQ_OK;
+}
+
+gptq_status gptq_expert_layer(void* stream, const void* X, int32_t xdt, int64_t T, int64_t n, int64_t ldx,
+                              const int32_t* expert_ids, int64_t ldi, int64_t k, const float* weights, int64_t E,
+                              const uint32_t* up_qweight, const float* up_scales, const uint8_t* up_zeros,
+                              const float* up_bias, const uint32_t* down_qweight, const float* down_scales,
+                              const uint8_t* down_zeros, const float* down_bias, int64_t d, int32_t bits,
+                              int32_t group, int32_t act, int32_t gated, const void* residual, int32_t rdt,
+                              int64_t ldr, void* Y, int32_t ydt, int64_t ldy, void* workspace, size_t ws_bytes) {
+  size_t need = 0;
+  gptq_status st = gptq_expert_layer_workspace_bytes(T, k, d, ydt, &need);
+  if (st != GPTQ_OK || (st = linear_sizes(T * k, n, d, gated, E, bits, group)) != GPTQ_OK ||
+      (st = act_check(act)) != GPTQ_OK || (residual && (st = dt_check(rdt)) != GPTQ_OK))
+    return st;
+  if (n > kLayerMaxWidth) return fail(GPTQ_EINVAL, "n and d may be at most 2^20");
+  if (d % group != 0) return fail(GPTQ_EINVAL, "group must divide d");
+  if (xdt != GPTQ_BF16) return fail(GPTQ_EINVAL, "expert_layer takes bf16 activations");
+  if (T == 0) return GPTQ_OK;
+  if (ldx < n || ldx % 8 != 0) return fail(GPTQ_EINVAL, "ldx must be a multiple of 8 and at least n");
+  if (ldi < k) return fail(GPTQ_EINVAL, "ldi < k");
+  if (ldy < n) return fail(GPTQ_EINVAL, "ldy < n");
+  if (residual && ldr < n) return fail(GPTQ_EINVAL, "ldr < n");
+  if (!X || !expert_ids || !up_qweight || !up_scales || !up_zeros || !down_qweight || !down_scales || !down_zeros || !Y)
+    return fail(GPTQ_EINVAL, "NULL pointer");
+  if (((uintptr_t)X & 15) != 0) return fail(GPTQ_EINVAL, "X must be 16-byte aligned");
+  if ((((uintptr_t)up_qweight | (uintptr_t)down_qweight) & 15) != 0)
+    return fail(GPTQ_EINVAL, "qweight must be 16-byte aligned");
+  if (mis(Y, ydt) || (residual && mis(residual, rdt)) || mis(expert_ids, GPTQ_F32) || mis(weights, GPTQ_F32) ||
+      mis(up_bias, GPTQ_F32) || mis(down_bias, GPTQ_F32) || mis(up_scales, GPTQ_F32) || mis(down_scales, GPTQ_F32))
+    return fail(GPTQ_EINVAL, "a matrix is not aligned to its elements");
+  if ((st = check_ws(workspace, ws_bytes, need)) != GPTQ_OK) return st;
+  LayerArgs a = {};
+  a.X = static_cast<const uint16_t*>(X);
+  a.T = (int)T;
+  a.n = n;
+  a.ldx = ldx;
+  a.ids = expert_ids;
+  a.ldi = ldi;
+  a.k = (int)k;
+  a.slots = (int)(T * k);
+  a.E = (int)E;
+  a.w = weights;
+  a.up = {up_qweight, up_scales, up_zeros};
+  a.down = {down_qweight, down_scales, down_zeros};
+  a.b1 = up_bias;
+  a.b2 = down_bias;
+  a.d = d;
+  a.bits = bits;
+  a.group = group;
+  a.act = act;
+  a.gated = gated;
+  a.res = residual;
+  a.res_bf16 = rdt == GPTQ_BF16;
+  a.ldr = ldr;
+  a.Y = Y;
+  a.y_bf16 = ydt == GPTQ_BF16;
+  a.ldy = ldy;
+  a.H = static_cast<uint16_t*>(workspace);
+  a.pieces = layer_pieces(a.y_bf16);
+  a.plane = (int64_t)a.slots * d;
+  HIP_TRY(launch_layer((hipStream_t)stream, a), "expert_layer");
+  return GPTQ_OK;
+}
+
 // ---------------------------------------------------------------- distillation
 static gptq_status distill_sizes(int64_t T, int64_t V) {
   if (T < 0 || V < 1) return fail(GPTQ_EINVAL, "need T >= 0 and V >= 1");

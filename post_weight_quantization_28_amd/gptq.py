@@ -112,6 +112,11 @@ def load():
         "gptq_linear_grad": [c_vp, c_vp, ctypes.c_int32, c_i64, c_vp, ctypes.c_int32, c_i64, c_i64, c_vp, c_i64, c_vp,
                              c_vp, c_vp, c_i64, c_i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                              c_vp, c_i64, c_vp, c_vp, ctypes.c_int32, c_i64, c_vp, c_sz],
+        "gptq_expert_layer_workspace_bytes": [c_i64, c_i64, c_i64, ctypes.c_int32, ctypes.POINTER(c_sz)],
+        "gptq_expert_layer": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp,
+                              c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, ctypes.c_int32, ctypes.c_int32,
+                              ctypes.c_int32, ctypes.c_int32, c_vp, ctypes.c_int32, c_i64, c_vp, ctypes.c_int32, c_i64,
+                              c_vp, c_sz],
         "gptq_distill_workspace_bytes": [c_i64, c_i64, ctypes.POINTER(c_sz)],
         "gptq_distill": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, ctypes.c_float,
                          ctypes.c_int32, c_vp, c_vp, c_vp, c_sz],
@@ -718,6 +723,46 @@ def linear_grad(dY, Z, qweight, scales, zeros, bits, group, n, act="none", gated
           group, code, gated, dzp, lddz, db.data_ptr() if want_bias else None, xp, _DTYPE_CODES[out.dtype], ldx, wsp,
           need)
     return out, dY if dZ is None else dZ, db
+
+
+def expert_layer(X, expert_ids, weights, up, down, bits, group, act="silu", gated=True, up_bias=None, down_bias=None,
+                 residual=None, out=None, out_dtype=torch.bfloat16, workspace=None):
+    """A whole layer of experts for a few tokens (T k at most 1024 slots):
+    Y[t] = residual[t] + sum_j weights[t, j] down_e(end(up_e(X[t]))), e =
+    expert_ids[t, j] (ids outside [0, E) add nothing), end as in linear. X bf16
+    T x n; expert_ids T x k int32; weights T x k fp32 (None: ones); up and down:
+    (qweight, scales, zeros) of E layers as quantize_layer packs them, without
+    act-order: up E x m x n (m = 2 d when gated), down E x n x d. An fp32 result
+    keeps the values between the layers in fp32, a bf16 one in bf16."""
+    lib = load()
+    xp, ldx = _rows2d(X, "X", (torch.bfloat16,))
+    T, n = X.shape
+    dev = X.device
+    ip, ldi = _rows2d(expert_ids, "expert_ids", (torch.int32,), dev)
+    rows, k = expert_ids.shape
+    if rows != T:
+        raise ValueError(f"expert_ids must have {T} rows")
+    if T == 1:
+        ldx = (n + 7) // 8 * 8
+    code, gated = _act_code(act), int(bool(gated))
+    uq, us, uz = up
+    dq, ds, dz = down
+    E, m, uqp, usp, uzp = _expert_layers(uq, us, uz, bits, group, n, dev)
+    d = _halves(m, gated)
+    E2, n2, dqp, dsp, dzp = _expert_layers(dq, ds, dz, bits, group, d, dev)
+    if (E2, n2) != (E, n):
+        raise ValueError(f"down must be {E} layers of {n} x {d}")
+    wp = None if weights is None else _dense(weights, "weights", torch.float32, dev, (T, k))
+    b1 = None if up_bias is None else _dense(up_bias, "up_bias", torch.float32, dev, uq.shape[:-1])
+    b2 = None if down_bias is None else _dense(down_bias, "down_bias", torch.float32, dev, dq.shape[:-1])
+    resp, rdt, ldr = _matrix(residual, "residual", (T, n), _FLOATS, dev)
+    out, yp, ldy = _result(out, (T, n), out_dtype, dev)
+    ydt = _DTYPE_CODES[out.dtype]
+    need = _bytes("gptq_expert_layer_workspace_bytes", T, k, d, ydt)
+    ws, wsp = _scratch(need, dev, workspace)
+    _call(dev, lib.gptq_expert_layer, xp, BF16, T, n, ldx, ip, ldi, k, wp, E, uqp, usp, uzp, b1, dqp, dsp, dzp, b2, d,
+          bits, group, code, gated, resp, rdt, ldr, yp, ydt, ldy, wsp, need)
+    return out
 
 
 # ---------------------------------------------------------------- distillation

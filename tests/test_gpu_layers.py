@@ -406,3 +406,182 @@ def test_linear_binding_refusals():
         G.linear_grad(dY, values(1, 6, 32), qw, sc, zr, 4, 32, 64, **ok)
     with pytest.raises(TypeError):
         G.linear_grad(dY, values(1, 6, 64), qw, sc, zr, 4, 32, 64, dZ=torch.zeros(6, 64, device="cuda"), **ok)
+
+
+# ---------------------------------------------------------------- a layer of experts for a few tokens
+def layer_bound(X, ids, w, up, down, bits, group, name, gated, b1, b2, res, pieces):
+    """Bound on expert_layer's fp32 sum, slot by slot: z and the product with h as
+    the matrix-vector form of product_bound, the activation's as above, h rounded to
+    bf16 (2^-8) or held in three pieces (u), k fused sums, a bias, the residual."""
+    T, k = ids.shape
+    E, n, d = up[0].shape[0], X.shape[1], up[0].shape[1] // (2 if gated else 1)
+    out = np.zeros((T, n))
+    for t in range(T):
+        for j in range(k):
+            e = ids[t, j]
+            if not 0 <= e < E:
+                continue
+            one = [0, 1]
+            x = np.abs(X[t:t + 1])
+            ez = product_bound(x, one, None, *(a[e:e + 1] for a in up), bits, group, n, 1, 1)
+            z = X[t:t + 1] @ dequantize(up[0][e], up[1][e], up[2][e], bits, group, n).T
+            if b1 is not None:
+                z = z + b1[e]
+                ez = ez + 2 * U32 * (np.abs(z) + np.abs(b1[e]))
+            eh = end_error(name, gated, z, ez, None)
+            h = L64.end(z, name, gated)
+            eh = eh + (UBF if pieces == 1 else 2 * U32) * (np.abs(h) + eh)
+            D = np.abs(dequantize(down[0][e], down[1][e], down[2][e], bits, group, d))
+            # the parts of K and the three pieces add at most as many sums again
+            eo = eh @ D.T + 3 * product_bound(np.abs(h) + eh, one, None, *(a[e:e + 1] for a in down), bits, group, d, 1, 1)
+            o = np.abs(h) @ D.T + (0 if b2 is None else np.abs(b2[e]))
+            out[t] += abs(float(w[t, j])) * (eo + (k + 3) * U32 * (o + eo))[0]
+        if res is not None:
+            out[t] += U32 * np.abs(res[t])
+    return out
+
+
+LAYERS = [   # T, k, E, n, d, group, drop, bias
+    (1, 1, 1, 32, 32, 32, 0.0, True), (1, 2, 8, 256, 384, 128, 0.0, False), (1, 8, 64, 128, 256, 128, 0.0, True),
+    (1, 3, 2, 96, 160, 32, 0.0, False),              # an expert twice in a row
+    (2, 2, 4, 640, 128, 64, 0.0, True), (5, 2, 3, 128, 96, 32, 0.3, True), (17, 1, 1, 256, 128, 128, 0.0, False),
+    (40, 2, 3, 128, 384, 128, 0.1, True),            # more than one tile an expert
+    (16, 4, 100, 64, 64, 64, 0.2, False),            # more than 64 experts
+    (64, 8, 16, 160, 96, 32, 0.1, True), (128, 8, 7, 64, 128, 32, 0.0, False), (1024, 1, 1024, 32, 64, 32, 0.0, True),
+    (3, 300, 9, 64, 64, 32, 0.5, False),             # many slots a token
+    (4, 2, 3, 512, 768, 256, 0.0, False),
+]
+
+
+@pytest.mark.parametrize("bits", [4, 3, 2])
+@pytest.mark.parametrize("T,k,E,n,d,group,drop,bias", LAYERS)
+def test_expert_layer(T, k, E, n, d, group, drop, bias, bits):
+    ids = expert_ids(T + E, T, k, E, drop)
+    r = np.random.default_rng(n + d)
+    for i, (name, gated, ydt, rdt) in enumerate([("silu", True, BF16, BF16), ("gelu", False, F32, F32), ("gelu_tanh", True, F32, None),
+                                                 ("none", False, BF16, F32)]):
+        if (bits < 4 or T * k > 100) and i > 1:
+            break
+        m = 2 * d if gated else d
+        up, down = fast_layers(bits + d, E, m, n, bits, group), fast_layers(bits + n, E, n, d, bits, group)
+        X, w = values(n + T, T, n), r.uniform(-0.2, 1.0, (T, k)).astype(np.float32)
+        b1 = r.standard_normal((E, m)).astype(np.float32) if bias else None
+        b2 = r.standard_normal((E, n)).astype(np.float32) if bias else None
+        res = None if rdt is None else values(7, T, n, dtype=rdt)
+        wide = torch.from_numpy(np.pad(ids, ((0, 0), (0, 3)), constant_values=0)).cuda()[:, :k]
+        args = (X, wide, torch.from_numpy(w).cuda(), cuda_layers(*up), cuda_layers(*down), bits, group)
+        kw = dict(act=name, gated=gated, up_bias=None if b1 is None else torch.from_numpy(b1).cuda(),
+                  down_bias=None if b2 is None else torch.from_numpy(b2).cuda(), residual=res)
+        out = torch.full((T, n + 5), 7.0, dtype=ydt, device="cuda")
+        Y = G.expert_layer(*args, out=out[:, 2:2 + n], **kw)
+        x64, r64 = arr(X), None if res is None else arr(res)
+        ref = L64.expert_layer(x64, ids, w, up, down, bits, group, name, gated, b1, b2, r64)
+        e = layer_bound(x64, ids, w, up, down, bits, group, name, gated, b1, b2, r64, 1 if ydt == BF16 else 3)
+        assert np.all(np.abs(arr(Y) - ref) <= e + last(ydt, np.abs(ref) + e))
+        assert torch.all(out[:, :2] == 7) and torch.all(out[:, 2 + n:] == 7)
+        assert torch.equal(G.expert_layer(*args, out_dtype=ydt, **kw), Y)
+
+
+def test_expert_layer_agrees_with_its_parts():
+    """route, linear, linear and combine of the same tokens, and tokens that are
+    dropped altogether keep their residual; the residual may be the result."""
+    T, k, E, n, d, group = 24, 4, 16, 256, 128, 64
+    ids = expert_ids(3, T, k, E, 0.2)
+    ids[5], ids[9] = -1, E
+    up, down = cuda_layers(*fast_layers(1, E, 2 * d, n, 4, group)), cuda_layers(*fast_layers(2, E, n, d, 4, group))
+    X, res = values(1, T, n), values(2, T, n, dtype=F32)
+    w = torch.rand(T, k, device="cuda")
+    idc = torch.from_numpy(ids).cuda()
+    r = G.route(idc, E)
+    h = G.linear(X, *up, 4, group, act="silu", gated=True, offsets=r.offsets, rows=r.rows)
+    y = G.linear(h, *down, 4, group, offsets=r.offsets, out_dtype=F32)
+    want = G.combine(y, r.inverse, w) + res
+    got = G.expert_layer(X, idc, w, up, down, 4, group, residual=res, out_dtype=F32)
+    # h rounded to bf16 on one side: 2^-8 of the sum of magnitudes
+    mag = G.combine(G.linear(h.abs(), down[0], down[1], down[2] * 0, 4, group, offsets=r.offsets, out_dtype=F32), r.inverse, w)
+    assert torch.all((got - want).abs() <= 2.0 ** -8 * mag + 1e-4)
+    assert torch.equal(got[5], res[5]) and torch.equal(got[9], res[9])
+    assert torch.equal(G.expert_layer(X, idc, w, up, down, 4, group, residual=res, out=res), got) and torch.equal(res, got)
+    empty = G.expert_layer(X[:2], idc[:2] * 0 - 1, None, up, down, 4, group)
+    assert torch.count_nonzero(empty) == 0
+
+
+def test_expert_layer_of_padded_ids():
+    """1024 slots of which a few have an expert: LDS holds what is in use."""
+    E, n, d = 6, 64, 96
+    up, down = fast_layers(1, E, 2 * d, n, 4, 32), fast_layers(2, E, n, d, 4, 32)
+    ids = np.full((128, 8), -1, np.int32)
+    ids[77, 3], ids[127, 7] = 4, 0
+    X = values(1, 128, n)
+    w = np.ones((128, 8), np.float32)
+    Y = arr(G.expert_layer(X, torch.from_numpy(ids).cuda(), None, cuda_layers(*up), cuda_layers(*down), 4, 32, out_dtype=F32))
+    ref = L64.expert_layer(arr(X), ids, w, up, down, 4, 32, "silu", True)
+    e = layer_bound(arr(X), ids, w, up, down, 4, 32, "silu", True, None, None, None, 3)
+    assert np.all(np.abs(Y - ref) <= e + U32 * np.abs(ref)) and np.count_nonzero(Y.any(1)) == 2
+
+
+def test_expert_layer_nonfinite_tokens_stay_apart():
+    E, n, d = 4, 128, 64
+    up, down = cuda_layers(*fast_layers(1, E, 2 * d, n, 4, 32)), cuda_layers(*fast_layers(2, E, n, d, 4, 32))
+    X = values(1, 9, n)
+    ids = torch.from_numpy(expert_ids(1, 9, 2, E)).cuda()
+    want = G.expert_layer(X, ids, None, up, down, 4, 32)
+    X[3, 5], X[6, 0] = float("nan"), float("inf")
+    got = G.expert_layer(X, ids, None, up, down, 4, 32)
+    keep = torch.tensor([0, 1, 2, 4, 5, 7, 8], device="cuda")
+    assert torch.equal(got[keep], want[keep]) and torch.isnan(got[3]).all() and not torch.isfinite(got[6]).any()
+
+
+@pytest.mark.parametrize("T", [1, 16])
+def test_expert_layer_captured_replays(T):
+    """Replayed on changing tokens and experts with eager work between; two graphs
+    with workspaces of their own."""
+    k, E, n, d = 4, 16, 256, 256
+    up, down = cuda_layers(*fast_layers(1, E, 2 * d, n, 4, 128)), cuda_layers(*fast_layers(2, E, n, d, 4, 128))
+    sets = [(values(i, T, n), torch.from_numpy(expert_ids(i, T, k, E, 0.1)).cuda(), torch.rand(T, k, device="cuda")) for i in range(3)]
+    want = [G.expert_layer(*s, up, down, 4, 128) for s in sets]
+    live = [t.clone() for t in sets[0]]
+    graphs, outs = [], []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        G.expert_layer(*live, up, down, 4, 128)
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(G.expert_layer(*live, up, down, 4, 128))
+        graphs.append(graph)
+    for i in (0, 1, 2, 1):
+        for a, b in zip(live, sets[i]):
+            a.copy_(b)
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[i]) and torch.equal(outs[1], want[i])
+        G.expert_layer(*sets[0], up, down, 4, 128)
+
+
+def test_expert_layer_binding_refusals():
+    E, n, d = 2, 64, 32
+    up, down = cuda_layers(*fast_layers(1, E, 2 * d, n, 4, 32)), cuda_layers(*fast_layers(2, E, n, d, 4, 32))
+    X, ids = values(1, 3, n), torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    G.expert_layer(X, ids, None, up, down, 4, 32)
+    for bad in (lambda: G.expert_layer(X, ids[:2], None, up, down, 4, 32), lambda: G.expert_layer(X, ids, None, up, up, 4, 32),
+                lambda: G.expert_layer(X, ids, torch.ones(3, 3, device="cuda"), up, down, 4, 32),
+                lambda: G.expert_layer(X, ids, None, up, down, 4, 32, up_bias=torch.ones(2, 32, device="cuda")),
+                lambda: G.expert_layer(X, ids, None, up, down, 4, 32, residual=X[:, :32]),
+                lambda: G.expert_layer(X, ids, None, up, down, 4, 32, act="swish")):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: G.expert_layer(X.float(), ids, None, up, down, 4, 32), lambda: G.expert_layer(X, ids.long(), None, up, down, 4, 32),
+                lambda: G.expert_layer(X, ids, None, up, down, 4, 32, out_dtype=torch.float16)):
+        with pytest.raises(TypeError):
+            bad()
+    wide = torch.zeros(3, n + 4, dtype=BF16, device="cuda")
+    many = torch.zeros(1025, 1, dtype=torch.int32, device="cuda")
+    for bad in (lambda: G.expert_layer(wide[:, :n], ids, None, up, down, 4, 32),
+                lambda: G.expert_layer(values(1, 1025, n), many, None, up, down, 4, 32)):
+        with pytest.raises(G.GPTQError):
+            bad()
+    assert G.expert_layer(X[:0], ids[:0], None, up, down, 4, 32).shape == (0, n)

@@ -189,6 +189,33 @@ def test_linear_refusals():
         assert need(16, 128, 64, 1, 4, 4, 64, None) == -1
 
 
+def test_expert_layer_refusals():
+    G, lib = _lib()
+    odd, one = ctypes.c_void_p((1 << 20) + 8), ctypes.c_void_p((1 << 20) + 1)
+
+    def call(X=FAKE, xdt=0, T=4, n=128, ldx=128, ids=FAKE, ldi=2, k=2, w=FAKE, E=4, uq=FAKE, us=FAKE, uz=FAKE, b1=FAKE,
+             dq=FAKE, ds=FAKE, dz=FAKE, b2=FAKE, d=64, bits=4, group=64, act=4, gated=1, res=FAKE, rdt=0, ldr=128, Y=FAKE,
+             ydt=0, ldy=128, ws=FAKE, wsb=1 << 30):
+        return lib.gptq_expert_layer(None, X, xdt, T, n, ldx, ids, ldi, k, w, E, uq, us, uz, b1, dq, ds, dz, b2, d, bits,
+                                     group, act, gated, res, rdt, ldr, Y, ydt, ldy, ws, wsb)
+    for bad in (dict(xdt=1), dict(ydt=2), dict(rdt=2), dict(T=-1), dict(T=513), dict(k=0), dict(k=1025), dict(n=0), dict(d=0),
+                dict(d=96), dict(n=2 ** 20 + 64, ldx=2 ** 21), dict(d=2 ** 20 + 64), dict(bits=1), dict(group=48), dict(group=128),
+                dict(E=0), dict(E=1025), dict(act=5), dict(gated=2), dict(ldx=120), dict(ldx=129), dict(ldi=1), dict(ldy=127),
+                dict(ldr=127), dict(X=NULL), dict(ids=NULL), dict(uq=NULL), dict(us=NULL), dict(uz=NULL), dict(dq=NULL),
+                dict(ds=NULL), dict(dz=NULL), dict(Y=NULL), dict(X=odd), dict(uq=odd), dict(dq=odd), dict(w=one), dict(b1=one),
+                dict(b2=one), dict(us=one), dict(ds=one), dict(ids=one), dict(res=one), dict(Y=one)):
+        assert call(**bad) == -1, bad
+    assert call(ws=NULL, wsb=0) == -5 and call(wsb=256) == -5 and call(ws=odd) == -5
+    assert call(T=0, X=NULL, Y=NULL, ws=NULL, wsb=0) == 0
+    out = ctypes.c_size_t(0)
+    need = lib.gptq_expert_layer_workspace_bytes
+    assert need(4, 2, 64, 0, ctypes.byref(out)) == 0 and out.value % 256 == 0 and out.value >= 4 * 2 * 64 * 2
+    assert need(4, 2, 64, 1, ctypes.byref(out)) == 0 and out.value >= 3 * 4 * 2 * 64 * 2
+    for bad in ((-1, 2, 64, 0), (4, 0, 64, 0), (4, 2, 0, 0), (4, 2, 64, 2), (1025, 1, 64, 0), (4, 2, 2 ** 20 + 1, 0)):
+        assert need(*bad, ctypes.byref(out)) == -1
+    assert need(4, 2, 64, 0, None) == -1
+
+
 def test_distill_refusals():
     G, lib = _lib()
     one = ctypes.c_void_p((1 << 20) + 1)
@@ -225,6 +252,6 @@ def test_binding_refuses_host_tensors():
     x, q = torch.zeros((2, 32), dtype=torch.bfloat16), torch.zeros((2, 4), dtype=torch.int32)
     f, i = torch.zeros((2, 1)), torch.zeros((2, 1), dtype=torch.int32)
     for call in (lambda: G.linear(x, q, f, f, 4, 32), lambda: G.linear_grad(x, x, q, f, f, 4, 32, 32),
-                 lambda: G.distill(x, i, f), lambda: G.distill_grad(x, i, f, f[0], f[0])):
+                 lambda: G.expert_layer(x, i, f, (q, f, f), (q, f, f), 4, 32), lambda: G.distill(x, i, f), lambda: G.distill_grad(x, i, f, f[0], f[0])):
         with pytest.raises(TypeError):
             call()
