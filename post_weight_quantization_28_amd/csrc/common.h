@@ -354,7 +354,6 @@ hipError_t launch_linear_grad(hipStream_t s, const LinearGradArgs& a);
 // ---- layer.hip: a layer of experts for a few tokens
 constexpr int kLayerMaxSlots = 1024;
 constexpr int64_t kLayerMaxWidth = 1 << 20;     // of n and d
-constexpr int kLayerDownWaves = 16;
 struct PackedLayers {
   const uint32_t* qw; const float* scales; const uint8_t* zeros;
 };
@@ -367,9 +366,11 @@ struct LayerArgs {
   int64_t d; int bits, group, act, gated;
   const void* res; int res_bf16; int64_t ldr;
   void* Y; int y_bf16; int64_t ldy;
-  uint16_t* H; int pieces; int64_t plane;     // `pieces` times slots x d, plane elements apart
+  void* ws;
+  // set by the launch: parts of the workspace, h in `pieces` times slots x d bf16 values, plane elements apart
+  void* table; uint16_t* H; int pieces; int64_t plane;
 };
-int layer_pieces(int y_bf16);                 // bf16 pieces in which h is kept for a result of this type
+size_t layer_workspace(int64_t T, int64_t k, int64_t E, int64_t d, int y_bf16);
 hipError_t launch_layer(hipStream_t s, const LayerArgs& a);
 
 // ---- distill.hip: distillation from a teacher's top logits

@@ -26,9 +26,9 @@ namespace gq {
 // ==================================================================== few rows
 //
 // Matrix-vector products: bound by reading the packed weights once. A
-// workgroup of WAVES waves owns 16 OB outputs of one expert and up to 16 of
+// workgroup of WAVES waves owns 16 OB outputs of one expert and up to TILE of
 // its rows (v_mfma_f32_16x16x32_bf16, X as the A operand), and its waves
-// split K. K advances in pieces of 128 codes.
+// split K (MvWave in expert_rows.h). K advances in pieces of 128 codes.
 //  * Groups that are multiples of 128 (WIDE): lane l (output l % 16,
 //    j = l / 16) loads the 32 consecutive codes 32 j .. of its output's piece
 //    in one go (16 bytes at 4 bits); MFMA step i then takes codes
@@ -38,7 +38,8 @@ namespace gq {
 //    the piece and lane j its codes 8 j .. + 7, and the sum is scaled after
 //    every chunk. At 4 bits a lane still loads a chunk in one go and four lane
 //    swaps hand out its words (360 rows over 64 experts, 322 x 4608 in groups
-//    of 32: 73 us with a word per load, 36 us so).
+//    of 32: 73 us with a word per load, 36 us so); 2 and 3 bits go chunk by
+//    chunk.
 //  * 4 bits: a code in bits 3..6 of the bf16 pattern of 16 is the number
 //    16 + q, so one shift and one and-or give two codes (pairs i, i + 4: X's
 //    fragment is permuted alike), one operation per code against three with
@@ -49,23 +50,22 @@ namespace gq {
 //    rounding. A row with an infinity gives NaN, and so may one whose sum of
 //    128 x (16 + q) leaves fp32: 128 31 2^116 is below 2^128.
 //
-// Measured (median kernel times; two experts of 11008 x 4096 for one token /
-// 64 experts of 1408 x 2048 for 256 rows, 4 bits, groups of 128; 48.6 and 99
-// MB, 10 and 20 us at the rate of a large copy): 19.9 / 31.8 us. Of it about 2
-// are the launch and the look-up, 6 / 10 the unpacking and the products,
-// the rest the weights' way from memory. One load per scale and piece instead
-// of one per S pieces: 22.9 / 42.5; 8 waves per workgroup 22.0 / 67;
-// 16 outputs per wave 19.8 / 40; 64 outputs 23.5 / 32.6; the weights loaded
-// past the caches 20.9 / 32.9. In captured calls, which take 20.3 / 32.5: four
-// pieces asked for at a time 19.6 / 33.0, one 24.6 / 38.0.
-template <int BITS, bool WIDE, int WAVES, int OB, int S>
-__global__ void __launch_bounds__(64 * WAVES)
+// Measured in captured calls (two experts of 11008 x 4096 for one token / 64
+// experts of 1408 x 2048 for 256 rows, 4 bits, groups of 128; 48.6 and 99 MB,
+// which are read in 9.4 and 17.6 us in the same pattern): 17.6 / 31 us, with
+// scales and rows of X loaded to where they are used 23.6 / 34.6. With tiles of
+// 8 rows up to 8 rows an expert; of 16: 20.6 / 33.5, and with 16 rows each 64 in
+// tiles of 8, 55 of 16.
+template <int BITS, bool WIDE, int WAVES, int OB, int TILE>
+__global__ void __launch_bounds__(64 * WAVES, 4)
 k_expert_mv(const uint16_t* __restrict__ X, int T, int64_t n, int64_t ldx, const int32_t* __restrict__ rows,
             const int32_t* __restrict__ offsets, int E, int R, const uint32_t* __restrict__ qw,
             const float* __restrict__ scales, const uint8_t* __restrict__ zeros, int64_t d_out, int group,
             void* __restrict__ Y, int ybf16, int64_t ldy) {
+  constexpr bool CHUNKS = BITS < 4 && !WIDE;             // a load per chunk, no LDS (TILE 16)
+  __shared__ __align__(16) uint8_t smem[WAVES][CHUNKS ? 16 : MvWave<BITS, WIDE, OB, 1, TILE>::BYTES];
   __shared__ float red[WAVES][OB][4][64];
-  const Seg sg = find_tile(offsets, E, R, 16, blockIdx.y);
+  const Seg sg = find_tile(offsets, E, R, TILE, blockIdx.y);
   if (sg.e < 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int li = lane & 15;
@@ -74,21 +74,16 @@ k_expert_mv(const uint16_t* __restrict__ X, int T, int64_t n, int64_t ldx, const
 #pragma unroll
   for (int b = 0; b < OB; ++b) orow[b] = obase + min((int64_t)blockIdx.x * (16 * OB) + 16 * b + li, d_out - 1);
   const MvRows<OB> w(qw, scales, zeros, orow, n, group, BITS);
-  // lanes of rows past the segment load nothing: rows of the product do not
-  // mix, and their results are not stored
-  const bool xok = sg.row0 + li < sg.hi;
-  const int prow = min(sg.row0 + li, sg.hi - 1);
-  int srcrow = rows ? rows[prow] : prow;
-
   ex_f32x4_t tot[OB];
 #pragma unroll
   for (int b = 0; b < OB; ++b) tot[b] = (ex_f32x4_t){0.f, 0.f, 0.f, 0.f};
-  mv_sum<BITS, WIDE, OB, S, 1>(w, n, group, wave, WAVES, xok, 0, [&]() {
-    // the weights leave before the row's index is waited for
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" : "+v"(srcrow));
-    return X + (int64_t)min(max(srcrow, 0), T - 1) * ldx;
-  }, tot);
+  const int nrows = min(sg.hi - sg.row0, TILE);
+  auto xrow = [&](int r) { return X + source_row(rows, sg.row0 + r, T) * ldx; };
+  if constexpr (CHUNKS)
+    mv_chunks<BITS, OB, 1>(w, MvK<false>(n, group), wave, WAVES, xrow(min(li, nrows - 1)), 0, tot);
+  else
+    mv_sum<BITS, WIDE, OB, 1, TILE>(w, n, group, wave, WAVES, nrows, 0, lds_addr(smem[wave]),
+                                    mv_vec(scales, zeros, n, group), xrow, tot);
 #pragma unroll
   for (int b = 0; b < OB; ++b)
 #pragma unroll
@@ -102,7 +97,7 @@ k_expert_mv(const uint16_t* __restrict__ X, int T, int64_t n, int64_t ldx, const
     for (int w = 0; w < WAVES; ++w) v += red[w][b][r][l];
     const int64_t o = (int64_t)blockIdx.x * (16 * OB) + 16 * b + (l & 15);
     const int row = sg.row0 + 4 * (l >> 4) + r;
-    if (o < d_out && row < sg.hi) store_out(Y, ybf16, (int64_t)row * ldy + o, v);
+    if (o < d_out && row < min(sg.hi, sg.row0 + TILE)) store_out(Y, ybf16, (int64_t)row * ldy + o, v);
   }
 }
 
@@ -138,9 +133,6 @@ using ExTile128 = ExTile<2, 2, 2, 2, 1, 2>;    // 128 x 128
 using ExTile64 = ExTile<2, 1, 1, 4, 4, 4>;     // 64 x 128: little work per stage to hide a load behind
 using ExTile32 = ExTile<1, 1, 1, 4, 4, 4>;     // 32 x 128
 
-typedef __attribute__((address_space(3))) ex_u32x4_t lds_piece_t;
-typedef __attribute__((address_space(3))) const ex_bf16x8_t lds_frag_t;
-
 __device__ __forceinline__ uint32_t row_piece(int r, int c) { return (uint32_t)r * 128u + 16u * (c ^ ((r >> 1) & 7)); }
 // W: columns of the tile
 template <int W>
@@ -148,11 +140,6 @@ __device__ __forceinline__ uint32_t col_piece(int t, int c) {
   const int x = W == 128 ? (t >> 1) & 1 : (c >> 4) & 1;
   return (uint32_t)t * (2 * W) + 16u * (c ^ dma_swz(t) ^ x);
 }
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
-}
-__device__ __forceinline__ void lds_write(uint32_t at, ex_u32x4_t v) { *reinterpret_cast<lds_piece_t*>(at) = v; }
-__device__ __forceinline__ ex_bf16x8_t lds_frag(uint32_t at) { return *reinterpret_cast<lds_frag_t*>(at); }
 
 // Address of this lane's fragment of columns c0 .. c0 + 31 in a [64][W] tile
 // (K slice kk at + 32 W kk): lane l gets K 8 (l / 32) .. + 7 of column
@@ -1544,16 +1531,16 @@ int64_t expert_threads(const ExpertArgs& a, int grad) {
                    : (row_tiles(a.R, a.E, bm) * ceil_div(cols, 128) + 8) * 256;
 }
 
-template <int BITS>
+template <int BITS, int TILE>
 static void mv_go(hipStream_t s, const ExpertArgs& a) {
-  constexpr int WAVES = 4, OB = 2, S = 2;
-  const dim3 grid((unsigned)ceil_div(a.d_out, 16 * OB), (unsigned)row_tiles(a.R, a.E, 16));
+  constexpr int WAVES = 4, OB = 2;
+  const dim3 grid((unsigned)ceil_div(a.d_out, 16 * OB), (unsigned)row_tiles(a.R, a.E, TILE));
   const uint16_t* X = static_cast<const uint16_t*>(a.A);
   if (a.group % 128 == 0)
-    hipLaunchKernelGGL((k_expert_mv<BITS, true, WAVES, OB, S>), grid, dim3(64 * WAVES), 0, s, X, a.T, a.n, a.lda, a.rows,
+    hipLaunchKernelGGL((k_expert_mv<BITS, true, WAVES, OB, TILE>), grid, dim3(64 * WAVES), 0, s, X, a.T, a.n, a.lda, a.rows,
                        a.offsets, a.E, a.R, a.qw, a.scales, a.zeros, a.d_out, a.group, a.Y, a.y_bf16, a.ldy);
   else
-    hipLaunchKernelGGL((k_expert_mv<BITS, false, WAVES, OB, S>), grid, dim3(64 * WAVES), 0, s, X, a.T, a.n, a.lda, a.rows,
+    hipLaunchKernelGGL((k_expert_mv<BITS, false, WAVES, OB, TILE>), grid, dim3(64 * WAVES), 0, s, X, a.T, a.n, a.lda, a.rows,
                        a.offsets, a.E, a.R, a.qw, a.scales, a.zeros, a.d_out, a.group, a.Y, a.y_bf16, a.ldy);
 }
 
@@ -1637,7 +1624,8 @@ static void ring_go(hipStream_t s, const ExpertArgs& a, int grad) {
 template <int BITS>
 static void fwd_bits(hipStream_t s, const ExpertArgs& a) {
   const int bm = expert_bm(a, 0);
-  if (bm == 16) mv_go<BITS>(s, a);
+  if (bm == 16 && (a.R > 8 * a.E || (BITS < 4 && a.group % 128 != 0))) mv_go<BITS, 16>(s, a);
+  else if (bm == 16) mv_go<BITS, 8>(s, a);
   else if (bm == 256) ring_go(s, a, 0);
   else if (bm == 64) mm_group<BITS, ExTile64>(s, a);
   else mm_group<BITS, ExTile128>(s, a);

@@ -1365,15 +1365,16 @@ gptq_status gptq_linear_grad(void* stream, const void* dY, int32_t dydt, int64_t
 static_assert(GPTQ_LAYER_MAX_SLOTS == kLayerMaxSlots && GPTQ_MAX_EXPERTS == kRouteMaxExperts, "limits of the kernels");
 static_assert(GPTQ_DISTILL_MAX_K == kDistillMaxK, "limits of the kernels");
 
-gptq_status gptq_expert_layer_workspace_bytes(int64_t T, int64_t k, int64_t d, int32_t ydt, size_t* bytes) {
+gptq_status gptq_expert_layer_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t d, int32_t ydt, size_t* bytes) {
   if (!bytes) return fail(GPTQ_EINVAL, "bytes is NULL");
   const gptq_status st = dt_check(ydt);
   if (st != GPTQ_OK) return st;
   if (T < 0 || k < 1 || d < 1) return fail(GPTQ_EINVAL, "need T >= 0, k >= 1 and d >= 1");
+  if (E < 1 || E > GPTQ_MAX_EXPERTS) return fail(GPTQ_EINVAL, "need 1 <= E <= GPTQ_MAX_EXPERTS");
   if (k > kLayerMaxSlots || T > kLayerMaxSlots / k)
     return fail(GPTQ_EINVAL, "T k may be at most GPTQ_LAYER_MAX_SLOTS: route, linear and combine take more");
   if (d > kLayerMaxWidth) return fail(GPTQ_EINVAL, "n and d may be at most 2^20");
-  *bytes = ((size_t)layer_pieces(ydt == GPTQ_BF16) * T * k * d * sizeof(uint16_t) + 255) / 256 * 256;
+  *bytes = layer_workspace(T, k, E, d, ydt == GPTQ_BF16);
   return GPTQ_OK;
 }
 
@@ -1385,7 +1386,7 @@ gptq_status gptq_expert_layer(void* stream, const void* X, int32_t xdt, int64_t 
                               int32_t group, int32_t act, int32_t gated, const void* residual, int32_t rdt,
                               int64_t ldr, void* Y, int32_t ydt, int64_t ldy, void* workspace, size_t ws_bytes) {
   size_t need = 0;
-  gptq_status st = gptq_expert_layer_workspace_bytes(T, k, d, ydt, &need);
+  gptq_status st = gptq_expert_layer_workspace_bytes(T, k, E, d, ydt, &need);
   if (st != GPTQ_OK || (st = linear_sizes(T * k, n, d, gated, E, bits, group)) != GPTQ_OK ||
       (st = act_check(act)) != GPTQ_OK || (residual && (st = dt_check(rdt)) != GPTQ_OK))
     return st;
@@ -1432,9 +1433,7 @@ gptq_status gptq_expert_layer(void* stream, const void* X, int32_t xdt, int64_t 
   a.Y = Y;
   a.y_bf16 = ydt == GPTQ_BF16;
   a.ldy = ldy;
-  a.H = static_cast<uint16_t*>(workspace);
-  a.pieces = layer_pieces(a.y_bf16);
-  a.plane = (int64_t)a.slots * d;
+  a.ws = workspace;
   HIP_TRY(launch_layer((hipStream_t)stream, a), "expert_layer");
   return GPTQ_OK;
 }

@@ -5,9 +5,9 @@
 //
 // Bound by reading the packed weights of the experts in use once. The slots
 // (t, j) of one expert go through the matrix-vector product together, up to 16
-// to a tile (v_mfma_f32_16x16x32_bf16). Every workgroup sorts the slots by
-// expert for itself: that costs it about a microsecond and spares the launches
-// that would order rows, move them, and add them up again.
+// to a tile (v_mfma_f32_16x16x32_bf16). Every workgroup of the first launch finds
+// the slots of its tile for itself, which spares the launches that would order
+// rows, move them, and add them up again.
 //  * k_layer_up: a workgroup owns 16 columns of h (32 without a gate) of one
 //    tile, gate and other factor side by side, and its waves split K. h goes to
 //    the workspace as bf16 pieces.
@@ -23,84 +23,105 @@
 
 namespace gq {
 
-constexpr int kLyMax = kLayerMaxSlots;
+constexpr int kLyMax = kLayerMaxSlots, kLyMost = 8;
 
-// Slots by expert: `sorted` lists them expert by expert (in slot order), tile i
-// holds the slots sorted[start[i]] .. of expert e[i], up to TILE of them.
-struct LySort {
-  uint16_t sorted[kLyMax], start[kLyMax], end[kLyMax], expert[kLyMax];
-  uint16_t tiles, places;                // places: slots with an expert
+// A tile: up to TILE slots of one expert, in slot order. The places of all tiles'
+// slots follow each other.
+struct LyTile {
+  int e, rows, first;                    // first: place of its first slot
+  uint16_t slot[kLyMost];
 };
-struct LyScratch {
-  int32_t id[kLyMax];                    // -1: no expert
-  uint16_t place[kLyMax];                // of a slot with an expert, in `sorted`
-  int32_t count[kRouteMaxExperts];       // then the expert's first place (low half) and first tile (high half)
+// What the first launch leaves for the second, in front of h.
+struct LyTable {
+  int tiles, places;
+  LyTile tile[1];
 };
 
-// Called by whole workgroups of THREADS threads.
+// The up to TILE slots of tile number `tile` (rows = 0: no such tile) by one
+// histogram of the slots' experts in LDS, which every wave of the workgroup
+// scans for itself.
 template <int THREADS, int TILE>
-__device__ __forceinline__ void ly_sort(const int32_t* __restrict__ ids, int64_t ldi, int slots, int k, int E, LySort& so,
-                                        LyScratch& sc) {
-  const int tid = threadIdx.x;
-  for (int i = tid; i < E; i += THREADS) sc.count[i] = 0;
-  for (int i = tid; i < slots; i += THREADS) {
-    const int t = i / k, id = ids[t * ldi + (i - t * k)];
-    sc.id[i] = id >= 0 && id < E ? id : -1;
+__device__ __forceinline__ LyTile ly_find(const LayerArgs& a, int tile, int16_t* id, int32_t* count, uint16_t* list,
+                                          int& tiles, int& places) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  for (int i = tid; i < a.E; i += THREADS) count[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < a.slots; i += THREADS) {
+    const int t = i / a.k, v = a.ids[t * a.ldi + (i - t * a.k)];
+    const bool ok = v >= 0 && v < a.E;
+    id[i] = (int16_t)(ok ? v : -1);
+    if (ok) atomicAdd(&count[v], 1);
   }
   __syncthreads();
-  for (int i = tid; i < slots; i += THREADS)
-    if (sc.id[i] >= 0) atomicAdd(&sc.count[sc.id[i]], 1);
-  __syncthreads();
-  if (tid < 64) {
-    int places = 0, tiles = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-      const int c = e0 + tid < E ? sc.count[e0 + tid] : 0, nt = (c + TILE - 1) / TILE;
-      const int pc = wave_scan(c), pt = wave_scan(nt);
-      if (e0 + tid < E) sc.count[e0 + tid] = (places + pc - c) | (tiles + pt - nt) << 16;
-      places += __builtin_amdgcn_readlane(pc, 63);
-      tiles += __builtin_amdgcn_readlane(pt, 63);
+  LyTile r;
+  r.e = -1;
+  r.rows = r.first = tiles = places = 0;
+  int skip = 0;                          // slots of the expert in its tiles before this one
+  for (int e0 = 0; e0 < a.E; e0 += 64) {
+    const int c = e0 + lane < a.E ? count[e0 + lane] : 0, nt = (c + TILE - 1) / TILE;
+    const int pc = wave_scan(c), pt = wave_scan(nt);
+    const uint64_t past = __ballot(tiles + pt > tile);
+    if (r.e < 0 && past) {
+      const int l = __ffsll((long long)past) - 1;
+      skip = TILE * (tile - tiles - __builtin_amdgcn_readlane(pt - nt, l));
+      r.e = e0 + l;
+      r.rows = min(TILE, __builtin_amdgcn_readlane(c, l) - skip);
+      r.first = places + __builtin_amdgcn_readlane(pc - c, l) + skip;
     }
-    if (tid == 0) {
-      so.tiles = (uint16_t)tiles;
-      so.places = (uint16_t)places;
-    }
+    places += __builtin_amdgcn_readlane(pc, 63);
+    tiles += __builtin_amdgcn_readlane(pt, 63);
   }
-  __syncthreads();
-  for (int i = tid; i < slots; i += THREADS) {
-    const int id = sc.id[i];
-    if (id < 0) continue;
-    int rank = 0, all = 0;                               // equal ids before this slot, and at all
-    for (int s = 0; s < slots; ++s) {
-      const bool same = sc.id[s] == id;
-      all += same;
-      rank += same && s < i;
-    }
-    const int place = (sc.count[id] & 0xFFFF) + rank, tile = (sc.count[id] >> 16) + rank / TILE;
-    so.sorted[place] = (uint16_t)i;
-    sc.place[i] = (uint16_t)place;
-    if (rank % TILE == 0) {
-      so.start[tile] = (uint16_t)place;
-      so.end[tile] = (uint16_t)(place + min(TILE, all - rank));
-      so.expert[tile] = (uint16_t)id;
-    }
+  int rank = -skip;
+  for (int s0 = 0; s0 < a.slots && rank < r.rows; s0 += 64) {
+    const bool mine = s0 + lane < a.slots && id[s0 + lane] == r.e;
+    const uint64_t all = __ballot(mine);
+    const int at = rank + __popcll(all & ((1ull << lane) - 1));
+    if (mine && at >= 0 && at < r.rows) list[at] = (uint16_t)(s0 + lane);   // every wave writes the same
+    rank += __popcll(all);
   }
-  __syncthreads();
+  return r;
 }
 
-template <int BITS, bool WIDE, bool GATED>
-__global__ void __launch_bounds__(256)
+template <int BITS, bool WIDE, bool GATED, int TILE>
+__global__ void __launch_bounds__(256, 4)
 k_layer_up(LayerArgs a) {
-  constexpr int WAVES = 4, OB = 2, S = 2;
-  __shared__ LySort so;
+  constexpr int WAVES = 4, OB = 2;
   __shared__ union {
-    LyScratch sort;
+    struct {
+      int16_t id[kLyMax];
+      int32_t count[kRouteMaxExperts];
+    } find;
     float red[WAVES][OB][4][64];
   } sh;
-  ly_sort<256, 16>(a.ids, a.ldi, a.slots, a.k, a.E, so, sh.sort);
-  const int tile = blockIdx.y;
-  if (tile >= so.tiles) return;
+  __shared__ __align__(16) uint8_t smem[WAVES][MvWave<BITS, WIDE, OB, 1, TILE>::BYTES];
+  __shared__ uint16_t list[TILE];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15;
-  const int e = so.expert[tile], first = so.start[tile], rows = so.end[tile] - first;
+  const int tile = blockIdx.y;
+  LyTile t;
+  if (a.T == 1) {                                        // a tile per slot
+    t.e = a.ids[tile];
+    t.rows = t.e >= 0 && t.e < a.E;
+    if (threadIdx.x == 0) list[0] = (uint16_t)tile;
+  } else {
+    int tiles, places;
+    t = ly_find<256, TILE>(a, tile, sh.find.id, sh.find.count, list, tiles, places);
+    if (blockIdx.x == 0 && threadIdx.x < TILE) {
+      LyTable* table = static_cast<LyTable*>(a.table);
+      if (tile == 0 && threadIdx.x == 0) {
+        table->tiles = tiles;
+        table->places = places;
+      }
+      if ((int)threadIdx.x < t.rows) table->tile[tile].slot[threadIdx.x] = list[threadIdx.x];
+      if (threadIdx.x == 0 && t.rows > 0) {
+        table->tile[tile].e = t.e;
+        table->tile[tile].rows = t.rows;
+        table->tile[tile].first = t.first;
+      }
+    }
+  }
+  if (t.rows == 0) return;
+  __syncthreads();                                       // the lists are read, or written: red takes their place
+  const int e = t.e, rows = t.rows;
   const int64_t m = GATED ? 2 * a.d : a.d, o0 = (int64_t)blockIdx.x * (GATED ? 16 : 32);
   // column of h and packed row of output b, li
   auto column = [&](int b, int l) { return o0 + (GATED ? 0 : 16 * b) + l; };
@@ -108,17 +129,18 @@ k_layer_up(LayerArgs a) {
 #pragma unroll
   for (int b = 0; b < OB; ++b) orow[b] = e * m + min(column(b, li), a.d - 1) + (GATED ? b * a.d : 0);
   const MvRows<OB> w(a.up.qw, a.up.scales, a.up.zeros, orow, a.n, a.group, BITS);
-  const uint16_t* x = a.X + (int64_t)(so.sorted[first + min(li, rows - 1)] / a.k) * a.ldx;
   ex_f32x4_t tot[OB];
 #pragma unroll
   for (int b = 0; b < OB; ++b) tot[b] = (ex_f32x4_t){0.f, 0.f, 0.f, 0.f};
-  mv_sum<BITS, WIDE, OB, S, 1>(w, a.n, a.group, wave, WAVES, li < rows, 0, [&]() { return x; }, tot);
+  mv_sum<BITS, WIDE, OB, 1, TILE>(w, a.n, a.group, wave, WAVES, rows, 0, lds_addr(smem[wave]),
+                                  mv_vec(a.up.scales, a.up.zeros, a.n, a.group),
+                                  [&](int r) { return a.X + (int64_t)(list[r] / a.k) * a.ldx; }, tot);
 #pragma unroll
   for (int b = 0; b < OB; ++b)
 #pragma unroll
     for (int r = 0; r < 4; ++r) sh.red[wave][b][r][lane] = tot[b][r];
   __syncthreads();
-  for (int i = threadIdx.x; i < (GATED ? 1 : OB) * 256; i += 256) {
+  for (int i = threadIdx.x; i < (GATED ? 1 : OB) * 256; i += 64 * WAVES) {
     const int b0 = i >> 8, r = (i >> 6) & 3, l = i & 63;
     const int64_t c = column(b0, l & 15);
     const int row = 4 * (l >> 4) + r;
@@ -132,7 +154,7 @@ k_layer_up(LayerArgs a) {
     }
     float h = act_value(a.act, z[0]);
     if constexpr (GATED) h *= z[1];
-    uint16_t* out = a.H + (int64_t)so.sorted[first + row] * a.d + c;
+    uint16_t* out = a.H + (int64_t)list[row] * a.d + c;
     for (int q = 0; q < a.pieces; ++q) {                 // what a piece leaves is exact
       const uint32_t p = ex_pack2(h, 0.f);
       out[q * a.plane] = (uint16_t)p;
@@ -141,26 +163,58 @@ k_layer_up(LayerArgs a) {
   }
 }
 
-template <int BITS, bool WIDE, int NP>
-__global__ void __launch_bounds__(64 * kLayerDownWaves)
+template <int BITS, bool WIDE, int NP, int TILE, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, 4)
 k_layer_down(LayerArgs a) {
-  constexpr int WAVES = kLayerDownWaves, S = 2;
-  __shared__ LySort so;
-  __shared__ LyScratch scratch;
+  // the tiles, and the slots' places (0xFFFF: none) and back
+  __shared__ uint16_t te[kLyMax], trows[kLyMax], tfirst[kLyMax], slot[kLyMax], place[kLyMax];
+  __shared__ __align__(16) uint8_t smem[WAVES][MvWave<BITS, WIDE, 1, NP, TILE>::BYTES];
   extern __shared__ float part[];                        // [part of K][place][column]
-  ly_sort<64 * WAVES, 16>(a.ids, a.ldi, a.slots, a.k, a.E, so, scratch);
-  const int tiles = so.tiles, places = so.places;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15;
+  int tiles, places;
+  if (a.T == 1) {
+    tiles = places = a.k;
+    for (int i = tid; i < a.k; i += 64 * WAVES) {
+      const int id = a.ids[i];
+      const bool ok = id >= 0 && id < a.E;
+      te[i] = (uint16_t)(ok ? id : 0);
+      trows[i] = ok;
+      tfirst[i] = slot[i] = (uint16_t)i;
+      place[i] = (uint16_t)(ok ? i : 0xFFFF);
+    }
+  } else {
+    const LyTable* table = static_cast<const LyTable*>(a.table);
+    tiles = table->tiles;
+    places = table->places;
+    for (int i = tid; i < a.slots; i += 64 * WAVES) place[i] = 0xFFFF;
+    __syncthreads();
+    for (int i = tid; i < tiles * TILE; i += 64 * WAVES) {
+      const LyTile& t = table->tile[i / TILE];
+      const int r = i % TILE;
+      if (r == 0) {
+        te[i / TILE] = (uint16_t)t.e;
+        trows[i / TILE] = (uint16_t)t.rows;
+        tfirst[i / TILE] = (uint16_t)t.first;
+      }
+      if (r < t.rows) {
+        slot[t.first + r] = t.slot[r];
+        place[t.slot[r]] = (uint16_t)(t.first + r);
+      }
+    }
+  }
+  __syncthreads();
   const int64_t o0 = (int64_t)blockIdx.x * 16;
   const int kp = tiles >= WAVES || tiles == 0 ? 1 : WAVES / tiles;
+  const bool vec = mv_vec(a.down.scales, a.down.zeros, a.d, a.group);
   for (int i = wave; i < tiles * kp; i += WAVES) {
     const int tile = i / kp, p = i - tile * kp;
-    const int e = so.expert[tile], first = so.start[tile], rows = so.end[tile] - first;
+    const int e = te[tile], first = tfirst[tile], rows = trows[tile];
+    if (rows == 0) continue;
     const int64_t orow[1] = {(int64_t)e * a.n + min(o0 + li, a.n - 1)};
     const MvRows<1> w(a.down.qw, a.down.scales, a.down.zeros, orow, a.d, a.group, BITS);
-    const uint16_t* h = a.H + (int64_t)so.sorted[first + min(li, rows - 1)] * a.d;
     ex_f32x4_t tot[1] = {{0.f, 0.f, 0.f, 0.f}};
-    mv_sum<BITS, WIDE, 1, S, NP>(w, a.d, a.group, p, kp, li < rows, a.plane, [&]() { return h; }, tot);
+    mv_sum<BITS, WIDE, 1, NP, TILE>(w, a.d, a.group, p, kp, rows, a.plane, lds_addr(smem[wave]), vec,
+                                    [&](int r) { return a.H + (int64_t)slot[first + r] * a.d; }, tot);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 4 * (lane >> 4) + r;
@@ -168,17 +222,17 @@ k_layer_down(LayerArgs a) {
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.T * 16; i += 64 * WAVES) {
+  for (int i = tid; i < a.T * 16; i += 64 * WAVES) {
     const int t = i >> 4, c = i & 15;
     const int64_t o = o0 + c;
     if (o >= a.n) continue;
     float y = 0.f;
     for (int j = 0; j < a.k; ++j) {
-      const int s = t * a.k + j, id = scratch.id[s];
-      if (id < 0) continue;
+      const int s = t * a.k + j, at = place[s];
+      if (at == 0xFFFF) continue;
       float v = 0.f;
-      for (int p = 0; p < kp; ++p) v += part[(p * places + scratch.place[s]) * 16 + c];
-      if (a.b2) v += a.b2[id * a.n + o];
+      for (int p = 0; p < kp; ++p) v += part[(p * places + at) * 16 + c];
+      if (a.b2) v += a.b2[a.ids[t * a.ldi + j] * a.n + o];
       y = fmaf(a.w ? a.w[s] : 1.f, v, y);
     }
     if (a.res) {
@@ -191,19 +245,47 @@ k_layer_down(LayerArgs a) {
 }
 
 // ---------------------------------------------------------------- host
-int layer_pieces(int y_bf16) { return y_bf16 ? 1 : 3; }
+// Slots of a tile. Three pieces of h take three times the LDS.
+static int layer_tile(int64_t T, int y_bf16) { return !y_bf16 || T <= 4 ? 4 : 8; }
+static int layer_pieces(int y_bf16) { return y_bf16 ? 1 : 3; }
+static int64_t layer_tiles(int64_t T, int64_t slots, int64_t E, int y_bf16) {
+  return T == 1 ? slots : std::min(slots, ceil_div(slots, layer_tile(T, y_bf16)) + E - 1);
+}
+static size_t table_bytes(int64_t T, int64_t slots, int64_t E, int y_bf16) {
+  return T == 1 ? 0 : (offsetof(LyTable, tile) + layer_tiles(T, slots, E, y_bf16) * sizeof(LyTile) + 255) / 256 * 256;
+}
+size_t layer_workspace(int64_t T, int64_t k, int64_t E, int64_t d, int y_bf16) {
+  return table_bytes(T, T * k, E, y_bf16) + ((size_t)layer_pieces(y_bf16) * T * k * d * sizeof(uint16_t) + 255) / 256 * 256;
+}
+
+template <int BITS, bool WIDE, int NP, int TILE, int WAVES>
+static void down_go(hipStream_t s, const LayerArgs& a) {
+  // K is in WAVES / tiles parts while the tiles are fewer than the waves: up to WAVES times TILE places
+  const size_t lds = std::max<size_t>(a.slots, (size_t)std::min(a.slots, TILE) * WAVES) * 64;
+  hipLaunchKernelGGL((k_layer_down<BITS, WIDE, NP, TILE, WAVES>), dim3((unsigned)ceil_div(a.n, 16)),
+                     dim3(64 * WAVES), lds, s, a);
+}
+template <int BITS, bool WIDE, int NP, int TILE>
+static void down_waves(hipStream_t s, const LayerArgs& a) {
+  // LDS holds 16 waves' share beside the results of 512 slots
+  constexpr bool BIG = MvWave<BITS, WIDE, 1, NP, TILE>::BYTES <= 6144;
+  if constexpr (BIG) {
+    if (a.slots <= 512) return down_go<BITS, WIDE, NP, TILE, 16>(s, a);
+  }
+  down_go<BITS, WIDE, NP, TILE, 8>(s, a);
+}
 
 template <int BITS, bool WIDE>
 static void ly_go(hipStream_t s, const LayerArgs& a) {
-  const int64_t tiles = std::min<int64_t>(a.slots, ceil_div(a.slots, 16) + a.E - 1);
-  const dim3 up((unsigned)ceil_div(a.d, a.gated ? 16 : 32), (unsigned)tiles), down((unsigned)ceil_div(a.n, 16));
-  if (a.gated) hipLaunchKernelGGL((k_layer_up<BITS, WIDE, true>), up, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_layer_up<BITS, WIDE, false>), up, dim3(256), 0, s, a);
-  // K is in waves / tiles parts while the tiles are fewer than the waves: 16 slots a tile, 16 waves times 16 places
-  const size_t lds = std::max<size_t>(a.slots, (size_t)std::min(a.slots, 16) * kLayerDownWaves) * 64;
-  const dim3 block(64 * kLayerDownWaves);
-  if (a.pieces == 1) hipLaunchKernelGGL((k_layer_down<BITS, WIDE, 1>), down, block, lds, s, a);
-  else hipLaunchKernelGGL((k_layer_down<BITS, WIDE, 3>), down, block, lds, s, a);
+  const dim3 up((unsigned)ceil_div(a.d, a.gated ? 16 : 32), (unsigned)layer_tiles(a.T, a.slots, a.E, a.y_bf16)), block(256);
+  const bool four = layer_tile(a.T, a.y_bf16) == 4;
+  if (a.gated && four) hipLaunchKernelGGL((k_layer_up<BITS, WIDE, true, 4>), up, block, 0, s, a);
+  else if (a.gated) hipLaunchKernelGGL((k_layer_up<BITS, WIDE, true, 8>), up, block, 0, s, a);
+  else if (four) hipLaunchKernelGGL((k_layer_up<BITS, WIDE, false, 4>), up, block, 0, s, a);
+  else hipLaunchKernelGGL((k_layer_up<BITS, WIDE, false, 8>), up, block, 0, s, a);
+  if (!a.y_bf16) down_waves<BITS, WIDE, 3, 4>(s, a);
+  else if (four) down_waves<BITS, WIDE, 1, 4>(s, a);
+  else down_waves<BITS, WIDE, 1, 8>(s, a);
 }
 
 template <int BITS>
@@ -212,7 +294,12 @@ static void ly_bits(hipStream_t s, const LayerArgs& a) {
   else ly_go<BITS, false>(s, a);
 }
 
-hipError_t launch_layer(hipStream_t s, const LayerArgs& a) {
+hipError_t launch_layer(hipStream_t s, const LayerArgs& args) {
+  LayerArgs a = args;
+  a.table = a.ws;
+  a.H = reinterpret_cast<uint16_t*>(static_cast<char*>(a.ws) + table_bytes(a.T, a.slots, a.E, a.y_bf16));
+  a.pieces = layer_pieces(a.y_bf16);
+  a.plane = (int64_t)a.slots * a.d;
   if (a.bits == 2) ly_bits<2>(s, a);
   else if (a.bits == 3) ly_bits<3>(s, a);
   else ly_bits<4>(s, a);

@@ -112,7 +112,7 @@ def load():
         "gptq_linear_grad": [c_vp, c_vp, ctypes.c_int32, c_i64, c_vp, ctypes.c_int32, c_i64, c_i64, c_vp, c_i64, c_vp,
                              c_vp, c_vp, c_i64, c_i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                              c_vp, c_i64, c_vp, c_vp, ctypes.c_int32, c_i64, c_vp, c_sz],
-        "gptq_expert_layer_workspace_bytes": [c_i64, c_i64, c_i64, ctypes.c_int32, ctypes.POINTER(c_sz)],
+        "gptq_expert_layer_workspace_bytes": [c_i64, c_i64, c_i64, c_i64, ctypes.c_int32, ctypes.POINTER(c_sz)],
         "gptq_expert_layer": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp,
                               c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, ctypes.c_int32, ctypes.c_int32,
                               ctypes.c_int32, ctypes.c_int32, c_vp, ctypes.c_int32, c_i64, c_vp, ctypes.c_int32, c_i64,
@@ -758,7 +758,7 @@ def expert_layer(X, expert_ids, weights, up, down, bits, group, act="silu", gate
     resp, rdt, ldr = _matrix(residual, "residual", (T, n), _FLOATS, dev)
     out, yp, ldy = _result(out, (T, n), out_dtype, dev)
     ydt = _DTYPE_CODES[out.dtype]
-    need = _bytes("gptq_expert_layer_workspace_bytes", T, k, d, ydt)
+    need = _bytes("gptq_expert_layer_workspace_bytes", T, k, E, d, ydt)
     ws, wsp = _scratch(need, dev, workspace)
     _call(dev, lib.gptq_expert_layer, xp, BF16, T, n, ldx, ip, ldi, k, wp, E, uqp, usp, uzp, b1, dqp, dsp, dzp, b2, d,
           bits, group, code, gated, resp, rdt, ldr, yp, ydt, ldy, wsp, need)

@@ -209,11 +209,12 @@ def test_expert_layer_refusals():
     assert call(T=0, X=NULL, Y=NULL, ws=NULL, wsb=0) == 0
     out = ctypes.c_size_t(0)
     need = lib.gptq_expert_layer_workspace_bytes
-    assert need(4, 2, 64, 0, ctypes.byref(out)) == 0 and out.value % 256 == 0 and out.value >= 4 * 2 * 64 * 2
-    assert need(4, 2, 64, 1, ctypes.byref(out)) == 0 and out.value >= 3 * 4 * 2 * 64 * 2
-    for bad in ((-1, 2, 64, 0), (4, 0, 64, 0), (4, 2, 0, 0), (4, 2, 64, 2), (1025, 1, 64, 0), (4, 2, 2 ** 20 + 1, 0)):
+    assert need(4, 2, 4, 64, 0, ctypes.byref(out)) == 0 and out.value % 256 == 0 and out.value >= 4 * 2 * 64 * 2
+    assert need(4, 2, 4, 64, 1, ctypes.byref(out)) == 0 and out.value >= 3 * 4 * 2 * 64 * 2
+    for bad in ((-1, 2, 4, 64, 0), (4, 0, 4, 64, 0), (4, 2, 4, 0, 0), (4, 2, 4, 64, 2), (1025, 1, 4, 64, 0), (4, 2, 0, 64, 0),
+                (4, 2, 1025, 64, 0), (4, 2, 4, 2 ** 20 + 1, 0)):
         assert need(*bad, ctypes.byref(out)) == -1
-    assert need(4, 2, 64, 0, None) == -1
+    assert need(4, 2, 4, 64, 0, None) == -1
 
 
 def test_distill_refusals():
