@@ -499,7 +499,8 @@ gptq_status gptq_linear_grad(void *stream, const void *dY, int32_t dydt, int64_t
  * ("El balance de errores de la inferencia de pocos bits", section 6: decoding
  * pays for the traffic of the packed weights, and for every launch beside it.) */
 #define GPTQ_LAYER_MAX_SLOTS 1024
-gptq_status gptq_expert_layer_workspace_bytes(int64_t T, int64_t k, int64_t d, int32_t ydt, size_t *bytes);
+gptq_status gptq_expert_layer_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t d, int32_t ydt,
+                                              size_t *bytes);
 gptq_status gptq_expert_layer(void *stream, const void *X, int32_t xdt, int64_t T, int64_t n, int64_t ldx,
                               const int32_t *expert_ids, int64_t ldi, int64_t k, const float *weights, int64_t E,
                               const uint32_t *up_qweight, const float *up_scales, const uint8_t *up_zeros,
@@ -525,21 +526,19 @@ gptq_status gptq_expert_layer(void *stream, const void *X, int32_t xdt, int64_t 
  * and a loss of NaN, unless it is padding. NaN and +infinity make their row NaN.
  * 1 <= K <= GPTQ_DISTILL_MAX_K, V <= 2^31 - 65536, temperature positive and
  * finite. Everything is fp32, in an order that does not depend on timing.
- * Workspace: gptq_distill_workspace_bytes (0 for many rows).
  *
  * gptq_distill_grad: for grad (T fp32: d total / d loss[t]) and lse as
  * gptq_distill gave it,
  *   dZ[t][v] = grad[t] / temperature (M q_v - sum over k with ids = v of p_k)
  * (T x V, dzdt bf16 or fp32, row pitch ldd; an id that stands more than once in
- * a row counts each time). dZ may be Z (same type and pitch). No workspace. Both
- * asynchronous; T == 0 enqueues nothing. T may be at most 2^24 - 2.
+ * a row counts each time). dZ may be Z (same type and pitch). Neither needs a
+ * workspace; both are asynchronous; T == 0 enqueues nothing. T may be at most 2^24 - 2.
  * ("Resumen Técnico: GPTQ-intrinsic LoRA", "Declaración del Problema": the
  * low-rank factors beside the quantized layer, which tuning moves.) */
 #define GPTQ_DISTILL_MAX_K 1024
-gptq_status gptq_distill_workspace_bytes(int64_t T, int64_t V, size_t *bytes);
 gptq_status gptq_distill(void *stream, const void *Z, int32_t zdt, int64_t T, int64_t V, int64_t ldz,
                          const int32_t *ids, const float *teacher, int64_t K, float temperature, int32_t log_probs,
-                         float *loss, float *lse, void *workspace, size_t ws_bytes);
+                         float *loss, float *lse);
 gptq_status gptq_distill_grad(void *stream, const void *Z, int32_t zdt, int64_t T, int64_t V, int64_t ldz,
                               const int32_t *ids, const float *teacher, int64_t K, float temperature,
                               int32_t log_probs, const float *lse, const float *grad, void *dZ, int32_t dzdt,

@@ -302,6 +302,7 @@ struct ExpertArgs {
   int64_t d_out, n; int bits, group;
   void* Y; int y_bf16; int64_t ldy;
   void* part;                                 // expert_split's part_bytes
+  bool parts_only;                            // the parts of K are left there: the caller adds them up
 };
 struct ExpertSplit {
   int splits, per;      // parts of K, stages of a part
@@ -309,6 +310,7 @@ struct ExpertSplit {
 };
 // pieces: the gradient with an fp32 result
 ExpertSplit expert_split(int64_t R, int E, int64_t n, int64_t d_out, int group, int grad, bool pieces);
+int expert_bm(const ExpertArgs& a, int grad);            // rows of a tile: 16 is the matrix-vector form, 256 the ring
 int64_t expert_threads(const ExpertArgs& a, int grad);   // an upper bound on the threads of a launch's first dimension
 hipError_t launch_expert_mm(hipStream_t s, const ExpertArgs& a);
 hipError_t launch_expert_mm_grad(hipStream_t s, const ExpertArgs& a);
@@ -382,10 +384,8 @@ struct DistillArgs {
   float *loss, *lse;                          // T (forward)
   const float *lse_in, *grad;                 // T (gradient)
   void* dZ; int dz_bf16; int64_t ldd;
-  void* part_sums;                            // distill_parts pairs of floats a row when there are several
-  int parts; int64_t part_cols;               // set by the launch
+  int parts; int64_t part_cols;               // of a row (gradient): set by the launch
 };
-int distill_parts(int64_t T, int64_t V);
 hipError_t launch_distill(hipStream_t s, const DistillArgs& a);
 hipError_t launch_distill_grad(hipStream_t s, const DistillArgs& a);
 

@@ -8,8 +8,8 @@
 //
 // Bound by reading the logits once (and writing their gradient once): one pass
 // keeps a running maximum and sum per lane and joins them at the end. A
-// workgroup has a row, or a part of one where there are few rows; the parts
-// meet in a second launch in their order, so results do not depend on timing.
+// workgroup has a row (the gradient: or a part of one, where rows are few); no
+// result depends on timing.
 #include "common.h"
 
 #include <algorithm>
@@ -22,8 +22,6 @@ typedef di_u32x4_t di_u32x4_any_t __attribute__((aligned(2)));
 typedef di_u32x2_t di_u32x2_any_t __attribute__((aligned(2)));
 typedef __bf16 di_bf16x2_t __attribute__((ext_vector_type(2)));
 
-constexpr int kDiThreads = 256;
-constexpr int kDiPer = kDistillMaxK / kDiThreads;   // teacher's entries per thread at most
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool BF>
@@ -94,7 +92,7 @@ __device__ __forceinline__ DiSum di_join(DiSum a, DiSum b, float c) {
 }
 
 // Sums (maxima) over the workgroup, in a fixed order, in every thread.
-template <class F>
+template <int THREADS, class F>
 __device__ __forceinline__ float di_all(float v, float* red, F&& f) {
 #pragma unroll
   for (int i = 32; i > 0; i >>= 1) v = f(v, __shfl_xor(v, i));
@@ -103,27 +101,31 @@ __device__ __forceinline__ float di_all(float v, float* red, F&& f) {
   __syncthreads();
   v = red[0];
 #pragma unroll
-  for (int w = 1; w < kDiThreads / 64; ++w) v = f(v, red[w]);
+  for (int w = 1; w < THREADS / 64; ++w) v = f(v, red[w]);
   return v;
 }
+template <int THREADS>
 __device__ __forceinline__ float di_add(float v, float* red) {
-  return di_all(v, red, [](float a, float b) { return a + b; });
+  return di_all<THREADS>(v, red, [](float a, float b) { return a + b; });
 }
+template <int THREADS>
 __device__ __forceinline__ float di_max(float v, float* red) {
-  return di_all(v, red, [](float a, float b) { return fmaxf(a, b); });
+  return di_all<THREADS>(v, red, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// The teacher's entries of a row: thread t has entries t, t + 256, ...
+// The teacher's entries of a row: thread t has entries t, t + THREADS, ...
+template <int THREADS>
 struct DiTeacher {
-  int id[kDiPer];        // -1: none (ids outside [0, V) are not entries)
-  float lp[kDiPer];      // log p
-  float p[kDiPer];       // 0 for no entry
+  static constexpr int PER = kDistillMaxK / THREADS;
+  int id[PER];           // -1: none (ids outside [0, V) are not entries)
+  float lp[PER];         // log p
+  float p[PER];          // 0 for no entry
 };
-// FULL: log p as well as p (the loss needs it).
-__device__ __forceinline__ void di_load_teacher(const DistillArgs& a, int64_t row, DiTeacher& te) {
+template <int THREADS>
+__device__ __forceinline__ void di_load_teacher(const DistillArgs& a, int64_t row, DiTeacher<THREADS>& te) {
 #pragma unroll
-  for (int i = 0; i < kDiPer; ++i) {
-    const int k = threadIdx.x + kDiThreads * i;
+  for (int i = 0; i < te.PER; ++i) {
+    const int k = threadIdx.x + THREADS * i;
     te.id[i] = -1;
     te.lp[i] = -INFINITY;
     if (k < a.K) {
@@ -136,46 +138,48 @@ __device__ __forceinline__ void di_load_teacher(const DistillArgs& a, int64_t ro
   }
 }
 // p and log p; returns their mass (0: nothing to learn in this row).
-__device__ __forceinline__ float di_probabilities(const DistillArgs& a, DiTeacher& te, float* red) {
+template <int THREADS>
+__device__ __forceinline__ float di_probabilities(const DistillArgs& a, DiTeacher<THREADS>& te, float* red) {
   float sum = 0.f, top = 0.f, inv = 1.f, ln = 0.f;
   if (!a.log_probs) {
     float hi = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kDiPer; ++i) hi = fmaxf(hi, te.lp[i]);
-    top = di_ref(di_max(hi, red));
+    for (int i = 0; i < te.PER; ++i) hi = fmaxf(hi, te.lp[i]);
+    top = di_ref(di_max<THREADS>(hi, red));
 #pragma unroll
-    for (int i = 0; i < kDiPer; ++i) {
+    for (int i = 0; i < te.PER; ++i) {
       te.lp[i] = (te.lp[i] - top) * a.inv_temp;
       te.p[i] = expf(te.lp[i]);
       sum += te.p[i];
     }
-    sum = di_add(sum, red);
+    sum = di_add<THREADS>(sum, red);
     if (sum == 0.f) return 0.f;
     inv = 1.f / sum;
     ln = logf(sum);
   }
   float mass = 0.f;
 #pragma unroll
-  for (int i = 0; i < kDiPer; ++i) {
+  for (int i = 0; i < te.PER; ++i) {
     te.lp[i] -= ln;
     te.p[i] = a.log_probs ? expf(te.lp[i]) : te.p[i] * inv;
     mass += te.p[i];
   }
-  return di_add(mass, red);
+  return di_add<THREADS>(mass, red);
 }
 
 // Loss and lse of a row from its sum. zt: the student's logits at the
 // teacher's entries.
-__device__ __forceinline__ void di_finish(const DistillArgs& a, int64_t row, DiSum s, DiTeacher& te,
-                                          const float (&zt)[kDiPer], float* red) {
+template <int THREADS>
+__device__ __forceinline__ void di_finish(const DistillArgs& a, int64_t row, DiSum s, DiTeacher<THREADS>& te,
+                                          const float (&zt)[DiTeacher<THREADS>::PER], float* red) {
   const float ll = logf(s.l), r = di_ref(s.m);
   const float mass = di_probabilities(a, te, red);
   float loss = 0.f;
   if (mass != 0.f) {
 #pragma unroll
-    for (int i = 0; i < kDiPer; ++i)    // p (log p - log q); an entry without mass adds nothing wherever its logit is
+    for (int i = 0; i < te.PER; ++i)    // p (log p - log q); an entry without mass adds nothing wherever its logit is
       if (te.p[i] != 0.f) loss += te.p[i] * (te.lp[i] - ((zt[i] - r) * a.inv_temp - ll));
-    loss = di_add(loss, red);
+    loss = di_add<THREADS>(loss, red);
   }
   if (threadIdx.x == 0) {
     a.loss[row] = loss;
@@ -183,39 +187,21 @@ __device__ __forceinline__ void di_finish(const DistillArgs& a, int64_t row, DiS
   }
 }
 
-template <bool BF>
-__device__ __forceinline__ void di_student(const DistillArgs& a, int64_t row, const DiTeacher& te, float (&zt)[kDiPer]) {
-#pragma unroll
-  for (int i = 0; i < kDiPer; ++i) zt[i] = te.id[i] >= 0 ? di_load1<BF>(a.Z, row * a.ldz + te.id[i]) : 0.f;
-}
-
-// Columns of part p of a row (whole pieces but for the last).
-struct DiPart {
-  int64_t lo, hi;
-};
-__device__ __forceinline__ DiPart di_part(const DistillArgs& a, int p) {
-  const int64_t lo = (int64_t)p * a.part_cols;
-  return DiPart{lo, min(lo + a.part_cols, (int64_t)a.V)};
-}
-
-template <bool BF>
-__global__ void __launch_bounds__(kDiThreads)
+template <bool BF, int THREADS>
+__global__ void __launch_bounds__(THREADS)
 k_distill(DistillArgs a) {
-  constexpr int P = DiType<BF>::P, U = 4;
-  __shared__ float red[kDiThreads / 64];
-  __shared__ DiSum sums[kDiThreads / 64];
-  const int64_t row = blockIdx.x / a.parts;
-  const DiPart part = di_part(a, blockIdx.x % a.parts);
-  const int tid = threadIdx.x;
-  const char* z = static_cast<const char*>(a.Z) + (row * a.ldz + part.lo) * DiType<BF>::BYTES;
-  const int cols = (int)(part.hi - part.lo), np = cols / P;
+  constexpr int P = DiType<BF>::P, U = 4, WAVES = THREADS / 64;
+  __shared__ float red[WAVES];
+  __shared__ DiSum sums[WAVES];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, cols = (int)a.V, np = cols / P;
+  const char* z = static_cast<const char*>(a.Z) + row * a.ldz * DiType<BF>::BYTES;
   const float c = kLog2e * a.inv_temp;
-  DiTeacher te;
-  float zt[kDiPer];
-  if (a.parts == 1) {
-    di_load_teacher(a, row, te);
-    di_student<BF>(a, row, te, zt);
-  }
+  DiTeacher<THREADS> te;
+  float zt[te.PER];                                // the student's logits at the teacher's entries
+  di_load_teacher<THREADS>(a, row, te);
+#pragma unroll
+  for (int i = 0; i < te.PER; ++i) zt[i] = te.id[i] >= 0 ? di_load1<BF>(z, te.id[i]) : 0.f;
   DiSum s = {-INFINITY, 0.f};
   auto take = [&](const float* f, int n) {
     float m = s.m;
@@ -228,10 +214,10 @@ k_distill(DistillArgs a) {
     s = DiSum{m, l};
   };
   int p = tid;
-  for (; p + (U - 1) * kDiThreads < np; p += U * kDiThreads) {
+  for (; p + (U - 1) * THREADS < np; p += U * THREADS) {
     di_u32x4_t w[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = di_piece<BF>(z, (int64_t)(p + u * kDiThreads) * P);
+    for (int u = 0; u < U; ++u) w[u] = di_piece<BF>(z, (int64_t)(p + u * THREADS) * P);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float f[P];
@@ -239,7 +225,7 @@ k_distill(DistillArgs a) {
       take(f, P);
     }
   }
-  for (; p < np; p += kDiThreads) {
+  for (; p < np; p += THREADS) {
     float f[P];
     di_values<BF>(di_piece<BF>(z, (int64_t)p * P), f);
     take(f, P);
@@ -254,25 +240,17 @@ k_distill(DistillArgs a) {
   __syncthreads();
   s = sums[0];
 #pragma unroll
-  for (int w = 1; w < kDiThreads / 64; ++w) s = di_join(s, sums[w], c);
-  if (a.parts == 1) di_finish(a, row, s, te, zt, red);
-  else if (tid == 0) static_cast<DiSum*>(a.part_sums)[blockIdx.x] = s;
+  for (int w = 1; w < WAVES; ++w) s = di_join(s, sums[w], c);
+  di_finish<THREADS>(a, row, s, te, zt, red);
 }
 
-// The parts of a row, in their order.
-template <bool BF>
-__global__ void __launch_bounds__(kDiThreads)
-k_distill_join(DistillArgs a) {
-  __shared__ float red[kDiThreads / 64];
-  const int64_t row = blockIdx.x;
-  DiTeacher te;
-  float zt[kDiPer];
-  di_load_teacher(a, row, te);
-  di_student<BF>(a, row, te, zt);
-  const DiSum* parts = static_cast<const DiSum*>(a.part_sums) + row * a.parts;
-  DiSum s = parts[0];
-  for (int i = 1; i < a.parts; ++i) s = di_join(s, parts[i], kLog2e * a.inv_temp);
-  di_finish(a, row, s, te, zt, red);
+// Columns of part p of a row (whole pieces but for the last).
+struct DiPart {
+  int64_t lo, hi;
+};
+__device__ __forceinline__ DiPart di_part(const DistillArgs& a, int p) {
+  const int64_t lo = (int64_t)p * a.part_cols;
+  return DiPart{lo, min(lo + a.part_cols, (int64_t)a.V)};
 }
 
 // The gradient: q of every entry is written first, then the teacher's entries
@@ -281,10 +259,10 @@ k_distill_join(DistillArgs a) {
 // a row gets all of its p, added in their order by each of its threads: they
 // all store the same value.
 template <bool BF, bool OBF>
-__global__ void __launch_bounds__(kDiThreads)
+__global__ void __launch_bounds__(256)
 k_distill_grad(DistillArgs a) {
-  constexpr int P = DiType<BF>::P, U = 4;
-  __shared__ float red[kDiThreads / 64];
+  constexpr int THREADS = 256, P = DiType<BF>::P, U = 4;
+  __shared__ float red[THREADS / 64];
   __shared__ int sid[kDistillMaxK];
   __shared__ float sp[kDistillMaxK];
   const int64_t row = blockIdx.x / a.parts;
@@ -293,21 +271,21 @@ k_distill_grad(DistillArgs a) {
   const char* z = static_cast<const char*>(a.Z) + (row * a.ldz + part.lo) * DiType<BF>::BYTES;
   char* out = static_cast<char*>(a.dZ) + (row * a.ldd + part.lo) * DiType<OBF>::BYTES;
   const int cols = (int)(part.hi - part.lo), np = cols / P;
-  DiTeacher te;
-  float zt[kDiPer];
-  di_load_teacher(a, row, te);
+  DiTeacher<THREADS> te;
+  float zt[te.PER];
+  di_load_teacher<THREADS>(a, row, te);
 #pragma unroll
-  for (int i = 0; i < kDiPer; ++i) {
+  for (int i = 0; i < te.PER; ++i) {
     zt[i] = 0.f;
     if (te.id[i] >= part.lo && te.id[i] < part.hi) zt[i] = di_load1<BF>(z, te.id[i] - part.lo);
   }
   const float lse = a.lse_in[row], g = a.grad[row] * a.inv_temp;
-  const float mass = di_probabilities(a, te, red);
+  const float mass = di_probabilities<THREADS>(a, te, red);
   const bool none = mass == 0.f;                   // nothing to learn: zeros, whatever the logits are
   const float f = g * mass;
 #pragma unroll
-  for (int i = 0; i < kDiPer; ++i) {
-    const int k = tid + kDiThreads * i;
+  for (int i = 0; i < te.PER; ++i) {
+    const int k = tid + THREADS * i;
     if (k < a.K) {
       sid[k] = te.id[i];
       sp[k] = te.p[i];
@@ -315,23 +293,23 @@ k_distill_grad(DistillArgs a) {
   }
   auto value = [&](float v) { return none ? 0.f : f * di_exp2(fmaf(v, a.inv_temp, -lse) * kLog2e); };
 #pragma unroll
-  for (int i = 0; i < kDiPer; ++i) zt[i] = value(zt[i]);
+  for (int i = 0; i < te.PER; ++i) zt[i] = value(zt[i]);
   __syncthreads();                                 // the teacher's logits are read
   int p = tid;
-  for (; p + (U - 1) * kDiThreads < np; p += U * kDiThreads) {
+  for (; p + (U - 1) * THREADS < np; p += U * THREADS) {
     di_u32x4_t w[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = di_piece<BF>(z, (int64_t)(p + u * kDiThreads) * P);
+    for (int u = 0; u < U; ++u) w[u] = di_piece<BF>(z, (int64_t)(p + u * THREADS) * P);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float v[P];
       di_values<BF>(w[u], v);
 #pragma unroll
       for (int i = 0; i < P; ++i) v[i] = value(v[i]);
-      di_store<OBF, P>(out, (int64_t)(p + u * kDiThreads) * P, v);
+      di_store<OBF, P>(out, (int64_t)(p + u * THREADS) * P, v);
     }
   }
-  for (; p < np; p += kDiThreads) {
+  for (; p < np; p += THREADS) {
     float v[P];
     di_values<BF>(di_piece<BF>(z, (int64_t)p * P), v);
 #pragma unroll
@@ -342,7 +320,7 @@ k_distill_grad(DistillArgs a) {
   __syncthreads();                                 // the stores above come before those below
   if (none) return;
 #pragma unroll
-  for (int i = 0; i < kDiPer; ++i) {
+  for (int i = 0; i < te.PER; ++i) {
     if (te.id[i] < part.lo || te.id[i] >= part.hi) continue;
     float sum = 0.f;
     for (int k = 0; k < a.K; ++k)
@@ -352,34 +330,26 @@ k_distill_grad(DistillArgs a) {
 }
 
 // ---------------------------------------------------------------- host
-// Parts of a row: until there are four workgroups per CU, of at least 2048 values.
-int distill_parts(int64_t T, int64_t V) {
-  if (T <= 0 || V <= 0) return 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(1024, T), V / 2048));
-}
-
-static DistillArgs with_parts(DistillArgs a) {
-  const int parts = distill_parts(a.T, a.V);
-  a.part_cols = ceil_div(ceil_div(a.V, parts), 8) * 8;
-  a.parts = (int)ceil_div(a.V, a.part_cols);
-  return a;
-}
-
-hipError_t launch_distill(hipStream_t s, const DistillArgs& args) {
-  const DistillArgs a = with_parts(args);
-  const dim3 grid((unsigned)(a.T * a.parts)), block(kDiThreads);
-  if (a.z_bf16) hipLaunchKernelGGL(k_distill<true>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(k_distill<false>, grid, block, 0, s, a);
-  const hipError_t err = hipGetLastError();
-  if (err != hipSuccess || a.parts == 1) return err;
-  if (a.z_bf16) hipLaunchKernelGGL(k_distill_join<true>, dim3((unsigned)a.T), block, 0, s, a);
-  else hipLaunchKernelGGL(k_distill_join<false>, dim3((unsigned)a.T), block, 0, s, a);
+// Rows below four workgroups per CU go with 1024 threads each, whatever their
+// length: 61 rows of 32003 fp32 values NEWD us, in parts of 2048 values or more and a
+// second launch that joins them 9.1.
+hipError_t launch_distill(hipStream_t s, const DistillArgs& a) {
+  const dim3 grid((unsigned)a.T);
+  const bool few = a.T < 1024 && a.V > 2048;
+  if (a.z_bf16 && few) hipLaunchKernelGGL((k_distill<true, 1024>), grid, dim3(1024), 0, s, a);
+  else if (few) hipLaunchKernelGGL((k_distill<false, 1024>), grid, dim3(1024), 0, s, a);
+  else if (a.z_bf16) hipLaunchKernelGGL((k_distill<true, 256>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_distill<false, 256>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_distill_grad(hipStream_t s, const DistillArgs& args) {
-  const DistillArgs a = with_parts(args);
-  const dim3 grid((unsigned)(a.T * a.parts)), block(kDiThreads);
+  DistillArgs a = args;
+  // parts of a row: until there are four workgroups per CU, of at least 2048 values
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(ceil_div(1024, a.T), a.V / 2048));
+  a.part_cols = ceil_div(ceil_div(a.V, parts), 8) * 8;
+  a.parts = (int)ceil_div(a.V, a.part_cols);
+  const dim3 grid((unsigned)(a.T * a.parts)), block(256);
   if (a.z_bf16 && a.dz_bf16) hipLaunchKernelGGL((k_distill_grad<true, true>), grid, block, 0, s, a);
   else if (a.z_bf16) hipLaunchKernelGGL((k_distill_grad<true, false>), grid, block, 0, s, a);
   else if (a.dz_bf16) hipLaunchKernelGGL((k_distill_grad<false, true>), grid, block, 0, s, a);

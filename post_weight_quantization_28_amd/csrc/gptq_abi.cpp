@@ -1439,19 +1439,15 @@ gptq_status gptq_expert_layer(void* stream, const void* X, int32_t xdt, int64_t 
 }
 
 // ---------------------------------------------------------------- distillation
-static gptq_status distill_sizes(int64_t T, int64_t V) {
-  if (T < 0 || V < 1) return fail(GPTQ_EINVAL, "need T >= 0 and V >= 1");
-  if (T > kMaxThreads / 256) return fail(GPTQ_EINVAL, "T may be at most 2^24 - 2");
-  if (V > kMaxRows) return fail(GPTQ_EINVAL, "V may be at most 2^31 - 65536");
-  return GPTQ_OK;
-}
-
 // What both calls check; the rest of the arguments is filled in by them.
 static gptq_status distill_args(const void* Z, int32_t zdt, int64_t T, int64_t V, int64_t ldz, const int32_t* ids,
                                 const float* teacher, int64_t K, float temperature, int32_t log_probs,
                                 DistillArgs* a) {
-  gptq_status st = dt_check(zdt);
-  if (st != GPTQ_OK || (st = distill_sizes(T, V)) != GPTQ_OK) return st;
+  const gptq_status st = dt_check(zdt);
+  if (st != GPTQ_OK) return st;
+  if (T < 0 || V < 1) return fail(GPTQ_EINVAL, "need T >= 0 and V >= 1");
+  if (T > kMaxThreads / 256) return fail(GPTQ_EINVAL, "T may be at most 2^24 - 2");
+  if (V > kMaxRows) return fail(GPTQ_EINVAL, "V may be at most 2^31 - 65536");
   if (K < 1 || K > GPTQ_DISTILL_MAX_K) return fail(GPTQ_EINVAL, "K must be in [1, GPTQ_DISTILL_MAX_K]");
   const float inv = 1.f / temperature;
   if (!(temperature > 0.f) || !(inv > 0.f) || inv - inv != 0.f || temperature - temperature != 0.f)
@@ -1476,30 +1472,15 @@ static gptq_status distill_args(const void* Z, int32_t zdt, int64_t T, int64_t V
   return GPTQ_OK;
 }
 
-static size_t distill_part_bytes(int64_t T, int64_t V) {
-  const int parts = distill_parts(T, V);
-  return parts > 1 ? ((size_t)T * parts * 2 * sizeof(float) + 255) / 256 * 256 : 0;
-}
-
-gptq_status gptq_distill_workspace_bytes(int64_t T, int64_t V, size_t* bytes) {
-  if (!bytes) return fail(GPTQ_EINVAL, "bytes is NULL");
-  const gptq_status st = distill_sizes(T, V);
-  if (st != GPTQ_OK) return st;
-  *bytes = distill_part_bytes(T, V);
-  return GPTQ_OK;
-}
-
 gptq_status gptq_distill(void* stream, const void* Z, int32_t zdt, int64_t T, int64_t V, int64_t ldz,
                          const int32_t* ids, const float* teacher, int64_t K, float temperature, int32_t log_probs,
-                         float* loss, float* lse, void* workspace, size_t ws_bytes) {
+                         float* loss, float* lse) {
   DistillArgs a;
-  gptq_status st = distill_args(Z, zdt, T, V, ldz, ids, teacher, K, temperature, log_probs, &a);
+  const gptq_status st = distill_args(Z, zdt, T, V, ldz, ids, teacher, K, temperature, log_probs, &a);
   if (st != GPTQ_OK || T == 0) return st;
   if (!loss || !lse) return fail(GPTQ_EINVAL, "NULL pointer");
-  if ((st = check_ws(workspace, ws_bytes, distill_part_bytes(T, V))) != GPTQ_OK) return st;
   a.loss = loss;
   a.lse = lse;
-  a.part_sums = workspace;
   HIP_TRY(launch_distill((hipStream_t)stream, a), "distill");
   return GPTQ_OK;
 }

@@ -117,9 +117,8 @@ def load():
                               c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, ctypes.c_int32, ctypes.c_int32,
                               ctypes.c_int32, ctypes.c_int32, c_vp, ctypes.c_int32, c_i64, c_vp, ctypes.c_int32, c_i64,
                               c_vp, c_sz],
-        "gptq_distill_workspace_bytes": [c_i64, c_i64, ctypes.POINTER(c_sz)],
         "gptq_distill": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, ctypes.c_float,
-                         ctypes.c_int32, c_vp, c_vp, c_vp, c_sz],
+                         ctypes.c_int32, c_vp, c_vp],
         "gptq_distill_grad": [c_vp, c_vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, ctypes.c_float,
                               ctypes.c_int32, c_vp, c_vp, c_vp, ctypes.c_int32, c_i64],
         "gptq_eora_workspace_bytes": [c_i64, c_i64, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(c_sz)],
@@ -776,7 +775,7 @@ def _teacher(Z, ids, teacher):
             _dense(teacher, "teacher", torch.float32, Z.device, (T, K)), K)
 
 
-def distill(Z, ids, teacher, temperature=1.0, log_probs=False, workspace=None):
+def distill(Z, ids, teacher, temperature=1.0, log_probs=False):
     """(loss, lse), both T fp32: the divergence of softmax(Z / temperature)
     (Z: T x V, bf16 or fp32) from the teacher's distribution over the K entries
     ids (T x K int32; ids outside [0, V) do not count). teacher (T x K fp32):
@@ -784,12 +783,10 @@ def distill(Z, ids, teacher, temperature=1.0, log_probs=False, workspace=None):
     probabilities as they are."""
     lib = load()
     args = _teacher(Z, ids, teacher)
-    T, V, dev = args[2], args[3], Z.device
+    T, dev = args[2], Z.device
     loss = torch.empty_strided((T,), (1,), dtype=torch.float32, device=dev)
     lse = torch.empty_strided((T,), (1,), dtype=torch.float32, device=dev)
-    need = _bytes("gptq_distill_workspace_bytes", T, V)
-    ws, wsp = _scratch(need, dev, workspace)
-    _call(dev, lib.gptq_distill, *args, temperature, int(bool(log_probs)), loss.data_ptr(), lse.data_ptr(), wsp, need)
+    _call(dev, lib.gptq_distill, *args, temperature, int(bool(log_probs)), loss.data_ptr(), lse.data_ptr())
     return loss, lse
 
 

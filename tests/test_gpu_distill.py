@@ -7,8 +7,8 @@ Tolerances, with u = 2^-24 (half a step of fp32, relative) and 2^-8 for bf16:
    sums and at most V additions of positive values: l is off by
    (3 A + 4 + depth) u relatively, where A is the largest exponent that counts
    (terms below exp(-A) of the largest add less than u for A = 30), and depth
-   the additions in one chain, at most V / 256 + 64. lse: that, plus 4 u of its
-   own magnitude and of m / tau.
+   the additions in one chain, at most V / 256 + 64 (one row's threads are 256
+   or 1024). lse: that, plus 4 u of its own magnitude and of m / tau.
  * p: exponents off by 4 u of their magnitude P, sums of K terms: (4 P + K / 256 +
    20) u relatively; log p: 4 u (P + log K + 1).
  * loss: sum over p (log p - log q) of the factors' errors, and K / 256 + 16
@@ -105,8 +105,8 @@ def check(Z, ids, teacher, grad, temp, logp, odt, out=None):
 
 CASES = [   # T, V, K, temperature, log probabilities
     (1, 1, 1, 1.0, False), (1, 7, 3, 2.0, True), (3, 8, 8, 1.0, False), (5, 9, 4, 0.5, False), (2, 255, 17, 1.0, True),
-    (4, 2047, 300, 4.0, False), (7, 2049, 64, 1.0, False), (3, 8193, 256, 3.0, True),     # parts of a row
-    (1, 50001, 1, 1.0, False), (2, 33333, 1024, 1.0, True), (1030, 1000, 5, 2.0, False),  # one part a row
+    (4, 2047, 300, 4.0, False), (7, 2049, 64, 1.0, False), (3, 8193, 256, 3.0, True),     # 1024 threads, parts of the gradient's
+    (1, 50001, 1, 1.0, False), (2, 33333, 1024, 1.0, True), (1030, 1000, 5, 2.0, False),  # 256 threads a row
     (1024, 2304, 2, 1.0, False), (40, 5000, 257, 1.5, False),
 ]
 
@@ -229,7 +229,7 @@ def test_rows_beyond_32_bits():
     teacher = torch.randn(T, 3, generator=g, device="cuda")
     grad = torch.rand(T, generator=g, device="cuda")
     loss, lse = G.distill(Z, ids, teacher)
-    part = slice(T - 1100, T)                              # as many rows: the same number of parts each
+    part = slice(T - 1100, T)                              # enough rows for the same code
     l2, e2 = G.distill(Z[part].clone(), ids[part], teacher[part])
     assert torch.equal(loss[part], l2) and torch.equal(lse[part], e2)
     d2 = G.distill_grad(Z[part].clone(), ids[part], teacher[part], e2, grad[part])
@@ -269,7 +269,7 @@ def test_captured_step_replays(T):
 
 
 def test_two_streams_at_once():
-    """Calls on two streams with workspaces of their own do not meet."""
+    """Calls on two streams do not meet."""
     sets = [inputs(s, 4, 40000, 8, False, F32) for s in (1, 2)]
     want = []
     for Z, ids, teacher, grad in sets:
