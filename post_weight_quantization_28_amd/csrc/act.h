@@ -34,8 +34,14 @@ __device__ __forceinline__ float act_both(int act, float z, float& slope) {
       slope = z > 0.f ? 1.f : (z == z ? 0.f : z);
       return z < 0.f ? 0.f : z;
     case GPTQ_ACT_GELU: {
-      const float p = normal_cdf(z);
-      slope = fmaf(c * 0.3989422804014327f, __expf(-0.5f * c * c), p);
+      // Phi(-|z|) = erfc(|z| / sqrt 2) / 2 by formula 7.1.26 of Abramowitz and
+      // Stegun (erfc within 1.5e-7), which shares its exponential with the slope
+      const float a = fabsf(c), e = __expf(-0.5f * a * a);
+      const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678118654752f, a, 1.f));
+      const float q = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                               0.254829592f);
+      const float tail = 0.5f * q * e, p = z < 0.f ? tail : 1.f - tail;
+      slope = fmaf(c * 0.3989422804014327f, e, p);
       return z * p;
     }
     case GPTQ_ACT_GELU_TANH: {

@@ -170,8 +170,19 @@ k_layer_down(LayerArgs a) {
   __shared__ uint16_t te[kLyMax], trows[kLyMax], tfirst[kLyMax], slot[kLyMax], place[kLyMax];
   __shared__ __align__(16) uint8_t smem[WAVES][MvWave<BITS, WIDE, 1, NP, TILE>::BYTES];
   extern __shared__ float part[];                        // [part of K][place][column]
+  __shared__ float weight[kLyMax];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15;
+  const int64_t o0 = (int64_t)blockIdx.x * 16;
   int tiles, places;
+  // what the end needs of memory: asked for now
+  for (int i = tid; i < a.slots; i += 64 * WAVES) weight[i] = a.w ? a.w[i] : 1.f;
+  auto residual = [&](int i) {
+    const int64_t at = (int64_t)(i >> 4) * a.ldr + o0 + (i & 15);
+    if (!a.res || i >= a.T * 16 || o0 + (i & 15) >= a.n) return 0.f;
+    return a.res_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.res)[at] << 16)
+                      : static_cast<const float*>(a.res)[at];
+  };
+  const float first_res = residual(tid);
   if (a.T == 1) {
     tiles = places = a.k;
     for (int i = tid; i < a.k; i += 64 * WAVES) {
@@ -203,7 +214,6 @@ k_layer_down(LayerArgs a) {
     }
   }
   __syncthreads();
-  const int64_t o0 = (int64_t)blockIdx.x * 16;
   const int kp = tiles >= WAVES || tiles == 0 ? 1 : WAVES / tiles;
   const bool vec = mv_vec(a.down.scales, a.down.zeros, a.d, a.group);
   for (int i = wave; i < tiles * kp; i += WAVES) {
@@ -233,13 +243,9 @@ k_layer_down(LayerArgs a) {
       float v = 0.f;
       for (int p = 0; p < kp; ++p) v += part[(p * places + at) * 16 + c];
       if (a.b2) v += a.b2[a.ids[t * a.ldi + j] * a.n + o];
-      y = fmaf(a.w ? a.w[s] : 1.f, v, y);
+      y = fmaf(weight[s], v, y);
     }
-    if (a.res) {
-      const int64_t at = t * a.ldr + o;
-      y += a.res_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.res)[at] << 16)
-                      : static_cast<const float*>(a.res)[at];
-    }
+    y += i == tid ? first_res : residual(i);
     store_out(a.Y, a.y_bf16, t * a.ldy + o, y);
   }
 }

@@ -292,9 +292,9 @@ hipError_t launch_linear(hipStream_t s, const LinearArgs& a) {
 // ---------------------------------------------------------------- gradient
 // dZ and the partial sums of dbias, bound by their bytes. A workgroup owns
 // kLgRows rows of one segment and 256 columns of dY: 32 lanes of eight
-// columns side by side, eight rows at a time. Its column sums go to
+// columns side by side, eight rows side by side. Its column sums go to
 // part[tile][m], and a second launch adds a segment's tiles in their order.
-constexpr int kLgRows = 64;
+constexpr int kLgRows = 32;
 
 // Row tiles of all segments, an upper bound known to the host.
 static int64_t li_tiles(int64_t R, int E) { return std::min<int64_t>(R, ceil_div(R, kLgRows) + E - 1); }
@@ -370,9 +370,10 @@ __device__ __forceinline__ void li_store8(uint16_t* p, int have, const float (&f
 template <int ACT, bool YBF, bool ZBF, bool GATED>
 __device__ __forceinline__ void li_dz(const LinearGradArgs& a, int r0, int r1, int64_t c, int have, float (&sg)[8],
                                       float (&su)[8]) {
-  constexpr int U = 2;                                     // rows on their way
+  constexpr int U = kLgRows / 8;                           // rows of a lane, all on their way at once
   const int rl = threadIdx.x >> 5;
-  for (int r = r0 + rl; r < r1; r += 8 * U) {
+  const int r = r0 + rl;
+  {
     float dy[U][8], z[U][8], u[U][8];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
