@@ -439,7 +439,8 @@ gptq_status gptq_checkpoint_weight_grad(void *stream, const void *P, int32_t pdt
  *   dX[p] = dZ[p] W_hat_e                                    (R x n, dxdt)
  * dZ (R x m bf16, row pitch lddz) is rounded to bf16 once, which is what the
  * matrix product takes, and is also P of gptq_checkpoint_weight_grad; dbias sums
- * its values before that rounding, in a fixed order. NULL dbias: not wanted. With
+ * its values before that rounding, in a fixed order (NULL: not wanted; at most
+ * 2^30 - 128 of them an expert). With
  * GPTQ_ACT_NONE and no gate Z is not read and may be NULL, and if dY is bf16 dZ
  * may be NULL too (the product then takes dY). The residual's gradient is dY, the
  * gradient of X by token is gptq_combine of dX. dX takes the weights as

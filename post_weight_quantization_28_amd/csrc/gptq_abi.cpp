@@ -1342,6 +1342,7 @@ gptq_status gptq_linear_grad(void* stream, const void* dY, int32_t dydt, int64_t
           m, n, bits, group, dX, dxdt == GPTQ_BF16, ldx, workspace};
   if (R > 0 && (st = expert_weights_check(a.mm, 1)) != GPTQ_OK) return st;
   if (linear_grad_threads(R, (int)E, d) > kMaxThreads) return fail(GPTQ_EINVAL, "R d is too large for one launch");
+  if (dbias && ceil_div(m, 64) * 256 > kMaxThreads) return fail(GPTQ_EINVAL, "dbias is too wide for one launch");
   if ((st = check_ws(workspace, ws_bytes, need)) != GPTQ_OK) return st;
   a.dY = dY;
   a.dy_bf16 = dydt == GPTQ_BF16;

@@ -7,8 +7,11 @@
 // Forward: the kernels of the experts' products with what stands behind the
 // product at their end, where the sums are in registers. It costs the bytes of
 // the residual and of the kept z, against writing and reading R x m fp32 sums in
-// a launch of its own. Only where K is in parts (few tiles) is it a launch of its
-// own, which adds the parts.
+// a launch of its own (captured: 2048 rows of 4096 x 11008 gated 484 to 395 us,
+// 4084 rows over 32 experts of 2048 x 1408 gated with z kept 157 to 133, one token
+// of 4096 x 4096 with four waves 17.1 to 15.3). Only where K is in parts (few
+// tiles) is it a launch of its own, which adds the parts (48 rows of 11008: 5.4 of
+// 27 us).
 #include "act.h"
 #include "common.h"
 #include "expert_tiles.h"
@@ -158,12 +161,11 @@ struct LinearEnd {
 };
 
 // Few rows: the matrix-vector form (MvWave), 32 packed rows (16 pairs when
-// gated) of up to TILE rows of X. (16 rows and 8 waves where workgroups are few:
-// 4096 x 4096 for one token 15.3 us captured either way.)
-template <int BITS, bool WIDE, bool GATED, int TILE>
-__global__ void __launch_bounds__(256, 4)
+// gated) of up to TILE rows of X.
+template <int BITS, bool WIDE, bool GATED, int TILE, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, 4)
 k_linear_mv(ExArgs p, LinearEnd<GATED> finish) {
-  constexpr int OB = 2, WAVES = 4, COLS = GATED ? 16 : 32;   // outputs
+  constexpr int OB = 2, COLS = GATED ? 16 : 32;            // outputs
   __shared__ __align__(16) uint8_t smem[WAVES][MvWave<BITS, WIDE, OB, 1, TILE>::BYTES];
   __shared__ float red[WAVES][OB][4][64];
   const Seg sg = find_tile(p.offsets, p.E, p.R, TILE, blockIdx.y);
@@ -200,14 +202,14 @@ k_linear_mv(ExArgs p, LinearEnd<GATED> finish) {
   }
 }
 
-// K in parts: their sums in order, and what follows.
+// K in parts: their sums in order, and what follows. (Parts are of few tiles: at
+// most 2^14 rows.)
 template <bool GATED>
 __global__ void __launch_bounds__(256)
 k_linear_end(const float* __restrict__ part, int splits, int64_t m, const int32_t* __restrict__ offsets, int E, int R,
              LinearEnd<GATED> finish) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, d = finish.d;
-  const int64_t row = i / (uint32_t)d, o = i - row * d;
-  if (row >= R || (offsets && (row < offsets[0] || row >= offsets[E]))) return;
+  const int64_t row = blockIdx.y, o = (int64_t)blockIdx.x * 256 + threadIdx.x, d = finish.d;
+  if (o >= d || (offsets && (row < offsets[0] || row >= offsets[E]))) return;
   const int e = finish.bias && offsets ? li_expert(offsets, E, row) : 0;
   float z[2] = {0.f, 0.f};
 #pragma unroll
@@ -220,11 +222,17 @@ size_t linear_workspace(int64_t R, int E, int64_t n, int64_t m, int group) {
   return expert_split(R, E, n, m, group, 0, false).part_bytes;
 }
 
+// Eight waves share K where workgroups are few: 4096 x 4096 for one token (128
+// workgroups) 9.0 us with four waves, 7.8 with eight, 11008 x 4096 (344) 11.6 and
+// 10.5, gated (688) 17.5 and 18.9 captured.
 template <int BITS, bool WIDE, bool GATED, int TILE>
 static void linear_mv(hipStream_t s, const LinearArgs& a) {
   const ExArgs p = ex_args(a.mm, TILE, 1, 1);
-  hipLaunchKernelGGL((k_linear_mv<BITS, WIDE, GATED, TILE>), dim3((unsigned)ceil_div(a.d, GATED ? 16 : 32), (unsigned)p.nrt),
-                     dim3(256), 0, s, p, LinearEnd<GATED>(a));
+  const dim3 grid((unsigned)ceil_div(a.d, GATED ? 16 : 32), (unsigned)p.nrt);
+  if ((int64_t)grid.x * std::min<int64_t>(p.nrt, a.mm.R) <= 512)
+    hipLaunchKernelGGL((k_linear_mv<BITS, WIDE, GATED, TILE, 8>), grid, dim3(512), 0, s, p, LinearEnd<GATED>(a));
+  else
+    hipLaunchKernelGGL((k_linear_mv<BITS, WIDE, GATED, TILE, 4>), grid, dim3(256), 0, s, p, LinearEnd<GATED>(a));
 }
 
 template <int BITS, bool GATED, class TL, bool G128>
@@ -265,7 +273,7 @@ static hipError_t linear_go(hipStream_t s, const LinearArgs& a) {
     e.parts_only = true;
     const hipError_t err = launch_expert_mm(s, e);
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(k_linear_end<GATED>, dim3((unsigned)ceil_div(e.R * a.d, 256)), dim3(256), 0, s,
+    hipLaunchKernelGGL(k_linear_end<GATED>, dim3((unsigned)ceil_div(a.d, 256), (unsigned)e.R), dim3(256), 0, s,
                        static_cast<const float*>(a.ws), sp.splits, e.d_out, e.offsets, e.E, e.R, LinearEnd<GATED>(a));
     return hipGetLastError();
   }
@@ -294,6 +302,9 @@ hipError_t launch_linear(hipStream_t s, const LinearArgs& a) {
 // kLgRows rows of one segment and 256 columns of dY: 32 lanes of eight
 // columns side by side, eight rows side by side. Its column sums go to
 // part[tile][m], and a second launch adds a segment's tiles in their order.
+// 4096 rows of 11008 with gelu 67 us (270 MB, 55 us at the rate of a copy), 1934
+// of 2 x 1408 with silu 14.6; with 64 rows, two on their way at a time, and
+// erfcf 93 and 21.
 constexpr int kLgRows = 32;
 
 // Row tiles of all segments, an upper bound known to the host.

@@ -381,6 +381,69 @@ def test_captured_step_replays(T):
         step(X[1])
 
 
+def test_a_tuning_step_end_to_end():
+    """An MLP of packed layers under a distillation loss, as a tuning step runs it:
+    linear (gated, z kept), linear (bias, residual), a packed head, distill, and
+    back. Every output against the oracle on the same inputs as the call had, and
+    the loss' change along the final gradient against the gradient's own length."""
+    T, n, d, V, K, group = 50, 128, 96, 352, 7, 32
+    up, down, head = fast_layers(1, 1, 2 * d, n, 4, group), fast_layers(2, 1, n, d, 4, group), fast_layers(3, 1, V, n, 4, group)
+    pu, pd, ph = cuda_layers(*up), cuda_layers(*down), cuda_layers(*head)
+    off = [0, T]
+    r = np.random.default_rng(9)
+    X = values(1, T, n, scale=0.3)
+    bias = torch.from_numpy(r.standard_normal((1, n)).astype(np.float32)).cuda()
+    ids = torch.from_numpy(np.stack([r.choice(V, K, replace=False) for _ in range(T)]).astype(np.int32)).cuda()
+    teacher = torch.from_numpy((2 * r.standard_normal((T, K))).astype(np.float32)).cuda()
+    g = torch.full((T,), 1.0 / T, device="cuda")
+    h, z = G.linear(X, *pu, 4, group, act="silu", gated=True, keep=BF16)
+    y = G.linear(h, *pd, 4, group, bias=bias, residual=X)
+    logits = G.linear(y, *ph, 4, group, out_dtype=F32)
+    loss, lse = G.distill(logits, ids, teacher)
+    dl = G.distill_grad(logits, ids, teacher, lse, g, out_dtype=BF16)
+    dy, _, _ = G.linear_grad(dl, None, *ph, 4, group, n)
+    dh, _, db = G.linear_grad(dy, None, *pd, 4, group, d, want_bias=True)
+    dx, dz, _ = G.linear_grad(dh, z, *pu, 4, group, n, act="silu", gated=True)
+
+    def forward(x):
+        hh, zz = L64.linear(x, off, *up, 4, group, "silu", True, np.zeros((T, d)), np.zeros((T, 2 * d)))
+        yy, _ = L64.linear(hh, off, *down, 4, group, "none", False, np.zeros((T, n)), np.zeros((T, n)), arr(bias), x)
+        ll, _ = L64.linear(yy, off, *head, 4, group, "none", False, np.zeros((T, V)), np.zeros((T, V)))
+        return hh, zz, yy, ll, L64.distill(ll, ids.cpu().numpy(), arr(teacher), 1.0, False)
+    x64 = arr(X)
+    hh, zz, yy, ll, (l64, e64, ps) = forward(x64)
+    # what rounding h, z and y to bf16 may do downstream: 2^-8 of the magnitudes that the weights add up
+    Wd, Wh = np.abs(dequantize(down[0][0], down[1][0], down[2][0], 4, group, d)), np.abs(dequantize(head[0][0], head[1][0], head[2][0], 4, group, n))
+    eh = 1.01 * UBF * np.abs(hh) + 1e-5 * (1 + np.abs(hh))
+    assert np.all(np.abs(arr(h) - hh) <= eh) and np.all(np.abs(arr(z) - zz) <= 1.01 * UBF * np.abs(zz) + 1e-5)
+    ey = 1.01 * (eh @ Wd.T) + 1.01 * UBF * np.abs(yy) + 1e-5 * (1 + np.abs(yy))
+    assert np.all(np.abs(arr(y) - yy) <= ey)
+    el = 1.01 * (ey @ Wh.T) + 1e-4
+    assert np.all(np.abs(arr(logits) - ll) <= el)
+    # a loss and its lse change by at most twice and once the largest change of a row's logits
+    assert np.all(np.abs(arr(lse) - e64) <= el.max(1) + 1e-5) and np.all(np.abs(arr(loss) - l64) <= 2 * el.max(1) + 1e-5)
+    # the way back, each call on what it was given
+    got_l = arr(logits)
+    _, e2, p2 = L64.distill(got_l, ids.cpu().numpy(), arr(teacher), 1.0, False)
+    ref = L64.distill_grad(got_l, e2, p2, arr(g), 1.0)
+    assert np.all(np.abs(arr(dl) - ref) <= 1.01 * UBF * np.abs(ref) + 1e-5 / T)
+    for got, grad, zin, packed, width, name, gated in ((dy, dl, None, head, n, "none", False), (dh, dy, None, down, d, "none", False),
+                                                       (dx, dh, z, up, n, "silu", True)):
+        m = packed[0].shape[1]
+        rx, rz, rb = L64.linear_grad(arr(grad), None if zin is None else arr(zin), off, *packed, 4, group, width, name, gated,
+                                     np.zeros((T, m)), np.zeros((T, width)))
+        W = np.abs(dequantize(packed[0][0], packed[1][0], packed[2][0], 4, group, width))
+        assert np.all(np.abs(arr(got) - rx) <= (2 * UBF + 1e-4) * (np.abs(rz) @ W) + UBF * np.abs(rx) + 1e-12)
+    assert np.all(np.abs(arr(db)[0] - arr(dy).sum(0)) <= (T + 4) * U32 * np.abs(arr(dy)).sum(0))
+    # along the gradient (with the residual's share) the oracle's loss changes by its squared length
+    full = arr(dx) + arr(dy)
+    step = 1e-3 / np.abs(full).max()
+    diff = (forward(x64 + step * full)[4][0].mean() - forward(x64 - step * full)[4][0].mean()) / (2 * step)
+    length = float((full * full).sum())
+    # the chain's roundings: six at most, 2^-8 each of magnitudes that add up to several times the gradient's own
+    assert abs(diff - length) <= 0.05 * length
+
+
 def test_linear_binding_refusals():
     qw, sc, zr = cuda_layers(*fast_layers(1, 2, 64, 64, 4, 32))
     X, off = values(1, 6, 64), torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")

@@ -179,6 +179,9 @@ def test_linear_refusals():
                 dict(dZ=NULL), dict(dX=NULL), dict(qw=odd), dict(dY=one), dict(Z=one), dict(dZ=one), dict(db=one),
                 dict(R=-1), dict(R=2 ** 31), dict(act=9), dict(gated=-1), dict(act=0, gated=0, dZ=NULL, dydt=1)):
         assert bwd(**bad) == -1, bad
+    wide = 2 ** 30 + 64                                           # dbias' launch; the product takes as many without it
+    assert bwd(R=0, E=1, off=NULL, d=wide, gated=0) == -1
+    assert bwd(R=2 ** 29, E=1, off=NULL, d=2 ** 16, ldy=2 ** 16, ldz=2 ** 17, lddz=2 ** 17) == -1   # rows times columns
     assert bwd() == -5 and bwd(ws=odd, wsb=1 << 30) == -5         # the bias' partial sums need a workspace
     out = ctypes.c_size_t(0)
     for need in (lib.gptq_linear_workspace_bytes, lib.gptq_linear_grad_workspace_bytes):
