@@ -239,10 +239,10 @@ __device__ __forceinline__ void run_stages(int nst, F&& stage) {
 
 // ---- forward: K = n. The codes minus the zero point are exact in bf16, the
 // group's sum is scaled once in fp32 (tot += s acc), as in the one-layer
-// product. G128: groups of 128, two stages each (the first product of a group
-// starts from zero, no test inside a stage); otherwise groups of any number of
-// 32-code chunks, tested after every chunk.
-template <int BITS, class TL, bool G128, class END>
+// product. GS: stages of a group where groups are whole stages, 1 (64 codes) or 2
+// (the first product of a group starts from zero, no test inside a stage);
+// 0: groups of any number of 32-code chunks, tested after every chunk.
+template <int BITS, class TL, int GS, class END>
 __global__ void __launch_bounds__(TL::THREADS, 512 / TL::THREADS)
 k_expert_mm(ExArgs p, END finish) {
   constexpr int MI = TL::MI, NI = TL::NI, BM = TL::BM, PA = TL::PA, NB = TL::NB, THREADS = TL::THREADS;
@@ -287,7 +287,7 @@ k_expert_mm(ExArgs p, END finish) {
   auto bload = [&](auto S, int st) {
     const int c = min(2 * (s0 + st) + bu / 4, nchunks - 1);      // a chunk past the end meets zeros of A
     rb[S % DB].load(qrow, 4 * c + bu % 4);
-    const int g = G128 ? (s0 + st) >> 1 : c / cpg;
+    const int g = GS == 2 ? (s0 + st) >> 1 : (GS == 1 ? min(s0 + st, (int)ngroups - 1) : c / cpg);
     rz[S % DB] = zrow[g];
   };
   auto awrite = [&](auto S, int st) {
@@ -365,9 +365,9 @@ k_expert_mm(ExArgs p, END finish) {
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni)
           acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              fa[kk & 1][mi], fb[kk & 1][ni], G128 && b == 0 && kk == 0 ? zero : acc[mi][ni], 0, 0, 0);
+              fa[kk & 1][mi], fb[kk & 1][ni], GS > 0 && kk == 0 && (GS == 1 || b == 0) ? zero : acc[mi][ni], 0, 0, 0);
       bwrite(next, KK);
-      if (!G128 && (kk & 1) == 1 && ++cin == cpg && g < ngroups) {   // the group is complete
+      if (GS == 0 && (kk & 1) == 1 && ++cin == cpg && g < ngroups) {   // the group is complete
         flush();
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi)
@@ -377,7 +377,7 @@ k_expert_mm(ExArgs p, END finish) {
       }
     });
     awrite(next, st + 1);
-    if (G128 && b == 1) flush();
+    if (GS == 1 || (GS == 2 && b == 1)) flush();
   };
   for_four([&](auto S) {
     if constexpr (S < DA) aload(S, min((int)S, nst - 1));

@@ -920,22 +920,27 @@ static void split_go(hipStream_t s, const ExpertArgs& a, ExArgs p, int64_t cols,
                        a.ldy);
 }
 
-template <int BITS, class TL, bool G128>
+template <int BITS, class TL, int GS>
 static void mm_go(hipStream_t s, const ExpertArgs& a) {
   split_go(s, a, ex_args(a, TL::BM, TL::BN, a.d_out), a.d_out, 0, [&](dim3 grid, const ExArgs& p) {
-    hipLaunchKernelGGL((k_expert_mm<BITS, TL, G128, NoEnd>), grid, dim3(TL::THREADS), 0, s, p, NoEnd{});
+    hipLaunchKernelGGL((k_expert_mm<BITS, TL, GS, NoEnd>), grid, dim3(TL::THREADS), 0, s, p, NoEnd{});
   });
 }
 
 // Groups of 128 are worth their own code at 4 bits, the common layer: 8 experts
 // of 4096 x 4096 with 32, 96, 200 and 400 rows each 51, 71, 121 and 183 us, in
-// the code for any group 56, 77, 135 and 196.
+// the code for any group 56, 77, 135 and 196. Groups of 64 in 64-row tiles: 96
+// rows each 75 and 86; in 128-row tiles their code spills (119 to 195 us for 4096
+// rows over 64 experts of 1408 x 2048).
 template <int BITS, class TL>
 static void mm_group(hipStream_t s, const ExpertArgs& a) {
   if constexpr (BITS == 4) {
-    if (a.group == 128) return mm_go<4, TL, true>(s, a);
+    if (a.group == 128) return mm_go<4, TL, 2>(s, a);
+    if constexpr (TL::BM == 64) {
+      if (a.group == 64) return mm_go<4, TL, 1>(s, a);
+    }
   }
-  mm_go<BITS, TL, false>(s, a);
+  mm_go<BITS, TL, 0>(s, a);
 }
 
 template <int BITS, int NP, class TL, bool WIDE>

@@ -235,21 +235,24 @@ static void linear_mv(hipStream_t s, const LinearArgs& a) {
     hipLaunchKernelGGL((k_linear_mv<BITS, WIDE, GATED, TILE, 4>), grid, dim3(256), 0, s, p, LinearEnd<GATED>(a));
 }
 
-template <int BITS, bool GATED, class TL, bool G128>
+template <int BITS, bool GATED, class TL, int GS>
 static void linear_tiles(hipStream_t s, const LinearArgs& a) {
   static_assert(TL::WM * TL::WN * LinearEnd<GATED>::LDS <= 2 * (TL::BM + TL::BN) * 128, "the blocks fit the tiles' LDS");
   ExArgs p = ex_args(a.mm, TL::BM, TL::BN, a.mm.d_out);
   p.nct = (int)ceil_div(a.d, GATED ? TL::BN / 2 : TL::BN);
   p.per_split = (int)ceil_div(a.mm.n, kExBK);
-  hipLaunchKernelGGL((k_expert_mm<BITS, TL, G128, LinearEnd<GATED>>), tile_grid(p.nrt, p.nct), dim3(TL::THREADS), 0, s, p,
+  hipLaunchKernelGGL((k_expert_mm<BITS, TL, GS, LinearEnd<GATED>>), tile_grid(p.nrt, p.nct), dim3(TL::THREADS), 0, s, p,
                      LinearEnd<GATED>(a));
 }
 template <int BITS, bool GATED, class TL>
 static void linear_group(hipStream_t s, const LinearArgs& a) {
   if constexpr (BITS == 4) {
-    if (a.mm.group == 128) return linear_tiles<4, GATED, TL, true>(s, a);
+    if (a.mm.group == 128) return linear_tiles<4, GATED, TL, 2>(s, a);
+    if constexpr (TL::BM == 64) {
+      if (a.mm.group == 64) return linear_tiles<4, GATED, TL, 1>(s, a);
+    }
   }
-  linear_tiles<BITS, GATED, TL, false>(s, a);
+  linear_tiles<BITS, GATED, TL, 0>(s, a);
 }
 
 // 64-row tiles in which a wave has two blocks of columns.
