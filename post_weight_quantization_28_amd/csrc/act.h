@@ -34,12 +34,20 @@ __device__ __forceinline__ float act_both(int act, float z, float& slope) {
       slope = z > 0.f ? 1.f : (z == z ? 0.f : z);
       return z < 0.f ? 0.f : z;
     case GPTQ_ACT_GELU: {
-      // Phi(-|z|) = erfc(|z| / sqrt 2) / 2 by formula 7.1.26 of Abramowitz and
-      // Stegun (erfc within 1.5e-7), which shares its exponential with the slope
+      // Phi(-|z|) = erfc(|z| / sqrt 2) / 2 with an exponential that the slope needs
+      // too: exp(x^2) erfc(x) is t times a polynomial in t = 1 / (1 + 0.3925 x)
+      // within 8e-8 of itself for all x up to 46 (fitted to the least largest
+      // relative error; 4e-7 in fp32), so that the tail is as good as the middle.
       const float a = fabsf(c), e = __expf(-0.5f * a * a);
-      const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678118654752f, a, 1.f));
-      const float q = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
-                               0.254829592f);
+      const float t = __builtin_amdgcn_rcpf(fmaf(0.3925f * 0.70710678118654752f, a, 1.f));
+      float q = fmaf(t, 0.052698649466f, -0.207043841481f);
+      q = fmaf(t, q, 0.226035580039f);
+      q = fmaf(t, q, -0.043806929141f);
+      q = fmaf(t, q, 0.161438837647f);
+      q = fmaf(t, q, 0.162571072578f);
+      q = fmaf(t, q, 0.205268085003f);
+      q = fmaf(t, q, 0.221392959356f);
+      q = t * fmaf(t, q, 0.22144556046f);
       const float tail = 0.5f * q * e, p = z < 0.f ? tail : 1.f - tail;
       slope = fmaf(c * 0.3989422804014327f, e, p);
       return z * p;

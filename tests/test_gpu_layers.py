@@ -194,6 +194,27 @@ def test_linear_grad(R, E, d, n, group, cuts, name, gated, bits):
         assert np.array_equal(arr(dX)[off[-1]:], xb[off[-1]:])
 
 
+def test_gelu_in_its_tail():
+    """Below z = -2, where Phi is a small difference of the slope's terms: value
+    and slope keep their relative precision. With x = z^2 / 2 the exponential's
+    argument is off by at most 3 u of itself, the other factors by 20 u together;
+    Phi is at most a quarter of |z| phi, so their difference is off by at most
+    (1 + 1/4) / (1 - 1/4) < 2 times as much, relative to itself."""
+    from scipy.special import erfc
+    z = np.linspace(-12, -2, 4096).astype(np.float32).astype(np.float64)
+    qw, sc, zr = layers(1, 1, 8192, 32, 4, 32)
+    packed = cuda_layers(qw, sc, zr)
+    phi, cdf = np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi), 0.5 * erfc(-z / np.sqrt(2))
+    rel = UBF + 1.01 * (3 * 0.5 * z * z + 20) * U32
+    Z = torch.from_numpy(np.stack([np.concatenate([z, np.ones_like(z)])])).float().cuda()
+    dY = torch.ones((1, 4096), device="cuda")
+    _, dZ, _ = G.linear_grad(dY, Z, *packed, 4, 32, 32, act="gelu", gated=True)
+    got = arr(dZ)[0]
+    slope = cdf + z * phi
+    assert np.all(np.abs(got[:4096] - slope) <= 2 * rel * np.abs(slope))
+    assert np.all(np.abs(got[4096:] - z * cdf) <= rel * np.abs(z * cdf))
+
+
 def test_linear_grad_of_a_plain_layer_needs_no_copy():
     """No activation, no gate: dY stands for dZ, Z is not read; an fp32 dY is
     rounded into a new dZ; an expert without rows has a bias gradient of zero."""
