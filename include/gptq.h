@@ -422,10 +422,11 @@ gptq_status gptq_checkpoint_weight_grad(void *stream, const void *P, int32_t pdt
  * E x m fp32 or NULL, residual R x d (rdt, row pitch ldr) or NULL, Y R x d (ydt,
  * row pitch ldy), Z R x m (zdt, row pitch ldz) or NULL: where z is kept for
  * gptq_linear_grad. X, rows, offsets, E, R, bits, group and the kernels' numbers
- * are those of gptq_expert_matmul; the epilogue is computed in fp32 and rounded
- * once. E = 1 and offsets NULL: one dense layer. Rows from offsets[E] on are
- * neither read nor written in any matrix. Y may be the residual (same type and
- * pitch); no other output may overlap an input.
+ * are those of gptq_expert_matmul (its matrix-vector form serves up to 48 rows an
+ * expert here); the epilogue is computed in fp32 and rounded once. E = 1 and
+ * offsets NULL: one dense layer. Rows from offsets[E] on are neither read nor
+ * written in any matrix. Y may be the residual (same type and pitch); no other
+ * output may overlap an input.
  *   act: GPTQ_ACT_NONE z; _RELU max(z, 0) (NaN stays NaN); _GELU z Phi(z);
  * _GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2; _SILU z / (1 +
  * exp(-z)). Of minus infinity the last three are NaN.
@@ -440,15 +441,13 @@ gptq_status gptq_checkpoint_weight_grad(void *stream, const void *P, int32_t pdt
  * dZ (R x m bf16, row pitch lddz) is rounded to bf16 once, which is what the
  * matrix product takes, and is also P of gptq_checkpoint_weight_grad; dbias sums
  * its values before that rounding, in a fixed order (NULL: not wanted; at most
- * 2^30 - 128 of them an expert). With
- * GPTQ_ACT_NONE and no gate Z is not read and may be NULL, and if dY is bf16 dZ
+ * 2^30 - 128 of them an expert). With GPTQ_ACT_NONE and no gate Z is not read and may be NULL, and if dY is bf16 dZ
  * may be NULL too (the product then takes dY). The residual's gradient is dY, the
  * gradient of X by token is gptq_combine of dX. dX takes the weights as
  * gptq_expert_matmul_grad does: of two rounded factors, with a bf16 dX its error
  * is about 1.7 times what its own rounding gives (0.0029 against 0.0017 of it).
- * act' of relu is 0 at 0. dZ may be Z or, ungated,
- * dY (bf16, same pitch). Workspace: gptq_linear_grad_workspace_bytes.
- * Asynchronous.
+ * act' of relu is 0 at 0. dZ may be Z or, ungated, dY (bf16, same pitch).
+ * Workspace: gptq_linear_grad_workspace_bytes. Asynchronous.
  * ("El balance de errores de la inferencia de pocos bits", section 6: what a
  * fused kernel saves is the traffic between its parts.) */
 typedef enum {

@@ -687,6 +687,10 @@ k_expert_ring(ExArgs p, END finish) {
 // ---------------------------------------------------------------- host
 inline int64_t row_tiles(int64_t R, int E, int BM) { return std::min<int64_t>(R, ceil_div(R, BM) + E - 1); }
 
+inline bool bf16_rows_vec(const void* p, int64_t ld, int64_t cols) {
+  return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && cols % 8 == 0;
+}
+
 inline dim3 tile_grid(int nr, int nc) { return dim3((unsigned)(8 * ceil_div((int64_t)nr * nc, 8))); }
 
 inline ExArgs ex_args(const ExpertArgs& a, int BM, int BN, int64_t cols) {

@@ -795,10 +795,6 @@ k_keep_grad_sum(const float* __restrict__ part, int splits, int64_t count, float
 }
 
 // ---------------------------------------------------------------- host
-static bool bf16_rows_vec(const void* p, int64_t ld, int64_t cols) {
-  return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && cols % 8 == 0;
-}
-
 // The ring kernels: 4 bits, whole blocks (forward) or stages and a bf16 result
 // (gradient), offsets from the bases that fit 32 bits, tiles for half of the
 // chip at least (fewer are better split along K), and more columns than the

@@ -10,8 +10,8 @@
 // a launch of its own (captured: 2048 rows of 4096 x 11008 gated 484 to 395 us,
 // 4084 rows over 32 experts of 2048 x 1408 gated with z kept 157 to 133, one token
 // of 4096 x 4096 with four waves 17.1 to 15.3). Only where K is in parts (few
-// tiles) is it a launch of its own, which adds the parts (48 rows of 11008: 5.4 of
-// 27 us).
+// tiles) is it a launch of its own, which adds the parts (64 rows of 11008: 5.4 of
+// 32 us).
 #include "act.h"
 #include "common.h"
 #include "expert_tiles.h"
@@ -258,9 +258,32 @@ static void linear_group(hipStream_t s, const LinearArgs& a) {
 // 64-row tiles in which a wave has two blocks of columns.
 using ExTile64Pair = ExTile<1, 2, 2, 2, 4, 4>;
 
+// The matrix-vector form beyond the 16 rows an expert of the plain product. Where
+// tiles are few, 64-row tiles have K in parts, and a launch that adds these.
+// Matrix-vector form and 64-row tiles, captured, us:
+//  * four parts or more: 17, 32, 40 and 48 rows of 11008 x 4096 19.5, 20.5, 27 and
+//    29 against 28, 28, 29 and 31 (64 rows: equal), 32 gated 32 and 43; 40 rows for
+//    each of 8 experts of 1024 x 4096 21.5 and 32; groups of 64 with 24, 32 and 40
+//    rows 24, 25, 34 and 28, 28, 29
+//  * two or three: 24 rows of 28672 x 8192 72 and 77, 48 rows 100 and 82; 24 for
+//    each of 8 of 4096 x 4096 43 and 54; groups of 64 95 and 86, 55 and 58
+//  * one: 24 rows for each of 32 of 1408 x 2048 41 and 46, of 64 76 and 71 (gated
+//    135 and 121), 32 of each of 32 48 and 46
+//  * 3 bits, whose tiles are slower: 24 and 48 rows of 11008 x 4096 24, 33 and 48,
+//    51; 48 of each of 8 of 4096 x 4096 82 and 122; 47 of each of 32 of 1408 x 2048
+//    70 and 77
+static bool linear_few(const LinearArgs& a) {
+  if (!bf16_rows_vec(a.mm.A, a.mm.lda, a.mm.n)) return false;
+  const int64_t avg = ceil_div(a.mm.R, a.mm.E);
+  if (a.mm.bits == 3) return avg <= 48;
+  const int parts = expert_split(a.mm.R, a.mm.E, a.mm.n, a.mm.d_out, a.mm.group, 0, false).splits;
+  const bool wide = a.mm.group % 128 == 0;
+  return avg <= (parts >= 4 ? (wide ? 48 : 32) : parts > 1 && wide ? 24 : 16);
+}
+
 template <int BITS, bool GATED>
 static hipError_t linear_go(hipStream_t s, const LinearArgs& a) {
-  const int bm = expert_bm(a.mm, 0);
+  const int bm = linear_few(a) ? 16 : expert_bm(a.mm, 0);
   if (bm == 16) {
     const bool wide = a.mm.group % 128 == 0, low = a.mm.R <= 8 * (int64_t)a.mm.E;
     if (wide && low) linear_mv<BITS, true, GATED, 8>(s, a);

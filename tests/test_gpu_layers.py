@@ -69,6 +69,21 @@ def fast_layers(seed, E, m, n, bits, group):
     return qw, sc / 4, zr
 
 
+def linear_bound(X, off, rows, qw, sc, zr, bits, group, n, R, E):
+    """product_bound, and up to 48 rows an expert, where either may be taken, the
+    larger one of the tiles and of few rows (as counted there)."""
+    bound = product_bound(X, off, rows, qw, sc, zr, bits, group, n, R, E)
+    if bits == 4 and 16 * E < R <= 48 * E:
+        piece = 128 if group % 128 == 0 else 32
+        for e in range(len(off) - 1):
+            W = np.abs(dequantize(qw[e], sc[e], zr[e], bits, group, n))
+            S = np.repeat(np.abs(sc[e].astype(np.float64)), group, axis=1)
+            p = slice(off[e], off[e + 1])
+            x = np.abs(X[p] if rows is None else X[rows[p]])
+            bound[p] = np.maximum(bound[p], U32 * ((piece + 2) * 62 * (x @ S.T) + (n // piece + 1) * (x @ W.T)))
+    return bound
+
+
 LINEARS = [   # T, k, E, d, n, group, drop, only, gathered
     (1, 1, 1, 33, 32, 32, 0.0, None, False),         # one token, one chunk of codes
     (1, 2, 8, 96, 512, 128, 0.0, None, True),
@@ -84,6 +99,13 @@ LINEARS = [   # T, k, E, d, n, group, drop, only, gathered
     (257, 2, 3, 96, 320, 160, 0.0, [0, 2], True),    # an empty expert between two
     (30, 4, 2, 70, 2048, 128, 0.1, None, True),      # parts of K
     (90, 1, 1, 33, 4128, 32, 0.0, None, False),
+    (17, 1, 1, 70, 2048, 128, 0.0, None, False),     # few rows up to 48 an expert
+    (47, 1, 1, 161, 1280, 256, 0.0, None, False),
+    (48, 2, 3, 90, 1024, 64, 0.1, None, True),
+    (37, 2, 3, 33, 544, 32, 0.1, None, True),
+    (70, 1, 3, 4100, 384, 128, 0.0, [0, 1, 2], True),
+    (70, 1, 1, 520, 2048, 128, 0.0, None, False),    # tiles with parts of K
+    (33, 1, 1, 150, 1088, 64, 0.0, None, False),
     (1200, 1, 2, 6550, 128, 128, 0.1, None, True),   # 256-row tiles (4 bits), ungated 26 of them wide
     (1100, 1, 2, 3201, 384, 128, 0.0, None, False),  # and gated
     (700, 1, 1, 5377, 512, 256, 0.2, None, True),
@@ -108,7 +130,7 @@ def test_linear(T, k, E, d, n, group, drop, only, gathered, name, gated, bits):
     rt = torch.from_numpy(rows).cuda() if gathered else None
     seg = None if E == 1 and drop == 0 else torch.from_numpy(off).cuda()
     src = rows if gathered else None
-    bound = product_bound(arr(X), off, src, qw, sc, zr, bits, group, n, R, E)
+    bound = linear_bound(arr(X), off, src, qw, sc, zr, bits, group, n, R, E)
     live = slice(0, off[-1])
     for i, (ydt, rdt, zdt) in enumerate([(BF16, BF16, BF16), (F32, F32, F32), (BF16, None, None), (F32, BF16, None)]):
         if bits != 4 and i > 1:
