@@ -441,9 +441,10 @@ gptq_status gptq_checkpoint_weight_grad(void *stream, const void *P, int32_t pdt
  * dZ (R x m bf16, row pitch lddz) is rounded to bf16 once, which is what the
  * matrix product takes, and is also P of gptq_checkpoint_weight_grad; dbias sums
  * its values before that rounding, in a fixed order (NULL: not wanted; at most
- * 2^30 - 128 of them an expert). With GPTQ_ACT_NONE and no gate Z is not read and may be NULL, and if dY is bf16 dZ
- * may be NULL too (the product then takes dY). The residual's gradient is dY, the
- * gradient of X by token is gptq_combine of dX. dX takes the weights as
+ * 2^30 - 128 of them an expert). With GPTQ_ACT_NONE and no gate Z is not read
+ * and may be NULL, and if dY is bf16 dZ may be NULL too (the product then takes
+ * dY). The residual's gradient is dY, the gradient of X by token is gptq_combine
+ * of dX. dX takes the weights as
  * gptq_expert_matmul_grad does: of two rounded factors, with a bf16 dX its error
  * is about 1.7 times what its own rounding gives (0.0029 against 0.0017 of it).
  * act' of relu is 0 at 0. dZ may be Z or, ungated, dY (bf16, same pitch).

@@ -4,7 +4,9 @@ lazy-batch trailing updates, and code packing, in hand-written HIP kernels
 behind a C ABI (include/gptq.h); for inference, the dequantising product of a
 packed layer; and for mixtures of experts the order of tokens by expert and
 back, the packed products of the experts and their gradients, and activations
-kept in 8 bits for the weight gradient. This package is its Python binding."""
+kept in 8 bits for the weight gradient; packed layers with bias, activation,
+gate and residual and their gradient, whole layers of experts for a decoding
+step, and distillation from a teacher. This package is its Python binding."""
 from .gptq import (ACTIVATIONS, BF16, F32, Checkpoint, GPTQError, NOALLOC_SCRATCH_BYTES, QuantResult, Route, accumulate_hessian,
                    checkpoint_restore, checkpoint_save, checkpoint_weight_grad, combine, combine_grad, dequant_matmul, distill, distill_grad, expert_layer, linear, linear_grad,
                    dequant_matmul_noalloc, dispatch, eora, eora_workspace_bytes, expert_matmul, expert_matmul_grad, refine_lowrank,

@@ -424,6 +424,30 @@ def test_captured_step_replays(T):
         step(X[1])
 
 
+def test_two_streams_at_once():
+    """The same layers on two streams, whose calls have their own workspaces."""
+    E, n, d = 4, 256, 128
+    up, down = fast_layers(1, E, 2 * d, n, 4, 64), fast_layers(2, E, n, d, 4, 64)
+    pu, pd = cuda_layers(*up), cuda_layers(*down)
+    dense = cuda_layers(*fast_layers(3, 1, 70, 2048, 4, 64))
+    ids = torch.from_numpy(expert_ids(4, 6, 2, E, 0.1, None)).cuda()
+    inputs = [(values(10 + i, 6, n), values(20 + i, 70, 2048), values(30 + i, 70, 70), values(40 + i, 70, 70)) for i in range(2)]
+
+    def step(x, wide, dy, z):
+        return (G.expert_layer(x, ids, None, pu, pd, 4, 64), G.linear(wide, *dense, 4, 64, act="silu"),
+                *G.linear_grad(dy, z, *dense, 4, 64, 2048, act="silu", want_bias=True))
+
+    want = [step(*i) for i in inputs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [None, None]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = step(*inputs[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
+
+
 def test_a_tuning_step_end_to_end():
     """An MLP of packed layers under a distillation loss, as a tuning step runs it:
     linear (gated, z kept), linear (bias, residual), a packed head, distill, and
