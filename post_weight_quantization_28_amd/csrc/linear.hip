@@ -486,9 +486,11 @@ k_linear_dz(LinearGradArgs a) {
 }
 
 // A segment's tiles in four parts, each in its order, then the parts. 64 columns
-// a workgroup.
+// a workgroup. `tiles`: li_tiles, what part holds. Segments that overlap (offsets
+// that fall) may have more between them: those beyond have no sums and count for
+// nothing, and the sums of their numbers stop there, so that none leaves 32 bits.
 __global__ void __launch_bounds__(256)
-k_linear_dbias(const float* __restrict__ part, const int32_t* __restrict__ offsets, int E, int R, int64_t m,
+k_linear_dbias(const float* __restrict__ part, const int32_t* __restrict__ offsets, int E, int R, int tiles, int64_t m,
                float* __restrict__ dbias) {
   __shared__ float sums[4][64];
   const int e = blockIdx.y, lane = threadIdx.x & 63, q = threadIdx.x >> 6;
@@ -504,9 +506,10 @@ k_linear_dbias(const float* __restrict__ part, const int32_t* __restrict__ offse
       if (e0 + 64 > e) count = __shfl(nt, e - e0);
       int t = e0 + lane < e ? nt : 0;
 #pragma unroll
-      for (int i = 32; i > 0; i >>= 1) t += __shfl_xor(t, i);
-      first += t;
+      for (int i = 32; i > 0; i >>= 1) t = min(t + __shfl_xor(t, i), tiles);
+      first = min(first + t, tiles);
     }
+    count = min(count, tiles - first);
   }
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   const int per = (count + 3) / 4, end = min(count, (q + 1) * per);
@@ -541,7 +544,7 @@ hipError_t launch_linear_grad(hipStream_t s, const LinearGradArgs& a) {
   }
   if (a.dbias) {
     hipLaunchKernelGGL(k_linear_dbias, dim3((unsigned)ceil_div(a.m, 64), (unsigned)a.mm.E), dim3(256), 0, s, a.part,
-                       a.mm.offsets, a.mm.E, a.mm.R, a.m, a.dbias);
+                       a.mm.offsets, a.mm.E, a.mm.R, (int)li_tiles(a.mm.R, a.mm.E), a.m, a.dbias);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }

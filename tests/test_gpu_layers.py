@@ -391,6 +391,35 @@ def test_wrong_offsets_stay_in_bounds():
             assert torch.all(t[:5] == 3) and torch.all(t[55:] == 3) and torch.all(t[:, w:] == 3)
 
 
+@pytest.mark.parametrize("E,R,off", [
+    (4, 3200, [0, 3200, 0, 3200, 0]),                        # two segments of all rows: 200 tiles of 32 rows, sums for 103
+    (4, 50, [0, 50, 0, 50, 0]), (3, 3, [0, 3, 0, 3]),
+    (130, 2000, [0, 2000] * 65 + [0]), (70, 96, [96, 0] * 35 + [96]),
+])
+def test_overlapping_segments_have_no_sums_beyond_their_tiles(E, R, off):
+    """Offsets that fall make segments overlap, with more tiles of 32 rows between
+    them than there are sums for (min(R, R / 32 + E - 1)): those that there are count,
+    in order, and nothing is read behind them (the bytes there are NaN)."""
+    n, m, tiles = 32, 33, min(R, -(-R // 32) + E - 1)
+    packed = cuda_layers(*layers(1, E, m, n, 4, 32))
+    dY = values(1, R, m)
+    need = G.gptq._bytes("gptq_linear_grad_workspace_bytes", R, n, m, 0, E, 4, 32)
+    first, want, mag = 0, np.zeros((E, m)), np.zeros((E, m))
+    for e in range(E):
+        lo = min(max(off[e], 0), R)
+        hi = min(max(off[e + 1], lo), R)
+        count = min(-(-(hi - lo) // 32), tiles - first)
+        p = slice(lo, min(hi, lo + 32 * count))
+        want[e], mag[e] = arr(dY)[p].sum(0), np.abs(arr(dY)[p]).sum(0)
+        first += count
+        assert 0 <= count and first <= tiles and 4 * first * m <= need
+    ws = torch.full((need + (1 << 20),), 255, dtype=torch.uint8, device="cuda")
+    _, _, db = G.linear_grad(dY, None, *packed, 4, 32, n, offsets=torch.tensor(off, dtype=torch.int32, device="cuda"),
+                             want_bias=True, workspace=ws[:need])
+    assert np.all(np.abs(arr(db) - want) <= U32 * (R / 8 + R / 64 + 12) * mag)
+    assert torch.all(ws[need:] == 255)
+
+
 @pytest.mark.parametrize("T", [4, 600])
 def test_captured_step_replays(T):
     """Forward and backward in a captured graph, replayed on changing inputs
