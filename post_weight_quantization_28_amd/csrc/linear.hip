@@ -272,8 +272,12 @@ using ExTile64Pair = ExTile<1, 2, 2, 2, 4, 4>;
 //  * 3 bits, whose tiles are slower: 24 and 48 rows of 11008 x 4096 24, 33 and 48,
 //    51; 48 of each of 8 of 4096 x 4096 82 and 122; 47 of each of 32 of 1408 x 2048
 //    70 and 77
+// Eight threads a packed row here, two in the tiles: beyond 2^29 rows only the
+// tiles' launch has fewer than 2^32.
+constexpr int64_t kMvMaxBlocks = (((int64_t)1 << 32) - 512) / 256;
 static bool linear_few(const LinearArgs& a) {
   if (!bf16_rows_vec(a.mm.A, a.mm.lda, a.mm.n)) return false;
+  if (ceil_div(a.mm.d_out, 32) > kMvMaxBlocks) return false;
   const int64_t avg = ceil_div(a.mm.R, a.mm.E);
   if (a.mm.bits == 3) return avg <= 48;
   const int parts = expert_split(a.mm.R, a.mm.E, a.mm.n, a.mm.d_out, a.mm.group, 0, false).splits;

@@ -298,6 +298,25 @@ def test_linear_at_any_alignment():
             assert torch.all(wz[:, :2] == 7) and torch.all(wz[:, 2 + m:] == 7)
 
 
+def test_more_packed_rows_than_the_matrix_vector_form_has_threads_for():
+    """17 rows at 3 bits go by that form, eight threads a packed row, while they
+    are below 2^32: 2^29 + 64 packed rows go in tiles."""
+    m, n, R = 2 ** 29 + 64, 32, 17
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    qw = torch.randint(-2 ** 31, 2 ** 31 - 1, (1, m, 3), generator=g, device="cuda", dtype=torch.int32)
+    sc = torch.rand((1, m, 1), generator=g, device="cuda") + 0.5
+    zr = torch.randint(0, 8, (1, m, 1), generator=g, device="cuda", dtype=torch.uint8)
+    X = values(1, R, n)
+    Y = G.linear(X, qw, sc, zr, 3, 32)
+    for at in (slice(0, 200), slice(2 ** 28 - 100, 2 ** 28 + 100), slice(m - 200, m)):
+        w = [t[:, at].cpu().numpy() for t in (qw, sc, zr)]
+        w[0] = w[0].view(np.uint32)
+        ref = arr(X) @ dequantize(w[0][0], w[1][0], w[2][0], 3, 32, n).T
+        e = product_bound(arr(X), [0, R], None, *w, 3, 32, n, R, 1)
+        assert np.all(np.abs(arr(Y[:, at]) - ref) <= e + last(BF16, np.abs(ref) + e))
+
+
 def test_nonfinite_activations_stay_in_their_rows():
     for R in (6, 60, 400):
         X = values(R, R, 128)
