@@ -534,7 +534,11 @@ gptq_status gptq_expert_layer(void *stream, const void *X, int32_t xdt, int64_t 
  * gptq_distill gave it,
  *   dZ[t][v] = grad[t] / temperature (M q_v - sum over k with ids = v of p_k)
  * (T x V, dzdt bf16 or fp32, row pitch ldd; an id that stands more than once in
- * a row counts each time). dZ may be Z (same type and pitch). Neither needs a
+ * a row counts each time). dZ may be Z (same type and pitch). What fp32 rounds
+ * off lse is relative in q: rows whose lse is beyond +-128 (2048 where dZ is
+ * bf16) form their sum anew and read their logits twice, so that it stays below
+ * 2^-18 (2^-14); a row of lowest values is the uniform distribution here as in
+ * the loss. Neither needs a
  * workspace; both are asynchronous; T == 0 enqueues nothing. T may be at most 2^24 - 2.
  * ("Resumen Técnico: GPTQ-intrinsic LoRA", "Declaración del Problema": the
  * low-rank factors beside the quantized layer, which tuning moves.) */

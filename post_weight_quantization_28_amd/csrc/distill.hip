@@ -189,21 +189,12 @@ __device__ __forceinline__ void di_finish(const DistillArgs& a, int64_t row, DiS
   }
 }
 
+// The sum of a row, in every thread (sums: one per wave, in LDS).
 template <bool BF, int THREADS>
-__global__ void __launch_bounds__(THREADS)
-k_distill(DistillArgs a) {
+__device__ __forceinline__ DiSum di_row_sum(const char* z, int cols, float inv_temp, DiSum* sums) {
   constexpr int P = DiType<BF>::P, U = 4, WAVES = THREADS / 64;
-  __shared__ float red[WAVES];
-  __shared__ DiSum sums[WAVES];
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x, cols = (int)a.V, np = cols / P;
-  const char* z = static_cast<const char*>(a.Z) + row * a.ldz * DiType<BF>::BYTES;
-  const float c = kLog2e * a.inv_temp;
-  DiTeacher<THREADS> te;
-  float zt[te.PER];                                // the student's logits at the teacher's entries
-  di_load_teacher<THREADS>(a, row, te);
-#pragma unroll
-  for (int i = 0; i < te.PER; ++i) zt[i] = te.id[i] >= 0 ? di_load1<BF>(z, te.id[i]) : 0.f;
+  const int tid = threadIdx.x, np = cols / P;
+  const float c = kLog2e * inv_temp;
   DiSum s = {-INFINITY, 0.f};
   auto take = [&](const float* f, int n) {
     float m = s.m;
@@ -243,6 +234,22 @@ k_distill(DistillArgs a) {
   s = sums[0];
 #pragma unroll
   for (int w = 1; w < WAVES; ++w) s = di_join(s, sums[w], c);
+  return s;
+}
+
+template <bool BF, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+k_distill(DistillArgs a) {
+  __shared__ float red[THREADS / 64];
+  __shared__ DiSum sums[THREADS / 64];
+  const int64_t row = blockIdx.x;
+  const char* z = static_cast<const char*>(a.Z) + row * a.ldz * DiType<BF>::BYTES;
+  DiTeacher<THREADS> te;
+  float zt[te.PER];                                // the student's logits at the teacher's entries
+  di_load_teacher<THREADS>(a, row, te);
+#pragma unroll
+  for (int i = 0; i < te.PER; ++i) zt[i] = te.id[i] >= 0 ? di_load1<BF>(z, te.id[i]) : 0.f;
+  const DiSum s = di_row_sum<BF, THREADS>(z, (int)a.V, a.inv_temp, sums);
   di_finish<THREADS>(a, row, s, te, zt, red);
 }
 
@@ -254,6 +261,16 @@ __device__ __forceinline__ DiPart di_part(const DistillArgs& a, int p) {
   const int64_t lo = (int64_t)p * a.part_cols;
   return DiPart{lo, min(lo + a.part_cols, (int64_t)a.V)};
 }
+
+// What fp32 rounds off lse is relative in every q: 2^-18 at 128, 2^-14 (of a bf16
+// result's 2^-9) at 2048. In rows whose lse is larger (all logits at the type's
+// lowest value, a large common offset, a low temperature) it would grow without
+// bound (q = 1 for 1 / V): one workgroup takes the row, forms its largest logit and
+// sum again as the loss has them, and writes all of it, so that dZ may still be Z.
+// 4096 such rows of 131072 bf16 logits 653 us for 449, 61 of 32003 13.5 for 6.8, 8
+// of 131072 41 for 8.
+template <bool OBF>
+constexpr float kDiFar = OBF ? 2048.f : 128.f;
 
 // The gradient: q of every entry is written first, then the teacher's entries
 // are written over it by the workgroup that owns their columns (their logits
@@ -267,24 +284,37 @@ k_distill_grad(DistillArgs a) {
   __shared__ float red[THREADS / 64];
   __shared__ int sid[kDistillMaxK];
   __shared__ float sp[kDistillMaxK];
+  __shared__ DiSum sums[THREADS / 64];
   const int64_t row = blockIdx.x / a.parts;
-  const DiPart part = di_part(a, blockIdx.x % a.parts);
+  DiPart part = di_part(a, blockIdx.x % a.parts);
   const int tid = threadIdx.x;
   const char* z = static_cast<const char*>(a.Z) + (row * a.ldz + part.lo) * DiType<BF>::BYTES;
-  char* out = static_cast<char*>(a.dZ) + (row * a.ldd + part.lo) * DiType<OBF>::BYTES;
-  const int cols = (int)(part.hi - part.lo), np = cols / P;
   DiTeacher<THREADS> te;
   float zt[te.PER];
   di_load_teacher<THREADS>(a, row, te);
+  auto load_logits = [&]() {
 #pragma unroll
-  for (int i = 0; i < te.PER; ++i) {
-    zt[i] = 0.f;
-    if (te.id[i] >= part.lo && te.id[i] < part.hi) zt[i] = di_load1<BF>(z, te.id[i] - part.lo);
-  }
+    for (int i = 0; i < te.PER; ++i) {
+      zt[i] = 0.f;
+      if (te.id[i] >= part.lo && te.id[i] < part.hi) zt[i] = di_load1<BF>(z, te.id[i] - part.lo);
+    }
+  };
+  load_logits();
   const float lse = a.lse_in[row], g = a.grad[row] * a.inv_temp;
   const float mass = di_probabilities<THREADS>(a, te, red);
   const bool none = mass == 0.f;                   // nothing to learn: zeros, whatever the logits are
   const float f = g * mass;
+  float top = 0.f, ll = lse;                       // log q = (z - top) / tau - ll
+  if (!none && !(fabsf(lse) <= kDiFar<OBF>)) {
+    if (part.lo > 0) return;                       // (all workgroups of the row come here)
+    part.hi = a.V;
+    load_logits();
+    const DiSum s = di_row_sum<BF, THREADS>(z, (int)a.V, a.inv_temp, sums);
+    top = di_ref(s.m);
+    ll = logf(s.l);
+  }
+  char* out = static_cast<char*>(a.dZ) + (row * a.ldd + part.lo) * DiType<OBF>::BYTES;
+  const int cols = (int)(part.hi - part.lo), np = cols / P;
 #pragma unroll
   for (int i = 0; i < te.PER; ++i) {
     const int k = tid + THREADS * i;
@@ -293,7 +323,7 @@ k_distill_grad(DistillArgs a) {
       sp[k] = te.p[i];
     }
   }
-  auto value = [&](float v) { return none ? 0.f : f * di_exp2(fmaf(v, a.inv_temp, -lse) * kLog2e); };
+  auto value = [&](float v) { return none ? 0.f : f * di_exp2(fmaf(v - top, a.inv_temp, -ll) * kLog2e); };
 #pragma unroll
   for (int i = 0; i < te.PER; ++i) zt[i] = value(zt[i]);
   __syncthreads();                                 // the teacher's logits are read

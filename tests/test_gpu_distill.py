@@ -174,6 +174,55 @@ def test_masked_entries_and_lowest_values():
             assert torch.isfinite(G.distill(Zm.cuda(), torch.from_numpy(one).cuda(), tm)[0]).all()
 
 
+@pytest.mark.parametrize("temp", [1.0, 0.02])
+@pytest.mark.parametrize("T,V", [(6, 100), (6, 20000), (1100, 2500)])   # one part a row, several, one of many rows
+def test_gradient_far_from_zero(T, V, temp):
+    """Rows whose lse is far from zero, where fp32's lse says little about the sum:
+    lowest values everywhere (uniform), in half of a row, large offsets, a low
+    temperature. Against the oracle on the logits less their largest, which changes
+    neither loss nor gradient. An exponent x = (z - m) / tau - log l is off by 6 u of
+    |x| + 2 log V (difference, tau, 1 / tau, fused product, log2 e, product; log l),
+    the exponential and its factors by 8 u, l as counted above; near rows
+    (|lse| <= 128, with a bf16 dZ 2048) by lse's error instead."""
+    for zdt in (BF16, F32):
+        low = torch.finfo(zdt).min
+        Z, ids, teacher, grad = inputs(V, T, V, 6, False, zdt)
+        ids[:] = np.arange(6) * 7 + 1
+        Z[0] = low
+        Z[1] += 1e4
+        Z[2] -= 1e5
+        Z[3, V // 2:] = low
+        Z[4] *= 1e3
+        z64 = arr(Z)
+        near = np.abs(L64.distill(z64, ids, teacher, temp, False)[1])
+        big = np.abs(z64).max(1) / temp
+        zs = z64 - z64.max(1, keepdims=True)
+        loss, lse, ps = L64.distill(zs, ids, teacher, temp, False)
+        ref = L64.distill_grad(zs, lse, ps, grad, temp)
+        x = np.abs(zs) / temp
+        f = (grad / temp)[:, None]
+        P = 2 * np.abs(teacher).max() / temp
+        rel_p = U32 * (4 * P + 6 / 256 + 20)
+        args = (torch.from_numpy(ids).cuda(), torch.from_numpy(teacher).cuda())
+        Zc, gc = Z.cuda(), torch.from_numpy(grad).cuda()
+        le = G.distill(Zc, *args, temperature=temp)[1]
+        for odt in (BF16, F32):
+            rel = 6 * (x + 2 * np.log(V)) + 8 + 3 * 30 + 4 + V / 256 + 64
+            rel += np.where(near <= (2048 if odt == BF16 else 128), 4 * (near + big), 0)[:, None]
+            e = (np.exp(-x - lse[:, None]) * (U32 * rel + rel_p) + 4 * U32 * np.abs(ref)) * f
+            e[:, ids[0]] += f * np.array([[p for _, p in row] for row in ps]) * (rel_p + 10 * U32)
+            # q below 2^-126, the smallest normal number, is 0 (the exponential has no subnormal results), which the
+            # factor grad / tau makes up to grad / tau 2^-126 of dZ (at tau = 0.02 2.7e-40 of an fp32 row 1 became 0)
+            e += f * 2.0 ** -126
+            d = G.distill_grad(Zc, *args, le, gc, temperature=temp, out_dtype=odt)
+            tol = e + ((UBF * (np.abs(ref) + e) + 2.0 ** -134) if odt == BF16 else U32 * np.abs(ref) + 2.0 ** -126)
+            assert np.all(np.abs(arr(d) - ref) <= tol)
+            if odt == zdt:
+                same = Zc.clone()
+                G.distill_grad(same, *args, le, gc, temperature=temp, out=same)
+                assert torch.equal(same, d)
+
+
 def test_repeated_ids_count_each_time():
     Z, ids, teacher, grad = inputs(5, 3, 4100, 600, True, F32)
     ids[:, ::2] = 17
