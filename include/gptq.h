@@ -425,8 +425,8 @@ gptq_status gptq_checkpoint_weight_grad(void *stream, const void *P, int32_t pdt
  * are those of gptq_expert_matmul (its matrix-vector form serves up to 48 rows an
  * expert here); the epilogue is computed in fp32 and rounded once. E = 1 and
  * offsets NULL: one dense layer. Rows from offsets[E] on are neither read nor
- * written in any matrix. Y may be the residual (same type and pitch); no other
- * output may overlap an input.
+ * written in any matrix. Y may be the residual (same type and pitch, refused
+ * with others); no other output may overlap an input.
  *   act: GPTQ_ACT_NONE z; _RELU max(z, 0) (NaN stays NaN); _GELU z Phi(z);
  * _GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2; _SILU z / (1 +
  * exp(-z)). Of minus infinity the last three are NaN.
@@ -447,7 +447,8 @@ gptq_status gptq_checkpoint_weight_grad(void *stream, const void *P, int32_t pdt
  * of dX. dX takes the weights as
  * gptq_expert_matmul_grad does: of two rounded factors, with a bf16 dX its error
  * is about 1.7 times what its own rounding gives (0.0029 against 0.0017 of it).
- * act' of relu is 0 at 0. dZ may be Z or, ungated, dY (bf16, same pitch).
+ * act' of relu is 0 at 0. dZ may be Z or, ungated, dY (bf16, same pitch; refused
+ * with others).
  * Workspace: gptq_linear_grad_workspace_bytes. Asynchronous.
  * ("El balance de errores de la inferencia de pocos bits", section 6: what a
  * fused kernel saves is the traffic between its parts.) */

@@ -1237,6 +1237,11 @@ static gptq_status linear_sizes(int64_t R, int64_t n, int64_t d, int32_t gated, 
   return expert_sizes(R, n, gated ? 2 * d : d, E, bits, group);
 }
 
+// out may be in where their elements lie alike (of one row the pitch does not matter).
+static bool in_place_ok(const void* out, int32_t odt, int64_t ldo, const void* in, int32_t idt, int64_t ldi, int64_t R) {
+  return out != in || (odt == idt && (ldo == ldi || R <= 1));
+}
+
 static gptq_status act_check(int32_t act) {
   return act >= GPTQ_ACT_NONE && act <= GPTQ_ACT_SILU ? GPTQ_OK : fail(GPTQ_EINVAL, "act must be a gptq_act");
 }
@@ -1291,6 +1296,8 @@ gptq_status gptq_linear(void* stream, const void* X, int32_t xdt, int64_t T, int
   a.ldy = ldy;
   a.ws = workspace;
   if ((st = check_ws(workspace, ws_bytes, linear_workspace(R, (int)E, n, m, group))) != GPTQ_OK) return st;
+  if (residual && !in_place_ok(Y, ydt, ldy, residual, rdt, ldr, R))
+    return fail(GPTQ_EINVAL, "Y may be the residual only with its type and pitch");
   HIP_TRY(launch_linear((hipStream_t)stream, a), "linear");
   return GPTQ_OK;
 }
@@ -1344,6 +1351,12 @@ gptq_status gptq_linear_grad(void* stream, const void* dY, int32_t dydt, int64_t
   if (linear_grad_threads(R, (int)E, d) > kMaxThreads) return fail(GPTQ_EINVAL, "R d is too large for one launch");
   if (dbias && ceil_div(m, 64) * 256 > kMaxThreads) return fail(GPTQ_EINVAL, "dbias is too wide for one launch");
   if ((st = check_ws(workspace, ws_bytes, need)) != GPTQ_OK) return st;
+  if (R > 0 && dZ) {
+    if (!straight && !in_place_ok(dZ, GPTQ_BF16, lddz, Z, zdt, ldz, R))
+      return fail(GPTQ_EINVAL, "dZ may be Z only with its type and pitch");
+    if ((gated && dZ == dY) || !in_place_ok(dZ, GPTQ_BF16, lddz, dY, dydt, ldy, R))
+      return fail(GPTQ_EINVAL, "dZ may be dY only without a gate, with its type and pitch");
+  }
   a.dY = dY;
   a.dy_bf16 = dydt == GPTQ_BF16;
   a.ldy = ldy;
@@ -1408,6 +1421,8 @@ gptq_status gptq_expert_layer(void* stream, const void* X, int32_t xdt, int64_t 
       mis(up_bias, GPTQ_F32) || mis(down_bias, GPTQ_F32) || mis(up_scales, GPTQ_F32) || mis(down_scales, GPTQ_F32))
     return fail(GPTQ_EINVAL, "a matrix is not aligned to its elements");
   if ((st = check_ws(workspace, ws_bytes, need)) != GPTQ_OK) return st;
+  if (residual && !in_place_ok(Y, ydt, ldy, residual, rdt, ldr, T))
+    return fail(GPTQ_EINVAL, "Y may be the residual only with its type and pitch");
   LayerArgs a = {};
   a.X = static_cast<const uint16_t*>(X);
   a.T = (int)T;

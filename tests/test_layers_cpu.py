@@ -242,6 +242,34 @@ def test_distill_refusals():
     assert fwd(T=0, Z=NULL) == 0 and bwd(T=0, Z=NULL, dZ=NULL) == 0
 
 
+def test_results_over_inputs_of_another_form_are_refused():
+    """A result may lie over an input only with its type and pitch, dZ over dY only
+    without a gate: otherwise values would be overwritten before they are read."""
+    G, lib = _lib()
+    p = [ctypes.c_void_p((i + 1) << 20) for i in range(8)]
+    A, B, C, D, E_, W, S, Q = p
+
+    def fwd(rdt=0, ldr=64, ydt=0, ldy=64, R=16):
+        return lib.gptq_linear(None, A, 0, 16, 128, 128, None, R, None, 1, Q, S, S, None, 64, 4, 64, 4, 0, B, rdt, ldr, None,
+                               0, 0, B, ydt, ldy, None, 0)
+
+    def layer(rdt=0, ldr=128, ydt=0, ldy=128, T=4):
+        return lib.gptq_expert_layer(None, A, 0, T, 128, 128, C, 2, 2, None, 4, Q, S, S, None, Q, S, S, None, 64, 4, 64, 4, 1,
+                                     B, rdt, ldr, B, ydt, ldy, W, 1 << 30)
+
+    def bwd(dY=A, Z=B, dZ=C, dydt=0, ldy=64, zdt=0, ldz=64, lddz=64, gated=0, R=16):
+        return lib.gptq_linear_grad(None, dY, dydt, ldy, Z, zdt, ldz, R, None, 1, Q, S, S, 64, 128, 4, 64, 4, gated, dZ, lddz,
+                                    None, D, 0, 128, W, 1 << 30)
+    for call, bad in [(fwd, dict(rdt=1)), (fwd, dict(ydt=1)), (fwd, dict(ldr=72)), (fwd, dict(ldy=65)), (fwd, dict(rdt=1, R=1)),
+                      (layer, dict(rdt=1)), (layer, dict(ydt=1)), (layer, dict(ldr=136)), (layer, dict(ldy=129)),
+                      (layer, dict(ydt=1, T=1)), (bwd, dict(dZ=B, zdt=1)), (bwd, dict(dZ=B, ldz=72)), (bwd, dict(dZ=B, lddz=65)),
+                      (bwd, dict(dZ=B, zdt=1, ldz=128, lddz=128, gated=1)), (bwd, dict(dZ=A, dydt=1)), (bwd, dict(dZ=A, ldy=72)),
+                      (bwd, dict(dZ=A, lddz=65)), (bwd, dict(dZ=A, ldy=128, ldz=128, lddz=128, gated=1)),
+                      (bwd, dict(dZ=A, ldy=128, ldz=128, lddz=128, gated=1, R=1))]:
+        assert call(**bad) == -1, bad
+        assert b"only with" in lib.gptq_last_error() or b"only without" in lib.gptq_last_error(), bad
+
+
 def test_binding_refuses_host_tensors():
     G, _ = _lib()
     import torch
