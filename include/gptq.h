@@ -529,7 +529,7 @@ gptq_status gptq_expert_layer(void *stream, const void *X, int32_t xdt, int64_t 
  * -infinity (masked entries) have q = 0; a row of nothing else has lse = -infinity
  * and a loss of NaN, unless it is padding. NaN and +infinity make their row NaN.
  * 1 <= K <= GPTQ_DISTILL_MAX_K, V <= 2^31 - 65536, temperature positive and
- * finite. Everything is fp32, in an order that does not depend on timing.
+ * finite, and log2(e) / temperature too. Everything is fp32, in an order that does not depend on timing.
  *
  * gptq_distill_grad: for grad (T fp32: d total / d loss[t]) and lse as
  * gptq_distill gave it,

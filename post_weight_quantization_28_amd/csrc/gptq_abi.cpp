@@ -1465,9 +1465,9 @@ static gptq_status distill_args(const void* Z, int32_t zdt, int64_t T, int64_t V
   if (T > kMaxThreads / 256) return fail(GPTQ_EINVAL, "T may be at most 2^24 - 2");
   if (V > kMaxRows) return fail(GPTQ_EINVAL, "V may be at most 2^31 - 65536");
   if (K < 1 || K > GPTQ_DISTILL_MAX_K) return fail(GPTQ_EINVAL, "K must be in [1, GPTQ_DISTILL_MAX_K]");
-  const float inv = 1.f / temperature;
-  if (!(temperature > 0.f) || !(inv > 0.f) || inv - inv != 0.f || temperature - temperature != 0.f)
-    return fail(GPTQ_EINVAL, "temperature must be positive and finite, and its inverse too");
+  const float inv = 1.f / temperature, c = inv * 1.4426950408889634f;   // the kernels form 2^(c z)
+  if (!(temperature > 0.f) || !(inv > 0.f) || c - c != 0.f || temperature - temperature != 0.f)
+    return fail(GPTQ_EINVAL, "temperature must be positive and finite, and log2(e) / temperature too");
   if (log_probs != 0 && log_probs != 1) return fail(GPTQ_EINVAL, "log_probs must be 0 or 1");
   if (T > 0) {
     if (ldz < V) return fail(GPTQ_EINVAL, "ldz < V");

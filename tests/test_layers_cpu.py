@@ -242,6 +242,17 @@ def test_distill_refusals():
     assert fwd(T=0, Z=NULL) == 0 and bwd(T=0, Z=NULL, dZ=NULL) == 0
 
 
+def test_temperatures_whose_exponents_have_no_factor_are_refused():
+    """From 2.94e-39 to 4.23e-39 1 / tau is in fp32's range and log2(e) / tau, the
+    exponential's factor, is not: infinity times the 0 of the largest logit."""
+    G, lib = _lib()
+    for temp in (3e-39, 4.2e-39):
+        assert lib.gptq_distill(None, FAKE, 0, 4, 100, 100, FAKE, FAKE, 3, temp, 0, FAKE, FAKE) == -1
+        assert b"temperature" in lib.gptq_last_error()
+        assert lib.gptq_distill_grad(None, FAKE, 0, 4, 100, 100, FAKE, FAKE, 3, temp, 0, FAKE, FAKE, FAKE, 0, 100) == -1
+        assert b"temperature" in lib.gptq_last_error()
+
+
 def test_results_over_inputs_of_another_form_are_refused():
     """A result may lie over an input only with its type and pitch, dZ over dY only
     without a gate: otherwise values would be overwritten before they are read."""
