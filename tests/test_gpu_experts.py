@@ -284,6 +284,16 @@ def test_expert_matmul(T, k, E, d, n, group, drop, only, gathered, bits):
         assert np.array_equal(Y[off[-1]:], before[off[-1]:])
 
 
+@pytest.mark.parametrize("bits", [4, 3, 2])
+@pytest.mark.parametrize("case", [
+    (3, 1, 1, 70, 4736, 128, 0.0, None, False),      # 37 groups, 10 for each of four waves: scales come 8 at a time
+    (30, 2, 5, 40, 5120, 128, 0.1, None, True),      # 40 groups, tiles of 16 rows
+    (7, 2, 3, 33, 9472, 256, 0.0, None, True),
+], ids=str)
+def test_expert_matmul_of_many_groups_a_wave(case, bits):
+    test_expert_matmul(*case, bits)
+
+
 def test_scales_of_any_size():
     """Zero, negative, tiny and huge scales, in tiles of every size: exact
     zeros for zero scales, and where a unit cannot be carried (outside

@@ -155,6 +155,28 @@ def test_linear(T, k, E, d, n, group, drop, only, gathered, name, gated, bits):
             assert np.array_equal(arr(Z)[off[-1]:], zbefore[off[-1]:])
 
 
+# A wave of the matrix-vector form holds the scales of 8 groups at a time: sizes at
+# which it comes back for more, in four loads of one and one of four.
+MANY_GROUPS = [   # T, k, E, d, n, group, drop, only, gathered
+    (3, 1, 1, 70, 10880, 128, 0.0, None, False),     # eight waves, 11 groups each; 85 groups of a row
+    (12, 1, 1, 33, 9728, 128, 0.0, None, False),     # 76 groups, 10 each
+    (5, 2, 4, 40, 18688, 256, 0.0, None, True),      # eight waves, 10 groups of 256 each
+    (40, 1, 1, 40, 10880, 128, 0.0, None, False),    # three tiles of 16 rows
+]
+
+
+@pytest.mark.parametrize("bits", [4, 3, 2])
+@pytest.mark.parametrize("case", MANY_GROUPS, ids=str)
+def test_linear_of_many_groups_a_wave(case, bits):
+    for name, gated in ENDS[:2]:
+        test_linear(*case, name, gated, bits)
+
+
+def test_linear_of_many_groups_in_many_workgroups():
+    """More than 512 of them: four waves, 10 groups each."""
+    test_linear(500, 1, 32, 135, 4736, 128, 0.0, None, True, "silu", True, 4)
+
+
 GRADS = [   # R, E, d, n, group, cuts (None: one layer without offsets)
     (1, 1, 32, 64, 32, None), (1, 1, 1, 32, 32, None), (3, 2, 70, 128, 128, [1, 3]), (50, 3, 65, 96, 96, [20, 20, 45]),
     (130, 1, 64, 160, 32, None), (400, 2, 257, 320, 64, [129, 400]), (300, 2, 100, 256, 256, [0, 290]),
@@ -658,6 +680,23 @@ def test_expert_layer(T, k, E, n, d, group, drop, bias, bits):
         assert np.all(np.abs(arr(Y) - ref) <= e + last(ydt, np.abs(ref) + e))
         assert torch.all(out[:, :2] == 7) and torch.all(out[:, 2 + n:] == 7)
         assert torch.equal(G.expert_layer(*args, out_dtype=ydt, **kw), Y)
+
+
+# As above: 8 groups a time in the first launch, 16 in the second, whose waves have
+# all of K where the tiles are as many as they are.
+LAYERS_OF_MANY_GROUPS = [
+    (20, 2, 20, 128, 2432, 128, 0.0, False), (20, 2, 20, 128, 2560, 128, 0.1, True),   # 19 and 20 groups of a row
+    (18, 2, 20, 64, 1312, 32, 0.0, True), (18, 2, 20, 96, 1920, 96, 0.1, False), (20, 2, 20, 64, 2688, 64, 0.0, False),
+    (2, 2, 3, 4736, 128, 128, 0.0, False), (6, 2, 4, 5120, 128, 128, 0.0, True),     # 37 and 40 groups for four waves
+    (1, 1, 2, 128, 34816, 128, 0.0, False),          # one tile: 272 groups for 16 or 8 waves
+    (3, 300, 9, 128, 2432, 128, 0.95, False),        # more than 512 slots, eight waves
+]
+
+
+@pytest.mark.parametrize("bits", [4, 3, 2])
+@pytest.mark.parametrize("case", LAYERS_OF_MANY_GROUPS, ids=str)
+def test_expert_layer_of_many_groups_a_wave(case, bits):
+    test_expert_layer(*case, bits)
 
 
 def test_expert_layer_agrees_with_its_parts():
