@@ -6,7 +6,9 @@
 
 namespace gq {
 
-// 1 / (1 + exp(-x)) within a few ulps; exp's overflow gives 0.
+// 1 / (1 + exp(-x)), relative to itself within 8 2^-24 for positive x and (1.3 |x| +
+// 8) 2^-24 for negative ones (the rounding of x log2 e is absolute in the exponent);
+// exp's overflow gives 0.
 __device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
 
 constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2 / pi): 1 + tanh(v) = 2 sigmoid(2 v)
@@ -36,8 +38,8 @@ __device__ __forceinline__ float act_both(int act, float z, float& slope) {
     case GPTQ_ACT_GELU: {
       // Phi(-|z|) = erfc(|z| / sqrt 2) / 2 with an exponential that the slope needs
       // too: exp(x^2) erfc(x) is t times a polynomial in t = 1 / (1 + 0.3925 x)
-      // within 8e-8 of itself for all x up to 46 (fitted to the least largest
-      // relative error; 4e-7 in fp32), so that the tail is as good as the middle.
+      // within 1.1e-7 of itself for all x up to 46 (fitted to the least largest
+      // relative error; 5e-7 in fp32), so that the tail is as good as the middle.
       const float a = fabsf(c), e = __expf(-0.5f * a * a);
       const float t = __builtin_amdgcn_rcpf(fmaf(0.3925f * 0.70710678118654752f, a, 1.f));
       float q = fmaf(t, 0.052698649466f, -0.207043841481f);

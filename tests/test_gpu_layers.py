@@ -259,6 +259,19 @@ def test_gelu_in_its_tail():
     assert np.all(np.abs(got[4096:] - z * cdf) <= rel * np.abs(z * cdf))
 
 
+def test_silu_in_its_tail():
+    """z from the bias alone, in fp32: relative to itself silu is off by 1.3 |z| u for
+    z < 0 (the rounding of z log2 e, and of log2 e itself, in the exponent), and by the
+    exponential's, the sum's, the reciprocal's, the product's and the result's 10 u."""
+    z = np.linspace(-80, 20, 8192).astype(np.float32)
+    packed = cuda_layers(*layers(1, 1, 8192, 32, 4, 32))
+    X = torch.zeros((1, 32), dtype=BF16, device="cuda")
+    Y = arr(G.linear(X, *packed, 4, 32, bias=torch.from_numpy(z[None]).cuda(), act="silu", out_dtype=F32))[0]
+    z64 = z.astype(np.float64)
+    ref = z64 / (1 + np.exp(-z64))
+    assert np.all(np.abs(Y - ref) <= U32 * (1.3 * np.maximum(-z64, 0) + 10) * np.abs(ref))
+
+
 def test_linear_grad_of_a_plain_layer_needs_no_copy():
     """No activation, no gate: dY stands for dZ, Z is not read; an fp32 dY is
     rounded into a new dZ; an expert without rows has a bias gradient of zero."""

@@ -40,6 +40,22 @@ def test_activations():
     assert abs(L64.act("gelu_tanh", np.array([1.0]))[0][0] - 0.5 * (1 + math.tanh(math.sqrt(2 / math.pi) * 1.044715))) < 1e-15
 
 
+def test_fit_of_the_normal_tail():
+    """The polynomial that linear_grad's gelu forms its tail with, as csrc/act.h has
+    it, against exp(x^2) erfc(x): relative error 1.1e-7 for x up to 46, where the
+    exponential beside it has long underflowed."""
+    import re
+    from scipy.special import erfcx
+    path = os.path.join(os.path.dirname(__file__), "..", "post_weight_quantization_28_amd", "csrc", "act.h")
+    text = open(path).read()
+    first = re.search(r"float q = fmaf\(t, ([-\d.]+)f, ([-\d.]+)f\)", text)
+    fit = [float(c) for c in first.groups()] + [float(c) for c in re.findall(r"q = (?:t \* )?fmaf\(t, q, ([-\d.]+)f\)", text)]
+    assert len(fit) == 9
+    x = np.linspace(0, 46, 100001)
+    t = 1 / (1 + 0.3925 * x)
+    assert np.abs(t * np.polyval(np.float32(fit).astype(np.float64), t) / erfcx(x) - 1).max() < 1.1e-7
+
+
 def _tiny(E, m, n, seed=0):
     r = np.random.default_rng(seed)
     codes = r.integers(0, 16, (E, m, n)).astype(np.uint8)
