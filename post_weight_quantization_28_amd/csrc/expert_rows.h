@@ -220,23 +220,6 @@ __device__ __forceinline__ void mv_transpose(uint32_t (&w)[4]) {
   mv_swap16(w[2], w[3]);
 }
 
-// Values of the N lane groups j mod N (N = 1, 2, 4), each in all lane groups.
-template <int N>
-__device__ __forceinline__ void mv_spread(uint32_t v, uint32_t (&out)[N]) {
-  out[0] = v;
-  if constexpr (N == 2) {
-    out[1] = v;
-    mv_swap16(out[0], out[1]);
-  } else if constexpr (N == 4) {
-    out[2] = v;
-    mv_swap32(out[0], out[2]);
-    out[1] = out[0];
-    out[3] = out[2];
-    mv_swap16(out[0], out[1]);
-    mv_swap16(out[2], out[3]);
-  }
-}
-
 // c / d for the same d again and again (d and c d below 2^32 or a division).
 struct MvDiv {
   uint32_t d, m;       // m = ceil(2^32 / d): exact while c d < 2^32

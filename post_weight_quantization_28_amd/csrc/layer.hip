@@ -4,7 +4,7 @@
 //   Y[t] = residual[t] + sum_j w[t, j] (D_e h[t, j] + b2_e)
 //
 // Bound by reading the packed weights of the experts in use once. The slots
-// (t, j) of one expert go through the matrix-vector product together, up to 16
+// (t, j) of one expert go through the matrix-vector product together, up to 8
 // to a tile (v_mfma_f32_16x16x32_bf16). Every workgroup of the first launch finds
 // the slots of its tile for itself, which spares the launches that would order
 // rows, move them, and add them up again.
@@ -15,8 +15,8 @@
 //    share the tiles (and K, when the tiles are fewer than the waves), leave
 //    their results by slot in LDS, and the slots of a token are added in their
 //    order: no result depends on timing.
-// Tiles are of 4 slots for up to 4 tokens and of 8 beyond (16 take LDS from the
-// second launch's 16 waves). Measured at 4 bits, groups of 128 (both launches of
+// Tiles are of 4 slots for up to 4 tokens and where Y is fp32 (h then has three
+// pieces), of 8 beyond (16 take LDS from the second launch's 16 waves). Measured at 4 bits, groups of 128 (both launches of
 // a call among others): one token through 2 of 8 experts of 3 x 11008 x 4096, 146
 // MB, 43 us (25 + 18); one through 8 of 64 of 3 x 1408 x 2048, 37 MB, 19 us (10 +
 // 11); 32 tokens through these 64, 294 MB, 107 us (55 + 47). Every workgroup
