@@ -132,19 +132,6 @@ __device__ __forceinline__ uint32_t pack_exact(float a, float b) {
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
 
-template <int BITS>
-__device__ __forceinline__ ex_bf16x8_t mv_window(const uint32_t* __restrict__ chunk, int j, float z) {
-  const int base = 8 * BITS * j, wi = base >> 5;
-  uint64_t v = chunk[wi];
-  if constexpr (BITS == 3) v |= (uint64_t)chunk[min(wi + 1, BITS - 1)] << 32;
-  v >>= base & 31;
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = (float)(uint32_t)((v >> (BITS * i)) & ((1u << BITS) - 1u)) - z;
-  const ex_u32x4_t u = {pack_exact(f[0], f[1]), pack_exact(f[2], f[3]), pack_exact(f[4], f[5]), pack_exact(f[6], f[7])};
-  return __builtin_bit_cast(ex_bf16x8_t, u);
-}
-
 // The bits of a code in each half of a word, and the patterns of 16.0 around
 // them: one from a scalar and one from a vector register, so that masking and
 // setting them is one instruction (v_and_or_b32).
@@ -470,35 +457,6 @@ struct MvWave {
     }
   }
 };
-
-// tot += the pieces beg, beg + step, .. below npieces, chunk by chunk (2 and 3
-// bits in groups that are no multiples of 128).
-template <int BITS, int OB, int NP>
-__device__ __forceinline__ void mv_chunks(const MvRows<OB>& rows, const MvK<false>& k, int beg, int step,
-                                          const uint16_t* __restrict__ xrow, int64_t xplane, ex_f32x4_t (&tot)[OB]) {
-  const int j = (threadIdx.x & 63) >> 4;
-  for (int p = beg; p < k.npieces; p += step) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = 4 * p + i;
-      if (c >= k.nchunks) break;
-      const uint32_t g = k.div((uint32_t)c);
-      ex_bf16x8_t a[NP];
-#pragma unroll
-      for (int q = 0; q < NP; ++q) a[q] = *reinterpret_cast<const ex_bf16x8_t*>(xrow + q * xplane + (int64_t)c * 32 + 8 * j);
-#pragma unroll
-      for (int b = 0; b < OB; ++b) {
-        const ex_bf16x8_t w = mv_window<BITS>(rows.q[b] + (int64_t)c * BITS, j, (float)rows.z[b][g]);
-        ex_f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < NP; ++q) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q], w, acc, 0, 0, 0);
-        const float s = rows.s[b][g];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) tot[b][r] = fmaf(s, acc[r], tot[b][r]);
-      }
-    }
-  }
-}
 
 // Scales and zero points of four groups can be loaded at once.
 __device__ __forceinline__ bool mv_vec(const float* scales, const uint8_t* zeros, int64_t n, int group) {

@@ -35,10 +35,11 @@ namespace gq {
 //    free as long as X's fragment follows it.
 //  * Other groups: a product must not mix groups, so step i takes chunk i of
 //    the piece and lane j its codes 8 j .. + 7, and the sum is scaled after
-//    every chunk. At 4 bits a lane still loads a chunk in one go and four lane
-//    swaps hand out its words (360 rows over 64 experts, 322 x 4608 in groups
-//    of 32: 73 us with a word per load, 36 us so); 2 and 3 bits go chunk by
-//    chunk.
+//    every chunk. A lane still loads a chunk in one go and four lane swaps hand
+//    out its quarters (360 rows over 64 experts, 322 x 4608 in groups of 32: 30
+//    us at 4 bits; at 3 and 2 bits, whose words were loaded chunk by chunk
+//    before, 97 and 73 to 33 and 31; two of 11008 x 4096 for one token each, groups
+//    of 64, 94 and 73 to 26 and 25).
 //  * 4 bits: a code in bits 3..6 of the bf16 pattern of 16 is the number
 //    16 + q, so one shift and one and-or give two codes (pairs i, i + 4: X's
 //    fragment is permuted alike), one operation per code against three with
@@ -61,8 +62,7 @@ k_expert_mv(const uint16_t* __restrict__ X, int T, int64_t n, int64_t ldx, const
             const int32_t* __restrict__ offsets, int E, int R, const uint32_t* __restrict__ qw,
             const float* __restrict__ scales, const uint8_t* __restrict__ zeros, int64_t d_out, int group,
             void* __restrict__ Y, int ybf16, int64_t ldy) {
-  constexpr bool CHUNKS = BITS < 4 && !WIDE;             // a load per chunk, no LDS (TILE 16)
-  __shared__ __align__(16) uint8_t smem[WAVES][CHUNKS ? 16 : MvWave<BITS, WIDE, OB, 1, TILE>::BYTES];
+  __shared__ __align__(16) uint8_t smem[WAVES][MvWave<BITS, WIDE, OB, 1, TILE>::BYTES];
   __shared__ float red[WAVES][OB][4][64];
   const Seg sg = find_tile(offsets, E, R, TILE, blockIdx.y);
   if (sg.e < 0) return;
@@ -78,11 +78,8 @@ k_expert_mv(const uint16_t* __restrict__ X, int T, int64_t n, int64_t ldx, const
   for (int b = 0; b < OB; ++b) tot[b] = (ex_f32x4_t){0.f, 0.f, 0.f, 0.f};
   const int nrows = min(sg.hi - sg.row0, TILE);
   auto xrow = [&](int r) { return X + source_row(rows, sg.row0 + r, T) * ldx; };
-  if constexpr (CHUNKS)
-    mv_chunks<BITS, OB, 1>(w, MvK<false>(n, group), wave, WAVES, xrow(min(li, nrows - 1)), 0, tot);
-  else
-    mv_sum<BITS, WIDE, OB, 1, TILE>(w, n, group, wave, WAVES, nrows, 0, lds_addr(smem[wave]),
-                                    mv_vec(scales, zeros, n, group), xrow, tot);
+  mv_sum<BITS, WIDE, OB, 1, TILE>(w, n, group, wave, WAVES, nrows, 0, lds_addr(smem[wave]),
+                                  mv_vec(scales, zeros, n, group), xrow, tot);
 #pragma unroll
   for (int b = 0; b < OB; ++b)
 #pragma unroll
@@ -956,7 +953,7 @@ static void ring_go(hipStream_t s, const ExpertArgs& a, int grad) {
 template <int BITS>
 static void fwd_bits(hipStream_t s, const ExpertArgs& a) {
   const int bm = expert_bm(a, 0);
-  if (bm == 16 && (a.R > 8 * a.E || (BITS < 4 && a.group % 128 != 0))) mv_go<BITS, 16>(s, a);
+  if (bm == 16 && a.R > 8 * a.E) mv_go<BITS, 16>(s, a);
   else if (bm == 16) mv_go<BITS, 8>(s, a);
   else if (bm == 256) ring_go(s, a, 0);
   else if (bm == 64) mm_group<BITS, ExTile64>(s, a);

@@ -289,6 +289,9 @@ def test_expert_matmul(T, k, E, d, n, group, drop, only, gathered, bits):
     (3, 1, 1, 70, 4736, 128, 0.0, None, False),      # 37 groups, 10 for each of four waves: scales come 8 at a time
     (30, 2, 5, 40, 5120, 128, 0.1, None, True),      # 40 groups, tiles of 16 rows
     (7, 2, 3, 33, 9472, 256, 0.0, None, True),
+    (20, 2, 8, 50, 4608, 96, 0.1, None, True),       # groups that share pieces, tiles of 8 rows
+    (60, 1, 4, 33, 4160, 64, 0.0, None, False),      # tiles of 16, half a piece at the end
+    (3, 1, 1, 40, 4128, 32, 0.0, None, True),
 ], ids=str)
 def test_expert_matmul_of_many_groups_a_wave(case, bits):
     test_expert_matmul(*case, bits)
