@@ -825,11 +825,15 @@ static int small_bm(int64_t R, int E, int64_t cols, int grad, bool pieces) {
 }
 
 // Rows of a tile: 16 is the matrix-vector form, 256 the ring kernel.
-//  * Matrix-vector form and 64-row tiles, 4 bits: 8 experts of 4096 x 4096 with
-//    4, 16, 20 and 32 rows each 26, 45, 54, 71 and 42, 46, 44, 49 us; 64 of
-//    1408 x 2048 with 4, 16, 20 and 24 rows 29, 57, 65, 74 and 53, 58, 59, 63;
-//    groups of 64 with 16 rows 58 and 57, 77 and 74. (3 bits stay ahead longer:
-//    24 rows 58 and 74, 74 and 108.)
+//  * Matrix-vector form and 64-row tiles, 4 bits, captured: 8 experts of 4096 x
+//    4096 with 1, 8, 16, 20 and 32 rows each 20, 22, 26, 38, 39 and 46, 46, 47, 44,
+//    46 us; 64 of 1408 x 2048 with 1, 8, 16, 20 and 32 30, 33, 41, 64, 70 and 60, 58,
+//    59, 59, 61; groups of 64 with 16 and 24 rows 37, 50 and 51, 51, 48, 81 and 64,
+//    65. 3 bits with 16 and 24 rows 30, 46 and 87, 79, 41, 71 and 112, 114; 2 bits
+//    29, 44 and 52, 48, 39, 67 and 65, 65. So from 17 rows on either may be ahead,
+//    by what a second tile costs and whether the tiles have K in parts (two of
+//    11008 x 4096 with 32 rows 31 and 41, at 3 bits 37 and 71): here the border is 16
+//    for all of them; linear, in linear.hip, goes by that.
 //  * Ring and 128-row tiles: 8 experts of 4096 x 4096 with 512, 640 and 1024
 //    rows each 247, 251, 381 and 219, 258, 392 us, gradient 222, 228, 348 and
 //    219, 257, 391; 8 of 11008 x 4096 506, 562, 901 and 568, 661, 1030. Fewer
