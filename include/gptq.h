@@ -446,7 +446,10 @@ gptq_status gptq_checkpoint_weight_grad(void *stream, const void *P, int32_t pdt
  * dY). The residual's gradient is dY, the gradient of X by token is gptq_combine
  * of dX. dX takes the weights as
  * gptq_expert_matmul_grad does: of two rounded factors, with a bf16 dX its error
- * is about 1.7 times what its own rounding gives (0.0029 against 0.0017 of it).
+ * is about 1.7 times what its own rounding gives (0.0029 against 0.0017 of it). An
+ * fp32 dX takes the weights' whole 24 bits, at three times the work, but the same
+ * dZ, whose one rounding is then its error (0.0017, 2^-8 of each term at most): it
+ * is no fp32 gradient.
  * act' of relu is 0 at 0. dZ may be Z or, ungated, dY (bf16, same pitch; refused
  * with others).
  * Workspace: gptq_linear_grad_workspace_bytes. Asynchronous.
@@ -529,7 +532,8 @@ gptq_status gptq_expert_layer(void *stream, const void *X, int32_t xdt, int64_t 
  * -infinity (masked entries) have q = 0; a row of nothing else has lse = -infinity
  * and a loss of NaN, unless it is padding. NaN and +infinity make their row NaN.
  * 1 <= K <= GPTQ_DISTILL_MAX_K, V <= 2^31 - 65536, temperature positive and
- * finite, and log2(e) / temperature too. Everything is fp32, in an order that does not depend on timing.
+ * finite, and log2(e) / temperature too. Everything is fp32, in an order that does
+ * not depend on timing.
  *
  * gptq_distill_grad: for grad (T fp32: d total / d loss[t]) and lse as
  * gptq_distill gave it,

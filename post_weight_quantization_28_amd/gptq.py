@@ -698,7 +698,8 @@ def linear_grad(dY, Z, qweight, scales, zeros, bits, group, n, act="none", gated
     and the kept Z, dX = dZ W_hat (R x n, for the sorted rows), dbias ((E x) m
     fp32) the sums of dZ over each segment, or None. dZ is also P of
     checkpoint_weight_grad. Z may be None where act is none and nothing is
-    gated. The residual's gradient is dY."""
+    gated. The residual's gradient is dY. An fp32 dX takes the weights unrounded,
+    at three times the work, but dZ in bf16 all the same."""
     lib = load()
     gp, ldy = _rows2d(dY, "dY", _FLOATS)
     R, d = dY.shape
